@@ -34,7 +34,10 @@ EXPORTED = ("kda_status_string", "kda_version", "kda_chunk_fwd_workspace_size",
             "kda_prep_fwd", "kda_prep_fwd_state", "kda_layer_replay", "kda_post_fwd",
             "kda_read_chunk_stats", "kda_chunk_fwd_transitions", "kda_state_combine",
             "kda_chunk_bwd", "kda_chunk_bwd_workspace_size", "kda_chunk_bwd_sched",
-            "kda_chunk_bwd_workspace_size_sched")
+            "kda_chunk_bwd_workspace_size_sched",
+            "kda_latent_fwd", "kda_latent_fwd_workspace_size", "kda_latent_bwd",
+            "kda_latent_bwd_workspace_size", "kda_latent_decode",
+            "kda_latent_decode_workspace_size", "kda_cache_write", "kda_cache_copy_pages")
 
 _lib = None
 
@@ -119,6 +122,29 @@ def library() -> ctypes.CDLL:
         lib.kda_decode_step.restype = ctypes.c_int
         lib.kda_decode_step.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32,
                                         ctypes.c_int, vp, vp]
+        f32, ci = ctypes.c_float, ctypes.c_int
+        for name in ("kda_latent_fwd_workspace_size", "kda_latent_bwd_workspace_size"):
+            getattr(lib, name).restype = ci
+            getattr(lib, name).argtypes = [i32, i64, i64, i32, i32, i32, i32, ci,
+                                           ctypes.POINTER(sz)]
+        expanded = [vp, vp, vp, vp, i64, i64, i64, i64, vp, vp, i32, i64, i64, i32, i32, i32, i32,
+                    ci, f32, ci]
+        lib.kda_latent_fwd.restype = ci
+        lib.kda_latent_fwd.argtypes = expanded + [vp, vp, vp, sz, vp]
+        lib.kda_latent_bwd.restype = ci
+        lib.kda_latent_bwd.argtypes = expanded + [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64,
+                                                  vp, sz, vp]
+        lib.kda_latent_decode_workspace_size.restype = ci
+        lib.kda_latent_decode_workspace_size.argtypes = [i32, i32, i32, i32, i32, ci,
+                                                         ctypes.POINTER(sz)]
+        lib.kda_latent_decode.restype = ci
+        lib.kda_latent_decode.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32,
+                                          i32, ci, f32, vp, vp, vp, sz, vp]
+        lib.kda_cache_write.restype = ci
+        lib.kda_cache_write.argtypes = [vp, vp, i64, i64, i64, vp, vp, vp, vp, i32, i32, i32, i64,
+                                        i32, i32, i32, vp, vp]
+        lib.kda_cache_copy_pages.restype = ci
+        lib.kda_cache_copy_pages.argtypes = [vp, vp, vp, i32, i32, i32, i64, vp, vp]
         _lib = lib
     return _lib
 

@@ -542,6 +542,179 @@ int kda_layer_replay(float *state, void *conv_state, const void *q_raw, const vo
 int kda_post_fwd(const void *o, const void *g, const float *gamma, int64_t n_tokens, int32_t H,
                  int32_t dv, int dtype, void *out, void *stream);
 
+/* ------------------------------------------------------------------ latent attention
+ *
+ * The softmax-attention layers of the hybrid stack ("Kimi K3: 架构、训练与系统
+ * 全景解析", section 2: KDA and latent-attention layers 3 : 1): keys and values
+ * of all heads come from one latent vector per token.  Two forms of the same
+ * attention:
+ *   expanded (training, prompts): the per-head keys k and values v have been
+ *     computed from the latents by the caller's projection, and an optional
+ *     rotary part k_rope is one row per token shared by all heads.  For query i
+ *     and key j of a head
+ *         s_ij = scale * (q_i[0:128] . k_j + q_i[128:128+dr] . k_rope_j)
+ *         o_i  = sum_j p_ij v_j,  p_i = softmax over the allowed j,
+ *         lse_i = log sum_j exp(s_ij)
+ *   absorbed (decode): the key projection is folded into the query and the value
+ *     projection is applied after it, so that a head reads the cached latent row
+ *     itself: s_tj = scale * (q_t . c_j) over 512 + dr channels,
+ *     o_t = sum_j p_tj c_j[0:512].
+ * dr is 0 (no positions) or 64.  bf16 inputs and outputs; scores, softmax
+ * statistics and every sum in fp32 (the probabilities, and in the gradient also
+ * ds, are rounded to bf16 as operands of their matrix products).  A row that may
+ * see no key gets o = 0 and lse = -inf.  Rows and keys outside a sequence never
+ * reach its result, whatever they hold; inside a sequence all keys must be
+ * finite (a masked key enters its product with a zero weight).
+ */
+
+/*
+ * Bytes of workspace of kda_latent_fwd: the device status word and device
+ * copies of host cu_seqlens arrays.
+ * Errors: KDA_ERR_INVALID_ARG (NULL bytes, negative sizes, n_seqs < 1, H <= 0),
+ * KDA_ERR_UNSUPPORTED (dk or dv != 128, dr not 0 or 64, dtype not KDA_BF16).
+ */
+int kda_latent_fwd_workspace_size(int32_t n_seqs, int64_t n_q, int64_t n_k, int32_t H, int32_t dk,
+                                  int32_t dr, int32_t dv, int dtype, size_t *bytes);
+
+/*
+ * Expanded form over packed variable-length sequences.
+ *   q       [n_q, H, dk + dr] bf16
+ *   k       [n_k, H, dk] bf16 with k_token_stride / k_head_stride (elements;
+ *           multiples of 8): k and v may be two views of one [n_k, H, 256]
+ *           projection
+ *   v       [n_k, H, dv] bf16 with v_token_stride / v_head_stride
+ *   k_rope  [n_k, dr] bf16, NULL if and only if dr = 0
+ *   cu_seqlens_q, cu_seqlens_k  [n_seqs + 1] int32, prefix sums of the query
+ *           and key counts, each host or device memory (rules as kda_chunk_fwd:
+ *           host arrays are validated here; device arrays in the kernel, which
+ *           then writes nothing and records KDA_ERR_INVALID_ARG in the status).
+ *           NULL, if n_seqs = 1: one sequence of all the rows
+ *   causal  non-zero: query i of a sequence with nq queries and nk keys sees
+ *           keys j <= i + nk - nq (the queries are the sequence's last tokens;
+ *           with nk > nq a prompt continues over its prefix)
+ *   scale   finite and positive
+ *   out     [n_q, H, dv] bf16;  lse [n_q, H] fp32
+ *   workspace  kda_latent_fwd_workspace_size() bytes, 16-byte aligned; its status
+ *           word is cleared at the start of the call (kda_read_device_status)
+ * Alignment: q, k, v, k_rope, out 16 bytes; lse 4 bytes.  At most 65535 heads,
+ * 2^31 - 129 tokens.
+ * Errors (before any launch): KDA_ERR_INVALID_ARG (NULL, sizes, alignment,
+ * strides that are no multiple of 8 or smaller than a row, scale, out or lse
+ * overlapping an input, bad host cu_seqlens), KDA_ERR_UNSUPPORTED,
+ * KDA_ERR_WORKSPACE, KDA_ERR_CUDA.
+ */
+int kda_latent_fwd(const void *q, const void *k, const void *v, const void *k_rope,
+                   int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                   int64_t v_head_stride, const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                   int32_t n_seqs, int64_t n_q, int64_t n_k, int32_t H, int32_t dk, int32_t dr,
+                   int32_t dv, int dtype, float scale, int causal, void *out, float *lse,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace of kda_latent_bwd (status, cu_seqlens copies, per-row statistics,
+ * per-head gradients of the shared rotary key).  Errors as above. */
+int kda_latent_bwd_workspace_size(int32_t n_seqs, int64_t n_q, int64_t n_k, int32_t H, int32_t dk,
+                                  int32_t dr, int32_t dv, int dtype, size_t *bytes);
+
+/*
+ * The gradient of kda_latent_fwd for a given gradient d_out [n_q, H, dv] of its
+ * output; out and lse are what the forward pass returned.
+ *   p_ij = exp(s_ij - lse_i), ds_ij = p_ij (d_out_i . v_j - d_out_i . out_i)
+ *   dv_j = sum_i p_ij d_out_i,  dq_i = scale sum_j ds_ij [k_j; k_rope_j],
+ *   d[k_j; k_rope_j] = scale sum_i ds_ij q_i, summed over all heads for k_rope.
+ *   dq [n_q, H, dk + dr], d_k_rope [n_k, dr] (NULL if dr = 0), contiguous;
+ *   d_k, d_v like k and v, with strides of their own (they may be two views of
+ *   one tensor).
+ * Every element of every gradient is written exactly once, by one thread, from
+ * sums in a fixed order: results do not vary between calls.  Other rules as
+ * kda_latent_fwd; no output may overlap an input or another output.
+ */
+int kda_latent_bwd(const void *q, const void *k, const void *v, const void *k_rope,
+                   int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                   int64_t v_head_stride, const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                   int32_t n_seqs, int64_t n_q, int64_t n_k, int32_t H, int32_t dk, int32_t dr,
+                   int32_t dv, int dtype, float scale, int causal, const void *out,
+                   const float *lse, const void *d_out, void *dq, void *d_k, void *d_v,
+                   void *d_k_rope, int64_t dk_token_stride, int64_t dk_head_stride,
+                   int64_t dv_token_stride, int64_t dv_head_stride, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/* Workspace of kda_latent_decode: the status word and the partial results of
+ * sequences whose keys are shared out over several CTAs.  It does not depend on
+ * the sequence lengths.  Errors as kda_latent_fwd_workspace_size. */
+int kda_latent_decode_workspace_size(int32_t B, int32_t T, int32_t H, int32_t dc, int32_t dr,
+                                     int dtype, size_t *bytes);
+
+/*
+ * Absorbed form over a paged cache: the last T tokens of each of B sequences
+ * (T = 1: one decode step; T > 1: drafted tokens) attend to the sequence's
+ * cached rows, their own among them.
+ *   q           [B, T, H, dc + dr] bf16, dc = 512
+ *   cache       [n_pages, page_size, dc + dr] bf16; page_size a multiple of 16
+ *   block_table [B, max_pages] int32, DEVICE: page of positions
+ *               [i * page_size, (i + 1) * page_size) of a sequence; entries past
+ *               a sequence's last page are not read
+ *   seq_lens    [B] int32, DEVICE: cached rows of each sequence, the T new ones
+ *               included
+ *   tree_mask   [B, T] int64, DEVICE, or NULL.  NULL: token t sees positions up
+ *               to its own, seq_len - T + t.  Else token t sees all positions
+ *               before seq_len - T and, among the last T, position
+ *               seq_len - T + j where bit j of its mask is set (a draft's
+ *               ancestors and itself); T <= 64
+ *   out         [B, T, H, dc] bf16;  lse [B, T, H] fp32 or NULL
+ * A sequence length that is negative or beyond max_pages * page_size, or a page
+ * id outside [0, n_pages), records KDA_ERR_INVALID_ARG in the status; nothing
+ * outside the pool is read, and that sequence's output is undefined.
+ * Alignment: q, cache, out 16 bytes; block_table, seq_lens, lse 4; tree_mask 8.
+ * Errors as kda_latent_fwd (n_pages * page_size at most 2^31 - 1,
+ * T * H at most 2^24).
+ */
+int kda_latent_decode(const void *q, const void *cache, const int32_t *block_table,
+                      const int32_t *seq_lens, const int64_t *tree_mask, int32_t B, int32_t T,
+                      int32_t H, int32_t dc, int32_t dr, int32_t n_pages, int32_t page_size,
+                      int32_t max_pages, int dtype, float scale, void *out, float *lse,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Rows of a paged cache [L, n_pages, page_size, row_bytes] (any element type),
+ * all L layers in one call.  For every sequence b, with n = n_write[b] clamped
+ * to [0, T] (n_write NULL: n = T), rows i = 0 .. n - 1 go to positions
+ * start[b] + i:
+ *   rows given:  row path[b, i] of the sequence (path NULL: row i) of rows
+ *                [L, B, T] with layer, sequence and token strides in bytes
+ *                (appending new tokens, or the accepted ones of a draft)
+ *   rows NULL:   the cached row at position start[b] + path[b, i] (compaction in
+ *                place of the accepted path of a draft tree whose T rows lie at
+ *                start[b] ...); path[b, 0 .. n - 1] strictly increasing
+ * block_table [B, max_pages], start [B], path [B, T], n_write [B]: int32, DEVICE.
+ * A sequence with a position outside its table or the pool, or with a path entry
+ * outside [0, T) or not increasing (compaction), has nothing moved, and
+ * KDA_ERR_INVALID_ARG is recorded in *status (DEVICE int32 or NULL; not cleared
+ * by the call).  No two sequences of a call may write the same page row.
+ * row_bytes and the strides are multiples of 16; cache and rows 16-byte aligned.
+ * T at most 1024.
+ * Errors (before any launch): KDA_ERR_INVALID_ARG (NULL, sizes, alignment, rows
+ * overlapping the cache, neither rows nor path), KDA_ERR_CUDA.
+ */
+int kda_cache_write(void *cache, const void *rows, int64_t rows_layer_stride,
+                    int64_t rows_seq_stride, int64_t rows_token_stride, const int32_t *block_table,
+                    const int32_t *start, const int32_t *path, const int32_t *n_write, int32_t L,
+                    int32_t n_pages, int32_t page_size, int64_t row_bytes, int32_t B, int32_t T,
+                    int32_t max_pages, int32_t *status, void *stream);
+
+/*
+ * Whole pages of a pool [L, n_pages, page_bytes] copied within every layer:
+ * page dst[i] becomes a copy of page src[i], i < n (a forked request's private
+ * page; a cached KDA state snapshot copied to a running state; pages moved
+ * together).  src, dst: int32, DEVICE.  The dst pages are distinct and none is
+ * another pair's src (the pairs run side by side).  A pair with a page outside
+ * [0, n_pages) copies nothing and records KDA_ERR_INVALID_ARG in *status (DEVICE
+ * int32 or NULL; not cleared).  page_bytes is a multiple of 16, cache 16-byte
+ * aligned.
+ * Errors: KDA_ERR_INVALID_ARG, KDA_ERR_CUDA.
+ */
+int kda_cache_copy_pages(void *cache, const int32_t *src, const int32_t *dst, int32_t n, int32_t L,
+                         int32_t n_pages, int64_t page_bytes, int32_t *status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
