@@ -232,7 +232,7 @@ int kda_latent_bwd(const void *q, const void *k, const void *v, const void *k_ro
 }
 
 static int check_decode(int32_t B, int32_t T, int32_t H, int32_t dc, int32_t dr, int dtype) {
-  if (B < 0 || T <= 0 || H <= 0 || dc <= 0 || dr < 0 || (int64_t)T * H > (1 << 24) ||
+  if (B < 0 || B > 65535 || T <= 0 || H <= 0 || dc <= 0 || dr < 0 || (int64_t)T * H > (1 << 24) ||
       (int64_t)B * T * H > 0x7fffffffLL)
     return KDA_ERR_INVALID_ARG;
   if (dc != kda::kLatentC || (dr != 0 && dr != kda::kLatentRope) || dtype != KDA_BF16)

@@ -173,74 +173,6 @@ __global__ void bwd_kv_kernel(LatentArgs a) {
   }
 }
 
-// Block per (row of the batch, head): its warps take every eighth key and are joined.
-__global__ void decode_kernel(LatentDecodeArgs a) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int64_t rh = blockIdx.x;
-  const int bt = (int)(rh / a.H), b = bt / a.T, t = bt % a.T;
-  const int W = kLatentC + a.dr;
-  int n = a.seq_lens[b];
-  if (n < 0 || n > (int64_t)a.max_pages * a.page_size) {
-    if (threadIdx.x == 0) record_device_status(a.status, KDA_ERR_INVALID_ARG, 0, b, 0);
-    n = 0;
-  }
-  const bf16 *q = static_cast<const bf16 *>(a.q) + rh * W;
-  float4 qc[4], o[4];
-  for (int c = 0; c < 4; ++c) {
-    qc[c] = ld4(q + 128 * c + 4 * lane);
-    o[c] = make_float4(0, 0, 0, 0);
-  }
-  const float2 qr = a.dr ? ld2(q + kLatentC + 2 * lane) : make_float2(0, 0);
-  const uint64_t seen = a.tree_mask ? (uint64_t)a.tree_mask[bt] : 0;
-  float m = -CUDART_INF_F, l = 0;
-  for (int j = w; j < n; j += kRows) {
-    const int d = j - (n - a.T);  // draft index
-    if (d >= 0 && (a.tree_mask ? !(seen >> d & 1) : d > t)) continue;
-    const int32_t pg = a.block_table[(int64_t)b * a.max_pages + j / a.page_size];
-    if (pg < 0 || pg >= a.n_pages) {
-      if (lane == 0) record_device_status(a.status, KDA_ERR_INVALID_ARG, 1, b, j);
-      continue;
-    }
-    const bf16 *row = static_cast<const bf16 *>(a.cache) +
-                      ((int64_t)pg * a.page_size + j % a.page_size) * W;
-    float4 kc[4];
-    float x = 0;
-    for (int c = 0; c < 4; ++c) {
-      kc[c] = ld4(row + 128 * c + 4 * lane);
-      x += dot4(qc[c], kc[c]);
-    }
-    if (a.dr) {
-      const float2 r = ld2(row + kLatentC + 2 * lane);
-      x += qr.x * r.x + qr.y * r.y;
-    }
-    x = warp_sum(x) * a.scale;
-    const float mn = fmaxf(m, x), ms = mn == -CUDART_INF_F ? 0.f : mn;
-    const float cor = expf(m - ms), p = expf(x - ms);
-    l = l * cor + p;
-    for (int c = 0; c < 4; ++c) {
-      o[c].x *= cor; o[c].y *= cor; o[c].z *= cor; o[c].w *= cor;
-      axpy(o[c], p, kc[c]);
-    }
-    m = mn;
-  }
-  __shared__ float sm[kRows], sl[kRows];
-  __shared__ float so[kRows][kLatentC];
-  if (lane == 0) { sm[w] = m; sl[w] = l; }
-  for (int c = 0; c < 4; ++c)
-    *reinterpret_cast<float4 *>(&so[w][128 * c + 4 * lane]) = o[c];
-  __syncthreads();
-  float mx = -CUDART_INF_F, sum = 0;
-  for (int k = 0; k < kRows; ++k) mx = fmaxf(mx, sm[k]);
-  const float ms = mx == -CUDART_INF_F ? 0.f : mx;
-  for (int k = 0; k < kRows; ++k) sum += sl[k] * expf(sm[k] - ms);
-  for (int c = threadIdx.x; c < kLatentC; c += blockDim.x) {
-    float v = 0;
-    for (int k = 0; k < kRows; ++k) v += so[k][c] * expf(sm[k] - ms);
-    static_cast<bf16 *>(a.out)[rh * kLatentC + c] = __float2bfloat16(sum == 0.f ? 0.f : v / sum);
-  }
-  if (a.lse && threadIdx.x == 0) a.lse[rh] = sum == 0.f ? -CUDART_INF_F : mx + logf(sum);
-}
-
 unsigned tiles(int64_t n, int32_t n_seqs) { return (unsigned)(n / kRows + n_seqs); }
 
 }  // namespace
@@ -257,16 +189,6 @@ cudaError_t launch_latent_bwd(const LatentArgs &a, cudaStream_t stream) {
   if (a.n_q > 0)
     bwd_q_kernel<<<dim3(tiles(a.n_q, a.n_seqs), a.H), 32 * kRows, 0, stream>>>(a);
   if (a.n_k > 0) bwd_kv_kernel<<<tiles(a.n_k, a.n_seqs), 32 * kRows, 0, stream>>>(a);
-  return cudaGetLastError();
-}
-
-size_t latent_decode_scratch_bytes(int32_t, int32_t, int32_t, int32_t) { return 0; }
-
-cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t stream) {
-  const int64_t blocks = (int64_t)a.B * a.T * a.H;
-  if (blocks == 0) return cudaSuccess;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  decode_kernel<<<(unsigned)blocks, 32 * kRows, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
