@@ -97,9 +97,16 @@ __device__ __forceinline__ int seq_len(const Params &p, int b) {
 }
 __device__ __forceinline__ int key_tiles(int n) { return (n + kTile - 1) / kTile; }
 
-// First tile of CTA c of G when the list has `total` tiles.
+// First tile of CTA c of G when the list has `total` tiles: the first total % G
+// CTAs take one more than the others.
 __device__ __forceinline__ int cta_begin(int c, int G, int total) {
-  return (int)((int64_t)c * total / G);
+  const int each = total / G, more = total - each * G;
+  return c * each + min(c, more);
+}
+// The CTA of tile x.
+__device__ __forceinline__ int cta_of(int x, int G, int total) {
+  const int each = total / G, more = total - each * G, wide = more * (each + 1);
+  return x < wide ? x / (each + 1) : more + (x - wide) / max(each, 1);
 }
 
 // Walks the CTA's tiles sequence by sequence; every role does so by itself.
@@ -676,74 +683,68 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
 }
 
 // Joins the parts of sequences that several CTAs shared, in the list's order, and
-// writes the rows of empty sequences.  Block per (sequence, row tile, 8 rows).
-constexpr int kJoinRows = 8;
+// writes the rows of empty sequences.  A warp per row and 128 channels; the parts
+// are read kJoinBatch at a time, all loads of a batch in flight.
+constexpr int kJoinRows = 2, kJoinBatch = 8;
 template <int N>
-__global__ void __launch_bounds__(32 * kJoinRows)
+__global__ void __launch_bounds__(128 * kJoinRows)
 kda_latent_join_kernel(const Params p) {
-  const int lane = threadIdx.x & 31;
-  const int b = blockIdx.y, r = blockIdx.x * kJoinRows + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = blockIdx.y, r = blockIdx.x * kJoinRows + (warp >> 2);
+  const int ch = (warp & 3) * 128 + 4 * lane;
+  const bool lead = threadIdx.x % 128 == 0;
   pdl_wait();
   if (r >= p.T * p.H) return;
   const int before = p.before[b], k = p.before[b + 1] - before, all = p.before[p.B];
-  __nv_bfloat16 *out = p.out + ((int64_t)b * p.T * p.H + r) * kLatentC;
-  if (k == 0) {
-    for (int c = 0; c < 4; ++c)
-      *reinterpret_cast<uint2 *>(out + 128 * c + 4 * lane) = make_uint2(0, 0);
-    if (p.lse && lane == 0) p.lse[(int64_t)b * p.T * p.H + r] = -CUDART_INF_F;
+  const int64_t row = (int64_t)b * p.T * p.H + r;
+  uint2 *out = reinterpret_cast<uint2 *>(p.out + row * kLatentC + ch);
+  if (k <= 0) {
+    *out = make_uint2(0, 0);
+    if (p.lse && lead) p.lse[row] = -CUDART_INF_F;
     return;
   }
-  // CTA of a tile x: the c with begin(c) <= x < begin(c + 1)
-  auto owner = [&](int x) {
-    int c = (int)(((int64_t)x * p.G + p.G - 1) / max(all, 1));
-    c = min(max(c, 0), p.G - 1);
-    while (c > 0 && cta_begin(c, p.G, all) > x) --c;
-    while (c + 1 < p.G && cta_begin(c + 1, p.G, all) <= x) ++c;
-    return c;
-  };
-  const int first = owner(before), last = owner(before + k - 1);
+  const int first = cta_of(before, p.G, all), last = cta_of(before + k - 1, p.G, all);
   if (first == last) return;             // one CTA had it all and wrote the output
   const int rt = r / N, col = r % N;
-  auto slot_of = [&](int c) {
-    // a CTA's first segment is in slot 0, its last in slot 1
-    return ((int64_t)rt * p.G + c) * 2 + (c == first && cta_begin(c, p.G, all) < before ? 1 : 0);
-  };
+  // a CTA's first segment is in slot 0, its last in slot 1
+  const int64_t slot0 = ((int64_t)rt * p.G + first) * 2;
+  const int late = cta_begin(first, p.G, all) < before ? 1 : 0;
+  const int parts = last - first + 1;
+  auto slot_of = [&](int i) { return slot0 + 2 * i + (i == 0 ? late : 0); };
   float ref = kNoRef;
-  for (int c = first + lane; c <= last; c += 32)
-    if (cta_begin(c + 1, p.G, all) > cta_begin(c, p.G, all)) {
-      const float y = p.part_ml[slot_of(c) * 192 + col];
-      ref = y > ref || y != y ? y : ref;
-    }
+  for (int i = lane; i < parts; i += 32) {
+    const float y = p.part_ml[slot_of(i) * 192 + col];
+    ref = y > ref || y != y ? y : ref;
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     const float y = __shfl_xor_sync(0xffffffffu, ref, o);
     ref = y > ref || y != y ? y : ref;
   }
   float sum = 0.f;
-  float4 acc[4];
+  float4 acc = make_float4(0, 0, 0, 0);
+  for (int i0 = 0; i0 < parts; i0 += kJoinBatch) {
+    float4 x[kJoinBatch];
+    float f[kJoinBatch], l[kJoinBatch];
 #pragma unroll
-  for (int c = 0; c < 4; ++c) acc[c] = make_float4(0, 0, 0, 0);
-  for (int c = first; c <= last; ++c) {
-    if (cta_begin(c + 1, p.G, all) == cta_begin(c, p.G, all)) continue;
-    const int64_t slot = slot_of(c);
-    const float f = ex2(p.part_ml[slot * 192 + col] - ref);
-    sum += f * p.part_ml[slot * 192 + 96 + col];
-    const float *o = p.part_o + (slot * N + col) * kLatentC;
+    for (int j = 0; j < kJoinBatch; ++j)
+      if (i0 + j < parts) {
+        const int64_t slot = slot_of(i0 + j);
+        x[j] = *reinterpret_cast<const float4 *>(p.part_o + (slot * N + col) * kLatentC + ch);
+        f[j] = p.part_ml[slot * 192 + col];
+        l[j] = p.part_ml[slot * 192 + 96 + col];
+      }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float4 x = *reinterpret_cast<const float4 *>(o + 128 * q + 4 * lane);
-      acc[q].x += f * x.x; acc[q].y += f * x.y; acc[q].z += f * x.z; acc[q].w += f * x.w;
-    }
+    for (int j = 0; j < kJoinBatch; ++j)
+      if (i0 + j < parts) {
+        const float w = ex2(f[j] - ref);
+        sum += w * l[j];
+        acc.x += w * x[j].x; acc.y += w * x[j].y; acc.z += w * x[j].z; acc.w += w * x[j].w;
+      }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    *reinterpret_cast<uint2 *>(out + 128 * q + 4 * lane) =
-        make_uint2(pack_bf16x2(acc[q].x * inv, acc[q].y * inv),
-                   pack_bf16x2(acc[q].z * inv, acc[q].w * inv));
-  if (p.lse && lane == 0)
-    p.lse[(int64_t)b * p.T * p.H + r] =
-        sum == 0.f ? -CUDART_INF_F : (ref + __log2f(sum)) * kLn2;
+  *out = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (p.lse && lead) p.lse[row] = sum == 0.f ? -CUDART_INF_F : (ref + __log2f(sum)) * kLn2;
 }
 
 // Rows of a CTA: the fewest tiles of at most 96 rows, each as narrow as they allow.
@@ -782,7 +783,7 @@ cudaError_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorM
   const unsigned gx = (unsigned)((p.T * p.H + kJoinRows - 1) / kJoinRows);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(gx, (unsigned)p.B);
-  cfg.blockDim = dim3(32 * kJoinRows);
+  cfg.blockDim = dim3(128 * kJoinRows);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

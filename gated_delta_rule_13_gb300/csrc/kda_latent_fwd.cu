@@ -1,0 +1,458 @@
+// Latent attention in its expanded form (kda_latent_fwd), tcgen05 / TMEM / TMA,
+// sm_103a.
+//
+// Per (sequence, head): o_i = sum_j softmax_j(scale [q_i] . [k_j; k_rope_j]) v_j
+// over the allowed keys.  A 256 x 128 tile of (query, key) pairs costs
+// 2 * 256 * 128 * (128 + dr + 128) operations, 2,560 cycles of an SM's tensor
+// cores at dr = 64, and reads 80 KB of keys and values: the matrix rate is the
+// bound, then the exponentials (32,768 a tile).
+//
+// One CTA takes 256 consecutive queries of a head, as two tiles of 128.  While one
+// tile's softmax runs on four warps, the tensor cores work for the other tile:
+//   S_t = Q_t K^T     (shared-memory operands, 128 x 128 fp32 in TMEM)
+//   P_t               bf16, written by the softmax over S_t's own columns
+//   O_t += P_t V      (P_t from TMEM)
+// so TMEM holds exactly S_0, S_1, O_0, O_1.  A thread owns a query row.  Its
+// exponents are taken against a reference that only moves when a score exceeds it
+// by more than 8 (log2): O_t is then rescaled in TMEM, which after the first
+// tiles hardly ever happens.
+//
+// Keys and values stream through a ring of 16 KB slots: 64-channel blocks of 128
+// keys, 64-key x 128-channel blocks of values.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <string.h>
+
+#include "kda_latent_tc.cuh"
+
+namespace kda {
+namespace {
+
+using namespace latent;
+
+constexpr int kRows = 256, kKeys = 128;
+constexpr int kThreads = 384;            // two softmax warpgroups; loader, MMA, cleaner, spare
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
+constexpr uint32_t kSlotBytes = 16384;
+constexpr uint32_t kSmemMax = 232448;
+constexpr float kSlack = 8.f;            // log2 units a score may exceed its reference by
+// 168 registers a thread at launch: 256 x 208 + 128 x 88 = 384 x 168
+constexpr uint32_t kLaunchRegs = 168, kSoftmaxRegs = 208, kIssueRegs = 88;
+constexpr int kMaxSlots = 10;
+
+struct Shared {
+  uint64_t full[kMaxSlots], empty[kMaxSlots], clean[kMaxSlots];
+  uint64_t q_full[2], s_full[2], p_ready[2], o_full[2], clean_req, fin;
+  uint32_t tmem, load_pos;
+  int abort;
+  SeqTile tile;
+};
+
+template <int DR>
+constexpr uint32_t q_bytes() { return kRows * (kLatentD + DR) * 2; }
+template <int DR>
+constexpr int slots() {
+  const int n = (int)((kSmemMax - 1024 - sizeof(Shared) - q_bytes<DR>()) / kSlotBytes);
+  return n > kMaxSlots ? kMaxSlots : n;
+}
+template <int DR>
+constexpr uint32_t smem_bytes() {
+  return 1024 + q_bytes<DR>() + slots<DR>() * kSlotBytes + sizeof(Shared);
+}
+
+struct Params {
+  const int32_t *cu_q, *cu_k;
+  int32_t n_seqs, H, tiles;
+  int64_t n_q, n_k;
+  float scale2;
+  int causal;
+  __nv_bfloat16 *out;
+  float *lse;
+  DeviceStatus *status;
+};
+
+template <int DR>
+__global__ void __launch_bounds__(kThreads, 1)
+kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
+                      const __grid_constant__ CUtensorMap map_k,
+                      const __grid_constant__ CUtensorMap map_r,
+                      const __grid_constant__ CUtensorMap map_v, const Params p) {
+  constexpr int S = slots<DR>();
+  constexpr int KB = (kLatentD + DR) / 64;   // 64-channel blocks of a key
+  constexpr int PER = KB + 2;                // slots of a key tile
+  constexpr uint32_t kRing = q_bytes<DR>();
+  constexpr uint32_t kQTile = 128 * 128;     // bytes of a 128-row block
+  constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false);
+  constexpr uint32_t ID_PV = idesc_bf16(128, 128, false, true);
+
+  extern __shared__ unsigned char raw[];
+  const uint32_t base = round_up_1k(smem_u32(raw));
+  unsigned char *const tiles = raw + (base - smem_u32(raw));
+  Shared &m = *reinterpret_cast<Shared *>(tiles + kRing + S * kSlotBytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int head = blockIdx.x / p.tiles;
+
+  if (warp == kCleanWarp) {
+    const SeqTile f = find_seq_tile(p.cu_q, p.cu_k, p.n_seqs, p.n_q, p.n_k, kRows, false,
+                                    blockIdx.x % p.tiles);
+    if (lane == 0) m.tile = f;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&m.full[i], 1);
+      mbar_init(&m.empty[i], 1);
+      mbar_init(&m.clean[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&m.q_full[t], 1);
+      mbar_init(&m.s_full[t], 1);
+      mbar_init(&m.p_ready[t], 4);
+      mbar_init(&m.o_full[t], 1);
+    }
+    mbar_init(&m.clean_req, 1);
+    mbar_init(&m.fin, 1);
+    m.abort = 0;
+    m.load_pos = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    prefetch_tensormap(&map_q);
+    prefetch_tensormap(&map_k);
+    prefetch_tensormap(&map_v);
+    if (DR) prefetch_tensormap(&map_r);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&m.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = m.tmem;
+  const SeqTile st = m.tile;
+  if (st.bad && blockIdx.x == 0 && tid == 0)
+    record_device_status(p.status, KDA_ERR_INVALID_ARG, 1, 0, 0);
+
+  // Longest first: the last queries of a sequence see the most keys.
+  const int row0 = (st.n_tiles - 1 - st.tile) * kRows;   // of the sequence
+  // Key tiles of the two query tiles (the second never has fewer).
+  auto key_tiles = [&](int t) {
+    const int first = row0 + 128 * t;
+    if (st.seq < 0 || first >= st.nq) return 0;
+    int n = st.nk;
+    if (p.causal) n = min(n, min(first + 128, st.nq) + st.nk - st.nq);
+    return n <= 0 ? 0 : (n + kKeys - 1) / kKeys;
+  };
+  const int nt[2] = {key_tiles(0), key_tiles(1)};
+  const int n_iter = max(nt[0], nt[1]);
+  const int last_live = min(kKeys, st.nk - (n_iter - 1) * kKeys);  // keys of the last tile
+  const int halves_last = last_live > 64 ? 2 : 1;
+  const WaitCtx cx{&m.abort, p.status, (int)blockIdx.x};
+
+  if (warp >= 8) {
+    setmaxnreg_dec<kIssueRegs>();
+    if (warp == kLoadWarp && lane == 0 && n_iter > 0) {
+      // ---- loader
+      auto load_q = [&](int t) {
+        mbar_arrive_expect_tx(&m.q_full[t], KB * kQTile);
+        for (int kb = 0; kb < KB; ++kb)
+          tma_load_3d_u(base + (t * KB + kb) * kQTile, &map_q, &m.q_full[t], 64 * kb, head,
+                        st.q0 + row0 + 128 * t);
+      };
+      uint32_t pos = 0;
+      bool ok = true;
+      auto slot = [&](int step) {  // waits for the next slot
+        const uint32_t s = pos % S;
+        if (pos >= S) ok = wait_or_abort(cx, &m.empty[s], (pos / S - 1) & 1, 10, step);
+        return s;
+      };
+      if (nt[0] > 0) load_q(0);
+      for (int i = 0; ok && i < n_iter; ++i) {
+        const int key = st.k0 + i * kKeys;
+        for (int kb = 0; kb < KB; ++kb) {
+          const uint32_t s = slot(i);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&m.full[s], kSlotBytes);
+          const uint32_t dst = base + kRing + s * kSlotBytes;
+          if (kb < 2)
+            tma_load_3d_u(dst, &map_k, &m.full[s], 64 * kb, head, key);
+          else
+            tma_load_2d(dst, &map_r, &m.full[s], 64 * (kb - 2), key);
+          ++pos;
+        }
+        if (i == 0 && nt[1] > 0) load_q(1);
+        const int halves = i + 1 < n_iter ? 2 : halves_last;
+        for (int hf = 0; ok && hf < halves; ++hf) {
+          const uint32_t s = slot(i);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&m.full[s], kSlotBytes);
+          const uint32_t dst = base + kRing + s * kSlotBytes;
+          tma_load_3d_u(dst, &map_v, &m.full[s], 0, head, key + 64 * hf);
+          tma_load_3d_u(dst + 8192, &map_v, &m.full[s], 64, head, key + 64 * hf);
+          ++pos;
+        }
+      }
+      if (ok) mbar_arrive(&m.clean_req);
+      m.load_pos = pos;
+    } else if (warp == kMmaWarp && lane == 0 && n_iter > 0) {
+      // ---- MMA issue
+      bool ok = true;
+      const int last_user = nt[1] > 0 ? 1 : 0;   // releases the slots
+      auto issue_s = [&](int t, int i) {
+        for (int kb = 0; ok && kb < KB; ++kb) {
+          const uint32_t pos = (uint32_t)i * PER + kb, s = pos % S;
+          ok = wait_or_abort(cx, &m.full[s], (pos / S) & 1, 20, i);
+          if (!ok) return;
+          const uint32_t a = base + (t * KB + kb) * kQTile, b = base + kRing + s * kSlotBytes;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_ss(tm + 128 * t, sdesc_sw128(a + ks * 32, 16, 1024),
+                    sdesc_sw128(b + ks * 32, 16, 1024), ID_S, kb + ks > 0);
+          if (t == last_user) umma_commit(&m.empty[s]);
+        }
+        umma_commit(&m.s_full[t]);
+      };
+      auto issue_pv = [&](int t, int i) {
+        const int halves = i + 1 < n_iter ? 2 : halves_last;
+        for (int hf = 0; ok && hf < halves; ++hf) {
+          const uint32_t pos = (uint32_t)i * PER + KB + hf, s = pos % S;
+          ok = wait_or_abort(cx, &m.full[s], (pos / S) & 1, 21, i);
+          // the last tile's rows past the sequence have been zeroed
+          if (ok && i + 1 == n_iter && last_live < 64 * (hf + 1))
+            ok = wait_or_abort(cx, &m.clean[s], 0, 22, i);
+          if (!ok) return;
+          const uint32_t b = base + kRing + s * kSlotBytes;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_ts(tm + 256 + 128 * t, tm + 128 * t + 32 * hf + 8 * ks,
+                    sdesc_sw128(b + ks * 2048, 8192, 1024), ID_PV, i + hf + ks > 0);
+          if (t == last_user) umma_commit(&m.empty[s]);
+        }
+      };
+      for (int t = 0; ok && t < 2; ++t)
+        if (nt[t] > 0) {
+          ok = wait_or_abort(cx, &m.q_full[t], 0, 23, t);
+          if (ok) issue_s(t, 0);
+        }
+      for (int i = 0; ok && i < n_iter; ++i)
+        for (int t = 0; ok && t < 2; ++t) {
+          if (i >= nt[t]) continue;
+          ok = wait_or_abort(cx, &m.p_ready[t], i & 1, 24, i);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(t, i);
+          if (!ok) break;
+          if (i + 1 < nt[t])
+            issue_s(t, i + 1);
+          else
+            umma_commit(&m.o_full[t]);
+        }
+    } else if (warp == kCleanWarp && n_iter > 0 && (last_live & 63) != 0) {
+      // ---- cleaner: value rows past the sequence's end are another sequence's, and
+      // may hold anything; zero them (0 * NaN would reach the sum).  The loader asks
+      // once the copies of the last tile are under way.
+      bool ok = wait_or_abort(cx, &m.clean_req, 0, 30, n_iter);
+      const uint32_t pos = (uint32_t)(n_iter - 1) * PER + KB + halves_last - 1, s = pos % S;
+      ok = ok && wait_or_abort(cx, &m.full[s], (pos / S) & 1, 31, n_iter);
+      if (__all_sync(0xffffffffu, ok)) {
+        const int from = last_live & 63;
+        const uint32_t dst = base + kRing + s * kSlotBytes + from * 128;
+        for (int j = lane; j < (64 - from) * 8; j += 32) {
+          st_shared_v4(dst + j * 16, 0, 0, 0, 0);
+          st_shared_v4(dst + 8192 + j * 16, 0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m.clean[s]);
+      }
+    }
+  } else {
+    setmaxnreg_inc<kSoftmaxRegs>();
+    // ---- softmax and output: thread = query row
+    const int t = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t tm_s = tm + lanes + 128 * t, tm_o = tm + lanes + 256 + 128 * t;
+    const int row = row0 + 128 * t + r;                  // of the sequence
+    // keys this row sees
+    int limit = st.nk;
+    if (p.causal) limit = min(limit, row + st.nk - st.nq + 1);
+    float ref = kNoRef, l = 0.f;
+    bool ok = true;
+    for (int i = 0; ok && i < nt[t]; ++i) {
+      ok = __all_sync(0xffffffffu, wait_or_abort(cx, &m.s_full[t], i & 1, 40, i));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t x[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(tm_s + 32 * c, x[c]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld_wait(x[c]);
+      const int seen = limit - i * kKeys;                // columns below it are allowed
+      if (__any_sync(0xffffffffu, seen < kKeys)) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (32 * c + j >= seen) x[c][j] = __float_as_uint(-CUDART_INF_F);
+      }
+      float mx[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        mx[c] = __uint_as_float(x[c][0]);
+#pragma unroll
+        for (int j = 1; j < 32; ++j) mx[c] = fmaxf(mx[c], __uint_as_float(x[c][j]));
+      }
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale2;
+      if (__any_sync(0xffffffffu, top > ref + kSlack)) {
+        const float now = fmaxf(ref, top), f = ex2(ref - now);
+        ref = now;
+        l *= f;
+        if (i > 0) {
+          // S of this tile was issued after the product of the tile before, so its
+          // completion covers that product
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tm_o + 32 * c, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st32(tm_o + 32 * c, o);
+          }
+        }
+      }
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          const float a = ex2(fmaf(__uint_as_float(x[c][j]), p.scale2, -ref));
+          const float b = ex2(fmaf(__uint_as_float(x[c][j + 1]), p.scale2, -ref));
+          sum[(j >> 1) & 3] += a + b;
+          pk[j / 2] = pack_bf16x2(a, b);
+        }
+        tmem_st16(tm_s + 16 * c, pk);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.p_ready[t]);
+    }
+    // ---- output: O / l through this warp's rows of its own query tile's buffer
+    // (all products with Q are done), so that rows leave whole
+    const bool live = st.seq >= 0 && row0 + 128 * t < st.nq;
+    if (ok && nt[t] > 0)
+      ok = __all_sync(0xffffffffu, wait_or_abort(cx, &m.o_full[t], 0, 41, n_iter));
+    if (ok && live) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const uint32_t buf = base + t * KB * kQTile + (warp & 3) * 32 * 256;
+      if (nt[t] > 0) tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        if (nt[t] > 0) {
+          tmem_ld32(tm_o + 32 * c, o);
+          tmem_ld_wait(o);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {   // 16-byte pieces, rotated by the row
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[j] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * j]) * inv,
+                               __uint_as_float(o[8 * q + 2 * j + 1]) * inv);
+          st_shared_v4(buf + lane * 256 + (((4 * c + q) ^ (lane & 15)) << 4), w[0], w[1], w[2],
+                       w[3]);
+        }
+      }
+      __syncwarp();
+      const int64_t first = st.q0 + row0 + 128 * t + (warp & 3) * 32;
+#pragma unroll 4
+      for (int k = 0; k < 16; ++k) {
+        const int rr = 2 * k + (lane >> 4), piece = lane & 15;
+        const uint4 v = ld_shared_v4(buf + rr * 256 + ((piece ^ (rr & 15)) << 4));
+        if (row - lane + rr < st.nq)
+          *reinterpret_cast<uint4 *>(p.out + ((first + rr) * p.H + head) * kLatentD + 8 * piece) = v;
+      }
+      if (row < st.nq)
+        p.lse[(st.q0 + row) * (int64_t)p.H + head] =
+            l == 0.f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
+    }
+  }
+
+  __syncwarp();
+  __syncthreads();
+  if (m.abort) {  // nothing in flight outlives the CTA
+    if (tid == 32 * kLoadWarp) {
+      const uint32_t pos = m.load_pos;
+      for (uint32_t k = pos > S ? pos - S : 0; k < pos; ++k)
+        mbar_wait(&m.full[k % S], (k / S) & 1, kWaitNs);
+      for (int t = 0; t < 2; ++t)
+        if (pos > 0 && nt[t] > 0 && (t == 0 || pos >= KB)) mbar_wait(&m.q_full[t], 0, kWaitNs);
+    }
+    if (tid == 32 * kMmaWarp) {
+      umma_commit(&m.fin);
+      mbar_wait(&m.fin, 0, kWaitNs);
+    }
+    __syncthreads();
+  }
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tmem_dealloc(tm, 512);
+  }
+}
+
+template <int DR>
+cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
+  CUtensorMap mq, mk, mr, mv;
+  const cuuint64_t W = kLatentD + DR, H = a.H;
+  const cuuint64_t qd[3] = {W, H, (cuuint64_t)a.n_q}, qs[2] = {W * 2, H * W * 2};
+  const cuuint64_t nk = a.n_k > 0 ? a.n_k : 1;
+  const cuuint64_t kd[3] = {kLatentD, H, nk};
+  const cuuint64_t ks[2] = {(cuuint64_t)a.k_hs * 2, (cuuint64_t)a.k_ts * 2};
+  const cuuint64_t vs[2] = {(cuuint64_t)a.v_hs * 2, (cuuint64_t)a.v_ts * 2};
+  const cuuint64_t rd[2] = {64, nk}, rs[1] = {128};
+  const cuuint32_t b128[3] = {64, 1, 128}, b64[3] = {64, 1, 64}, br[2] = {64, 128};
+  memset(&mr, 0, sizeof(mr));
+  // without keys nothing is loaded; the maps only need a valid base
+  const void *any = a.q;
+  if (!make_bf16_map(&mq, a.q, 3, qd, qs, b128) ||
+      !make_bf16_map(&mk, a.n_k > 0 ? a.k : any, 3, kd, ks, b128) ||
+      !make_bf16_map(&mv, a.n_k > 0 ? a.v : any, 3, kd, vs, b64) ||
+      (DR && !make_bf16_map(&mr, a.n_k > 0 ? a.k_rope : any, 2, rd, rs, br)))
+    return cudaErrorInvalidValue;
+  auto kernel = kda_latent_fwd_kernel<DR>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       smem_bytes<DR>());
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kernel);
+  if (e != cudaSuccess) return e;
+  // the register split must not exceed what the block is launched with
+  if ((uint32_t)fa.numRegs < kLaunchRegs) return cudaErrorNotSupported;
+  Params p;
+  p.cu_q = a.cu_q; p.cu_k = a.cu_k; p.n_seqs = a.n_seqs; p.H = a.H;
+  p.tiles = (int32_t)(a.n_q / kRows + a.n_seqs);
+  p.n_q = a.n_q; p.n_k = a.n_k; p.scale2 = a.scale * kLog2e; p.causal = a.causal;
+  p.out = static_cast<__nv_bfloat16 *>(a.out); p.lse = a.lse; p.status = a.status;
+  const int64_t blocks = (int64_t)p.tiles * a.H;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  kernel<<<(unsigned)blocks, kThreads, smem_bytes<DR>(), stream>>>(mq, mk, mr, mv, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_latent_fwd(const LatentArgs &a, cudaStream_t stream) {
+  if (a.n_q == 0) return cudaSuccess;
+  if (!latent::encode_tiled()) return cudaErrorNotSupported;
+  return a.dr ? launch<64>(a, stream) : launch<0>(a, stream);
+}
+
+}  // namespace kda

@@ -53,39 +53,6 @@ __device__ bool row_tile(const LatentArgs &a, bool by_key, SeqTile &t) {
   return t.seq >= 0;
 }
 
-__global__ void fwd_kernel(LatentArgs a) {
-  SeqTile t;
-  if (!row_tile(a, false, t)) return;
-  const int lane = threadIdx.x & 31, i = t.tile * kRows + (threadIdx.x >> 5), h = blockIdx.y;
-  if (i >= t.nq) return;
-  const int W = kLatentD + a.dr;
-  const bf16 *q = static_cast<const bf16 *>(a.q) + ((int64_t)(t.q0 + i) * a.H + h) * W;
-  const float4 qn = ld4(q + 4 * lane);
-  const float2 qr = a.dr ? ld2(q + kLatentD + 2 * lane) : make_float2(0, 0);
-  const int n = a.causal ? min(t.nk, max(0, t.nk - t.nq + i + 1)) : t.nk;
-  float m = -CUDART_INF_F, l = 0;
-  float4 o = make_float4(0, 0, 0, 0);
-  for (int j = 0; j < n; ++j) {
-    const int64_t kj = t.k0 + j;
-    float x = dot4(qn, ld4(static_cast<const bf16 *>(a.k) + kj * a.k_ts + h * a.k_hs + 4 * lane));
-    if (a.dr) {
-      const float2 r = ld2(static_cast<const bf16 *>(a.k_rope) + kj * a.dr + 2 * lane);
-      x += qr.x * r.x + qr.y * r.y;
-    }
-    x = warp_sum(x) * a.scale;
-    const float mn = fmaxf(m, x), ms = mn == -CUDART_INF_F ? 0.f : mn;
-    const float c = expf(m - ms), p = expf(x - ms);
-    l = l * c + p;
-    o.x *= c; o.y *= c; o.z *= c; o.w *= c;
-    axpy(o, p, ld4(static_cast<const bf16 *>(a.v) + kj * a.v_ts + h * a.v_hs + 4 * lane));
-    m = mn;
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
-  st4(static_cast<bf16 *>(a.out) + ((int64_t)(t.q0 + i) * a.H + h) * kLatentD + 4 * lane, o);
-  if (lane == 0) a.lse[(int64_t)(t.q0 + i) * a.H + h] = l == 0.f ? -CUDART_INF_F : m + logf(l);
-}
-
 struct Row {
   float4 qn, g;
   float2 qr;
@@ -176,12 +143,6 @@ __global__ void bwd_kv_kernel(LatentArgs a) {
 unsigned tiles(int64_t n, int32_t n_seqs) { return (unsigned)(n / kRows + n_seqs); }
 
 }  // namespace
-
-cudaError_t launch_latent_fwd(const LatentArgs &a, cudaStream_t stream) {
-  if (a.n_q == 0) return cudaSuccess;
-  fwd_kernel<<<dim3(tiles(a.n_q, a.n_seqs), a.H), 32 * kRows, 0, stream>>>(a);
-  return cudaGetLastError();
-}
 
 size_t latent_bwd_scratch_bytes(int64_t, int64_t, int32_t, int32_t) { return 0; }
 
