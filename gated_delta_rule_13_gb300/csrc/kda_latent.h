@@ -37,7 +37,7 @@ struct LatentArgs {
 };
 cudaError_t launch_latent_fwd(const LatentArgs &a, cudaStream_t stream);
 cudaError_t launch_latent_bwd(const LatentArgs &a, cudaStream_t stream);
-size_t latent_bwd_scratch_bytes(int64_t n_q, int64_t n_k, int32_t H, int32_t dr);
+size_t latent_bwd_scratch_bytes(int32_t n_seqs, int64_t n_q, int64_t n_k, int32_t H, int32_t dr);
 
 // Absorbed form over a paged cache.
 struct LatentDecodeArgs {

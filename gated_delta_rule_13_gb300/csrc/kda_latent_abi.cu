@@ -171,7 +171,7 @@ int kda_latent_bwd_workspace_size(int32_t n_seqs, int64_t n_q, int64_t n_k, int3
   if (!bytes) return KDA_ERR_INVALID_ARG;
   const int d = check_sizes(n_seqs, n_q, n_k, H, dk, dr, dv, dtype);
   if (d != KDA_OK) return d;
-  *bytes = base_bytes(n_seqs) + round_up(kda::latent_bwd_scratch_bytes(n_q, n_k, H, dr), 256);
+  *bytes = base_bytes(n_seqs) + round_up(kda::latent_bwd_scratch_bytes(n_seqs, n_q, n_k, H, dr), 256);
   return KDA_OK;
 }
 
@@ -220,7 +220,7 @@ int kda_latent_bwd(const void *q, const void *k, const void *v, const void *k_ro
                       {d_v, span_bytes(a.dv_ts, a.dv_hs, H, n_k)}};
   if (any_overlap(in, o1) || any_overlap(in, o2) || (n_k > 0 && d_k == d_v))
     return KDA_ERR_INVALID_ARG;
-  const size_t scratch = round_up(kda::latent_bwd_scratch_bytes(n_q, n_k, H, dr), 256);
+  const size_t scratch = round_up(kda::latent_bwd_scratch_bytes(n_seqs, n_q, n_k, H, dr), 256);
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < base_bytes(n_seqs) + scratch)
     return KDA_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -1,0 +1,597 @@
+// Gradient of latent attention in its expanded form (kda_latent_bwd), tcgen05 /
+// TMEM / TMA, sm_103a.
+//
+//   p_ij = exp(s_ij - lse_i),  ds_ij = p_ij (do_i . v_j - delta_i),
+//   delta_i = do_i . o_i
+//   dv_j = sum_i p_ij do_i,  dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j
+//
+// Two passes of one shape in one launch, each output element owned by one CTA
+// (no atomics, so the result does not depend on the order of execution; the price
+// is that s and dp are computed twice, 1152 multiply-adds a pair at dr = 64
+// instead of 832).  A CTA keeps 128 rows X1, X2 in shared memory and streams
+// tiles of 64 rows Y1, Y2 past them:
+//   S  = X1 Y1^T,  dP = X2 Y2^T              (fp32, TMEM)
+//   P  = exp2(S scale log2e - lse log2e),  dS = P (dP - delta)
+//   A1 += dS Y1,   A2 += P Y2                (fp32, TMEM, over all tiles)
+// keys pass:    X = (keys, values), Y = (queries, d_out): A1 = dk, A2 = dv
+// queries pass: X = (queries, d_out), Y = (keys, values): A1 = dq
+// P and dS are bf16 operands in TMEM, over the columns they were computed from.
+// A1 (192 columns) and A2 (128) leave 192 columns: two S buffers and one dP, so the
+// tensor cores run S two tiles ahead and dP one ahead of the elementwise work.
+// A tile costs 1,600 (keys) and 1,344 (queries) cycles of the tensor cores at
+// dr = 64; the elementwise work (64 x 128 exponentials) hides behind it.
+//
+// The rotary key is shared by the heads: every head leaves its fp32 gradient in
+// the workspace and a last kernel adds them in head order.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <string.h>
+
+#include "kda_latent_tc.cuh"
+
+namespace kda {
+namespace {
+
+using namespace latent;
+
+constexpr int kX = 128, kY = 64;
+constexpr int kThreads = 384;            // 8 elementwise warps; loader, MMA, cleaner, spare
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
+constexpr int kMaxStages = 4;
+constexpr uint32_t kXBlock = 16384, kYBlock = 8192;  // 128 or 64 rows x 64 channels
+
+struct Shared {
+  uint64_t full[kMaxStages], empty[kMaxStages], s_full[2];
+  uint64_t x_full, dp_full, ds_ready, clean_req, clean, acc_full, fin;
+  uint32_t tmem;
+  int abort, loaded;
+  SeqTile tile;
+  alignas(16) float lse2[kMaxStages][kY];
+  float delta[kMaxStages][kY];
+};
+
+template <int DR>
+constexpr uint32_t x_bytes() { return ((kLatentD + DR) / 64 + 2) * kXBlock; }
+template <int DR>
+constexpr uint32_t stage_bytes() { return ((kLatentD + DR) / 64 + 2) * kYBlock; }
+template <int DR>
+constexpr int stages() { return DR ? 3 : 4; }
+template <int DR>
+constexpr uint32_t smem_bytes() {
+  return 1024 + x_bytes<DR>() + stages<DR>() * stage_bytes<DR>() + sizeof(Shared);
+}
+
+struct Params {
+  const int32_t *cu_q, *cu_k;
+  int32_t n_seqs, H, k_tiles, q_tiles;   // tiles a head: upper bounds
+  int64_t n_q, n_k, stat_rows;
+  float scale, scale2;
+  int causal;
+  __nv_bfloat16 *dq, *dk, *dv;
+  int64_t dk_ts, dk_hs, dv_ts, dv_hs;
+  const float *lse2, *delta;             // [H][stat_rows]
+  float *rope;                           // [H][n_k][64]
+  DeviceStatus *status;
+};
+
+// Row statistics are kept per head in tiles of 64 that no two sequences share:
+// the first tile of sequence s is floor(q0 / 64) + s.
+__host__ __device__ inline int64_t stat_tile(int64_t q0, int64_t s) { return q0 / kY + s; }
+
+struct Maps {
+  CUtensorMap q128, q64, g128, g64, k128, k64, v128, v64, r128, r64;
+};
+
+// The 64 columns at `col` of this warpgroup's 128 accumulator rows, times `mul`, as
+// bf16 rows of dst (row stride `stride` elements); rows >= n_rows are not written.
+// `buf`: 4 KB of shared memory of this warp.
+__device__ __forceinline__ void store_cols(uint32_t col, float mul, bool zero,
+                                           __nv_bfloat16 *dst, int64_t stride, int n_rows,
+                                           uint32_t buf, int warp4, int lane) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t o[32];
+    if (zero) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] = 0;
+    } else {
+      tmem_ld32(col + 32 * c, o);
+      tmem_ld_wait(o);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * j]) * mul,
+                           __uint_as_float(o[8 * q + 2 * j + 1]) * mul);
+      st_shared_v4(buf + lane * 128 + (((4 * c + q) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int rr = 4 * k + (lane >> 3), piece = lane & 7, row = warp4 * 32 + rr;
+    const uint4 v = ld_shared_v4(buf + rr * 128 + ((piece ^ (rr & 7)) << 4));
+    if (row < n_rows) *reinterpret_cast<uint4 *>(dst + row * stride + 8 * piece) = v;
+  }
+  __syncwarp();
+}
+
+template <int DR, bool kKeys>
+__device__ __forceinline__ void pass(const Maps &maps, const Params &p, int index, int head,
+                                     unsigned char *tiles, uint32_t base, Shared &m) {
+  constexpr int KB = (kLatentD + DR) / 64, ST = stages<DR>();
+  constexpr uint32_t kStage = x_bytes<DR>();
+  constexpr int N1 = kLatentD + DR;
+  constexpr uint32_t TM_A1 = 0, TM_A2 = 192, TM_S = 320, TM_DP = 448;
+  constexpr uint32_t ID_S = idesc_bf16(128, kY, false, false);
+  constexpr uint32_t ID_A1 = idesc_bf16(128, N1, false, true);
+  constexpr uint32_t ID_A2 = idesc_bf16(128, kLatentD, false, true);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  (void)tiles;
+
+  if (warp == kCleanWarp) {
+    const SeqTile f = find_seq_tile(p.cu_q, p.cu_k, p.n_seqs, p.n_q, p.n_k, kX, kKeys, index);
+    if (lane == 0) m.tile = f;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&m.full[i], 1);
+      mbar_init(&m.empty[i], 1);
+    }
+    mbar_init(&m.s_full[0], 1);
+    mbar_init(&m.s_full[1], 1);
+    mbar_init(&m.x_full, 1);
+    mbar_init(&m.dp_full, 1);
+    mbar_init(&m.ds_ready, 8);
+    mbar_init(&m.clean_req, 1);
+    mbar_init(&m.clean, 1);
+    mbar_init(&m.acc_full, 1);
+    mbar_init(&m.fin, 1);
+    m.abort = 0;
+    m.loaded = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&m.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = m.tmem;
+  const SeqTile st = m.tile;
+  if (st.bad && index == 0 && head == 0 && tid == 0)
+    record_device_status(p.status, KDA_ERR_INVALID_ARG, 1, 0, 0);
+
+  // The CTA's rows [x0, x0 + 128) of the sequence, longest first: the first keys are
+  // seen by the most queries, the last queries see the most keys.  It streams
+  // tiles [y_first, y_first + n) of 64.
+  const int x0 = (kKeys ? st.tile : st.n_tiles - 1 - st.tile) * kX;
+  const int nx = kKeys ? st.nk : st.nq, ny = kKeys ? st.nq : st.nk;
+  const int shift = st.nk - st.nq;       // query i sees keys <= i + shift
+  int y_first = 0, y_end = ny;
+  if (p.causal) {
+    if (kKeys) y_first = max(0, x0 - shift) / kY;
+    else y_end = min(ny, min(x0 + kX, nx) + shift);
+  }
+  int n = y_end > 0 ? (y_end + kY - 1) / kY - y_first : 0;
+  if (st.seq < 0 || n < 0) n = 0;
+  const int live = min(kY, ny - (y_first + n - 1) * kY);  // rows of the last tile
+  const WaitCtx cx{&m.abort, p.status, (int)blockIdx.x};
+
+  if (warp == kLoadWarp && lane == 0 && n > 0) {
+    // ---- loader
+    const int xr = (kKeys ? st.k0 : st.q0) + x0;
+    mbar_arrive_expect_tx(&m.x_full, (KB + 2) * kXBlock);
+    for (int kb = 0; kb < KB; ++kb) {
+      const uint32_t dst = base + kb * kXBlock;
+      if (!kKeys) tma_load_3d_u(dst, &maps.q128, &m.x_full, 64 * kb, head, xr);
+      else if (kb < 2) tma_load_3d_u(dst, &maps.k128, &m.x_full, 64 * kb, head, xr);
+      else tma_load_2d(dst, &maps.r128, &m.x_full, 0, xr);
+    }
+    for (int c = 0; c < 2; ++c)
+      tma_load_3d_u(base + (KB + c) * kXBlock, kKeys ? &maps.v128 : &maps.g128, &m.x_full, 64 * c,
+                    head, xr);
+    bool ok = true;
+    int i = 0;
+    for (; i < n; ++i) {
+      const int s = i % ST;
+      if (i >= ST) ok = wait_or_abort(cx, &m.empty[s], (i / ST - 1) & 1, 10, i);
+      if (!ok) break;
+      const int yr = (kKeys ? st.q0 : st.k0) + (y_first + i) * kY;
+      const uint32_t dst = base + kStage + s * stage_bytes<DR>();
+      mbar_arrive_expect_tx(&m.full[s], stage_bytes<DR>() + (kKeys ? 2 * kY * 4 : 0));
+      for (int kb = 0; kb < KB; ++kb) {
+        if (kKeys) tma_load_3d_u(dst + kb * kYBlock, &maps.q64, &m.full[s], 64 * kb, head, yr);
+        else if (kb < 2) tma_load_3d_u(dst + kb * kYBlock, &maps.k64, &m.full[s], 64 * kb, head, yr);
+        else tma_load_2d(dst + kb * kYBlock, &maps.r64, &m.full[s], 0, yr);
+      }
+      for (int c = 0; c < 2; ++c)
+        tma_load_3d_u(dst + (KB + c) * kYBlock, kKeys ? &maps.g64 : &maps.v64, &m.full[s], 64 * c,
+                      head, yr);
+      if (kKeys) {
+        const int64_t at = head * p.stat_rows + (stat_tile(st.q0, st.seq) + y_first + i) * kY;
+        bulk_load(smem_u32(m.lse2[s]), p.lse2 + at, kY * 4, &m.full[s]);
+        bulk_load(smem_u32(m.delta[s]), p.delta + at, kY * 4, &m.full[s]);
+      }
+    }
+    if (ok) mbar_arrive(&m.clean_req);
+    m.loaded = i;
+  } else if (warp == kMmaWarp && lane == 0 && n > 0) {
+    // ---- MMA issue
+    auto stage = [&](int i) { return base + kStage + (uint32_t)(i % ST) * stage_bytes<DR>(); };
+    bool ok = wait_or_abort(cx, &m.x_full, 0, 20, 0);
+    auto issue_s = [&](int i) {
+      ok = ok && wait_or_abort(cx, &m.full[i % ST], (i / ST) & 1, 21, i);
+      if (!ok) return;
+      const uint32_t y = stage(i);
+#pragma unroll
+      for (int k = 0; k < 4 * KB; ++k)
+        umma_ss(tm + TM_S + 64 * (i & 1),
+                sdesc_sw128(base + (k >> 2) * kXBlock + (k & 3) * 32, 16, 1024),
+                sdesc_sw128(y + (k >> 2) * kYBlock + (k & 3) * 32, 16, 1024), ID_S, k > 0);
+      umma_commit(&m.s_full[i & 1]);
+    };
+    auto issue_dp = [&](int i) {
+      const uint32_t y = stage(i) + KB * kYBlock;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        umma_ss(tm + TM_DP, sdesc_sw128(base + (KB + (k >> 2)) * kXBlock + (k & 3) * 32, 16, 1024),
+                sdesc_sw128(y + (k >> 2) * kYBlock + (k & 3) * 32, 16, 1024), ID_S, k > 0);
+      umma_commit(&m.dp_full);
+    };
+    issue_s(0);
+    if (ok) issue_dp(0);
+    if (n > 1) issue_s(1);
+    for (int i = 0; ok && i < n; ++i) {
+      ok = wait_or_abort(cx, &m.ds_ready, i & 1, 22, i);
+      if (ok && i + 1 == n && live < kY) ok = wait_or_abort(cx, &m.clean, 0, 23, i);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t y = stage(i), sb = tm + TM_S + 64 * (i & 1);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // bf16 columns: rows 0 .. 31 at +0, 32 .. 63 at +32
+        const uint32_t a = (k >> 1) * 32 + (k & 1) * 8;
+        if (kKeys)
+          umma_ts(tm + TM_A2, sb + a, sdesc_sw128(y + KB * kYBlock + k * 2048, kYBlock, 1024),
+                  ID_A2, i + k > 0);
+        umma_ts(tm + TM_A1, tm + TM_DP + a, sdesc_sw128(y + k * 2048, kYBlock, 1024), ID_A1,
+                i + k > 0);
+      }
+      umma_commit(&m.empty[i % ST]);
+      if (i + 1 < n) issue_dp(i + 1);
+      if (i + 2 < n) issue_s(i + 2);
+    }
+    if (ok) umma_commit(&m.acc_full);
+  } else if (warp == kCleanWarp && n > 0 && live < kY) {
+    // ---- cleaner: rows of the last tile past the sequence's end are another
+    // sequence's and may hold anything; as operands of the sums they are zeroed
+    // (0 * NaN would reach the result).  The loader asks once their copy is under
+    // way; the products that read them wait for it.
+    bool ok = wait_or_abort(cx, &m.clean_req, 0, 30, n);
+    ok = ok && wait_or_abort(cx, &m.full[(n - 1) % ST], ((n - 1) / ST) & 1, 31, n);
+    if (__all_sync(0xffffffffu, ok)) {
+      const uint32_t y = base + kStage + (uint32_t)((n - 1) % ST) * stage_bytes<DR>();
+      for (int b = 0; b < KB + 2; ++b)
+        for (int j = lane; j < (kY - live) * 8; j += 32)
+          st_shared_v4(y + b * kYBlock + live * 128 + j * 16, 0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.clean);
+    }
+  } else if (warp < 8) {
+    // ---- elementwise: thread = row of X, warpgroup = half of a tile's columns
+    const int wg = warp >> 2, xr = x0 + (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t col = 32 * wg;
+    float lse2 = 0.f, delta = 0.f;
+    if (!kKeys && st.seq >= 0 && xr < nx) {
+      const int64_t at = head * p.stat_rows + stat_tile(st.q0, st.seq) * kY + xr;
+      lse2 = p.lse2[at];
+      delta = p.delta[at];
+    }
+    // columns [lo, hi) of the streamed rows pair with this row
+    int lo = 0, hi = ny;
+    if (p.causal) {
+      if (kKeys) lo = max(0, xr - shift);
+      else hi = min(ny, xr + shift + 1);
+    }
+    bool ok = true;
+    for (int i = 0; ok && i < n; ++i) {
+      ok = __all_sync(0xffffffffu,
+                      wait_or_abort(cx, &m.s_full[i & 1], (i >> 1) & 1, 40, i));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t r[32];
+      const uint32_t ts = tm + lanes + TM_S + 64 * (i & 1) + col, td = tm + lanes + TM_DP + col;
+      tmem_ld32(ts, r);
+      tmem_ld_wait(r);
+      const int y0 = (y_first + i) * kY + (int)col;
+      const bool edge = __any_sync(0xffffffffu, y0 < lo || y0 + 32 > hi);
+      float pr[32];
+      if constexpr (kKeys) {
+        const uint32_t sl = smem_u32(&m.lse2[i % ST][col]);
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 l = ld_shared_f32x4(sl + 4 * j);
+          pr[j] = ex2(fmaf(__uint_as_float(r[j]), p.scale2, -l.x));
+          pr[j + 1] = ex2(fmaf(__uint_as_float(r[j + 1]), p.scale2, -l.y));
+          pr[j + 2] = ex2(fmaf(__uint_as_float(r[j + 2]), p.scale2, -l.z));
+          pr[j + 3] = ex2(fmaf(__uint_as_float(r[j + 3]), p.scale2, -l.w));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) pr[j] = ex2(fmaf(__uint_as_float(r[j]), p.scale2, -lse2));
+      }
+      if (edge) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (y0 + j < lo || y0 + j >= hi) pr[j] = 0.f;
+      }
+      if constexpr (kKeys) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(pr[2 * j], pr[2 * j + 1]);
+        tmem_st16(ts, pk);
+      }
+      ok = __all_sync(0xffffffffu, wait_or_abort(cx, &m.dp_full, i & 1, 41, i));
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld32(td, r);
+      tmem_ld_wait(r);
+      if constexpr (kKeys) {
+        const uint32_t sd = smem_u32(&m.delta[i % ST][col]);
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 d = ld_shared_f32x4(sd + 4 * j);
+          r[j] = __float_as_uint(pr[j] * (__uint_as_float(r[j]) - d.x));
+          r[j + 1] = __float_as_uint(pr[j + 1] * (__uint_as_float(r[j + 1]) - d.y));
+          r[j + 2] = __float_as_uint(pr[j + 2] * (__uint_as_float(r[j + 2]) - d.z));
+          r[j + 3] = __float_as_uint(pr[j + 3] * (__uint_as_float(r[j + 3]) - d.w));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          r[j] = __float_as_uint(pr[j] * (__uint_as_float(r[j]) - delta));
+      }
+      if (edge) {  // dP of a pair outside may be anything
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (y0 + j < lo || y0 + j >= hi) r[j] = 0;
+      }
+      uint32_t pk[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        pk[j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+      tmem_st16(td, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.ds_ready);
+    }
+    if (ok && n > 0) {
+      ok = __all_sync(0xffffffffu, wait_or_abort(cx, &m.acc_full, 0, 42, n));
+      tc_fence_after();
+    }
+    // ---- output, 64 columns at a time, through the rows of X (all products are done)
+    if (ok && st.seq >= 0) {
+      const bool zero = n == 0;
+      const uint32_t buf = base + warp * 8192, acc = tm + lanes;
+      const int rows = nx - x0, w4 = warp & 3;
+      if constexpr (kKeys) {
+        const int64_t kr = st.k0 + x0;
+        store_cols(acc + TM_A2 + 64 * wg, 1.f, zero, p.dv + kr * p.dv_ts + head * p.dv_hs + 64 * wg,
+                   p.dv_ts, rows, buf, w4, lane);
+        store_cols(acc + TM_A1 + 64 * wg, p.scale, zero,
+                   p.dk + kr * p.dk_ts + head * p.dk_hs + 64 * wg, p.dk_ts, rows, buf, w4, lane);
+        if (DR) {  // fp32, 32 columns a warpgroup
+          uint32_t o[32];
+          if (zero) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = 0;
+          } else {
+            tmem_ld32(acc + TM_A1 + kLatentD + 32 * wg, o);
+            tmem_ld_wait(o);
+          }
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            st_shared_v4(buf + lane * 128 + ((q ^ (lane & 7)) << 4), o[4 * q], o[4 * q + 1],
+                         o[4 * q + 2], o[4 * q + 3]);
+          __syncwarp();
+          float *dst = p.rope + ((int64_t)head * p.n_k + kr + w4 * 32) * kLatentRope + 32 * wg;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int rr = 4 * k + (lane >> 3), piece = lane & 7;
+            const uint4 v = ld_shared_v4(buf + rr * 128 + ((piece ^ (rr & 7)) << 4));
+            if (w4 * 32 + rr < rows)
+              *reinterpret_cast<uint4 *>(dst + rr * kLatentRope + 4 * piece) = v;
+          }
+        }
+      } else {
+        const int64_t qr = st.q0 + x0;
+        for (int c = wg; c < KB; c += 2)
+          store_cols(acc + TM_A1 + 64 * c, p.scale, zero, p.dq + (qr * p.H + head) * N1 + 64 * c,
+                     (int64_t)p.H * N1, rows, buf, w4, lane);
+      }
+    }
+  }
+
+  __syncwarp();
+  __syncthreads();
+  if (m.abort) {  // nothing in flight outlives the CTA
+    if (tid == 32 * kLoadWarp && n > 0) {
+      for (int k = max(0, m.loaded - ST); k < m.loaded; ++k)
+        mbar_wait(&m.full[k % ST], (k / ST) & 1, kWaitNs);
+      mbar_wait(&m.x_full, 0, kWaitNs);
+    }
+    if (tid == 32 * kMmaWarp) {
+      umma_commit(&m.fin);
+      mbar_wait(&m.fin, 0, kWaitNs);
+    }
+    __syncthreads();
+  }
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tmem_dealloc(tm, 512);
+  }
+}
+
+// Blocks [0, k_tiles * H): the keys pass, then the queries pass.
+template <int DR>
+__global__ void __launch_bounds__(kThreads, 1)
+kda_latent_bwd_kernel(const __grid_constant__ Maps maps, const Params p) {
+  extern __shared__ unsigned char raw[];
+  const uint32_t base = round_up_1k(smem_u32(raw));
+  unsigned char *const tiles = raw + (base - smem_u32(raw));
+  Shared &m =
+      *reinterpret_cast<Shared *>(tiles + x_bytes<DR>() + stages<DR>() * stage_bytes<DR>());
+  const int first_q = p.k_tiles * p.H;
+  if ((int)blockIdx.x < first_q)
+    pass<DR, true>(maps, p, blockIdx.x % p.k_tiles, blockIdx.x / p.k_tiles, tiles, base, m);
+  else
+    pass<DR, false>(maps, p, (blockIdx.x - first_q) % p.q_tiles, (blockIdx.x - first_q) / p.q_tiles,
+                    tiles, base, m);
+}
+
+// lse * log2(e) and delta = d_out . out of 64 rows of a head, in the padded layout.
+// A row without any key has lse = -inf: +inf stands for it, so that exp2 gives 0.
+constexpr int kStatThreads = 256;
+__global__ void __launch_bounds__(kStatThreads)
+kda_latent_stat_kernel(const __nv_bfloat16 *__restrict__ out,
+                       const __nv_bfloat16 *__restrict__ d_out, const float *__restrict__ lse,
+                       float *__restrict__ lse2, float *__restrict__ delta, const Params p) {
+  __shared__ SeqTile st;
+  const int tid = threadIdx.x, head = blockIdx.y;
+  if (tid < 32) {
+    const SeqTile f =
+        find_seq_tile(p.cu_q, p.cu_k, p.n_seqs, p.n_q, p.n_k, kY, false, blockIdx.x);
+    if (tid == 0) st = f;
+  }
+  __syncthreads();
+  if (st.seq < 0) return;
+  const int64_t at = head * p.stat_rows + (stat_tile(st.q0, st.seq) + st.tile) * kY;
+#pragma unroll
+  for (int k = 0; k < kY * 16 / kStatThreads; ++k) {  // 16 lanes a row, 8 channels each
+    const int r = (k * kStatThreads + tid) >> 4, c = tid & 15, row = st.tile * kY + r;
+    float sum = 0.f;
+    if (row < st.nq) {
+      const int64_t e = (((int64_t)st.q0 + row) * p.H + head) * kLatentD + 8 * c;
+      const uint4 a = *reinterpret_cast<const uint4 *>(out + e);
+      const uint4 b = *reinterpret_cast<const uint4 *>(d_out + e);
+      const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 u = unpack_bf16x2(x[j]), v = unpack_bf16x2(y[j]);
+        sum = fmaf(u.x, v.x, sum);
+        sum = fmaf(u.y, v.y, sum);
+      }
+    }
+#pragma unroll
+    for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (c == 0) {
+      float l = CUDART_INF_F;
+      if (row < st.nq) {
+        l = lse[((int64_t)st.q0 + row) * p.H + head];
+        l = l == -CUDART_INF_F ? CUDART_INF_F : l * kLog2e;
+      }
+      lse2[at + r] = l;
+      delta[at + r] = sum;
+    }
+  }
+}
+
+// d_k_rope = scale * sum over the heads, in head order.
+__global__ void kda_latent_rope_kernel(const float *__restrict__ rope, int64_t n, int32_t H,
+                                       float scale, const DeviceStatus *status,
+                                       __nv_bfloat16 *__restrict__ out) {
+  const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
+  if (i >= n || status->code == KDA_ERR_INVALID_ARG) return;
+  float4 a = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+  for (int h = 0; h < H; ++h) {
+    const float4 x = *reinterpret_cast<const float4 *>(rope + h * n + i);
+    a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+  }
+  *reinterpret_cast<uint2 *>(out + i) =
+      make_uint2(pack_bf16x2(a.x * scale, a.y * scale), pack_bf16x2(a.z * scale, a.w * scale));
+}
+
+int64_t stat_rows(int64_t n_q, int32_t n_seqs) { return (n_q / kY + n_seqs) * kY; }
+
+template <int DR>
+cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
+  Maps mp;
+  memset(&mp, 0, sizeof(mp));
+  const cuuint64_t W = kLatentD + DR, H = a.H;
+  const cuuint64_t nq = a.n_q > 0 ? a.n_q : 1, nk = a.n_k > 0 ? a.n_k : 1;
+  // without queries or keys nothing is loaded; the maps only need a valid base
+  const void *any = a.n_q > 0 ? a.q : a.k;
+  const void *q = a.n_q > 0 ? a.q : any, *g = a.n_q > 0 ? a.d_out : any;
+  const void *k = a.n_k > 0 ? a.k : any, *v = a.n_k > 0 ? a.v : any;
+  const void *r = a.n_k > 0 ? a.k_rope : any;
+  const cuuint64_t qd[3] = {W, H, nq}, qs[2] = {W * 2, H * W * 2};
+  const cuuint64_t gd[3] = {kLatentD, H, nq}, gs[2] = {kLatentD * 2, H * kLatentD * 2};
+  const cuuint64_t kd[3] = {kLatentD, H, nk};
+  const cuuint64_t ks[2] = {(cuuint64_t)a.k_hs * 2, (cuuint64_t)a.k_ts * 2};
+  const cuuint64_t vs[2] = {(cuuint64_t)a.v_hs * 2, (cuuint64_t)a.v_ts * 2};
+  const cuuint64_t rd[2] = {64, nk}, rs[1] = {128};
+  const cuuint32_t b128[3] = {64, 1, 128}, b64[3] = {64, 1, 64};
+  const cuuint32_t r128[2] = {64, 128}, r64[2] = {64, 64};
+  if (!make_bf16_map(&mp.q128, q, 3, qd, qs, b128) || !make_bf16_map(&mp.q64, q, 3, qd, qs, b64) ||
+      !make_bf16_map(&mp.g128, g, 3, gd, gs, b128) || !make_bf16_map(&mp.g64, g, 3, gd, gs, b64) ||
+      !make_bf16_map(&mp.k128, k, 3, kd, ks, b128) || !make_bf16_map(&mp.k64, k, 3, kd, ks, b64) ||
+      !make_bf16_map(&mp.v128, v, 3, kd, vs, b128) || !make_bf16_map(&mp.v64, v, 3, kd, vs, b64) ||
+      (DR && (!make_bf16_map(&mp.r128, r, 2, rd, rs, r128) ||
+              !make_bf16_map(&mp.r64, r, 2, rd, rs, r64))))
+    return cudaErrorInvalidValue;
+  Params p;
+  p.cu_q = a.cu_q; p.cu_k = a.cu_k; p.n_seqs = a.n_seqs; p.H = a.H; p.n_q = a.n_q; p.n_k = a.n_k;
+  p.k_tiles = a.n_k > 0 ? (int32_t)(a.n_k / kX + a.n_seqs) : 0;
+  p.q_tiles = a.n_q > 0 ? (int32_t)(a.n_q / kX + a.n_seqs) : 0;
+  p.stat_rows = stat_rows(a.n_q, a.n_seqs);
+  p.scale = a.scale; p.scale2 = a.scale * kLog2e; p.causal = a.causal;
+  p.dq = static_cast<__nv_bfloat16 *>(a.dq); p.dk = static_cast<__nv_bfloat16 *>(a.dk);
+  p.dv = static_cast<__nv_bfloat16 *>(a.dv);
+  p.dk_ts = a.dk_ts; p.dk_hs = a.dk_hs; p.dv_ts = a.dv_ts; p.dv_hs = a.dv_hs;
+  float *lse2 = static_cast<float *>(a.scratch), *delta = lse2 + p.stat_rows * a.H;
+  p.lse2 = lse2; p.delta = delta; p.rope = delta + p.stat_rows * a.H;
+  p.status = a.status;
+  const int64_t blocks = ((int64_t)p.k_tiles + p.q_tiles) * a.H;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  auto kernel = kda_latent_bwd_kernel<DR>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       smem_bytes<DR>());
+  if (e != cudaSuccess) return e;
+  if (a.n_q > 0) {
+    const dim3 grid((unsigned)(a.n_q / kY + a.n_seqs), (unsigned)a.H);
+    kda_latent_stat_kernel<<<grid, kStatThreads, 0, stream>>>(
+        static_cast<const __nv_bfloat16 *>(a.out), static_cast<const __nv_bfloat16 *>(a.d_out),
+        a.lse, lse2, delta, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<(unsigned)blocks, kThreads, smem_bytes<DR>(), stream>>>(mp, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !DR || a.n_k == 0) return e;
+  const int64_t elems = a.n_k * kLatentRope;
+  kda_latent_rope_kernel<<<(unsigned)((elems / 4 + 255) / 256), 256, 0, stream>>>(
+      p.rope, elems, a.H, a.scale, a.status, static_cast<__nv_bfloat16 *>(a.d_k_rope));
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t latent_bwd_scratch_bytes(int32_t n_seqs, int64_t n_q, int64_t n_k, int32_t H, int32_t dr) {
+  return (size_t)H * sizeof(float) * (2 * (size_t)stat_rows(n_q, n_seqs) + (size_t)n_k * dr);
+}
+
+cudaError_t launch_latent_bwd(const LatentArgs &a, cudaStream_t stream) {
+  if (a.n_q == 0 && a.n_k == 0) return cudaSuccess;
+  if (!latent::encode_tiled()) return cudaErrorNotSupported;
+  return a.dr ? launch<64>(a, stream) : launch<0>(a, stream);
+}
+
+}  // namespace kda
