@@ -41,10 +41,16 @@ constexpr float kSlack = 8.f;            // log2 units a score may exceed its re
 constexpr uint32_t kLaunchRegs = 168, kSoftmaxRegs = 208, kIssueRegs = 88;
 constexpr int kMaxSlots = 10;
 
+// A unit of the ring is a key tile (KB slots) or a value tile (2 slots); units are
+// loaded, used and released in the order K0 V0 K1 V1 .., so the barriers of eight
+// consecutive units are enough (at most five are resident).
+constexpr int kUnits = 8;
+
 struct Shared {
-  uint64_t full[kMaxSlots], empty[kMaxSlots], clean[kMaxSlots];
-  uint64_t q_full[2], s_full[2], p_ready[2], o_full[2], clean_req, fin;
-  uint32_t tmem, load_pos;
+  uint64_t full[kUnits], empty[kUnits];
+  uint64_t q_full[2], s_full[2], p_ready[2][2], o_full[2], clean_req, clean, fin;
+  uint32_t tmem;
+  int loaded;                              // units loaded
   int abort;
   SeqTile tile;
 };
@@ -99,21 +105,22 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     if (lane == 0) m.tile = f;
   }
   if (tid == 0) {
-    for (int i = 0; i < S; ++i) {
+    for (int i = 0; i < kUnits; ++i) {
       mbar_init(&m.full[i], 1);
       mbar_init(&m.empty[i], 1);
-      mbar_init(&m.clean[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&m.q_full[t], 1);
       mbar_init(&m.s_full[t], 1);
-      mbar_init(&m.p_ready[t], 4);
+      mbar_init(&m.p_ready[t][0], 4);
+      mbar_init(&m.p_ready[t][1], 4);
       mbar_init(&m.o_full[t], 1);
     }
     mbar_init(&m.clean_req, 1);
+    mbar_init(&m.clean, 1);
     mbar_init(&m.fin, 1);
     m.abort = 0;
-    m.load_pos = 0;
+    m.loaded = 0;
     fence_mbarrier_init();
   }
   if (warp == kLoadWarp && lane == 0) {
@@ -160,103 +167,139 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
           tma_load_3d_u(base + (t * KB + kb) * kQTile, &map_q, &m.q_full[t], 64 * kb, head,
                         st.q0 + row0 + 128 * t);
       };
-      uint32_t pos = 0;
+      // Slots [at, at + PER) hold key tile i and its values; before a unit is loaded,
+      // the last unit that had one of its slots has been released.
       bool ok = true;
-      auto slot = [&](int step) {  // waits for the next slot
-        const uint32_t s = pos % S;
-        if (pos >= S) ok = wait_or_abort(cx, &m.empty[s], (pos / S - 1) & 1, 10, step);
-        return s;
+      uint32_t at = 0;
+      int u = 0;
+      auto before = [&](int count) {  // slots `at` .. `at + count` of unit u
+        // unit of slot position end - S, where positions run on without wrapping
+        const int end = (u >> 1) * PER + (u & 1) * KB + count - 1 - S;
+        if (end < 0) return;
+        const int v = end / PER * 2 + (end % PER >= KB ? 1 : 0);
+        ok = wait_or_abort(cx, &m.empty[v % kUnits], (v / kUnits) & 1, 10, u);
+      };
+      auto next = [&]() {
+        const uint32_t dst = base + kRing + at * kSlotBytes;
+        at = at + 1 == S ? 0 : at + 1;
+        return dst;
       };
       if (nt[0] > 0) load_q(0);
-      for (int i = 0; ok && i < n_iter; ++i) {
+      for (int i = 0; i < n_iter; ++i) {
         const int key = st.k0 + i * kKeys;
+        before(KB);
+        if (!ok) break;
+        uint64_t *bar = &m.full[u % kUnits];
+        mbar_arrive_expect_tx(bar, KB * kSlotBytes);
         for (int kb = 0; kb < KB; ++kb) {
-          const uint32_t s = slot(i);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&m.full[s], kSlotBytes);
-          const uint32_t dst = base + kRing + s * kSlotBytes;
-          if (kb < 2)
-            tma_load_3d_u(dst, &map_k, &m.full[s], 64 * kb, head, key);
-          else
-            tma_load_2d(dst, &map_r, &m.full[s], 64 * (kb - 2), key);
-          ++pos;
+          if (kb < 2) tma_load_3d_u(next(), &map_k, bar, 64 * kb, head, key);
+          else tma_load_2d(next(), &map_r, bar, 64 * (kb - 2), key);
         }
+        ++u;
         if (i == 0 && nt[1] > 0) load_q(1);
         const int halves = i + 1 < n_iter ? 2 : halves_last;
-        for (int hf = 0; ok && hf < halves; ++hf) {
-          const uint32_t s = slot(i);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&m.full[s], kSlotBytes);
-          const uint32_t dst = base + kRing + s * kSlotBytes;
-          tma_load_3d_u(dst, &map_v, &m.full[s], 0, head, key + 64 * hf);
-          tma_load_3d_u(dst + 8192, &map_v, &m.full[s], 64, head, key + 64 * hf);
-          ++pos;
+        before(2);
+        if (!ok) break;
+        bar = &m.full[u % kUnits];
+        mbar_arrive_expect_tx(bar, halves * kSlotBytes);
+        for (int hf = 0; hf < halves; ++hf) {
+          const uint32_t dst = next();
+          tma_load_3d_u(dst, &map_v, bar, 0, head, key + 64 * hf);
+          tma_load_3d_u(dst + 8192, &map_v, bar, 64, head, key + 64 * hf);
         }
+        ++u;
       }
       if (ok) mbar_arrive(&m.clean_req);
-      m.load_pos = pos;
-    } else if (warp == kMmaWarp && lane == 0 && n_iter > 0) {
-      // ---- MMA issue
+      m.loaded = u;
+    } else if (warp == kMmaWarp && n_iter > 0) {
+      // ---- MMA issue: the whole warp walks the loop, so that descriptors stay in
+      // uniform registers; one lane issues
+      const bool lead = elect_one();
       bool ok = true;
-      const int last_user = nt[1] > 0 ? 1 : 0;   // releases the slots
-      auto issue_s = [&](int t, int i) {
-        for (int kb = 0; ok && kb < KB; ++kb) {
-          const uint32_t pos = (uint32_t)i * PER + kb, s = pos % S;
-          ok = wait_or_abort(cx, &m.full[s], (pos / S) & 1, 20, i);
-          if (!ok) return;
-          const uint32_t a = base + (t * KB + kb) * kQTile, b = base + kRing + s * kSlotBytes;
+      const int last_user = nt[1] > 0 ? 1 : 0;   // releases the units
+      const Desc ring_k(base + kRing, 16), ring_v(base + kRing, 8192);
+      auto issue_s = [&](int t, int i, uint32_t at) {  // at: first slot of key tile i
+        const Desc a(base + t * KB * kQTile, 16);
+        ok = warp_wait(cx, &m.full[(2 * i) % kUnits], (2 * i / kUnits) & 1, 20, i);
+        if (!ok) return;
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma_ss(tm + 128 * t, sdesc_sw128(a + ks * 32, 16, 1024),
-                    sdesc_sw128(b + ks * 32, 16, 1024), ID_S, kb + ks > 0);
-          if (t == last_user) umma_commit(&m.empty[s]);
+        for (int kb = 0; kb < KB; ++kb) {
+          const uint32_t off = at * kSlotBytes;
+          at = at + 1 == S ? 0 : at + 1;
+          if (lead) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              umma_ss(tm + 128 * t, a.at(kb * kQTile + ks * 32), ring_k.at(off + ks * 32), ID_S,
+                      kb + ks > 0);
+          }
         }
-        umma_commit(&m.s_full[t]);
-      };
-      auto issue_pv = [&](int t, int i) {
-        const int halves = i + 1 < n_iter ? 2 : halves_last;
-        for (int hf = 0; ok && hf < halves; ++hf) {
-          const uint32_t pos = (uint32_t)i * PER + KB + hf, s = pos % S;
-          ok = wait_or_abort(cx, &m.full[s], (pos / S) & 1, 21, i);
-          // the last tile's rows past the sequence have been zeroed
-          if (ok && i + 1 == n_iter && last_live < 64 * (hf + 1))
-            ok = wait_or_abort(cx, &m.clean[s], 0, 22, i);
-          if (!ok) return;
-          const uint32_t b = base + kRing + s * kSlotBytes;
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma_ts(tm + 256 + 128 * t, tm + 128 * t + 32 * hf + 8 * ks,
-                    sdesc_sw128(b + ks * 2048, 8192, 1024), ID_PV, i + hf + ks > 0);
-          if (t == last_user) umma_commit(&m.empty[s]);
+        if (lead) {
+          if (t == last_user) umma_commit(&m.empty[(2 * i) % kUnits]);
+          umma_commit(&m.s_full[t]);
         }
       };
-      for (int t = 0; ok && t < 2; ++t)
-        if (nt[t] > 0) {
-          ok = wait_or_abort(cx, &m.q_full[t], 0, 23, t);
-          if (ok) issue_s(t, 0);
+      auto issue_pv = [&](int t, int i, uint32_t at) {  // at: first slot of value tile i
+        const int u = 2 * i + 1;
+        const bool last = i + 1 == n_iter;
+        ok = warp_wait(cx, &m.full[u % kUnits], (u / kUnits) & 1, 21, i);
+        // the last tile's rows past the sequence have been zeroed
+        if (ok && last && (last_live & 63) != 0) ok = warp_wait(cx, &m.clean, 0, 22, i);
+        ok = ok && warp_wait(cx, &m.p_ready[t][0], i & 1, 23, i);
+        if (!ok) return;
+        tc_fence_after();
+        if (lead) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_ts(tm + 256 + 128 * t, tm + 128 * t + 8 * ks, ring_v.at(at * kSlotBytes + ks * 2048),
+                    ID_PV, i + ks > 0);
         }
-      for (int i = 0; ok && i < n_iter; ++i)
-        for (int t = 0; ok && t < 2; ++t) {
-          if (i >= nt[t]) continue;
-          ok = wait_or_abort(cx, &m.p_ready[t], i & 1, 24, i);
-          if (!ok) break;
-          tc_fence_after();
-          issue_pv(t, i);
-          if (!ok) break;
-          if (i + 1 < nt[t])
-            issue_s(t, i + 1);
-          else
+        at = at + 1 == S ? 0 : at + 1;
+        ok = warp_wait(cx, &m.p_ready[t][1], i & 1, 24, i);
+        if (!ok) return;
+        tc_fence_after();
+        if (lead) {
+          if (!last || halves_last == 2) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              umma_ts(tm + 256 + 128 * t, tm + 128 * t + 32 + 8 * ks,
+                      ring_v.at(at * kSlotBytes + ks * 2048), ID_PV, 1);
+          }
+          if (t == last_user) umma_commit(&m.empty[u % kUnits]);
+        }
+      };
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (ok && nt[t] > 0) {
+          ok = warp_wait(cx, &m.q_full[t], 0, 25, t);
+          if (ok) issue_s(t, 0, 0);
+        }
+      uint32_t at = 0;                           // first slot of key tile i
+      for (int i = 0; ok && i < n_iter; ++i) {
+        const uint32_t at_v = at + KB >= S ? at + KB - S : at + KB;
+        const uint32_t at_n = at + PER >= S ? at + PER - S : at + PER;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || i >= nt[t]) continue;
+          issue_pv(t, i, at_v);
+          if (!ok) continue;
+          if (i + 1 < nt[t]) {
+            issue_s(t, i + 1, at_n);
+          } else if (lead) {
             umma_commit(&m.o_full[t]);
+          }
         }
+        at = at_n;
+      }
     } else if (warp == kCleanWarp && n_iter > 0 && (last_live & 63) != 0) {
       // ---- cleaner: value rows past the sequence's end are another sequence's, and
       // may hold anything; zero them (0 * NaN would reach the sum).  The loader asks
       // once the copies of the last tile are under way.
-      bool ok = wait_or_abort(cx, &m.clean_req, 0, 30, n_iter);
-      const uint32_t pos = (uint32_t)(n_iter - 1) * PER + KB + halves_last - 1, s = pos % S;
-      ok = ok && wait_or_abort(cx, &m.full[s], (pos / S) & 1, 31, n_iter);
-      if (__all_sync(0xffffffffu, ok)) {
+      const int u = 2 * n_iter - 1;
+      bool ok = warp_wait(cx, &m.clean_req, 0, 30, n_iter);
+      ok = ok && warp_wait(cx, &m.full[u % kUnits], (u / kUnits) & 1, 31, n_iter);
+      if (ok) {
         const int from = last_live & 63;
+        const uint32_t s = ((uint32_t)(n_iter - 1) * PER + KB + halves_last - 1) % S;
         const uint32_t dst = base + kRing + s * kSlotBytes + from * 128;
         for (int j = lane; j < (64 - from) * 8; j += 32) {
           st_shared_v4(dst + j * 16, 0, 0, 0, 0);
@@ -264,7 +307,7 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&m.clean[s]);
+        if (lane == 0) mbar_arrive(&m.clean);
       }
     }
   } else {
@@ -280,7 +323,7 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     float ref = kNoRef, l = 0.f;
     bool ok = true;
     for (int i = 0; ok && i < nt[t]; ++i) {
-      ok = __all_sync(0xffffffffu, wait_or_abort(cx, &m.s_full[t], i & 1, 40, i));
+      ok = warp_wait(cx, &m.s_full[t], i & 1, 40, i);
       if (!ok) break;
       tc_fence_after();
       uint32_t x[4][32];
@@ -334,18 +377,20 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
           pk[j / 2] = pack_bf16x2(a, b);
         }
         tmem_st16(tm_s + 16 * c, pk);
+        if (c & 1) {  // 64 keys are ready for their product
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&m.p_ready[t][c >> 1]);
+        }
       }
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&m.p_ready[t]);
     }
     // ---- output: O / l through this warp's rows of its own query tile's buffer
     // (all products with Q are done), so that rows leave whole
     const bool live = st.seq >= 0 && row0 + 128 * t < st.nq;
     if (ok && nt[t] > 0)
-      ok = __all_sync(0xffffffffu, wait_or_abort(cx, &m.o_full[t], 0, 41, n_iter));
+      ok = warp_wait(cx, &m.o_full[t], 0, 41, n_iter);
     if (ok && live) {
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const uint32_t buf = base + t * KB * kQTile + (warp & 3) * 32 * 256;
@@ -390,11 +435,11 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
   __syncthreads();
   if (m.abort) {  // nothing in flight outlives the CTA
     if (tid == 32 * kLoadWarp) {
-      const uint32_t pos = m.load_pos;
-      for (uint32_t k = pos > S ? pos - S : 0; k < pos; ++k)
-        mbar_wait(&m.full[k % S], (k / S) & 1, kWaitNs);
+      const int u = m.loaded;
+      for (int v = max(0, u - kUnits); v < u; ++v)
+        mbar_wait(&m.full[v % kUnits], (v / kUnits) & 1, kWaitNs);
       for (int t = 0; t < 2; ++t)
-        if (pos > 0 && nt[t] > 0 && (t == 0 || pos >= KB)) mbar_wait(&m.q_full[t], 0, kWaitNs);
+        if (nt[t] > 0) mbar_wait(&m.q_full[t], 0, kWaitNs);
     }
     if (tid == 32 * kMmaWarp) {
       umma_commit(&m.fin);

@@ -32,7 +32,7 @@ struct WaitCtx {
 };
 __device__ __forceinline__ bool wait_or_abort(const WaitCtx &cx, uint64_t *bar, uint32_t parity,
                                               int where, int step) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_test_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   for (;;) {
 #pragma unroll 1
@@ -45,6 +45,13 @@ __device__ __forceinline__ bool wait_or_abort(const WaitCtx &cx, uint64_t *bar, 
       return false;
     }
   }
+}
+
+// The same by a converged warp, whose lanes leave together.
+__device__ __forceinline__ bool warp_wait(const WaitCtx &cx, uint64_t *bar, uint32_t parity,
+                                          int where, int step) {
+  if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_or_abort(cx, bar, parity, where, step)) != 0;
 }
 
 // Barrier `id` over nthreads (a multiple of 32); returns whether any of them passed true.
@@ -75,6 +82,32 @@ __device__ __forceinline__ void tma_load_3d_u(uint32_t dst, const CUtensorMap *m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
+
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// A shared-memory matrix descriptor (128-byte swizzle) as its two words, so that
+// stepping along an operand is one 32-bit addition: the address sits in the low
+// word in units of 16 bytes.
+struct Desc {
+  uint32_t lo, hi;
+  __device__ __forceinline__ Desc(uint32_t addr, uint32_t lbo) {
+    const uint64_t d = sdesc_sw128(addr, lbo, 1024);
+    lo = (uint32_t)d;
+    hi = (uint32_t)(d >> 32);
+  }
+  __device__ __forceinline__ uint64_t at(uint32_t bytes) const {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo + (bytes >> 4)), "r"(hi));
+    return d;
+  }
+};
 
 // Programmatic launch: the next kernel's blocks may start; wait for the previous grid.
 __device__ __forceinline__ void pdl_launch_dependents() {
