@@ -220,50 +220,49 @@ __device__ __forceinline__ void pass(const Maps &maps, const Params &p, int inde
     }
     if (ok) mbar_arrive(&m.clean_req);
     m.loaded = i;
-  } else if (warp == kMmaWarp && lane == 0 && n > 0) {
+  } else if (warp == kMmaWarp && n > 0 && elect_one()) {
     // ---- MMA issue
-    auto stage = [&](int i) { return base + kStage + (uint32_t)(i % ST) * stage_bytes<DR>(); };
+    const Desc x_s(base, 16), y_s(base + kStage, 16), y_a(base + kStage, kYBlock);
+    constexpr uint32_t SB = stage_bytes<DR>();
     bool ok = wait_or_abort(cx, &m.x_full, 0, 20, 0);
-    auto issue_s = [&](int i) {
-      ok = ok && wait_or_abort(cx, &m.full[i % ST], (i / ST) & 1, 21, i);
+    auto issue_s = [&](int i, int s) {   // s: stage of tile i
+      ok = ok && wait_or_abort(cx, &m.full[s], (i / ST) & 1, 21, i);
       if (!ok) return;
-      const uint32_t y = stage(i);
 #pragma unroll
       for (int k = 0; k < 4 * KB; ++k)
-        umma_ss(tm + TM_S + 64 * (i & 1),
-                sdesc_sw128(base + (k >> 2) * kXBlock + (k & 3) * 32, 16, 1024),
-                sdesc_sw128(y + (k >> 2) * kYBlock + (k & 3) * 32, 16, 1024), ID_S, k > 0);
+        umma_ss(tm + TM_S + 64 * (i & 1), x_s.at((k >> 2) * kXBlock + (k & 3) * 32),
+                y_s.at(s * SB + (k >> 2) * kYBlock + (k & 3) * 32), ID_S, k > 0);
       umma_commit(&m.s_full[i & 1]);
     };
-    auto issue_dp = [&](int i) {
-      const uint32_t y = stage(i) + KB * kYBlock;
+    auto issue_dp = [&](int s) {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        umma_ss(tm + TM_DP, sdesc_sw128(base + (KB + (k >> 2)) * kXBlock + (k & 3) * 32, 16, 1024),
-                sdesc_sw128(y + (k >> 2) * kYBlock + (k & 3) * 32, 16, 1024), ID_S, k > 0);
+        umma_ss(tm + TM_DP, x_s.at((KB + (k >> 2)) * kXBlock + (k & 3) * 32),
+                y_s.at(s * SB + (KB + (k >> 2)) * kYBlock + (k & 3) * 32), ID_S, k > 0);
       umma_commit(&m.dp_full);
     };
-    issue_s(0);
+    issue_s(0, 0);
     if (ok) issue_dp(0);
-    if (n > 1) issue_s(1);
+    if (n > 1) issue_s(1, 1);
+    int s0 = 0;                          // stage of tile i
     for (int i = 0; ok && i < n; ++i) {
+      const int s1 = s0 + 1 == ST ? 0 : s0 + 1, s2 = s1 + 1 == ST ? 0 : s1 + 1;
       ok = wait_or_abort(cx, &m.ds_ready, i & 1, 22, i);
       if (ok && i + 1 == n && live < kY) ok = wait_or_abort(cx, &m.clean, 0, 23, i);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t y = stage(i), sb = tm + TM_S + 64 * (i & 1);
+      const uint32_t sb = tm + TM_S + 64 * (i & 1);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {  // bf16 columns: rows 0 .. 31 at +0, 32 .. 63 at +32
         const uint32_t a = (k >> 1) * 32 + (k & 1) * 8;
         if (kKeys)
-          umma_ts(tm + TM_A2, sb + a, sdesc_sw128(y + KB * kYBlock + k * 2048, kYBlock, 1024),
-                  ID_A2, i + k > 0);
-        umma_ts(tm + TM_A1, tm + TM_DP + a, sdesc_sw128(y + k * 2048, kYBlock, 1024), ID_A1,
-                i + k > 0);
+          umma_ts(tm + TM_A2, sb + a, y_a.at(s0 * SB + KB * kYBlock + k * 2048), ID_A2, i + k > 0);
+        umma_ts(tm + TM_A1, tm + TM_DP + a, y_a.at(s0 * SB + k * 2048), ID_A1, i + k > 0);
       }
-      umma_commit(&m.empty[i % ST]);
-      if (i + 1 < n) issue_dp(i + 1);
-      if (i + 2 < n) issue_s(i + 2);
+      umma_commit(&m.empty[s0]);
+      if (i + 1 < n) issue_dp(s1);
+      if (i + 2 < n) issue_s(i + 2, s2);
+      s0 = s1;
     }
     if (ok) umma_commit(&m.acc_full);
   } else if (warp == kCleanWarp && n > 0 && live < kY) {
@@ -271,9 +270,9 @@ __device__ __forceinline__ void pass(const Maps &maps, const Params &p, int inde
     // sequence's and may hold anything; as operands of the sums they are zeroed
     // (0 * NaN would reach the result).  The loader asks once their copy is under
     // way; the products that read them wait for it.
-    bool ok = wait_or_abort(cx, &m.clean_req, 0, 30, n);
-    ok = ok && wait_or_abort(cx, &m.full[(n - 1) % ST], ((n - 1) / ST) & 1, 31, n);
-    if (__all_sync(0xffffffffu, ok)) {
+    bool ok = warp_wait(cx, &m.clean_req, 0, 30, n);
+    ok = ok && warp_wait(cx, &m.full[(n - 1) % ST], ((n - 1) / ST) & 1, 31, n);
+    if (ok) {
       const uint32_t y = base + kStage + (uint32_t)((n - 1) % ST) * stage_bytes<DR>();
       for (int b = 0; b < KB + 2; ++b)
         for (int j = lane; j < (kY - live) * 8; j += 32)
@@ -301,8 +300,7 @@ __device__ __forceinline__ void pass(const Maps &maps, const Params &p, int inde
     }
     bool ok = true;
     for (int i = 0; ok && i < n; ++i) {
-      ok = __all_sync(0xffffffffu,
-                      wait_or_abort(cx, &m.s_full[i & 1], (i >> 1) & 1, 40, i));
+      ok = warp_wait(cx, &m.s_full[i & 1], (i >> 1) & 1, 40, i);
       if (!ok) break;
       tc_fence_after();
       uint32_t r[32];
@@ -337,7 +335,7 @@ __device__ __forceinline__ void pass(const Maps &maps, const Params &p, int inde
         for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(pr[2 * j], pr[2 * j + 1]);
         tmem_st16(ts, pk);
       }
-      ok = __all_sync(0xffffffffu, wait_or_abort(cx, &m.dp_full, i & 1, 41, i));
+      ok = warp_wait(cx, &m.dp_full, i & 1, 41, i);
       if (!ok) break;
       tc_fence_after();
       tmem_ld32(td, r);
@@ -373,7 +371,7 @@ __device__ __forceinline__ void pass(const Maps &maps, const Params &p, int inde
       if (lane == 0) mbar_arrive(&m.ds_ready);
     }
     if (ok && n > 0) {
-      ok = __all_sync(0xffffffffu, wait_or_abort(cx, &m.acc_full, 0, 42, n));
+      ok = warp_wait(cx, &m.acc_full, 0, 42, n);
       tc_fence_after();
     }
     // ---- output, 64 columns at a time, through the rows of X (all products are done)

@@ -211,66 +211,59 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       }
       if (ok) mbar_arrive(&m.clean_req);
       m.loaded = u;
-    } else if (warp == kMmaWarp && n_iter > 0) {
-      // ---- MMA issue: the whole warp walks the loop, so that descriptors stay in
-      // uniform registers; one lane issues
-      const bool lead = elect_one();
+    } else if (warp == kMmaWarp && n_iter > 0 && elect_one()) {
+      // ---- MMA issue, by the elected lane (elect.sync lets the compiler keep the
+      // descriptors in uniform registers: 270 us against 441 under lane == 0 with
+      // descriptors built for each product, and 311 with the warp converged and a
+      // branch per product; 4 x 4096 tokens, 16 heads)
       bool ok = true;
       const int last_user = nt[1] > 0 ? 1 : 0;   // releases the units
       const Desc ring_k(base + kRing, 16), ring_v(base + kRing, 8192);
       auto issue_s = [&](int t, int i, uint32_t at) {  // at: first slot of key tile i
         const Desc a(base + t * KB * kQTile, 16);
-        ok = warp_wait(cx, &m.full[(2 * i) % kUnits], (2 * i / kUnits) & 1, 20, i);
+        ok = wait_or_abort(cx, &m.full[(2 * i) % kUnits], (2 * i / kUnits) & 1, 20, i);
         if (!ok) return;
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
           const uint32_t off = at * kSlotBytes;
           at = at + 1 == S ? 0 : at + 1;
-          if (lead) {
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_ss(tm + 128 * t, a.at(kb * kQTile + ks * 32), ring_k.at(off + ks * 32), ID_S,
-                      kb + ks > 0);
-          }
+          for (int ks = 0; ks < 4; ++ks)
+            umma_ss(tm + 128 * t, a.at(kb * kQTile + ks * 32), ring_k.at(off + ks * 32), ID_S,
+                    kb + ks > 0);
         }
-        if (lead) {
-          if (t == last_user) umma_commit(&m.empty[(2 * i) % kUnits]);
-          umma_commit(&m.s_full[t]);
-        }
+        if (t == last_user) umma_commit(&m.empty[(2 * i) % kUnits]);
+        umma_commit(&m.s_full[t]);
       };
       auto issue_pv = [&](int t, int i, uint32_t at) {  // at: first slot of value tile i
         const int u = 2 * i + 1;
         const bool last = i + 1 == n_iter;
-        ok = warp_wait(cx, &m.full[u % kUnits], (u / kUnits) & 1, 21, i);
+        ok = wait_or_abort(cx, &m.full[u % kUnits], (u / kUnits) & 1, 21, i);
         // the last tile's rows past the sequence have been zeroed
-        if (ok && last && (last_live & 63) != 0) ok = warp_wait(cx, &m.clean, 0, 22, i);
-        ok = ok && warp_wait(cx, &m.p_ready[t][0], i & 1, 23, i);
+        if (ok && last && (last_live & 63) != 0) ok = wait_or_abort(cx, &m.clean, 0, 22, i);
+        ok = ok && wait_or_abort(cx, &m.p_ready[t][0], i & 1, 23, i);
         if (!ok) return;
         tc_fence_after();
-        if (lead) {
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          umma_ts(tm + 256 + 128 * t, tm + 128 * t + 8 * ks, ring_v.at(at * kSlotBytes + ks * 2048),
+                  ID_PV, i + ks > 0);
+        at = at + 1 == S ? 0 : at + 1;
+        ok = wait_or_abort(cx, &m.p_ready[t][1], i & 1, 24, i);
+        if (!ok) return;
+        tc_fence_after();
+        if (!last || halves_last == 2) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            umma_ts(tm + 256 + 128 * t, tm + 128 * t + 8 * ks, ring_v.at(at * kSlotBytes + ks * 2048),
-                    ID_PV, i + ks > 0);
+            umma_ts(tm + 256 + 128 * t, tm + 128 * t + 32 + 8 * ks,
+                    ring_v.at(at * kSlotBytes + ks * 2048), ID_PV, 1);
         }
-        at = at + 1 == S ? 0 : at + 1;
-        ok = warp_wait(cx, &m.p_ready[t][1], i & 1, 24, i);
-        if (!ok) return;
-        tc_fence_after();
-        if (lead) {
-          if (!last || halves_last == 2) {
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_ts(tm + 256 + 128 * t, tm + 128 * t + 32 + 8 * ks,
-                      ring_v.at(at * kSlotBytes + ks * 2048), ID_PV, 1);
-          }
-          if (t == last_user) umma_commit(&m.empty[u % kUnits]);
-        }
+        if (t == last_user) umma_commit(&m.empty[u % kUnits]);
       };
 #pragma unroll
       for (int t = 0; t < 2; ++t)
         if (ok && nt[t] > 0) {
-          ok = warp_wait(cx, &m.q_full[t], 0, 25, t);
+          ok = wait_or_abort(cx, &m.q_full[t], 0, 25, t);
           if (ok) issue_s(t, 0, 0);
         }
       uint32_t at = 0;                           // first slot of key tile i
@@ -284,7 +277,7 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
           if (!ok) continue;
           if (i + 1 < nt[t]) {
             issue_s(t, i + 1, at_n);
-          } else if (lead) {
+          } else {
             umma_commit(&m.o_full[t]);
           }
         }
