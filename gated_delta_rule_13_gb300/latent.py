@@ -3,54 +3,82 @@
 Like ``kda``: every function has the name of the C entry point it wraps
 (include/kda.h), checks shapes, dtypes and devices, allocates what the caller
 did not pass, and forwards pointers with the current CUDA stream.
+
+The smallest calls take a few microseconds on the device, so the checks are one
+expression per tensor; the reason for a refusal is worked out only when there is
+one.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 
 import torch
 
-from .kda import (HEAD_DIM, KDA_BF16, _check, _need_cuda, _ptr, _stream_handle, library)
+from .kda import HEAD_DIM, KDA_BF16, _check, _need_cuda, library
 
 LATENT_DIM = 512    # latent channels of a cached row
 ROPE_DIM = 64       # rotary channels of a row, or none
 
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
 
-def _view3(name, t, shape):
-    """A bf16 ``[N, H, 128]`` view with contiguous rows; its token and head strides."""
+
+def _refuse(name, t, dtype, shape, device):
+    _need_cuda(name, t, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _tensor(name, t, dtype, shape, device):
+    """A contiguous tensor of this dtype and shape (None: any) on the device."""
+    try:
+        good = (t.dtype is dtype and t.device == device and t.is_contiguous()
+                and (shape is None or t.shape == shape))
+    except AttributeError:
+        good = False
+    if not good:
+        _refuse(name, t, dtype, shape, device)
+
+
+def _view(name, t, n, H, device):
+    """Token and head strides of a bf16 ``[n, H, 128]`` view with contiguous rows."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not _BF16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.stride(2) != 1:
+    if t.shape != (n, H, HEAD_DIM):
+        raise ValueError(f"{name} must have shape {(n, H, HEAD_DIM)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    ts, hs, one = t.stride()
+    if one != 1:
         raise ValueError(f"{name} must have contiguous rows")
     # torch leaves the strides of a dimension of size 1 (or 0) open
-    ts = t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-    hs = t.stride(1) if t.shape[1] > 1 else t.shape[2]
-    return ts, hs
+    return ts if n > 1 else H * HEAD_DIM, hs if H > 1 else HEAD_DIM
 
 
-def _on(stream):
-    """What a call allocates belongs to the stream it runs on, so that the caching
-    allocator hands the memory on in that stream's order."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
-
-def _cu(name, cu):
-    if not isinstance(cu, torch.Tensor) or cu.dtype != torch.int32 or cu.dim() != 1 \
+def _cu(name, cu, device):
+    if not isinstance(cu, torch.Tensor) or cu.dtype is not _I32 or cu.dim() != 1 \
             or cu.shape[0] < 2 or not cu.is_contiguous():
         raise TypeError(f"{name} must be a contiguous 1-D int32 tensor of n_seqs + 1 entries")
-    return cu
+    if cu.is_cuda and cu.device != device:
+        raise ValueError(f"{name} is on {cu.device}, not on {device}")
+    return cu.data_ptr()
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.is_cuda and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, q on {device}")
+def _new(stream, shape, dtype, device):
+    """A tensor that belongs to the stream of the call, so that the caching allocator
+    hands its memory on in that stream's order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _stream(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _scale(scale, dim):
@@ -60,9 +88,12 @@ def _scale(scale, dim):
     return scale
 
 
-def _expanded(q, k, v, k_rope, cu_seqlens_q, cu_seqlens_k, scale):
-    """The checked arguments both directions share."""
-    _need_cuda("q", q, torch.bfloat16)
+def _expanded(q, k, v, k_rope, cu_q, cu_k, scale):
+    """The checked arguments both directions share: those of the C call, then sizes."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise TypeError("q must be a CUDA tensor")
+    dev = q.device
+    _tensor("q", q, _BF16, None, dev)
     if q.dim() != 3 or q.shape[2] not in (HEAD_DIM, HEAD_DIM + ROPE_DIM):
         raise ValueError(f"q must be [n_q, H, 128] or [n_q, H, 192], got {tuple(q.shape)}")
     n_q, H, width = q.shape
@@ -70,39 +101,42 @@ def _expanded(q, k, v, k_rope, cu_seqlens_q, cu_seqlens_k, scale):
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must be [n_k, H, 128]")
     n_k = k.shape[0]
-    ks = _view3("k", k, (n_k, H, HEAD_DIM))
-    vs = _view3("v", v, (n_k, H, HEAD_DIM))
+    k_ts, k_hs = _view("k", k, n_k, H, dev)
+    v_ts, v_hs = _view("v", v, n_k, H, dev)
     if (k_rope is not None) != (dr > 0):
         raise ValueError("k_rope is given if and only if q has its 64 rotary channels")
+    rope = None
     if k_rope is not None:
-        _need_cuda("k_rope", k_rope, torch.bfloat16, (n_k, dr))
-    cu_q, cu_k = cu_seqlens_q, cu_seqlens_k
+        _tensor("k_rope", k_rope, _BF16, (n_k, dr), dev)
+        rope = k_rope.data_ptr()
     if cu_k is None and (cu_q is None or n_q == n_k):
         cu_k = cu_q
     if (cu_q is None) != (cu_k is None):
         raise ValueError("cu_seqlens_q and cu_seqlens_k are both needed when there are not as "
                          "many keys as queries")
-    n_seqs = 1
+    n_seqs, at_q, at_k = 1, None, None
     if cu_q is not None:
-        n_seqs = _cu("cu_seqlens_q", cu_q).shape[0] - 1
-        if _cu("cu_seqlens_k", cu_k).shape != cu_q.shape:
+        at_q, at_k = _cu("cu_seqlens_q", cu_q, dev), _cu("cu_seqlens_k", cu_k, dev)
+        n_seqs = cu_q.shape[0] - 1
+        if cu_k.shape[0] != n_seqs + 1:
             raise ValueError("cu_seqlens_q and cu_seqlens_k must have the same length")
-    _same_device(q.device, k=k, v=v, k_rope=k_rope, cu_seqlens_q=cu_q, cu_seqlens_k=cu_k)
-    head = (_ptr(q), _ptr(k), _ptr(v), _ptr(k_rope), *ks, *vs, _ptr(cu_q), _ptr(cu_k), n_seqs,
-            n_q, n_k, H, HEAD_DIM, dr, HEAD_DIM, KDA_BF16)
-    return head, _scale(scale, width), (n_seqs, n_q, n_k, H, dr)
+    head = (q.data_ptr(), k.data_ptr(), v.data_ptr(), rope, k_ts, k_hs, v_ts, v_hs, at_q, at_k,
+            n_seqs, n_q, n_k, H, HEAD_DIM, dr, HEAD_DIM, KDA_BF16, _scale(scale, width))
+    return head, (n_seqs, n_q, n_k, H, dr), dev
 
 
 def _workspace(workspace, size, device, stream):
     if workspace is None:
-        with _on(stream):
-            return torch.empty(size, dtype=torch.uint8, device=device)
+        return _new(stream, size, torch.uint8, device)
     _need_cuda("workspace", workspace)
-    _same_device(device, workspace=workspace)
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, not on {device}")
     return workspace
 
 
+@functools.lru_cache(maxsize=1024)
 def _size(fn, *args):
+    """A workspace size: it follows from the sizes and the device's SM count alone."""
     out = ctypes.c_size_t(0)
     _check(getattr(library(), fn)(*args, ctypes.byref(out)), fn)
     return out.value
@@ -130,23 +164,23 @@ def kda_latent_fwd(q, k, v, k_rope=None, cu_seqlens_q=None, cu_seqlens_k=None, *
     strided views of one projection), k_rope ``[n_k, 64]`` shared by the heads
     (given if and only if q has the 64 rotary channels).  ``cu_seqlens_q`` /
     ``cu_seqlens_k``: int32 prefix sums (CUDA or CPU), None for one sequence; with as
-    many keys as queries a missing ``cu_seqlens_k`` is ``cu_seqlens_q``.  With ``causal`` the queries are
-    the last tokens of their sequence's keys.  ``scale`` defaults to
-    1 / sqrt(128 + dr).  Returns ``(out [n_q, H, 128], lse [n_q, H])``."""
-    head, sc, (n_seqs, n_q, n_k, H, dr) = _expanded(q, k, v, k_rope, cu_seqlens_q, cu_seqlens_k,
-                                                    scale)
-    with _on(stream):
-        if out is None:
-            out = torch.empty(n_q, H, HEAD_DIM, dtype=q.dtype, device=q.device)
-        if lse is None:
-            lse = torch.empty(n_q, H, dtype=torch.float32, device=q.device)
-    _need_cuda("out", out, q.dtype, (n_q, H, HEAD_DIM))
-    _need_cuda("lse", lse, torch.float32, (n_q, H))
-    ws = _workspace(workspace, kda_latent_fwd_workspace_size(n_seqs, n_q, n_k, H, dr=dr),
-                    q.device, stream)
-    _same_device(q.device, out=out, lse=lse)
-    _check(library().kda_latent_fwd(*head, sc, int(bool(causal)), _ptr(out), _ptr(lse), _ptr(ws),
-                                    ws.numel() * ws.element_size(), _stream_handle(stream)),
+    many keys as queries a missing ``cu_seqlens_k`` is ``cu_seqlens_q``.  With
+    ``causal`` the queries are the last tokens of their sequence's keys.  ``scale``
+    defaults to 1 / sqrt(128 + dr).  Returns ``(out [n_q, H, 128], lse [n_q, H])``."""
+    head, sizes, dev = _expanded(q, k, v, k_rope, cu_seqlens_q, cu_seqlens_k, scale)
+    n_seqs, n_q, n_k, H, dr = sizes
+    if out is None:
+        out = _new(stream, (n_q, H, HEAD_DIM), _BF16, dev)
+    else:
+        _tensor("out", out, _BF16, (n_q, H, HEAD_DIM), dev)
+    if lse is None:
+        lse = _new(stream, (n_q, H), _F32, dev)
+    else:
+        _tensor("lse", lse, _F32, (n_q, H), dev)
+    ws = _workspace(workspace, kda_latent_fwd_workspace_size(n_seqs, n_q, n_k, H, dr=dr), dev,
+                    stream)
+    _check(library().kda_latent_fwd(*head, 1 if causal else 0, out.data_ptr(), lse.data_ptr(),
+                                    ws.data_ptr(), ws.nbytes, _stream(stream, dev)),
            "kda_latent_fwd")
     return out, lse
 
@@ -157,27 +191,25 @@ def kda_latent_bwd(q, k, v, k_rope, out, lse, d_out, cu_seqlens_q=None, cu_seqle
     and ``lse`` are what it returned.  Returns ``(dq, d_k, d_v, d_k_rope)`` in the
     layouts of the inputs (d_k_rope None without a rotary part).  ``d_k`` and
     ``d_v`` may be given as strided views, as k and v may."""
-    head, sc, (n_seqs, n_q, n_k, H, dr) = _expanded(q, k, v, k_rope, cu_seqlens_q, cu_seqlens_k,
-                                                    scale)
-    _need_cuda("out", out, q.dtype, (n_q, H, HEAD_DIM))
-    _need_cuda("lse", lse, torch.float32, (n_q, H))
-    _need_cuda("d_out", d_out, q.dtype, (n_q, H, HEAD_DIM))
-    with _on(stream):
-        dq = torch.empty_like(q)
-        if d_k is None:
-            d_k = torch.empty(n_k, H, HEAD_DIM, dtype=q.dtype, device=q.device)
-        if d_v is None:
-            d_v = torch.empty(n_k, H, HEAD_DIM, dtype=q.dtype, device=q.device)
-        d_rope = torch.empty(n_k, dr, dtype=q.dtype, device=q.device) if dr else None
-    dks = _view3("d_k", d_k, (n_k, H, HEAD_DIM))
-    dvs = _view3("d_v", d_v, (n_k, H, HEAD_DIM))
-    ws = _workspace(workspace, kda_latent_bwd_workspace_size(n_seqs, n_q, n_k, H, dr=dr),
-                    q.device, stream)
-    _same_device(q.device, out=out, lse=lse, d_out=d_out, d_k=d_k, d_v=d_v)
-    _check(library().kda_latent_bwd(*head, sc, int(bool(causal)), _ptr(out), _ptr(lse),
-                                    _ptr(d_out), _ptr(dq), _ptr(d_k), _ptr(d_v), _ptr(d_rope),
-                                    *dks, *dvs, _ptr(ws), ws.numel() * ws.element_size(),
-                                    _stream_handle(stream)), "kda_latent_bwd")
+    head, sizes, dev = _expanded(q, k, v, k_rope, cu_seqlens_q, cu_seqlens_k, scale)
+    n_seqs, n_q, n_k, H, dr = sizes
+    _tensor("out", out, _BF16, (n_q, H, HEAD_DIM), dev)
+    _tensor("lse", lse, _F32, (n_q, H), dev)
+    _tensor("d_out", d_out, _BF16, (n_q, H, HEAD_DIM), dev)
+    dq = _new(stream, q.shape, _BF16, dev)
+    if d_k is None:
+        d_k = _new(stream, (n_k, H, HEAD_DIM), _BF16, dev)
+    if d_v is None:
+        d_v = _new(stream, (n_k, H, HEAD_DIM), _BF16, dev)
+    strides = _view("d_k", d_k, n_k, H, dev) + _view("d_v", d_v, n_k, H, dev)
+    d_rope = _new(stream, (n_k, dr), _BF16, dev) if dr else None
+    ws = _workspace(workspace, kda_latent_bwd_workspace_size(n_seqs, n_q, n_k, H, dr=dr), dev,
+                    stream)
+    _check(library().kda_latent_bwd(*head, 1 if causal else 0, out.data_ptr(), lse.data_ptr(),
+                                    d_out.data_ptr(), dq.data_ptr(), d_k.data_ptr(),
+                                    d_v.data_ptr(), d_rope.data_ptr() if dr else None, *strides,
+                                    ws.data_ptr(), ws.nbytes, _stream(stream, dev)),
+           "kda_latent_bwd")
     return dq, d_k, d_v, d_rope
 
 
@@ -193,44 +225,44 @@ def kda_latent_decode(q, cache, block_table, seq_lens, *, tree_mask=None, scale=
     T new rows; None: the new rows are consecutive tokens.  ``scale`` defaults to
     1 / sqrt(128 + dr), the expanded form's.  ``lse`` (``[B, T, H]`` fp32) is
     written when given.  Returns out ``[B, T, H, 512]``."""
-    _need_cuda("q", q, torch.bfloat16)
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise TypeError("q must be a CUDA tensor")
+    dev = q.device
+    _tensor("q", q, _BF16, None, dev)
     if q.dim() != 4 or q.shape[3] not in (LATENT_DIM, LATENT_DIM + ROPE_DIM):
         raise ValueError(f"q must be [B, T, H, 512] or [B, T, H, 576], got {tuple(q.shape)}")
     B, T, H, width = q.shape
     dr = width - LATENT_DIM
-    _need_cuda("cache", cache, torch.bfloat16)
+    _tensor("cache", cache, _BF16, None, dev)
     if cache.dim() != 3 or cache.shape[2] != width:
         raise ValueError(f"cache must be [n_pages, page_size, {width}], got {tuple(cache.shape)}")
-    _need_cuda("block_table", block_table, torch.int32)
+    _tensor("block_table", block_table, _I32, None, dev)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B, max_pages]")
-    _need_cuda("seq_lens", seq_lens, torch.int32, (B,))
+    _tensor("seq_lens", seq_lens, _I32, (B,), dev)
     if tree_mask is not None:
-        _need_cuda("tree_mask", tree_mask, torch.int64, (B, T))
+        _tensor("tree_mask", tree_mask, _I64, (B, T), dev)
     if out is None:
-        with _on(stream):
-            out = torch.empty(B, T, H, LATENT_DIM, dtype=q.dtype, device=q.device)
-    _need_cuda("out", out, q.dtype, (B, T, H, LATENT_DIM))
+        out = _new(stream, (B, T, H, LATENT_DIM), _BF16, dev)
+    else:
+        _tensor("out", out, _BF16, (B, T, H, LATENT_DIM), dev)
     if lse is not None:
-        _need_cuda("lse", lse, torch.float32, (B, T, H))
-    sc = _scale(scale, HEAD_DIM + dr)
-    ws = _workspace(workspace, kda_latent_decode_workspace_size(B, T, H, dr=dr),
-                    q.device, stream)
-    _same_device(q.device, cache=cache, block_table=block_table, seq_lens=seq_lens,
-                 tree_mask=tree_mask, out=out, lse=lse)
+        _tensor("lse", lse, _F32, (B, T, H), dev)
+    ws = _workspace(workspace, kda_latent_decode_workspace_size(B, T, H, dr=dr), dev, stream)
     _check(library().kda_latent_decode(
-        _ptr(q), _ptr(cache), _ptr(block_table), _ptr(seq_lens), _ptr(tree_mask), B, T, H,
-        LATENT_DIM, dr, cache.shape[0], cache.shape[1], block_table.shape[1], KDA_BF16, sc,
-        _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream_handle(stream)),
-        "kda_latent_decode")
+        q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        None if tree_mask is None else tree_mask.data_ptr(), B, T, H, LATENT_DIM, dr,
+        cache.shape[0], cache.shape[1], block_table.shape[1], KDA_BF16,
+        _scale(scale, HEAD_DIM + dr), out.data_ptr(), None if lse is None else lse.data_ptr(),
+        ws.data_ptr(), ws.nbytes, _stream(stream, dev)), "kda_latent_decode")
     return out
 
 
-def _status_arg(status, device):
-    if status is not None:
-        _need_cuda("status", status, torch.int32, (1,))
-        _same_device(device, status=status)
-    return _ptr(status)
+def _status(status, device):
+    if status is None:
+        return None
+    _tensor("status", status, _I32, (1,), device)
+    return status.data_ptr()
 
 
 def kda_cache_write(cache, rows, block_table, start, *, path=None, n_write=None, status=None,
@@ -245,52 +277,61 @@ def kda_cache_write(cache, rows, block_table, start, *, path=None, n_write=None,
     block_table ``[B, max_pages]``, start ``[B]``, path ``[B, T]``, n_write ``[B]``:
     int32 on the device.  ``status`` (int32 ``[1]`` on the device) receives an
     error code if a sequence's positions or path are refused.  Returns cache."""
-    _need_cuda("cache", cache)
-    if cache.dim() not in (3, 4):
+    if not isinstance(cache, torch.Tensor) or not cache.is_cuda:
+        raise TypeError("cache must be a CUDA tensor")
+    dev, dtype = cache.device, cache.dtype
+    _tensor("cache", cache, dtype, None, dev)
+    layered = cache.dim() == 4
+    if not layered and cache.dim() != 3:
         raise ValueError("cache must be [n_pages, page_size, W] or [L, n_pages, page_size, W]")
-    layers = cache.shape[0] if cache.dim() == 4 else 1
+    L = cache.shape[0] if layered else 1
     n_pages, page, W = cache.shape[-3:]
     esz = cache.element_size()
-    _need_cuda("block_table", block_table, torch.int32)
+    _tensor("block_table", block_table, _I32, None, dev)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_pages]")
     B, max_pages = block_table.shape
-    _need_cuda("start", start, torch.int32, (B,))
+    _tensor("start", start, _I32, (B,), dev)
+    at_path = at_n = None
     if path is not None:
-        _need_cuda("path", path, torch.int32)
+        _tensor("path", path, _I32, None, dev)
         if path.dim() != 2 or path.shape[0] != B:
             raise ValueError("path must be [B, T]")
+        at_path = path.data_ptr()
     if n_write is not None:
-        _need_cuda("n_write", n_write, torch.int32, (B,))
+        _tensor("n_write", n_write, _I32, (B,), dev)
+        at_n = n_write.data_ptr()
+    at_status = _status(status, dev)
     if rows is None:
         if path is None:
             raise ValueError("compaction (rows None) needs path")
-        T, strides = path.shape[1], (0, 0, 0)
+        T, ls, bs, ts, at_rows = path.shape[1], 0, 0, 0, None
     else:
-        if not isinstance(rows, torch.Tensor) or not rows.is_cuda or rows.dtype != cache.dtype:
-            raise TypeError(f"rows must be a CUDA tensor of {cache.dtype}")
+        if not isinstance(rows, torch.Tensor) or not rows.is_cuda or rows.dtype is not dtype:
+            raise TypeError(f"rows must be a CUDA tensor of {dtype}")
+        if rows.device != dev:
+            raise ValueError(f"rows is on {rows.device}, not on {dev}")
         if rows.dim() != cache.dim():
             raise ValueError("rows must be [B, T, W], or [L, B, T, W] for a cache with layers")
         T = rows.shape[-2]
-        want = ((layers,) if cache.dim() == 4 else ()) + (B, T, W)
-        if tuple(rows.shape) != want or (path is not None and path.shape[1] != T):
-            raise ValueError(f"rows must have shape {want} and path [B, T]")
-        if W > 1 and rows.stride(-1) != 1:
+        if rows.shape != ((L, B, T, W) if layered else (B, T, W)) \
+                or (path is not None and path.shape[1] != T):
+            raise ValueError(f"rows must be {'[L, ' if layered else '['}{B}, T, {W}] and path "
+                             f"[{B}, T], got {tuple(rows.shape)}")
+        stride = rows.stride()
+        if W > 1 and stride[-1] != 1:
             raise ValueError("rows must have contiguous channels")
         # torch leaves the strides of a dimension of size 1 open
-        strides = tuple(0 if n == 1 else st * esz for n, st in
-                        zip(((1,) if rows.dim() == 3 else ()) + tuple(rows.shape[:-1]),
-                            ((0,) if rows.dim() == 3 else ()) + tuple(rows.stride()[:-1])))
-    for name, t in dict(rows=rows, block_table=block_table, start=start, path=path,
-                        n_write=n_write).items():
-        if t is not None and t.device != cache.device:
-            raise ValueError(f"{name} is on {t.device}, cache on {cache.device}")
-    if layers == 0 or B == 0 or T == 0:
+        ls = stride[0] * esz if L > 1 else 0
+        bs = stride[-3] * esz if B > 1 else 0
+        ts = stride[-2] * esz if T > 1 else 0
+        at_rows = rows.data_ptr()
+    if L == 0 or B == 0 or T == 0:
         return cache
     _check(library().kda_cache_write(
-        _ptr(cache), _ptr(rows), *strides, _ptr(block_table), _ptr(start), _ptr(path),
-        _ptr(n_write), layers, n_pages, page, W * esz, B, T, max_pages,
-        _status_arg(status, cache.device), _stream_handle(stream)), "kda_cache_write")
+        cache.data_ptr(), at_rows, ls, bs, ts, block_table.data_ptr(), start.data_ptr(), at_path,
+        at_n, L, n_pages, page, W * esz, B, T, max_pages, at_status, _stream(stream, dev)),
+        "kda_cache_write")
     return cache
 
 
@@ -299,21 +340,23 @@ def kda_cache_copy_pages(cache, src, dst, *, status=None, stream=None):
     copy of page ``src[i]``, in place (any dtype; a page is all that lies behind the
     first two dimensions).  src, dst: int32 ``[n]`` on the device; the dst pages are
     distinct and none is a src.  Returns cache."""
-    _need_cuda("cache", cache)
+    if not isinstance(cache, torch.Tensor) or not cache.is_cuda:
+        raise TypeError("cache must be a CUDA tensor")
+    dev = cache.device
+    _tensor("cache", cache, cache.dtype, None, dev)
     if cache.dim() < 3:
         raise ValueError("cache must be [L, n_pages, ...]")
-    _need_cuda("src", src, torch.int32)
+    _tensor("src", src, _I32, None, dev)
     if src.dim() != 1:
         raise ValueError("src must be one-dimensional")
-    _need_cuda("dst", dst, torch.int32, src.shape)
-    for name, t in dict(src=src, dst=dst).items():
-        if t.device != cache.device:
-            raise ValueError(f"{name} is on {t.device}, cache on {cache.device}")
+    n = src.shape[0]
+    _tensor("dst", dst, _I32, (n,), dev)
+    at_status = _status(status, dev)
     L, n_pages = cache.shape[:2]
-    if L == 0 or src.shape[0] == 0:
+    if L == 0 or n == 0:
         return cache
     page_bytes = math.prod(cache.shape[2:]) * cache.element_size()
-    _check(library().kda_cache_copy_pages(
-        _ptr(cache), _ptr(src), _ptr(dst), src.shape[0], L, n_pages, page_bytes,
-        _status_arg(status, cache.device), _stream_handle(stream)), "kda_cache_copy_pages")
+    _check(library().kda_cache_copy_pages(cache.data_ptr(), src.data_ptr(), dst.data_ptr(), n, L,
+                                          n_pages, page_bytes, at_status, _stream(stream, dev)),
+           "kda_cache_copy_pages")
     return cache
