@@ -82,6 +82,11 @@ __device__ __forceinline__ void record_device_status(DeviceStatus *st, int32_t c
   }
 }
 
+// Status of a call that has one writer of its validity: cleared, or the error.
+__device__ __forceinline__ void set_device_status(DeviceStatus *st, int32_t code, int32_t detail) {
+  *st = DeviceStatus{code, detail, 0, 0, 0, 0};
+}
+
 // A tile of `rows` packed rows of one sequence: which sequence and which rows.
 struct SeqTile {
   int32_t seq, tile, n_tiles;      // n_tiles of the sequence; seq < 0: no such tile

@@ -113,10 +113,11 @@ int prepare(kda::LatentArgs &a, int32_t dk, int32_t dv, int dtype, const int32_t
   return KDA_OK;
 }
 
-// Clears the status block and resolves both cu_seqlens arrays.
+// Resolves both cu_seqlens arrays.  The first kernel clears the status block; a
+// call without queries has none.
 int begin(kda::LatentArgs &a, const int32_t *cu_q, const int32_t *cu_k, unsigned char *ws,
           cudaStream_t st) {
-  int r = cuda_result(cudaMemsetAsync(ws, 0, kStatusBytes, st));
+  int r = a.n_q > 0 ? KDA_OK : cuda_result(cudaMemsetAsync(ws, 0, kStatusBytes, st));
   if (r == KDA_OK) r = resolve_cu(cu_q, a.n_seqs, a.n_q, ws + kStatusBytes, st, &a.cu_q);
   if (r == KDA_OK)
     r = resolve_cu(cu_k, a.n_seqs, a.n_k, ws + kStatusBytes + cu_bytes(a.n_seqs), st, &a.cu_k);

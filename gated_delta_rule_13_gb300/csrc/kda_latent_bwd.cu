@@ -154,6 +154,13 @@ __device__ __forceinline__ void pass(const Maps &maps, const Params &p, int inde
     m.loaded = 0;
     fence_mbarrier_init();
   }
+  if (warp == kLoadWarp && lane == 0) {
+    prefetch_tensormap(kKeys ? &maps.k128 : &maps.q128);
+    prefetch_tensormap(kKeys ? &maps.v128 : &maps.g128);
+    prefetch_tensormap(kKeys ? &maps.q64 : &maps.k64);
+    prefetch_tensormap(kKeys ? &maps.g64 : &maps.v64);
+    if (DR) prefetch_tensormap(kKeys ? &maps.r128 : &maps.r64);
+  }
   if (warp == kMmaWarp) {
     tmem_alloc(&m.tmem, 512);
     tmem_relinquish();
@@ -163,8 +170,9 @@ __device__ __forceinline__ void pass(const Maps &maps, const Params &p, int inde
   tc_fence_after();
   const uint32_t tm = m.tmem;
   const SeqTile st = m.tile;
-  if (st.bad && index == 0 && head == 0 && tid == 0)
-    record_device_status(p.status, KDA_ERR_INVALID_ARG, 1, 0, 0);
+
+  if (st.bad && p.n_q == 0 && index == 0 && head == 0 && tid == 0)  // no first kernel
+    set_device_status(p.status, KDA_ERR_INVALID_ARG, 1);
 
   // The CTA's rows [x0, x0 + 128) of the sequence, longest first: the first keys are
   // seen by the most queries, the last queries see the most keys.  It streams
@@ -469,6 +477,8 @@ kda_latent_stat_kernel(const __nv_bfloat16 *__restrict__ out,
     if (tid == 0) st = f;
   }
   __syncthreads();
+  if (blockIdx.x == 0 && head == 0 && tid == 0)  // the call's first kernel
+    set_device_status(p.status, st.bad ? KDA_ERR_INVALID_ARG : KDA_OK, st.bad);
   if (st.seq < 0) return;
   const int64_t at = head * p.stat_rows + (stat_tile(st.q0, st.seq) + st.tile) * kY;
 #pragma unroll

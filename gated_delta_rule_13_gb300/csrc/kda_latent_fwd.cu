@@ -138,8 +138,10 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
   tc_fence_after();
   const uint32_t tm = m.tmem;
   const SeqTile st = m.tile;
-  if (st.bad && blockIdx.x == 0 && tid == 0)
-    record_device_status(p.status, KDA_ERR_INVALID_ARG, 1, 0, 0);
+  // every block sees a malformed array; block 0 says so, or clears the status (a
+  // wait that gives up does so seconds later)
+  if (blockIdx.x == 0 && tid == 0)
+    set_device_status(p.status, st.bad ? KDA_ERR_INVALID_ARG : KDA_OK, st.bad);
 
   // Longest first: the last queries of a sequence see the most keys.
   const int row0 = (st.n_tiles - 1 - st.tile) * kRows;   // of the sequence
