@@ -279,8 +279,6 @@ int kda_latent_decode(const void *q, const void *cache, const int32_t *block_tab
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < need) return KDA_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   unsigned char *ws = static_cast<unsigned char *>(workspace);
-  const int r = cuda_result(cudaMemsetAsync(ws, 0, kStatusBytes, st));
-  if (r != KDA_OK) return r;
   kda::LatentDecodeArgs a;
   a.q = q; a.cache = cache; a.block_table = block_table; a.seq_lens = seq_lens;
   a.tree_mask = tree_mask; a.B = B; a.T = T; a.H = H; a.dr = dr; a.n_pages = n_pages;

@@ -23,6 +23,38 @@ constexpr float kLn2 = 0.6931471805599453f;
 // scores (-inf) stay -inf against it, and below every real score.
 constexpr float kNoRef = -3.0e38f;
 
+// Thread-block clusters: an address of another CTA's shared memory, 16 bytes stored
+// there asynchronously (counted by a barrier of the receiver), and an arrival on a
+// barrier there.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_async_v4(uint32_t dst, uint32_t a, uint32_t b, uint32_t c,
+                                            uint32_t d, uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, "
+      "[%5];" ::"r"(dst),
+      "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
+      : "memory");
+}
+// Without a release: what precedes it in the other direction must already have
+// reached registers (a release at cluster scope takes about 1,700 cycles).
+__device__ __forceinline__ void remote_arrive_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+          : "memory");
+}
 // Where a wait gave up: the abort flag in shared memory ends every other wait of
 // the block, so that each role leaves its loop.
 struct WaitCtx {
