@@ -19,13 +19,14 @@
 // sum of the two parts is the same in both CTAs, bit for bit.
 //
 // The way of a tile, S -> exchange -> softmax -> P -> O, takes about three times as
-// long as the tensor cores need for it, so S runs up to three tiles ahead of O.  TMEM (512 columns): Q 96 (three of the four
-// 64-channel blocks, first operand of S), P 32 (first operand of O), O 256, S 2 x 64.
-// The fourth block of Q and the rotary one are in shared memory, and the rotary
-// blocks of the tiles have a ring of their own, because they are done with S.
-// A thread of the softmax owns a row; its exponents are taken against a reference
-// that moves only when a score exceeds it by more than 8 (log2), and only then O is
-// rescaled.
+// long as the tensor cores need for it, so the ways of several tiles overlap: two
+// warpgroups take the tiles in turn, each a tile all the way, and S of the next tile
+// is issued as soon as S of this one is in registers.  TMEM (512 columns): Q 128
+// (first operand of S; its rotary block is in shared memory), P 2 x 32 (first operand
+// of O), O 256, S 64.  The rotary blocks of the tiles have a ring of their own,
+// because they are done with S.  A thread owns a row of every other tile; exponents
+// are taken against a reference per row, handed from tile to tile, that moves only
+// when a score exceeds it by more than 8 (log2), and only then O is rescaled.
 //
 // The 64-key tiles of all sequences form one list, cut evenly over the pairs
 // whatever the lengths.  A pair's first and last sequence may be shared with its
@@ -46,20 +47,21 @@ using namespace latent;
 constexpr int kTile = 64;                // keys per tile
 constexpr int kRows = 128;               // query rows of a pair
 constexpr int kHalf = kLatentC / 2;      // channels of a CTA's values
-constexpr int kThreads = 384;            // 4 softmax and 4 sending warps, loader, MMA, cleaner, spare
-constexpr int kSendWarp = 4, kLoadWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
+constexpr int kThreads = 384;            // 2 x 4 softmax warps, loader, MMA, cleaner, spare
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
 constexpr uint32_t kBlock = 8192;        // 64 keys x 64 channels
 constexpr uint32_t kStage = 4 * kBlock;  // a CTA's half of a tile without the rotary block
 constexpr uint32_t kQBlock = 16384;      // 128 rows x 64 channels
 constexpr uint32_t kSmem = 232448;
 constexpr float kSlack = 8.f;            // log2 units a score may exceed its reference by
 constexpr int kMaxStages = 6;
-constexpr uint32_t TM_Q = 0, TM_P = 96, TM_O = 128, TM_S = 384;
+constexpr uint32_t TM_Q = 0, TM_P = 128, TM_O = 192, TM_S = 448;
 
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages], clean_req[kMaxStages], clean[kMaxStages];
-  uint64_t rope_free[kMaxStages], s_full[2], s_free[2], recv_full[2], send_ok[2];
-  uint64_t q_full, q_ready, q_empty, p_ready, pv_done, fin;
+  uint64_t rope_free[kMaxStages], s_full[2], recv_full[2], send_ok[2], p_ready[2];
+  uint64_t q_full, q_ready, q_empty[2], s_free, pv_done[2], o_free, fin;
+  uint64_t ref_ready[4][2], l_ready[4], l_taken[4];  // by warp of a warpgroup
   uint32_t tmem;
   int abort;
   int seq0, tile0, total;                // the pair's first sequence and tile, all tiles
@@ -67,8 +69,11 @@ struct Shared {
   uint32_t load_pos;                     // tiles loaded, segments begun (loader)
   int load_seg;
   DeviceStatus error;                    // the CTA's first error
+  float ref[2][kRows];                   // reference after a tile, by its parity
+  float2 part[kRows];                    // the last but one tile's warpgroup: its sum, and of what
 };
-static_assert(sizeof(Shared) <= 2048, "fits beside the tiles");
+constexpr uint32_t kSharedBytes = 3072;
+static_assert(sizeof(Shared) <= kSharedBytes, "fits beside the tiles");
 
 struct Params {
   const int32_t *table, *lens;
@@ -141,9 +146,8 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
   constexpr uint32_t ID_S = idesc_bf16(128, kTile, false, false);
   constexpr uint32_t ID_PV = idesc_bf16(128, kHalf, false, true);
 
-  extern __shared__ unsigned char raw[];
-  const uint32_t base = round_up_1k(smem_u32(raw));
-  unsigned char *const tiles = raw + (base - smem_u32(raw));
+  extern __shared__ __align__(1024) unsigned char tiles[];
+  const uint32_t base = smem_u32(tiles);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
   const int pair = blockIdx.x >> 1, rt = pair % p.row_tiles, slice = pair / p.row_tiles;
@@ -151,11 +155,11 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
   const int nb = rope ? 5 : 4;                          // blocks of a tile
   const int NS = p.stages[rank], NR = p.rope_slots;
   const int rows = p.warps * 32;                        // rows in use
-  // shared memory: two tiles that the other CTA sends (at one offset in both), two
-  // blocks of Q, tiles, their rotary blocks, the rest
+  // shared memory: two tiles that the other CTA sends (at one offset in both), the
+  // rotary block of Q, tiles, their rotary blocks, the rest
   const uint32_t sm_recv = base, recv_bytes = rows * kTile * 4, sm_q = sm_recv + 2 * recv_bytes;
-  const uint32_t sm_ring = sm_q + (rope ? 2 : 1) * kQBlock, sm_rope = sm_ring + NS * kStage;
-  Shared &m = *reinterpret_cast<Shared *>(tiles + (kSmem - 1024 - 2048));
+  const uint32_t sm_ring = sm_q + (rope ? kQBlock : 0), sm_rope = sm_ring + NS * kStage;
+  Shared &m = *reinterpret_cast<Shared *>(tiles + (kSmem - kSharedBytes));
 
   if (tid == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
@@ -167,15 +171,24 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
     }
     mbar_init(&m.q_full, 1);
     mbar_init(&m.q_ready, p.warps);
-    mbar_init(&m.q_empty, 1);
+    mbar_init(&m.q_empty[0], 1);
+    mbar_init(&m.q_empty[1], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&m.s_full[i], 1);
-      mbar_init(&m.s_free[i], 2 * p.warps);
+      mbar_init(&m.p_ready[i], p.warps);
       mbar_init(&m.recv_full[i], 1);
       mbar_init(&m.send_ok[i], p.warps);
     }
-    mbar_init(&m.p_ready, p.warps);
-    mbar_init(&m.pv_done, 1);
+    mbar_init(&m.s_free, p.warps);
+    mbar_init(&m.pv_done[0], 1);
+    mbar_init(&m.pv_done[1], 1);
+    mbar_init(&m.o_free, p.warps);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&m.ref_ready[i][0], 1);
+      mbar_init(&m.ref_ready[i][1], 1);
+      mbar_init(&m.l_ready[i], 1);
+      mbar_init(&m.l_taken[i], 1);
+    }
     mbar_init(&m.fin, 1);
     m.abort = 0;
     m.seq0 = p.B;
@@ -274,12 +287,14 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
         return id * p.page_size + at - page * p.page_size;
       };
       int row = box_row(walk.ta);
-      if (seg > 0) ok = warp_wait(cx, &m.q_empty, (seg - 1) & 1, 10, seg);
-      if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&m.q_full, (rope ? 2 : 1) * kQBlock);
-        tma_load_3d_u(sm_q, &map_q, &m.q_full, rank * kHalf + 192, rt * kRows, b);
-        if (rope) tma_load_3d_u(sm_q + kQBlock, &map_q, &m.q_full, kLatentC, rt * kRows, b);
+      if (rope) {
+        if (seg > 0)
+          ok = warp_wait(cx, &m.q_empty[(seg - 1) & 1], ((seg - 1) >> 1) & 1, 10, seg);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&m.q_full, kQBlock);
+          tma_load_3d_u(sm_q, &map_q, &m.q_full, kLatentC, rt * kRows, b);
+        }
       }
       ++seg;
       for (int t = walk.ta; t < walk.tb; ++t) {
@@ -306,40 +321,54 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
       m.load_seg = seg;
     }
   } else if (warp == kMmaWarp && elect_one()) {
-    // ---- MMA issue: whichever of the next S and the next O has its operands, S first
-    // (the exchange and the softmax wait for it).  S is at most three tiles ahead of
-    // O, and goes into the buffer of the S two before, once that has been read.
+    // ---- MMA issue: whichever of the next O and the next S has its operands, O first
+    // (stages wait for it).  S waits until the S before it has been read, and is at
+    // most three tiles ahead of O.
     const Desc q_s(sm_q, 16), c_s(sm_ring, 16), r_s(sm_rope, 16), c_v(sm_ring, kBlock);
     uint32_t pos = 0, done = 0, cleaned = 0;  // S and O issued; parity bit per stage
     uint32_t first = 0, ragged = 0;      // of the tiles in between, bit 0 the oldest
-    int s = 0, sr = 0, sv = 0, seg = -1, t = 0;
+    int s = 0, sr = 0, sv = 0, seg = -1, seg_o = -1, t = 0;
     bool more = walk.next(&b);           // a tile is left for S
     t = walk.ta;
     uint64_t idle = 0;                   // since when nothing could be issued
     while (more || done < pos) {
-      if (more && pos - done < 3 && mbar_test_wait(&m.full[s], (pos / NS) & 1) &&
-          (pos < 2 || mbar_test_wait(&m.s_free[pos & 1], ((pos >> 1) - 1) & 1)) &&
+      if (done < pos && mbar_test_wait(&m.p_ready[done & 1], (done >> 1) & 1) &&
+                 (!(ragged & 1) || mbar_test_wait(&m.clean[sv], cleaned >> sv & 1)) &&
+                 (!(first & 1) || seg_o < 0 || mbar_test_wait(&m.o_free, seg_o & 1))) {
+        idle = 0;
+        tc_fence_after();
+        if (first & 1) ++seg_o;
+        if (ragged & 1) cleaned ^= 1u << sv;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          umma_ts(tm + TM_O, tm + TM_P + 32 * (done & 1) + 8 * k, c_v.at(sv * kStage + k * 2048), ID_PV,
+                  k > 0 || !(first & 1));
+        umma_commit(&m.empty[sv]);
+        umma_commit(&m.pv_done[done & 1]);
+        ++done;
+        first >>= 1;
+        ragged >>= 1;
+        sv = sv + 1 == NS ? 0 : sv + 1;
+      } else if (more && pos - done < 3 && mbar_test_wait(&m.full[s], (pos / NS) & 1) &&
+          (pos < 1 || mbar_test_wait(&m.s_free, (pos - 1) & 1)) &&
           (t > walk.ta || (mbar_test_wait(&m.q_ready, (seg + 1) & 1) &&
-                           mbar_test_wait(&m.q_full, (seg + 1) & 1)))) {
+                           (!rope || mbar_test_wait(&m.q_full, (seg + 1) & 1))))) {
         idle = 0;
         tc_fence_after();
         if (t == walk.ta) ++seg;
-        const uint32_t at = s * kStage, ts = tm + TM_S + 64 * (pos & 1);
+        const uint32_t at = s * kStage, ts = tm + TM_S;
 #pragma unroll
-        for (int k = 0; k < 12; ++k)
+        for (int k = 0; k < 16; ++k)
           umma_ts(ts, tm + TM_Q + 8 * k, c_s.at(at + (k >> 2) * kBlock + (k & 3) * 32), ID_S, k > 0);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          umma_ss(ts, q_s.at(k * 32), c_s.at(at + 3 * kBlock + k * 32), ID_S, 1);
         if (rope) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            umma_ss(ts, q_s.at(kQBlock + k * 32), r_s.at(sr * kBlock + k * 32), ID_S, 1);
+            umma_ss(ts, q_s.at(k * 32), r_s.at(sr * kBlock + k * 32), ID_S, 1);
           umma_commit(&m.rope_free[sr]);
           sr = sr + 1 == NR ? 0 : sr + 1;
         }
         umma_commit(&m.s_full[pos & 1]);
-        if (t + 1 == walk.tb) umma_commit(&m.q_empty);
+        if (t + 1 == walk.tb) umma_commit(&m.q_empty[seg & 1]);
         const uint32_t bit = pos - done;
         first |= (t == walk.ta ? 1u : 0u) << bit;
         ragged |= (walk.n - t * kTile < kTile ? 1u : 0u) << bit;
@@ -349,21 +378,6 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
           more = walk.next(&b);
           t = walk.ta;
         }
-      } else if (done < pos && mbar_test_wait(&m.p_ready, done & 1) &&
-                 (!(ragged & 1) || mbar_test_wait(&m.clean[sv], cleaned >> sv & 1))) {
-        idle = 0;
-        tc_fence_after();
-        if (ragged & 1) cleaned ^= 1u << sv;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          umma_ts(tm + TM_O, tm + TM_P + 8 * k, c_v.at(sv * kStage + k * 2048), ID_PV,
-                  k > 0 || !(first & 1));
-        umma_commit(&m.empty[sv]);
-        umma_commit(&m.pv_done);
-        ++done;
-        first >>= 1;
-        ragged >>= 1;
-        sv = sv + 1 == NS ? 0 : sv + 1;
       } else {
         if (*cx.abort) break;
         const uint64_t now = global_timer_ns();
@@ -400,86 +414,77 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
       __syncwarp();
       if (lane == 0) mbar_arrive(&m.clean[s]);
     }
-  } else if (warp >= kSendWarp && warp < kSendWarp + p.warps) {
-    // ---- sender: Q of each segment into TMEM, then every partial S to the other CTA
-    const int r = (warp - kSendWarp) * 32 + lane;       // row of the tile
-    const uint32_t lanes = (uint32_t)(warp - kSendWarp) << 21;
-    const uint32_t dst = map_rank(sm_recv, peer) + r * 16;
-    const uint32_t bar = map_rank(smem_u32(&m.recv_full[0]), peer);
+  } else if (warp < 8 && (warp & 3) < p.warps) {
+    // ---- softmax and output: thread = row; warpgroup = parity of the tiles
+    const int wg = warp >> 2, w4 = warp & 3;
+    const int r = w4 * 32 + lane, row = rt * kRows + r, tok = row / p.H;
+    const uint32_t lanes = (uint32_t)w4 << 21;
+    const uint32_t ts = tm + lanes + TM_S;
+    const uint32_t src = sm_recv + wg * recv_bytes + r * 16;
+    const uint32_t dst = map_rank(src, peer), bar = map_rank(smem_u32(&m.recv_full[wg]), peer);
+    const uint32_t credit = map_rank(smem_u32(&m.send_ok[wg]), peer);
     uint32_t pos = 0;
+    int seg = 0, joined = 0;             // segments; those of two tiles and more
     bool ok = true;
-    while (ok && walk.next(&b)) {
-      // the segment before has been multiplied: its last S was waited for below
-      const int row = rt * kRows + r;
-      const __nv_bfloat16 *src = p.q + ((int64_t)b * p.R + row) * p.W + rank * kHalf;
+    for (; ok && walk.next(&b); ++seg) {
+      const int n = walk.n, t_draft = n - p.T;          // position of the first draft
+      const bool several = walk.tb - walk.ta > 1;
+      if ((pos & 1) == (uint32_t)wg) {
+        // Q of the segment into TMEM, once the segment before has used its own.  A
+        // warpgroup has a tile in at least one of two consecutive segments, so with
+        // a barrier for each parity it is never two phases behind.
+        if (seg > 0)
+          ok = warp_wait(cx, &m.q_empty[(seg - 1) & 1], ((seg - 1) >> 1) & 1, 40, seg);
+        if (!ok) break;
+        tc_fence_after();
+        const __nv_bfloat16 *q = p.q + ((int64_t)b * p.R + row) * p.W + rank * kHalf;
 #pragma unroll
-      for (int c = 0; c < 3; ++c) {
-        uint32_t x[32];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t x[32];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (row < p.R) v = *reinterpret_cast<const uint4 *>(src + 64 * c + 8 * j);
-          x[4 * j] = v.x; x[4 * j + 1] = v.y; x[4 * j + 2] = v.z; x[4 * j + 3] = v.w;
+          for (int j = 0; j < 8; ++j) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (row < p.R) v = *reinterpret_cast<const uint4 *>(q + 64 * c + 8 * j);
+            x[4 * j] = v.x; x[4 * j + 1] = v.y; x[4 * j + 2] = v.z; x[4 * j + 3] = v.w;
+          }
+          tmem_st32(tm + lanes + TM_Q + 32 * c, x);
         }
-        tmem_st32(tm + lanes + TM_Q + 32 * c, x);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m.q_ready);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&m.q_ready);
+      // the drafts this row sees, by index
+      uint64_t seen = 0;
+      if (p.mask && tok < p.T) seen = (uint64_t)p.mask[(int64_t)b * p.T + tok];
+      if (p.T < 64) seen &= (1ull << p.T) - 1;
+      float ref = kNoRef, l = 0.f;                      // l is relative to ref
       for (int t = walk.ta; t < walk.tb; ++t, ++pos) {
-        ok = warp_wait(cx, &m.s_full[pos & 1], (pos >> 1) & 1, 40, t);
+        if ((pos & 1) != (uint32_t)wg) continue;
+        const uint32_t par = (pos >> 1) & 1;
+        if (w4 == 0 && lane == 0) mbar_arrive_expect_tx(&m.recv_full[wg], recv_bytes);
+        ok = warp_wait(cx, &m.s_full[wg], par, 41, t);
         if (!ok) break;
         tc_fence_after();
         uint32_t x[2][32];
-        tmem_ld32(tm + lanes + TM_S + 64 * (pos & 1), x[0]);
-        tmem_ld32(tm + lanes + TM_S + 64 * (pos & 1) + 32, x[1]);
+        tmem_ld32(ts, x[0]);
+        tmem_ld32(ts + 32, x[1]);
         tmem_ld_wait(x[0]);
         tmem_ld_wait(x[1]);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&m.s_free[pos & 1]);
-        // the other CTA has read the tile that the buffer had
-        if (pos > 1) ok = warp_wait(cx, &m.send_ok[pos & 1], ((pos >> 1) - 1) & 1, 41, t);
+        if (lane == 0) mbar_arrive(&m.s_free);
+        // this CTA's part to the other one, which has read the tile that the buffer had
+        if (pos > 1) ok = warp_wait(cx, &m.send_ok[wg], par ^ 1, 42, t);
         if (!ok) break;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            st_async_v4(dst + (pos & 1) * recv_bytes + (8 * c + j) * rows * 16, x[c][4 * j],
-                        x[c][4 * j + 1], x[c][4 * j + 2], x[c][4 * j + 3], bar + 8 * (pos & 1));
-      }
-    }
-  } else if (warp < p.warps) {
-    // ---- softmax and output: thread = row
-    const int r = warp * 32 + lane, row = rt * kRows + r, tok = row / p.H;
-    const uint32_t lanes = (uint32_t)warp << 21;
-    const uint32_t bar = map_rank(smem_u32(&m.send_ok[0]), peer);
-    uint32_t pos = 0;
-    int seg = 0;
-    bool ok = true;
-    while (ok && walk.next(&b)) {
-      const int n = walk.n, t_draft = n - p.T;          // position of the first draft
-      // the drafts this row sees, by index
-      uint64_t seen = 0;
-      if (p.mask && tok < p.T) seen = (uint64_t)p.mask[(int64_t)b * p.T + tok];
-      if (p.T < 64) seen &= (1ull << p.T) - 1;
-      float ref = kNoRef, l = 0.f;
-      for (int t = walk.ta; t < walk.tb; ++t, ++pos) {
-        if (tid == 0) mbar_arrive_expect_tx(&m.recv_full[pos & 1], recv_bytes);
-        ok = warp_wait(cx, &m.s_full[pos & 1], (pos >> 1) & 1, 50, t) &&
-             warp_wait(cx, &m.recv_full[pos & 1], (pos >> 1) & 1, 51, t);
+            st_async_v4(dst + (8 * c + j) * rows * 16, x[c][4 * j], x[c][4 * j + 1],
+                        x[c][4 * j + 2], x[c][4 * j + 3], bar);
+        ok = warp_wait(cx, &m.recv_full[wg], par, 43, t);
         if (!ok) break;
-        tc_fence_after();
-        uint32_t x[2][32];
-        tmem_ld32(tm + lanes + TM_S + 64 * (pos & 1), x[0]);
-        tmem_ld32(tm + lanes + TM_S + 64 * (pos & 1) + 32, x[1]);
-        tmem_ld_wait(x[0]);
-        tmem_ld_wait(x[1]);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&m.s_free[pos & 1]);
-        const uint32_t src = sm_recv + (pos & 1) * recv_bytes + r * 16;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -515,17 +520,21 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
             mx[c] = fmaxf(mx[c], __uint_as_float(x[c >> 1][16 * (c & 1) + j]));
         }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale2;
-        const bool move = __any_sync(0xffffffffu, top > ref + kSlack);
+        // The reference after the tile before, from the other warpgroup's same warp
+        // (across segments only the turn: it has read what is overwritten below).
+        if (pos > 0) ok = warp_wait(cx, &m.ref_ready[w4][wg ^ 1], ((pos - 1) >> 1) & 1, 44, t);
+        if (!ok) break;
+        const float before = t > walk.ta ? m.ref[wg ^ 1][r] : kNoRef;
+        const bool move = __any_sync(0xffffffffu, top > before + kSlack);
         // The vote has consumed every value read from what the other CTA sent: it may
-        // send the next tile.
-        if (lane == 0) remote_arrive_relaxed(bar + 8 * (pos & 1));
-        float f = 1.f;
-        if (move) {
-          const float now = fmaxf(ref, top);
-          f = ex2(ref - now);
-          ref = now;
-          l *= f;
-        }
+        // send into the buffer again.
+        if (lane == 0) remote_arrive_relaxed(credit);
+        const float now = move ? fmaxf(before, top) : before;
+        m.ref[wg][r] = now;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m.ref_ready[w4][wg]);
+        l *= ex2(ref - now);
+        ref = now;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
         uint32_t pk[32];
 #pragma unroll
@@ -538,11 +547,15 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
             pk[16 * c + j / 2] = pack_bf16x2(u, v);
           }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        // P and O are free once the product of the tile before is done
-        if (pos > 0) ok = warp_wait(cx, &m.pv_done, (pos - 1) & 1, 52, t);
+        // this P's buffer is free once the product of two tiles before is done
+        if (pos > 1) ok = warp_wait(cx, &m.pv_done[wg], par ^ 1, 45, t);
         if (!ok) break;
         tc_fence_after();
-        if (move && t > walk.ta) {
+        if (move && t > walk.ta) {  // and O once that of the tile before is
+          ok = warp_wait(cx, &m.pv_done[wg ^ 1], ((pos - 1) >> 1) & 1, 48, t);
+          if (!ok) break;
+          tc_fence_after();
+          const float f = ex2(before - now);
 #pragma unroll 1
           for (int c = 0; c < kHalf / 32; ++c) {
             uint32_t o[32];
@@ -553,15 +566,32 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
             tmem_st32(tm + lanes + TM_O + 32 * c, o);
           }
         }
-        tmem_st32(tm + lanes + TM_P, pk);
+        tmem_st32(tm + lanes + TM_P + 32 * wg, pk);
         tmem_st_wait();
         tc_fence_before();
+        if (t + 1 == walk.tb && several) {
+          ok = warp_wait(cx, &m.l_ready[w4], joined & 1, 46, seg);
+          if (!ok) break;
+          const float2 other = m.part[r];
+          l += other.x * ex2(other.y - ref);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&m.l_taken[w4]);
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&m.p_ready);
+        if (lane == 0) mbar_arrive(&m.p_ready[wg]);
+        if (t + 2 == walk.tb) {  // the other warpgroup ends the segment: hand it the sum
+          if (joined > 0) ok = warp_wait(cx, &m.l_taken[w4], (joined - 1) & 1, 49, t);
+          if (!ok) break;
+          m.part[r] = make_float2(l, ref);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&m.l_ready[w4]);
+        }
       }
       if (!ok) break;
+      joined += several;
+      if (((pos - 1) & 1) != (uint32_t)wg) continue;    // the other warpgroup's last tile
       // ---- the segment's output
-      ok = warp_wait(cx, &m.pv_done, (pos - 1) & 1, 53, seg);
+      ok = warp_wait(cx, &m.pv_done[wg], ((pos - 1) >> 1) & 1, 47, seg);
       if (!ok) break;
       tc_fence_after();
       const bool whole = walk.ta == 0 && walk.tb == key_tiles(n);
@@ -584,7 +614,7 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
         tmem_ld32(tm + lanes + TM_O + 32 * c, o);
         tmem_ld_wait(o);
         if (whole) {
-          uint4 *dst = reinterpret_cast<uint4 *>(p.out + out_row * kLatentC + rank * kHalf + 32 * c);
+          uint4 *to = reinterpret_cast<uint4 *>(p.out + out_row * kLatentC + rank * kHalf + 32 * c);
           if (row < p.R)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -593,18 +623,19 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
               for (int k = 0; k < 4; ++k)
                 w[k] = pack_bf16x2(__uint_as_float(o[8 * j + 2 * k]) * inv,
                                    __uint_as_float(o[8 * j + 2 * k + 1]) * inv);
-              dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
+              to[j] = make_uint4(w[0], w[1], w[2], w[3]);
             }
         } else {
-          uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + (slot * kRows + r) * kLatentC +
-                                                 rank * kHalf + 32 * c);
+          uint4 *to = reinterpret_cast<uint4 *>(p.part_o + (slot * kRows + r) * kLatentC +
+                                                rank * kHalf + 32 * c);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            to[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
         }
       }
       tc_fence_before();
-      ++seg;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.o_free);
     }
   }
 
@@ -790,11 +821,11 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t stream)
   p.page_size = a.page_size; p.max_pages = a.max_pages; p.box_rows = box;
   p.row_tiles = pl.row_tiles; p.G = pl.G;
   p.warps = ((R < kRows ? R : kRows) + 31) / 32;
-  const uint32_t space = kSmem - 1024 - 2048 - 2 * p.warps * 32 * kTile * 4;
+  const uint32_t space = kSmem - kSharedBytes - 2 * p.warps * 32 * kTile * 4;
   // rank 0: two rotary slots at least, more where a stage does not fit
-  const uint32_t space0 = space - (a.dr ? 2 : 1) * kQBlock;
+  const uint32_t space0 = space - (a.dr ? kQBlock : 0);
   p.stages[0] = (int)((space0 - (a.dr ? 2 * kBlock : 0)) / kStage);
-  p.stages[1] = (int)((space - kQBlock) / kStage);
+  p.stages[1] = (int)(space / kStage);
   for (int &n : p.stages)
     if (n > kMaxStages) n = kMaxStages;
   p.rope_slots = a.dr ? (int)((space0 - p.stages[0] * kStage) / kBlock) : 1;
