@@ -48,7 +48,7 @@ constexpr int kTile = 64;                // keys per tile
 constexpr int kRows = 128;               // query rows of a pair
 constexpr int kHalf = kLatentC / 2;      // channels of a CTA's values
 constexpr int kThreads = 384;            // 2 x 4 softmax warps, loader, MMA, cleaner, spare
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kCleanWarp = 10, kSpareWarp = 11;
 constexpr uint32_t kBlock = 8192;        // 64 keys x 64 channels
 constexpr uint32_t kStage = 4 * kBlock;  // a CTA's half of a tile without the rotary block
 constexpr uint32_t kQBlock = 16384;      // 128 rows x 64 channels
@@ -90,8 +90,9 @@ struct Params {
   float *lse;
   DeviceStatus *status;
   DeviceStatus *errors; // [CTAs]
-  int32_t *before;      // [B + 1] tiles before each sequence
-  float *part_o;        // [row tiles][G][2][128][512]
+  int2 *begins;         // [G] sequence and tile a pair begins with
+  int32_t *total;       // all tiles
+  float *part_o;        // [row tiles][G][2][512 / 4][128 rows][4]
   float *part_ml;       // [row tiles][G][2][2][128]
 };
 
@@ -230,14 +231,6 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
       if (w < warp) before += m.warp_sum[w];
       total += m.warp_sum[w];
     }
-    if (blockIdx.x == 0) {
-      int at = before;
-      for (int b = b0; b < b1; ++b) {
-        p.before[b] = at;
-        at += key_tiles(seq_len(p, b));
-      }
-      if (tid == 0) p.before[p.B] = total;
-    }
     const int begin = pair_begin(slice, p.G, total);
     if (begin >= before && begin < before + mine) {
       int at = before;
@@ -258,6 +251,10 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
   tc_fence_after();
   pdl_launch_dependents();
   const uint32_t tm = m.tmem;
+  if (rt == 0 && rank == 0 && tid == 0) {  // for the kernel that joins the parts
+    p.begins[slice] = make_int2(m.seq0, m.tile0);
+    if (slice == 0) *p.total = m.total;
+  }
   const int begin = pair_begin(slice, p.G, m.total);
   const int mine = pair_begin(slice + 1, p.G, m.total) - begin;
   const WaitCtx cx{&m.abort, &m.error, (int)blockIdx.x};
@@ -439,15 +436,17 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
         tc_fence_after();
         const __nv_bfloat16 *q = p.q + ((int64_t)b * p.R + row) * p.W + rank * kHalf;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t x[32];
+        for (int c = 0; c < 4; c += 2) {                // 16 loads in flight
+          uint32_t x[2][32];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 16; ++j) {
             uint4 v = make_uint4(0, 0, 0, 0);
             if (row < p.R) v = *reinterpret_cast<const uint4 *>(q + 64 * c + 8 * j);
-            x[4 * j] = v.x; x[4 * j + 1] = v.y; x[4 * j + 2] = v.z; x[4 * j + 3] = v.w;
+            uint32_t *y = &x[j >> 3][4 * (j & 7)];
+            y[0] = v.x; y[1] = v.y; y[2] = v.z; y[3] = v.w;
           }
-          tmem_st32(tm + lanes + TM_Q + 32 * c, x);
+          tmem_st32(tm + lanes + TM_Q + 32 * c, x[0]);
+          tmem_st32(tm + lanes + TM_Q + 32 * c + 32, x[1]);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -626,17 +625,32 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
               to[j] = make_uint4(w[0], w[1], w[2], w[3]);
             }
         } else {
-          uint4 *to = reinterpret_cast<uint4 *>(p.part_o + (slot * kRows + r) * kLatentC +
-                                                rank * kHalf + 32 * c);
+          // four channels of the 32 rows beside one another
+          uint4 *to = reinterpret_cast<uint4 *>(p.part_o) +
+                      (slot * (kLatentC / 4) + (rank * kHalf + 32 * c) / 4) * kRows + r;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            to[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            to[j * kRows] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&m.o_free);
     }
+  }
+
+  if (warp == kSpareWarp) {
+    // ---- rows of empty sequences see nothing
+    for (int e = slice; e < p.B; e += p.G)
+      if (key_tiles(seq_len(p, e)) == 0)
+        for (int i = lane; i < kRows * kHalf / 8; i += 32) {
+          const int row = rt * kRows + i / (kHalf / 8), c = i % (kHalf / 8);
+          if (row >= p.R) break;
+          const int64_t at = (int64_t)e * p.R + row;
+          *reinterpret_cast<uint4 *>(p.out + at * kLatentC + rank * kHalf + 8 * c) =
+              make_uint4(0, 0, 0, 0);
+          if (p.lse && rank == 0 && c == 0) p.lse[at] = -CUDART_INF_F;
+        }
   }
 
   __syncwarp();
@@ -666,19 +680,19 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
   cluster_sync_all();  // the other CTA is done with this one's shared memory
 }
 
-// Joins the parts of sequences that several pairs shared, in the list's order, and
-// writes the rows of empty sequences.  A warp per row and 128 channels; the parts
-// are read kJoinBatch at a time, all loads of a batch in flight.  Its first block
-// also sets the call's status: the first error of any CTA, or none.
-constexpr int kJoinRows = 2, kJoinBatch = 8;
-__global__ void __launch_bounds__(128 * kJoinRows)
+// Joins the parts of sequences that several pairs shared, in the list's order.
+// Block (x: 32 rows and 16 channels, y: a border between two pairs): the first border
+// inside a sequence joins it.  A lane is a row; the eight warps take the parts in
+// turn, so that a long list is read by all of them, and their sums are added in
+// warp order.  The first block also sets the call's status: the first error of any
+// CTA, or none.
+constexpr int kJoinWarps = 8, kJoinCh = 16;
+__global__ void __launch_bounds__(32 * kJoinWarps)
 kda_latent_join_kernel(const Params p) {
+  __shared__ float s_o[kJoinWarps][kJoinCh][32], s_ref[kJoinWarps][32], s_l[kJoinWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = blockIdx.y, r = blockIdx.x * kJoinRows + (warp >> 2);
-  const int ch = (warp & 3) * 128 + 4 * lane;
-  const bool lead = threadIdx.x % 128 == 0;
   pdl_wait();
-  if (blockIdx.x == 0 && b == 0 && warp == 0) {
+  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
     int at = 0x7fffffff;
     const int ctas = p.G * p.row_tiles * 2;
     for (int i = lane; i < ctas; i += 32)
@@ -690,56 +704,72 @@ kda_latent_join_kernel(const Params p) {
       *p.status = st;
     }
   }
-  if (r >= p.R) return;
-  const int before = p.before[b], k = p.before[b + 1] - before, all = p.before[p.B];
-  const int64_t row = (int64_t)b * p.R + r;
-  uint2 *out = reinterpret_cast<uint2 *>(p.out + row * kLatentC + ch);
-  if (k <= 0) {
-    *out = make_uint2(0, 0);
-    if (p.lse && lead) p.lse[row] = -CUDART_INF_F;
-    return;
-  }
-  const int first = pair_of(before, p.G, all), last = pair_of(before + k - 1, p.G, all);
-  if (first == last) return;             // one pair had it all and wrote the output
-  const int rt = r / kRows, col = r % kRows;
+  const int border = blockIdx.y + 1;
+  if (border >= p.G) return;
+  const int2 at = p.begins[border];
+  if (at.y == 0) return;                 // a sequence begins with the pair
+  const int all = *p.total, start = pair_begin(border, p.G, all) - at.y, first = border - 1;
+  if (pair_begin(first, p.G, all) > start) return;  // an earlier border joins it
+  const int last = pair_of(start + key_tiles(seq_len(p, at.x)) - 1, p.G, all);
+  const int groups = (p.R + 31) / 32;
+  const int group = blockIdx.x % groups, ch = blockIdx.x / groups * kJoinCh;
+  const int rt = group / 4, r = (group & 3) * 32 + lane, row = group * 32 + lane;
+  // a pair's first segment is in slot 0, its last in slot 1
   const int64_t slot0 = ((int64_t)rt * p.G + first) * 2;
-  const int late = pair_begin(first, p.G, all) < before ? 1 : 0;
+  const int late = pair_begin(first, p.G, all) < start ? 1 : 0;
   const int parts = last - first + 1;
-  auto slot_of = [&](int i) { return slot0 + 2 * i + (i == 0 ? late : 0); };
-  float ref = kNoRef;
-  for (int i = lane; i < parts; i += 32) {
-    const float y = p.part_ml[slot_of(i) * 2 * kRows + col];
+  float ref = kNoRef, l = 0.f, o[kJoinCh];
+#pragma unroll
+  for (int c = 0; c < kJoinCh; ++c) o[c] = 0.f;
+#pragma unroll 2
+  for (int i = warp; i < parts; i += kJoinWarps) {
+    const int64_t slot = slot0 + 2 * i + (i == 0 ? late : 0);
+    const float4 *x = reinterpret_cast<const float4 *>(p.part_o) +
+                      (slot * (kLatentC / 4) + ch / 4) * kRows + r;
+    float4 v[kJoinCh / 4];
+#pragma unroll
+    for (int c = 0; c < kJoinCh / 4; ++c) v[c] = x[c * kRows];
+    const float m = p.part_ml[slot * 2 * kRows + r], s = p.part_ml[slot * 2 * kRows + kRows + r];
+    const float now = m > ref || m != m ? m : ref;
+    const float a = ex2(ref - now), b = ex2(m - now);
+    ref = now;
+    l = l * a + s * b;
+#pragma unroll
+    for (int c = 0; c < kJoinCh / 4; ++c) {
+      o[4 * c] = o[4 * c] * a + v[c].x * b;
+      o[4 * c + 1] = o[4 * c + 1] * a + v[c].y * b;
+      o[4 * c + 2] = o[4 * c + 2] * a + v[c].z * b;
+      o[4 * c + 3] = o[4 * c + 3] * a + v[c].w * b;
+    }
+  }
+  s_ref[warp][lane] = ref;
+  s_l[warp][lane] = l;
+#pragma unroll
+  for (int c = 0; c < kJoinCh; ++c) s_o[warp][c][lane] = o[c];
+  __syncthreads();
+  // warp w: channels 2 w and 2 w + 1 of all rows
+  ref = s_ref[0][lane];
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) {
+    const float y = s_ref[w][lane];
     ref = y > ref || y != y ? y : ref;
   }
+  l = 0.f;
+  float u = 0.f, v = 0.f;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const float y = __shfl_xor_sync(0xffffffffu, ref, o);
-    ref = y > ref || y != y ? y : ref;
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const float f = ex2(s_ref[w][lane] - ref);
+    l += f * s_l[w][lane];
+    u += f * s_o[w][2 * warp][lane];
+    v += f * s_o[w][2 * warp + 1][lane];
   }
-  float sum = 0.f;
-  float4 acc = make_float4(0, 0, 0, 0);
-  for (int i0 = 0; i0 < parts; i0 += kJoinBatch) {
-    float4 x[kJoinBatch];
-    float f[kJoinBatch], l[kJoinBatch];
-#pragma unroll
-    for (int j = 0; j < kJoinBatch; ++j)
-      if (i0 + j < parts) {
-        const int64_t slot = slot_of(i0 + j);
-        x[j] = *reinterpret_cast<const float4 *>(p.part_o + (slot * kRows + col) * kLatentC + ch);
-        f[j] = p.part_ml[slot * 2 * kRows + col];
-        l[j] = p.part_ml[slot * 2 * kRows + kRows + col];
-      }
-#pragma unroll
-    for (int j = 0; j < kJoinBatch; ++j)
-      if (i0 + j < parts) {
-        const float w = ex2(f[j] - ref);
-        sum += w * l[j];
-        acc.x += w * x[j].x; acc.y += w * x[j].y; acc.z += w * x[j].z; acc.w += w * x[j].w;
-      }
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  *out = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (p.lse && lead) p.lse[row] = sum == 0.f ? -CUDART_INF_F : (ref + log2f(sum)) * kLn2;
+  if (row >= p.R) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t out_row = (int64_t)at.x * p.R + row;
+  *reinterpret_cast<uint32_t *>(p.out + out_row * kLatentC + ch + 2 * warp) =
+      pack_bf16x2(u * inv, v * inv);
+  if (p.lse && ch == 0 && warp == 0)
+    p.lse[out_row] = l == 0.f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
 }
 
 // Pairs of CTAs the device runs at once (0 without a device), asked once.
@@ -770,9 +800,9 @@ int resident_pairs() {
 
 struct Plan {
   int row_tiles, G;
-  size_t before, errors, ml, o;          // bytes of the workspace's pieces
+  size_t begins, errors, ml, o;          // bytes of the workspace's pieces
 };
-Plan make_plan(int B, int T, int H) {
+Plan make_plan(int T, int H) {
   Plan pl;
   pl.row_tiles = (T * H + kRows - 1) / kRows;
   const int pairs = resident_pairs();
@@ -781,7 +811,7 @@ Plan make_plan(int B, int T, int H) {
   auto round = [](size_t x) { return (x + 255) / 256 * 256; };
   // partial results: none when one pair has all keys of its rows
   const size_t parts = pl.G > 1 ? (size_t)pl.row_tiles * pl.G * 2 : 0;
-  pl.before = round(((size_t)B + 1) * sizeof(int32_t));
+  pl.begins = round((size_t)pl.G * sizeof(int2)) + 256;  // and the total
   pl.errors = round((size_t)pl.row_tiles * pl.G * 2 * sizeof(DeviceStatus));
   pl.ml = parts * 2 * kRows * sizeof(float);
   pl.o = parts * kRows * kLatentC * sizeof(float);
@@ -791,15 +821,16 @@ Plan make_plan(int B, int T, int H) {
 }  // namespace
 
 size_t latent_decode_scratch_bytes(int32_t B, int32_t T, int32_t H, int32_t dr) {
+  (void)B;
   (void)dr;
-  const Plan pl = make_plan(B, T, H);
-  return pl.before + pl.errors + pl.ml + pl.o;
+  const Plan pl = make_plan(T, H);
+  return pl.begins + pl.errors + pl.ml + pl.o;
 }
 
 cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t stream) {
   if (a.B == 0) return cudaMemsetAsync(a.status, 0, sizeof(DeviceStatus), stream);
   if (!latent::encode_tiled() || resident_pairs() < 1) return cudaErrorNotSupported;
-  const Plan pl = make_plan(a.B, a.T, a.H);
+  const Plan pl = make_plan(a.T, a.H);
   const int W = kLatentC + a.dr, R = a.T * a.H;
   // Rows of a copied box: as many as lie in one page and one tile.
   int box = kTile;
@@ -833,16 +864,18 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t stream)
   p.scale2 = a.scale * kLog2e;
   p.out = static_cast<__nv_bfloat16 *>(a.out); p.lse = a.lse; p.status = a.status;
   unsigned char *ws = static_cast<unsigned char *>(a.scratch);
-  p.before = reinterpret_cast<int32_t *>(ws);
-  p.errors = reinterpret_cast<DeviceStatus *>(ws + pl.before);
-  p.part_ml = reinterpret_cast<float *>(ws + pl.before + pl.errors);
-  p.part_o = reinterpret_cast<float *>(ws + pl.before + pl.errors + pl.ml);
+  p.begins = reinterpret_cast<int2 *>(ws);
+  p.total = reinterpret_cast<int32_t *>(ws + pl.begins - 256);
+  p.errors = reinterpret_cast<DeviceStatus *>(ws + pl.begins);
+  p.part_ml = reinterpret_cast<float *>(ws + pl.begins + pl.errors);
+  p.part_o = reinterpret_cast<float *>(ws + pl.begins + pl.errors + pl.ml);
   kda_latent_decode_kernel<<<2 * pl.G * pl.row_tiles, kThreads, kSmem, stream>>>(mq, mc, p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((R + kJoinRows - 1) / kJoinRows), (unsigned)a.B);
-  cfg.blockDim = dim3(128 * kJoinRows);
+  cfg.gridDim = dim3((unsigned)((R + 31) / 32 * (kLatentC / kJoinCh)),
+                     (unsigned)(pl.G > 2 ? pl.G - 1 : 1));
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
