@@ -48,7 +48,7 @@ constexpr int kTile = 64;                // keys per tile
 constexpr int kRows = 128;               // query rows of a pair
 constexpr int kHalf = kLatentC / 2;      // channels of a CTA's values
 constexpr int kThreads = 384;            // 2 x 4 softmax warps, loader, MMA, cleaner, spare
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kCleanWarp = 10, kSpareWarp = 11;
+constexpr int kLoadWarp = 8, kMmaWarp = 11, kCleanWarp = 10, kSpareWarp = 9;
 constexpr uint32_t kBlock = 8192;        // 64 keys x 64 channels
 constexpr uint32_t kStage = 4 * kBlock;  // a CTA's half of a tile without the rotary block
 constexpr uint32_t kQBlock = 16384;      // 128 rows x 64 channels
