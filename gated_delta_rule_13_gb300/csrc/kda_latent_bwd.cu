@@ -57,10 +57,17 @@ template <int DR>
 constexpr uint32_t stage_bytes() { return ((kLatentD + DR) / 64 + 2) * kYBlock; }
 template <int DR>
 constexpr int stages() { return DR ? 3 : 4; }
-template <int DR>
-constexpr uint32_t smem_bytes() {
-  return 1024 + x_bytes<DR>() + stages<DR>() * stage_bytes<DR>() + sizeof(Shared);
-}
+constexpr uint32_t kSmem = 232448, kSharedBytes = 3072;
+struct QShared {                         // of the queries pass
+  uint64_t k_full[4], k_empty[4], v_full[2], v_empty[2];
+  uint64_t x_full, x2_ready, s_full, s_free, dp_full, ds_ready, clean_req, clean, acc_full, fin;
+  uint32_t tmem;
+  int abort, loaded_k, loaded_v;
+  SeqTile tile;
+};
+static_assert(sizeof(Shared) <= kSharedBytes && sizeof(QShared) <= kSharedBytes, "shared memory");
+static_assert(x_bytes<64>() + stages<64>() * stage_bytes<64>() + kSharedBytes <= kSmem &&
+              x_bytes<0>() + stages<0>() * stage_bytes<0>() + kSharedBytes <= kSmem, "shared memory");
 
 struct Params {
   const int32_t *cu_q, *cu_k;
@@ -119,9 +126,10 @@ __device__ __forceinline__ void store_cols(uint32_t col, float mul, bool zero,
   __syncwarp();
 }
 
-template <int DR, bool kKeys>
-__device__ __forceinline__ void pass(const Maps &maps, const Params &p, int index, int head,
-                                     unsigned char *tiles, uint32_t base, Shared &m) {
+template <int DR>
+__device__ __forceinline__ void keys_pass(const Maps &maps, const Params &p, int index, int head,
+                                          uint32_t base, Shared &m) {
+  constexpr bool kKeys = true;
   constexpr int KB = (kLatentD + DR) / 64, ST = stages<DR>();
   constexpr uint32_t kStage = x_bytes<DR>();
   constexpr int N1 = kLatentD + DR;
@@ -130,7 +138,6 @@ __device__ __forceinline__ void pass(const Maps &maps, const Params &p, int inde
   constexpr uint32_t ID_A1 = idesc_bf16(128, N1, false, true);
   constexpr uint32_t ID_A2 = idesc_bf16(128, kLatentD, false, true);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  (void)tiles;
 
   if (warp == kCleanWarp) {
     const SeqTile f = find_seq_tile(p.cu_q, p.cu_k, p.n_seqs, p.n_q, p.n_k, kX, kKeys, index);
@@ -445,21 +452,304 @@ __device__ __forceinline__ void pass(const Maps &maps, const Params &p, int inde
   }
 }
 
+// The queries pass: X = 128 queries and their d_out, streamed tiles of 128 keys.  S and
+// dP have one buffer each (128 columns): S of the next tile is issued as soon as S of
+// this one is in registers, dP of the next tile after the product that read dS.  d_out
+// moves to TMEM (64 columns, the first operand of dP), which gives its 32 KB to the
+// streamed tiles: keys in three (dr = 0: four) buffers, because they are held from S
+// to the product with dS, values in one (two), because they are done with dP.
+template <int DR>
+__device__ __forceinline__ void queries_pass(const Maps &maps, const Params &p, int index, int head,
+                                             uint32_t base, QShared &m) {
+  constexpr int KB = (kLatentD + DR) / 64, KT = DR ? 3 : 4, VT = DR ? 1 : 2;
+  constexpr uint32_t kRingK = KB * kXBlock, kRingV = kRingK + KT * KB * kXBlock;
+  constexpr uint32_t kX2 = kRingK + 2 * KB * kXBlock;    // d_out, where the keys of tile 2 go
+  static_assert(kRingV + VT * 2 * kXBlock + kSharedBytes <= kSmem, "shared memory");
+  constexpr int N1 = kLatentD + DR;
+  constexpr uint32_t TM_A1 = 0, TM_X2 = 192, TM_S = 256, TM_DP = 384;
+  constexpr uint32_t ID_S = idesc_bf16(128, 128, false, false);
+  constexpr uint32_t ID_A1 = idesc_bf16(128, N1, false, true);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (warp == kCleanWarp) {
+    const SeqTile f = find_seq_tile(p.cu_q, p.cu_k, p.n_seqs, p.n_q, p.n_k, kX, false, index);
+    if (lane == 0) m.tile = f;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&m.k_full[i], 1);
+      mbar_init(&m.k_empty[i], 1);
+      mbar_init(&m.v_full[i & 1], 1);
+      mbar_init(&m.v_empty[i & 1], 1);
+    }
+    mbar_init(&m.x2_ready, 8);
+    mbar_init(&m.x_full, 1);
+    mbar_init(&m.s_full, 1);
+    mbar_init(&m.s_free, 8);
+    mbar_init(&m.dp_full, 1);
+    mbar_init(&m.ds_ready, 8);
+    mbar_init(&m.clean_req, 1);
+    mbar_init(&m.clean, 1);
+    mbar_init(&m.acc_full, 1);
+    mbar_init(&m.fin, 1);
+    m.abort = 0;
+    m.loaded_k = m.loaded_v = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    prefetch_tensormap(&maps.q128);
+    prefetch_tensormap(&maps.g128);
+    prefetch_tensormap(&maps.k128);
+    prefetch_tensormap(&maps.v128);
+    if (DR) prefetch_tensormap(&maps.r128);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&m.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = m.tmem;
+  const SeqTile st = m.tile;
+
+  // longest first: the last queries of a sequence see the most keys
+  const int x0 = (st.n_tiles - 1 - st.tile) * kX;
+  const int shift = st.nk - st.nq;       // query i sees keys <= i + shift
+  const int y_end = p.causal ? min(st.nk, min(x0 + kX, st.nq) + shift) : st.nk;
+  const int n = st.seq >= 0 && y_end > 0 ? (y_end + 127) / 128 : 0;
+  const int live = min(128, st.nk - (n - 1) * 128);      // keys of the last tile
+  const WaitCtx cx{&m.abort, p.status, (int)blockIdx.x};
+
+  if (warp == kLoadWarp && lane == 0 && n > 0) {
+    // ---- loader
+    const int xr = st.q0 + x0;
+    mbar_arrive_expect_tx(&m.x_full, (KB + 2) * kXBlock);
+    for (int c = 0; c < 2; ++c)
+      tma_load_3d_u(base + kX2 + c * kXBlock, &maps.g128, &m.x_full, 64 * c, head, xr);
+    for (int kb = 0; kb < KB; ++kb)
+      tma_load_3d_u(base + kb * kXBlock, &maps.q128, &m.x_full, 64 * kb, head, xr);
+    bool ok = true;
+    int i = 0, iv = 0;
+    for (; i < n; ++i) {
+      const int yr = st.k0 + i * 128, sk = i % KT, sv = i % VT;
+      if (i >= KT) ok = wait_or_abort(cx, &m.k_empty[sk], (i / KT - 1) & 1, 10, i);
+      if (ok && i == 2) ok = wait_or_abort(cx, &m.x2_ready, 0, 11, i);
+      if (!ok) break;
+      mbar_arrive_expect_tx(&m.k_full[sk], KB * kXBlock);
+      const uint32_t dk = base + kRingK + sk * KB * kXBlock;
+      for (int kb = 0; kb < KB; ++kb) {
+        if (kb < 2) tma_load_3d_u(dk + kb * kXBlock, &maps.k128, &m.k_full[sk], 64 * kb, head, yr);
+        else tma_load_2d(dk + kb * kXBlock, &maps.r128, &m.k_full[sk], 0, yr);
+      }
+      if (i >= VT) ok = wait_or_abort(cx, &m.v_empty[sv], (i / VT - 1) & 1, 12, i);
+      if (!ok) { ++i; break; }
+      mbar_arrive_expect_tx(&m.v_full[sv], 2 * kXBlock);
+      const uint32_t dv = base + kRingV + sv * 2 * kXBlock;
+      for (int c = 0; c < 2; ++c)
+        tma_load_3d_u(dv + c * kXBlock, &maps.v128, &m.v_full[sv], 64 * c, head, yr);
+      iv = i + 1;
+    }
+    if (ok) mbar_arrive(&m.clean_req);
+    m.loaded_k = i;
+    m.loaded_v = iv;
+  } else if (warp == kMmaWarp && n > 0 && elect_one()) {
+    // ---- MMA issue
+    const Desc x_s(base, 16), k_s(base + kRingK, 16), v_s(base + kRingV, 16),
+        k_a(base + kRingK, kXBlock);
+    bool ok = wait_or_abort(cx, &m.x_full, 0, 20, 0);
+    auto issue_s = [&](int i) {
+      const int sk = i % KT;
+      ok = ok && wait_or_abort(cx, &m.k_full[sk], (i / KT) & 1, 21, i);
+      if (ok && i > 0) ok = wait_or_abort(cx, &m.s_free, (i - 1) & 1, 22, i);
+      if (!ok) return;
+      tc_fence_after();
+      const uint32_t off = sk * KB * kXBlock;
+#pragma unroll
+      for (int k = 0; k < 4 * KB; ++k)
+        umma_ss(tm + TM_S, x_s.at((k >> 2) * kXBlock + (k & 3) * 32),
+                k_s.at(off + (k >> 2) * kXBlock + (k & 3) * 32), ID_S, k > 0);
+      umma_commit(&m.s_full);
+    };
+    auto issue_dp = [&](int i) {
+      const int sv = i % VT;
+      ok = ok && wait_or_abort(cx, &m.v_full[sv], (i / VT) & 1, 23, i);
+      if (!ok) return;
+      const uint32_t off = sv * 2 * kXBlock;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        umma_ts(tm + TM_DP, tm + TM_X2 + 8 * k, v_s.at(off + (k >> 2) * kXBlock + (k & 3) * 32),
+                ID_S, k > 0);
+      umma_commit(&m.dp_full);
+      umma_commit(&m.v_empty[sv]);
+    };
+    issue_s(0);
+    ok = ok && wait_or_abort(cx, &m.x2_ready, 0, 26, 0);
+    tc_fence_after();
+    issue_dp(0);
+    if (n > 1) issue_s(1);
+    for (int i = 0; ok && i < n; ++i) {
+      ok = wait_or_abort(cx, &m.ds_ready, i & 1, 24, i);
+      if (ok && i + 1 == n && live < 128) ok = wait_or_abort(cx, &m.clean, 0, 25, i);
+      if (!ok) break;
+      tc_fence_after();
+      // dS is over dP, keys 0 .. 63 at column 0, 64 .. 127 at column 64
+      const uint32_t off = (i % KT) * KB * kXBlock;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        umma_ts(tm + TM_A1, tm + TM_DP + (k >> 2) * 64 + (k & 3) * 8, k_a.at(off + k * 2048), ID_A1,
+                i + k > 0);
+      umma_commit(&m.k_empty[i % KT]);
+      if (i + 1 < n) issue_dp(i + 1);
+      if (ok && i + 2 < n) issue_s(i + 2);
+    }
+    if (ok) umma_commit(&m.acc_full);
+  } else if (warp == kCleanWarp && n > 0 && live < 128) {
+    // ---- cleaner: keys of the last tile past the sequence's end, as in the other pass
+    const int sk = (n - 1) % KT;
+    bool ok = warp_wait(cx, &m.clean_req, 0, 30, n);
+    ok = ok && warp_wait(cx, &m.k_full[sk], ((n - 1) / KT) & 1, 31, n);
+    if (ok) {
+      const uint32_t y = base + kRingK + sk * KB * kXBlock + live * 128;
+      for (int kb = 0; kb < KB; ++kb)
+        for (int j = lane; j < (128 - live) * 8; j += 32)
+          st_shared_v4(y + kb * kXBlock + j * 16, 0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.clean);
+    }
+  } else if (warp < 8) {
+    // ---- elementwise: thread = query, warpgroup = half of a tile's keys
+    const int wg = warp >> 2, xr = x0 + (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    float lse2 = 0.f, delta = 0.f;
+    if (st.seq >= 0 && xr < st.nq) {
+      const int64_t at = head * p.stat_rows + stat_tile(st.q0, st.seq) * kY + xr;
+      lse2 = p.lse2[at];
+      delta = p.delta[at];
+    }
+    const int hi = p.causal ? min(st.nk, xr + shift + 1) : st.nk;  // keys this row sees
+    bool ok = n == 0 || warp_wait(cx, &m.x_full, 0, 43, 0);
+    if (ok && n > 0) {  // this row's 64 channels of d_out (a warpgroup's half) into TMEM
+      uint32_t x[32];
+      const int r = (warp & 3) * 32 + lane;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const uint4 v = ld_shared_v4(base + kX2 + wg * kXBlock + sw128_offset(r, 16 * q));
+        x[4 * q] = v.x; x[4 * q + 1] = v.y; x[4 * q + 2] = v.z; x[4 * q + 3] = v.w;
+      }
+      tmem_st32(tm + lanes + TM_X2 + 32 * wg, x);
+      tmem_st_wait();
+      tc_fence_before();
+      fence_proxy_async_smem();          // its place is loaded again
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.x2_ready);
+    }
+    for (int i = 0; ok && i < n; ++i) {
+      ok = warp_wait(cx, &m.s_full, i & 1, 40, i);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t x[2][32];
+      const uint32_t ts = tm + lanes + TM_S + 64 * wg, td = tm + lanes + TM_DP + 64 * wg;
+      tmem_ld32(ts, x[0]);
+      tmem_ld32(ts + 32, x[1]);
+      tmem_ld_wait(x[0]);
+      tmem_ld_wait(x[1]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.s_free);
+      const int seen = hi - (i * 128 + 64 * wg);         // columns below it are allowed
+      const bool edge = __any_sync(0xffffffffu, seen < 64);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          x[c][j] = __float_as_uint(ex2(fmaf(__uint_as_float(x[c][j]), p.scale2, -lse2)));
+      if (edge) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (32 * c + j >= seen) x[c][j] = 0;
+      }
+      ok = warp_wait(cx, &m.dp_full, i & 1, 41, i);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t pk[2][16];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t d[32];
+        tmem_ld32(td + 32 * c, d);
+        tmem_ld_wait(d);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          d[j] = __float_as_uint(__uint_as_float(x[c][j]) * (__uint_as_float(d[j]) - delta));
+        if (edge) {  // dP of a pair outside may be anything
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (32 * c + j >= seen) d[j] = 0;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          pk[c][j] = pack_bf16x2(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]));
+      }
+      // over dP, all of whose columns here are in registers
+      tmem_st16(td, pk[0]);
+      tmem_st16(td + 16, pk[1]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.ds_ready);
+    }
+    if (ok && n > 0) {
+      ok = warp_wait(cx, &m.acc_full, 0, 42, n);
+      tc_fence_after();
+    }
+    if (ok && st.seq >= 0) {
+      const int64_t qr = st.q0 + x0;
+      for (int c = wg; c < KB; c += 2)
+        store_cols(tm + lanes + TM_A1 + 64 * c, p.scale, n == 0,
+                   p.dq + (qr * p.H + head) * N1 + 64 * c, (int64_t)p.H * N1, st.nq - x0,
+                   base + warp * 8192, warp & 3, lane);
+    }
+  }
+
+  __syncwarp();
+  __syncthreads();
+  if (m.abort) {  // nothing in flight outlives the CTA
+    if (tid == 32 * kLoadWarp && n > 0) {
+      for (int k = max(0, m.loaded_k - KT); k < m.loaded_k; ++k)
+        mbar_wait(&m.k_full[k % KT], (k / KT) & 1, kWaitNs);
+      for (int k = max(0, m.loaded_v - VT); k < m.loaded_v; ++k)
+        mbar_wait(&m.v_full[k % VT], (k / VT) & 1, kWaitNs);
+      mbar_wait(&m.x_full, 0, kWaitNs);
+    }
+    if (tid == 32 * kMmaWarp) {
+      umma_commit(&m.fin);
+      mbar_wait(&m.fin, 0, kWaitNs);
+    }
+    __syncthreads();
+  }
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tmem_dealloc(tm, 512);
+  }
+}
+
 // Blocks [0, k_tiles * H): the keys pass, then the queries pass.
 template <int DR>
 __global__ void __launch_bounds__(kThreads, 1)
 kda_latent_bwd_kernel(const __grid_constant__ Maps maps, const Params p) {
-  extern __shared__ unsigned char raw[];
-  const uint32_t base = round_up_1k(smem_u32(raw));
-  unsigned char *const tiles = raw + (base - smem_u32(raw));
-  Shared &m =
-      *reinterpret_cast<Shared *>(tiles + x_bytes<DR>() + stages<DR>() * stage_bytes<DR>());
+  extern __shared__ __align__(1024) unsigned char tiles[];
+  const uint32_t base = smem_u32(tiles);
   const int first_q = p.k_tiles * p.H;
   if ((int)blockIdx.x < first_q)
-    pass<DR, true>(maps, p, blockIdx.x % p.k_tiles, blockIdx.x / p.k_tiles, tiles, base, m);
+    keys_pass<DR>(maps, p, blockIdx.x % p.k_tiles, blockIdx.x / p.k_tiles, base,
+                  *reinterpret_cast<Shared *>(tiles + kSmem - kSharedBytes));
   else
-    pass<DR, false>(maps, p, (blockIdx.x - first_q) % p.q_tiles, (blockIdx.x - first_q) / p.q_tiles,
-                    tiles, base, m);
+    queries_pass<DR>(maps, p, (blockIdx.x - first_q) % p.q_tiles,
+                     (blockIdx.x - first_q) / p.q_tiles, base,
+                     *reinterpret_cast<QShared *>(tiles + kSmem - kSharedBytes));
 }
 
 // lse * log2(e) and delta = d_out . out of 64 rows of a head, in the padded layout.
@@ -571,7 +861,7 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   auto kernel = kda_latent_bwd_kernel<DR>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       smem_bytes<DR>());
+                                       kSmem);
   if (e != cudaSuccess) return e;
   if (a.n_q > 0) {
     const dim3 grid((unsigned)(a.n_q / kY + a.n_seqs), (unsigned)a.H);
@@ -581,7 +871,7 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  kernel<<<(unsigned)blocks, kThreads, smem_bytes<DR>(), stream>>>(mp, p);
+  kernel<<<(unsigned)blocks, kThreads, kSmem, stream>>>(mp, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || !DR || a.n_k == 0) return e;
   const int64_t elems = a.n_k * kLatentRope;
