@@ -33,10 +33,11 @@ struct LatentArgs {
   const void *d_out;
   void *dq, *dk, *dv, *d_k_rope;
   int64_t dk_ts, dk_hs, dv_ts, dv_hs;
-  void *scratch;       // latent_bwd_scratch_bytes()
+  void *scratch;       // latent_fwd_scratch_bytes() or latent_bwd_scratch_bytes()
 };
 cudaError_t launch_latent_fwd(const LatentArgs &a, cudaStream_t stream);
 cudaError_t launch_latent_bwd(const LatentArgs &a, cudaStream_t stream);
+size_t latent_fwd_scratch_bytes(int64_t n_q, int64_t n_k, int32_t H);
 size_t latent_bwd_scratch_bytes(int32_t n_seqs, int64_t n_q, int64_t n_k, int32_t H, int32_t dr);
 
 // Absorbed form over a paged cache.

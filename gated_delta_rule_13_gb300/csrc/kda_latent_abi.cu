@@ -134,7 +134,7 @@ int kda_latent_fwd_workspace_size(int32_t n_seqs, int64_t n_q, int64_t n_k, int3
   if (!bytes) return KDA_ERR_INVALID_ARG;
   const int d = check_sizes(n_seqs, n_q, n_k, H, dk, dr, dv, dtype);
   if (d != KDA_OK) return d;
-  *bytes = base_bytes(n_seqs);
+  *bytes = base_bytes(n_seqs) + round_up(kda::latent_fwd_scratch_bytes(n_q, n_k, H), 256);
   return KDA_OK;
 }
 
@@ -159,11 +159,14 @@ int kda_latent_fwd(const void *q, const void *k, const void *v, const void *k_ro
                       {k_rope, (size_t)n_k * dr * 2}};
   const Range outs[] = {{out, rows * dv * 2}, {lse, rows * 4}};
   if (any_overlap(in, outs)) return KDA_ERR_INVALID_ARG;
-  if (!workspace || !aligned(workspace, 16) || workspace_bytes < base_bytes(n_seqs))
+  const size_t scratch = round_up(kda::latent_fwd_scratch_bytes(n_q, n_k, H), 256);
+  if (!workspace || !aligned(workspace, 16) || workspace_bytes < base_bytes(n_seqs) + scratch)
     return KDA_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int r = begin(a, cu_seqlens_q, cu_seqlens_k, static_cast<unsigned char *>(workspace), st);
+  unsigned char *ws = static_cast<unsigned char *>(workspace);
+  const int r = begin(a, cu_seqlens_q, cu_seqlens_k, ws, st);
   if (r != KDA_OK) return r;
+  a.scratch = ws + base_bytes(n_seqs);
   return cuda_result(kda::launch_latent_fwd(a, st));
 }
 

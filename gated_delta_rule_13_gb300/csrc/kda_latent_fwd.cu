@@ -17,6 +17,14 @@
 // by more than 8 (log2): O_t is then rescaled in TMEM, which after the first
 // tiles hardly ever happens.
 //
+// Work items are (256 queries, head).  They run in groups of as many heads as fill the
+// SMs once, inside a group longest first: a group's keys are read by its tiles at
+// about the same time, and the last items to start are short ones.  What does not fill
+// the SMs a whole time at the end has its keys shared out over the idle ones; these
+// items leave (reference, sum, O) in the workspace and a second small kernel joins
+// them (2048 queries over 32768 keys, 96 heads: 768 items on 152 SMs are five rounds
+// and eight items, which as a sixth round cost a fifth of the time).
+//
 // Keys and values stream through a ring of 16 KB slots: 64-channel blocks of 128
 // keys, 64-key x 128-channel blocks of values.
 #include <cuda_bf16.h>
@@ -46,13 +54,20 @@ constexpr int kMaxSlots = 10;
 // consecutive units are enough (at most five are resident).
 constexpr int kUnits = 8;
 
+// What a block works on: a tile of a sequence, a head, and part `part` of `parts` of
+// its keys; seq < 0: nothing.
+struct Item {
+  SeqTile tile;
+  int head, part, parts, slot;           // slot: of its partial results
+};
+
 struct Shared {
   uint64_t full[kUnits], empty[kUnits];
   uint64_t q_full[2], s_full[2], p_ready[2][2], o_full[2], clean_req, clean, fin;
   uint32_t tmem;
   int loaded;                              // units loaded
   int abort;
-  SeqTile tile;
+  Item item;
 };
 
 template <int DR>
@@ -67,16 +82,137 @@ constexpr uint32_t smem_bytes() {
   return 1024 + q_bytes<DR>() + slots<DR>() * kSlotBytes + sizeof(Shared);
 }
 
+constexpr int kMinPart = 4;              // key tiles of a part, at least
+
 struct Params {
   const int32_t *cu_q, *cu_k;
-  int32_t n_seqs, H, tiles;
+  int32_t n_seqs, H, sms;
+  int32_t split;                         // whether keys may be shared out
   int64_t n_q, n_k;
   float scale2;
   int causal;
   __nv_bfloat16 *out;
   float *lse;
   DeviceStatus *status;
+  float *part_o;                         // [slot][2][128 / 4 channels][128 rows][4]
+  float *part_ml;                        // [slot][2][2][128]
 };
+
+// Key tiles of query tile t (of 128) of a work item.
+__device__ __forceinline__ int key_tiles(const SeqTile &st, int row0, int t, int causal) {
+  const int first = row0 + 128 * t;
+  if (st.seq < 0 || first >= st.nq) return 0;
+  int n = st.nk;
+  if (causal) n = min(n, min(first + 128, st.nq) + st.nk - st.nq);
+  return n <= 0 ? 0 : (n + kKeys - 1) / kKeys;
+}
+// First query of a work item: the last queries of a sequence, which see the most
+// keys, come first.
+__device__ __forceinline__ int first_row(const SeqTile &st) {
+  return (st.n_tiles - 1 - st.tile) * kRows;
+}
+
+// Tile `index` of all sequences, by one warp: every sequence's last tile, then every
+// sequence's last but one, and so on (up to 32 sequences; more of them in sequence
+// order, where a sequence is a small part of the whole anyway).
+__device__ inline SeqTile ordered_tile(const Params &p, int64_t index) {
+  const int lane = threadIdx.x & 31;
+  if (p.n_seqs > 32)
+    return find_seq_tile(p.cu_q, p.cu_k, p.n_seqs, p.n_q, p.n_k, kRows, false, index);
+  int q0 = 0, nq = 0, k0 = 0, nk = 0;
+  if (lane < p.n_seqs) {  // checked by the caller's count
+    q0 = cu_at(p.cu_q, lane, p.n_q);
+    nq = cu_at(p.cu_q, lane + 1, p.n_q) - q0;
+    k0 = cu_at(p.cu_k, lane, p.n_k);
+    nk = cu_at(p.cu_k, lane + 1, p.n_k) - k0;
+  }
+  const int tiles = (nq + kRows - 1) / kRows;
+  // the largest level (tiles from the end) with at most `index` tiles before it
+  int lo = 0, hi = __reduce_max_sync(0xffffffffu, tiles);
+  while (lo + 1 < hi) {
+    const int mid = (lo + hi) / 2;
+    if (__reduce_add_sync(0xffffffffu, min(tiles, mid)) <= index) lo = mid;
+    else hi = mid;
+  }
+  const int rank = (int)(index - __reduce_add_sync(0xffffffffu, min(tiles, lo)));
+  const unsigned have = __ballot_sync(0xffffffffu, tiles > lo);
+  const int s = __popc(have) > rank ? (int)__fns(have, 0, rank + 1) : -1;
+  SeqTile r;
+  r.bad = 0;
+  r.seq = s;
+  r.tile = lo;
+  const int from = max(s, 0);
+  r.n_tiles = __shfl_sync(0xffffffffu, tiles, from);
+  r.q0 = __shfl_sync(0xffffffffu, q0, from);
+  r.nq = __shfl_sync(0xffffffffu, nq, from);
+  r.k0 = __shfl_sync(0xffffffffu, k0, from);
+  r.nk = __shfl_sync(0xffffffffu, nk, from);
+  return r;
+}
+
+// All tiles, or -1 for malformed cu_seqlens; by one warp.
+__device__ inline int64_t count_tiles(const Params &p) {
+  const int lane = threadIdx.x & 31;
+  bool bad = cu_at(p.cu_q, 0, p.n_q) != 0 || cu_at(p.cu_k, 0, p.n_k) != 0 ||
+             cu_at(p.cu_q, p.n_seqs, p.n_q) != p.n_q || cu_at(p.cu_k, p.n_seqs, p.n_k) != p.n_k;
+  int mine = 0;
+  for (int s = lane; s < p.n_seqs; s += 32) {
+    const int qa = cu_at(p.cu_q, s, p.n_q), qb = cu_at(p.cu_q, s + 1, p.n_q);
+    const int ka = cu_at(p.cu_k, s, p.n_k), kb = cu_at(p.cu_k, s + 1, p.n_k);
+    bad = bad || qb < qa || kb < ka || qa < 0 || ka < 0 || qb > p.n_q || kb > p.n_k;
+    if (!bad) mine += (qb - qa + kRows - 1) / kRows;
+  }
+  if (__any_sync(0xffffffffu, bad)) return -1;
+  return __reduce_add_sync(0xffffffffu, mine);
+}
+
+// Tile and head of work item `index` among `tiles` * H.
+__device__ inline void place_item(const Params &p, int64_t tiles, int64_t index, Item &it) {
+  const int64_t group = max((int64_t)1, p.sms / tiles);  // heads that run side by side
+  const int64_t g = index / (tiles * group), heads = min(group, p.H - g * group);
+  const int64_t in = index - g * tiles * group;
+  it.head = (int)(g * group + in % heads);
+  it.tile = ordered_tile(p, in / heads);
+}
+
+// Items of whole rounds run undivided, one a block; item `whole` + j of the `rest` in
+// `ways` parts each (fewer when its keys are few).
+struct Rounds {
+  int64_t whole;
+  int rest, ways;
+  __device__ Rounds(const Params &p, int64_t items) {
+    whole = p.split ? items / p.sms * p.sms : items;
+    rest = (int)(items - whole);
+    ways = rest > 0 ? p.sms / rest : 1;
+  }
+};
+__device__ __forceinline__ int parts_of(const SeqTile &st, int ways, int causal) {
+  const int row0 = first_row(st);
+  const int n = max(key_tiles(st, row0, 0, causal), key_tiles(st, row0, 1, causal));
+  return max(1, min(ways, n / kMinPart));
+}
+
+__device__ inline Item find_item(const Params &p, int64_t block) {
+  Item it;
+  it.tile.seq = -1; it.tile.bad = 0; it.tile.n_tiles = it.tile.tile = 0;
+  it.tile.q0 = it.tile.nq = it.tile.k0 = it.tile.nk = 0;
+  it.head = it.part = it.slot = 0;
+  it.parts = 1;
+  const int64_t tiles = count_tiles(p);
+  if (tiles < 0) it.tile.bad = 1;
+  if (tiles <= 0) return it;
+  const Rounds r(p, tiles * p.H);
+  if (block < r.whole) {
+    place_item(p, tiles, block, it);
+  } else if (block - r.whole < (int64_t)r.rest * r.ways) {
+    it.slot = (int)(block - r.whole);
+    place_item(p, tiles, r.whole + it.slot / r.ways, it);
+    it.part = it.slot % r.ways;
+    it.parts = parts_of(it.tile, r.ways, p.causal);
+    if (it.part >= it.parts) it.tile.seq = -1;
+  }
+  return it;
+}
 
 template <int DR>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -97,12 +233,10 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
   unsigned char *const tiles = raw + (base - smem_u32(raw));
   Shared &m = *reinterpret_cast<Shared *>(tiles + kRing + S * kSlotBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int head = blockIdx.x / p.tiles;
 
   if (warp == kCleanWarp) {
-    const SeqTile f = find_seq_tile(p.cu_q, p.cu_k, p.n_seqs, p.n_q, p.n_k, kRows, false,
-                                    blockIdx.x % p.tiles);
-    if (lane == 0) m.tile = f;
+    const Item f = find_item(p, blockIdx.x);
+    if (lane == 0) m.item = f;
   }
   if (tid == 0) {
     for (int i = 0; i < kUnits; ++i) {
@@ -137,25 +271,25 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = m.tmem;
-  const SeqTile st = m.tile;
+  const Item item = m.item;
+  const SeqTile st = item.tile;
+  const int head = item.head;
   // every block sees a malformed array; block 0 says so, or clears the status (a
   // wait that gives up does so seconds later)
   if (blockIdx.x == 0 && tid == 0)
     set_device_status(p.status, st.bad ? KDA_ERR_INVALID_ARG : KDA_OK, st.bad);
+  pdl_launch_dependents();
 
-  // Longest first: the last queries of a sequence see the most keys.
-  const int row0 = (st.n_tiles - 1 - st.tile) * kRows;   // of the sequence
-  // Key tiles of the two query tiles (the second never has fewer).
-  auto key_tiles = [&](int t) {
-    const int first = row0 + 128 * t;
-    if (st.seq < 0 || first >= st.nq) return 0;
-    int n = st.nk;
-    if (p.causal) n = min(n, min(first + 128, st.nq) + st.nk - st.nq);
-    return n <= 0 ? 0 : (n + kKeys - 1) / kKeys;
-  };
-  const int nt[2] = {key_tiles(0), key_tiles(1)};
-  const int n_iter = max(nt[0], nt[1]);
-  const int last_live = min(kKeys, st.nk - (n_iter - 1) * kKeys);  // keys of the last tile
+  const int row0 = first_row(st);
+  // Key tiles [i0, i1) of this part, and those of the two query tiles among them (the
+  // second never has fewer).
+  const int all0 = key_tiles(st, row0, 0, p.causal), all1 = key_tiles(st, row0, 1, p.causal);
+  const int n_all = max(all0, all1);
+  const int i0 = (int)((int64_t)n_all * item.part / item.parts);
+  const int i1 = (int)((int64_t)n_all * (item.part + 1) / item.parts);
+  const int nt[2] = {max(0, min(all0, i1) - i0), max(0, min(all1, i1) - i0)};
+  const int n_iter = i1 - i0;
+  const int last_live = min(kKeys, st.nk - (i1 - 1) * kKeys);  // keys of the last tile
   const int halves_last = last_live > 64 ? 2 : 1;
   const WaitCtx cx{&m.abort, p.status, (int)blockIdx.x};
 
@@ -188,7 +322,7 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       };
       if (nt[0] > 0) load_q(0);
       for (int i = 0; i < n_iter; ++i) {
-        const int key = st.k0 + i * kKeys;
+        const int key = st.k0 + (i0 + i) * kKeys;
         before(KB);
         if (!ok) break;
         uint64_t *bar = &m.full[u % kUnits];
@@ -326,7 +460,7 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       for (int c = 0; c < 4; ++c) tmem_ld32(tm_s + 32 * c, x[c]);
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld_wait(x[c]);
-      const int seen = limit - i * kKeys;                // columns below it are allowed
+      const int seen = limit - (i0 + i) * kKeys;         // columns below it are allowed
       if (__any_sync(0xffffffffu, seen < kKeys)) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -387,42 +521,74 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     if (ok && nt[t] > 0)
       ok = warp_wait(cx, &m.o_full[t], 0, 41, n_iter);
     if (ok && live) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const uint32_t buf = base + t * KB * kQTile + (warp & 3) * 32 * 256;
       if (nt[t] > 0) tc_fence_after();
+      if (item.parts > 1) {
+        // four channels of the 32 rows beside one another
+        const int64_t at = (int64_t)item.slot * 2 + t;
+        p.part_ml[at * 256 + r] = ref;
+        p.part_ml[at * 256 + 128 + r] = l;
+        uint4 *to = reinterpret_cast<uint4 *>(p.part_o) + at * (kLatentD / 4) * 128 + r;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[32];
-        if (nt[t] > 0) {
-          tmem_ld32(tm_o + 32 * c, o);
-          tmem_ld_wait(o);
-        } else {
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          if (nt[t] > 0) {
+            tmem_ld32(tm_o + 32 * c, o);
+            tmem_ld_wait(o);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0;
+            for (int j = 0; j < 32; ++j) o[j] = 0;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            to[(8 * c + j) * 128] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
         }
+      } else {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const uint32_t buf = base + t * KB * kQTile + (warp & 3) * 32 * 256;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {   // 16-byte pieces, rotated by the row
-          uint32_t w[4];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          if (nt[t] > 0) {
+            tmem_ld32(tm_o + 32 * c, o);
+            tmem_ld_wait(o);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            w[j] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * j]) * inv,
-                               __uint_as_float(o[8 * q + 2 * j + 1]) * inv);
-          st_shared_v4(buf + lane * 256 + (((4 * c + q) ^ (lane & 15)) << 4), w[0], w[1], w[2],
-                       w[3]);
+            for (int j = 0; j < 32; ++j) o[j] = 0;
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {   // 16-byte pieces, rotated by the row
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              w[j] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * j]) * inv,
+                                 __uint_as_float(o[8 * q + 2 * j + 1]) * inv);
+            st_shared_v4(buf + lane * 256 + (((4 * c + q) ^ (lane & 15)) << 4), w[0], w[1], w[2],
+                         w[3]);
+          }
         }
+        __syncwarp();
+        const int64_t first = st.q0 + row0 + 128 * t + (warp & 3) * 32;
+#pragma unroll
+        for (int k0 = 0; k0 < 16; k0 += 8) {
+          uint4 v[8];
+          const int piece = lane & 15;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int rr = 2 * (k0 + k) + (lane >> 4);
+            v[k] = ld_shared_v4(buf + rr * 256 + ((piece ^ (rr & 15)) << 4));
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int rr = 2 * (k0 + k) + (lane >> 4);
+            if (row - lane + rr < st.nq)
+              *reinterpret_cast<uint4 *>(p.out + ((first + rr) * p.H + head) * kLatentD +
+                                         8 * piece) = v[k];
+          }
+        }
+        if (row < st.nq)
+          p.lse[(st.q0 + row) * (int64_t)p.H + head] =
+              l == 0.f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
       }
-      __syncwarp();
-      const int64_t first = st.q0 + row0 + 128 * t + (warp & 3) * 32;
-#pragma unroll 4
-      for (int k = 0; k < 16; ++k) {
-        const int rr = 2 * k + (lane >> 4), piece = lane & 15;
-        const uint4 v = ld_shared_v4(buf + rr * 256 + ((piece ^ (rr & 15)) << 4));
-        if (row - lane + rr < st.nq)
-          *reinterpret_cast<uint4 *>(p.out + ((first + rr) * p.H + head) * kLatentD + 8 * piece) = v;
-      }
-      if (row < st.nq)
-        p.lse[(st.q0 + row) * (int64_t)p.H + head] =
-            l == 0.f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
     }
   }
 
@@ -447,6 +613,77 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     tmem_dealloc(tm, 512);
   }
 }
+
+// Joins the parts of divided items in their order.  Block (x: 32 rows, y: item); a lane
+// is a row, a warp 16 channels.
+__global__ void __launch_bounds__(256) kda_latent_fwd_join_kernel(const Params p) {
+  __shared__ Item s_item;
+  __shared__ int s_ways;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
+  if (warp == 0) {
+    Item it;
+    it.tile.seq = -1;
+    it.parts = 1;
+    int ways = 1;
+    const int64_t tiles = count_tiles(p);
+    if (tiles > 0) {
+      const Rounds r(p, tiles * p.H);
+      ways = r.ways;
+      if ((int)blockIdx.y < r.rest) {
+        place_item(p, tiles, r.whole + blockIdx.y, it);
+        it.parts = parts_of(it.tile, r.ways, p.causal);
+      }
+    }
+    if (lane == 0) {
+      s_item = it;
+      s_ways = ways;
+    }
+  }
+  __syncthreads();
+  const Item it = s_item;
+  if (it.tile.seq < 0 || it.parts < 2) return;
+  const int t = blockIdx.x >> 2, r = (blockIdx.x & 3) * 32 + lane;
+  const int row = first_row(it.tile) + 128 * t + r;
+  if (row >= it.tile.nq) return;
+  const int64_t slot0 = (int64_t)blockIdx.y * s_ways;
+  float ref = kNoRef, l = 0.f, o[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c) o[c] = 0.f;
+#pragma unroll 2
+  for (int i = 0; i < it.parts; ++i) {
+    const int64_t at = (slot0 + i) * 2 + t;
+    const float4 *x =
+        reinterpret_cast<const float4 *>(p.part_o) + (at * (kLatentD / 4) + 4 * warp) * 128 + r;
+    float4 v[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = x[c * 128];
+    const float m = p.part_ml[at * 256 + r], s = p.part_ml[at * 256 + 128 + r];
+    const float now = m > ref || m != m ? m : ref;
+    const float a = ex2(ref - now), b = ex2(m - now);
+    ref = now;
+    l = l * a + s * b;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      o[4 * c] = o[4 * c] * a + v[c].x * b;
+      o[4 * c + 1] = o[4 * c + 1] * a + v[c].y * b;
+      o[4 * c + 2] = o[4 * c + 2] * a + v[c].z * b;
+      o[4 * c + 3] = o[4 * c + 3] * a + v[c].w * b;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t at = (it.tile.q0 + row) * (int64_t)p.H + it.head;
+  uint32_t w[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) w[c] = pack_bf16x2(o[2 * c] * inv, o[2 * c + 1] * inv);
+  uint4 *to = reinterpret_cast<uint4 *>(p.out + at * kLatentD + 16 * warp);
+  to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  if (warp == 0) p.lse[at] = l == 0.f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
+}
+
+// Whether any item can have keys enough for two parts (lengths are on the device).
+bool may_split(int64_t n_k) { return n_k >= (2 * kMinPart - 1) * kKeys + 1; }
 
 template <int DR>
 cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
@@ -478,16 +715,39 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
   if ((uint32_t)fa.numRegs < kLaunchRegs) return cudaErrorNotSupported;
   Params p;
   p.cu_q = a.cu_q; p.cu_k = a.cu_k; p.n_seqs = a.n_seqs; p.H = a.H;
-  p.tiles = (int32_t)(a.n_q / kRows + a.n_seqs);
+  p.sms = max(1, sm_count());
+  p.split = may_split(a.n_k) && p.sms > 1;
+  p.part_ml = static_cast<float *>(a.scratch);
+  p.part_o = p.part_ml + (int64_t)p.sms * 2 * 256;
   p.n_q = a.n_q; p.n_k = a.n_k; p.scale2 = a.scale * kLog2e; p.causal = a.causal;
   p.out = static_cast<__nv_bfloat16 *>(a.out); p.lse = a.lse; p.status = a.status;
-  const int64_t blocks = (int64_t)p.tiles * a.H;
+  // as many items as there can be (one sequence: exactly that many), and the parts
+  const int64_t tiles = a.n_seqs == 1 ? (a.n_q + kRows - 1) / kRows : a.n_q / kRows + a.n_seqs;
+  const int64_t blocks = tiles * a.H + (p.split ? p.sms : 0);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   kernel<<<(unsigned)blocks, kThreads, smem_bytes<DR>(), stream>>>(mq, mk, mr, mv, p);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !p.split) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kRows / 32, (unsigned)(tiles * a.H < p.sms ? tiles * a.H : p.sms));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kda_latent_fwd_join_kernel, p);
 }
 
 }  // namespace
+
+size_t latent_fwd_scratch_bytes(int64_t n_q, int64_t n_k, int32_t H) {
+  (void)H;
+  if (n_q == 0 || !may_split(n_k)) return 0;
+  const int sms = sm_count();
+  return (size_t)(sms > 1 ? sms : 1) * 2 * (256 + 128 * kLatentD) * sizeof(float);
+}
 
 cudaError_t launch_latent_fwd(const LatentArgs &a, cudaStream_t stream) {
   if (a.n_q == 0) return cudaSuccess;

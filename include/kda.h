@@ -568,8 +568,9 @@ int kda_post_fwd(const void *o, const void *g, const float *gamma, int64_t n_tok
  */
 
 /*
- * Bytes of workspace of kda_latent_fwd: the device status word and device
- * copies of host cu_seqlens arrays.
+ * Bytes of workspace of kda_latent_fwd: the device status word, device copies of
+ * host cu_seqlens arrays and, where keys are long enough to be shared out over
+ * several CTAs, the partial results of at most one tile an SM.
  * Errors: KDA_ERR_INVALID_ARG (NULL bytes, negative sizes, n_seqs < 1, H <= 0),
  * KDA_ERR_UNSUPPORTED (dk or dv != 128, dr not 0 or 64, dtype not KDA_BF16).
  */
