@@ -149,6 +149,103 @@ __device__ inline SeqTile find_seq_tile(const int32_t *__restrict__ cu_q,
   if (r.bad) r.seq = -1;
   return r;
 }
+// The packed sequences of a call, as its kernels need them to find their work.
+struct Packed {
+  const int32_t *cu_q, *cu_k;
+  int32_t n_seqs, H, sms;
+  int64_t n_q, n_k;
+};
+
+// Up to 32 sequences, one a lane, loaded once; `bad`: the arrays are malformed.
+struct LaneSeqs {
+  int32_t q0, nq, k0, nk;
+  bool bad, many;  // many: more than 32, looked up in memory instead
+  __device__ explicit LaneSeqs(const Packed &p) : q0(0), nq(0), k0(0), nk(0), many(p.n_seqs > 32) {
+    const int lane = threadIdx.x & 31;
+    int32_t qb = 0, kb = 0;
+    if (!many && lane < p.n_seqs) {
+      q0 = cu_at(p.cu_q, lane, p.n_q);
+      qb = cu_at(p.cu_q, lane + 1, p.n_q);
+      k0 = cu_at(p.cu_k, lane, p.n_k);
+      kb = cu_at(p.cu_k, lane + 1, p.n_k);
+    }
+    nq = qb - q0;
+    nk = kb - k0;
+    bool wrong = q0 < 0 || k0 < 0 || nq < 0 || nk < 0 || qb > p.n_q || kb > p.n_k;
+    wrong = wrong || (!many && ((lane == 0 && (q0 != 0 || k0 != 0)) ||
+                                (lane == p.n_seqs - 1 && (qb != p.n_q || kb != p.n_k))));
+    bad = __any_sync(0xffffffffu, wrong);
+  }
+};
+
+// All tiles (of `rows` queries, by_key: keys), or -1 for malformed arrays; by one warp.
+__device__ inline int64_t count_tiles(const Packed &p, const LaneSeqs &l, int32_t rows,
+                                      bool by_key) {
+  if (!l.many) {
+    if (l.bad) return -1;
+    return __reduce_add_sync(0xffffffffu, ((by_key ? l.nk : l.nq) + rows - 1) / rows);
+  }
+  const int lane = threadIdx.x & 31;
+  bool bad = cu_at(p.cu_q, 0, p.n_q) != 0 || cu_at(p.cu_k, 0, p.n_k) != 0 ||
+             cu_at(p.cu_q, p.n_seqs, p.n_q) != p.n_q || cu_at(p.cu_k, p.n_seqs, p.n_k) != p.n_k;
+  int mine = 0;
+  for (int s = lane; s < p.n_seqs; s += 32) {
+    const int qa = cu_at(p.cu_q, s, p.n_q), qb = cu_at(p.cu_q, s + 1, p.n_q);
+    const int ka = cu_at(p.cu_k, s, p.n_k), kb = cu_at(p.cu_k, s + 1, p.n_k);
+    bad = bad || qb < qa || kb < ka || qa < 0 || ka < 0 || qb > p.n_q || kb > p.n_k;
+    if (!bad) mine += ((by_key ? kb - ka : qb - qa) + rows - 1) / rows;
+  }
+  if (__any_sync(0xffffffffu, bad)) return -1;
+  return __reduce_add_sync(0xffffffffu, mine);
+}
+
+// Tile `index` of all sequences, by one warp: every sequence's tile 0, then every
+// sequence's tile 1, and so on (up to 32 sequences; more of them in sequence order,
+// where a sequence is a small part of the whole anyway).  Callers count tiles from
+// the end of a sequence that has the most work.
+__device__ inline SeqTile ordered_tile(const Packed &p, const LaneSeqs &l, int32_t rows,
+                                       bool by_key, int64_t index) {
+  if (l.many)
+    return find_seq_tile(p.cu_q, p.cu_k, p.n_seqs, p.n_q, p.n_k, rows, by_key, index);
+  const int tiles = ((by_key ? l.nk : l.nq) + rows - 1) / rows;
+  // the largest tile number with at most `index` tiles before it
+  int lo = 0, s = 0;
+  if (p.n_seqs == 1) {
+    lo = (int)index;
+  } else {
+    int hi = __reduce_max_sync(0xffffffffu, tiles);
+    while (lo + 1 < hi) {
+      const int mid = (lo + hi) / 2;
+      if (__reduce_add_sync(0xffffffffu, min(tiles, mid)) <= index) lo = mid;
+      else hi = mid;
+    }
+    const int rank = (int)(index - __reduce_add_sync(0xffffffffu, min(tiles, lo)));
+    const unsigned have = __ballot_sync(0xffffffffu, tiles > lo);
+    s = __popc(have) > rank ? (int)__fns(have, 0, rank + 1) : -1;
+  }
+  SeqTile r;
+  r.bad = 0;
+  r.seq = s;
+  r.tile = lo;
+  const int from = max(s, 0);
+  r.n_tiles = __shfl_sync(0xffffffffu, tiles, from);
+  r.q0 = __shfl_sync(0xffffffffu, l.q0, from);
+  r.nq = __shfl_sync(0xffffffffu, l.nq, from);
+  r.k0 = __shfl_sync(0xffffffffu, l.k0, from);
+  r.nk = __shfl_sync(0xffffffffu, l.nk, from);
+  return r;
+}
+
+// Tile and head of work item `index` of `tiles` * H.  Items run in groups of as many
+// heads as fill the SMs once, inside a group tile by tile.
+__device__ inline SeqTile place_item(const Packed &p, const LaneSeqs &l, int32_t rows, bool by_key,
+                                     int64_t tiles, int64_t index, int *head) {
+  const int64_t fill = p.sms / tiles, group = fill > 1 ? fill : 1;
+  const int64_t g = index / (tiles * group), left = p.H - g * group;
+  const int64_t heads = group < left ? group : left, in = index - g * tiles * group;
+  *head = (int)(g * group + in % heads);
+  return ordered_tile(p, l, rows, by_key, in / heads);
+}
 #endif
 
 }  // namespace kda

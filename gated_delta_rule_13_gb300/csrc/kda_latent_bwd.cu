@@ -44,9 +44,7 @@ constexpr uint32_t kXBlock = 16384, kYBlock = 8192;  // 128 or 64 rows x 64 chan
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages], s_full[2];
   uint64_t x_full, dp_full, ds_ready, clean_req, clean, acc_full, fin;
-  uint32_t tmem;
   int abort, loaded;
-  SeqTile tile;
   alignas(16) float lse2[kMaxStages][kY];
   float delta[kMaxStages][kY];
 };
@@ -57,22 +55,20 @@ template <int DR>
 constexpr uint32_t stage_bytes() { return ((kLatentD + DR) / 64 + 2) * kYBlock; }
 template <int DR>
 constexpr int stages() { return DR ? 3 : 4; }
-constexpr uint32_t kSmem = 232448, kSharedBytes = 3072;
+constexpr uint32_t kSmem = 232448 - 1024, kSharedBytes = 2048;  // dynamic; the item is static
 struct QShared {                         // of the queries pass
   uint64_t k_full[4], k_empty[4], v_full[2], v_empty[2];
   uint64_t x_full, x2_ready, s_full, s_free, dp_full, ds_ready, clean_req, clean, acc_full, fin;
-  uint32_t tmem;
   int abort, loaded_k, loaded_v;
-  SeqTile tile;
 };
-static_assert(sizeof(Shared) <= kSharedBytes && sizeof(QShared) <= kSharedBytes, "shared memory");
-static_assert(x_bytes<64>() + stages<64>() * stage_bytes<64>() + kSharedBytes <= kSmem &&
-              x_bytes<0>() + stages<0>() * stage_bytes<0>() + kSharedBytes <= kSmem, "shared memory");
+static_assert(sizeof(QShared) <= kSharedBytes, "shared memory");
+template <int DR>
+constexpr uint32_t keys_bytes() { return x_bytes<DR>() + stages<DR>() * stage_bytes<DR>(); }
+static_assert(keys_bytes<64>() + sizeof(Shared) <= kSmem &&
+              keys_bytes<0>() + sizeof(Shared) <= kSmem, "shared memory");
 
-struct Params {
-  const int32_t *cu_q, *cu_k;
-  int32_t n_seqs, H, k_tiles, q_tiles;   // tiles a head: upper bounds
-  int64_t n_q, n_k, stat_rows;
+struct Params : Packed {
+  int64_t stat_rows;
   float scale, scale2;
   int causal;
   __nv_bfloat16 *dq, *dk, *dv;
@@ -127,8 +123,8 @@ __device__ __forceinline__ void store_cols(uint32_t col, float mul, bool zero,
 }
 
 template <int DR>
-__device__ __forceinline__ void keys_pass(const Maps &maps, const Params &p, int index, int head,
-                                          uint32_t base, Shared &m) {
+__device__ __forceinline__ void keys_pass(const Maps &maps, const Params &p, const SeqTile &st, int head,
+                                          uint32_t base, uint32_t tm, Shared &m) {
   constexpr bool kKeys = true;
   constexpr int KB = (kLatentD + DR) / 64, ST = stages<DR>();
   constexpr uint32_t kStage = x_bytes<DR>();
@@ -139,10 +135,6 @@ __device__ __forceinline__ void keys_pass(const Maps &maps, const Params &p, int
   constexpr uint32_t ID_A2 = idesc_bf16(128, kLatentD, false, true);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  if (warp == kCleanWarp) {
-    const SeqTile f = find_seq_tile(p.cu_q, p.cu_k, p.n_seqs, p.n_q, p.n_k, kX, kKeys, index);
-    if (lane == 0) m.tile = f;
-  }
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&m.full[i], 1);
@@ -168,18 +160,7 @@ __device__ __forceinline__ void keys_pass(const Maps &maps, const Params &p, int
     prefetch_tensormap(kKeys ? &maps.g64 : &maps.v64);
     if (DR) prefetch_tensormap(kKeys ? &maps.r128 : &maps.r64);
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc(&m.tmem, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tm = m.tmem;
-  const SeqTile st = m.tile;
-
-  if (st.bad && p.n_q == 0 && index == 0 && head == 0 && tid == 0)  // no first kernel
-    set_device_status(p.status, KDA_ERR_INVALID_ARG, 1);
 
   // The CTA's rows [x0, x0 + 128) of the sequence, longest first: the first keys are
   // seen by the most queries, the last queries see the most keys.  It streams
@@ -446,10 +427,6 @@ __device__ __forceinline__ void keys_pass(const Maps &maps, const Params &p, int
     }
     __syncthreads();
   }
-  if (warp == kMmaWarp) {
-    __syncwarp();
-    tmem_dealloc(tm, 512);
-  }
 }
 
 // The queries pass: X = 128 queries and their d_out, streamed tiles of 128 keys.  S and
@@ -459,8 +436,8 @@ __device__ __forceinline__ void keys_pass(const Maps &maps, const Params &p, int
 // streamed tiles: keys in three (dr = 0: four) buffers, because they are held from S
 // to the product with dS, values in one (two), because they are done with dP.
 template <int DR>
-__device__ __forceinline__ void queries_pass(const Maps &maps, const Params &p, int index, int head,
-                                             uint32_t base, QShared &m) {
+__device__ __forceinline__ void queries_pass(const Maps &maps, const Params &p, const SeqTile &st, int head,
+                                             uint32_t base, uint32_t tm, QShared &m) {
   constexpr int KB = (kLatentD + DR) / 64, KT = DR ? 3 : 4, VT = DR ? 1 : 2;
   constexpr uint32_t kRingK = KB * kXBlock, kRingV = kRingK + KT * KB * kXBlock;
   constexpr uint32_t kX2 = kRingK + 2 * KB * kXBlock;    // d_out, where the keys of tile 2 go
@@ -471,10 +448,6 @@ __device__ __forceinline__ void queries_pass(const Maps &maps, const Params &p, 
   constexpr uint32_t ID_A1 = idesc_bf16(128, N1, false, true);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  if (warp == kCleanWarp) {
-    const SeqTile f = find_seq_tile(p.cu_q, p.cu_k, p.n_seqs, p.n_q, p.n_k, kX, false, index);
-    if (lane == 0) m.tile = f;
-  }
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
       mbar_init(&m.k_full[i], 1);
@@ -503,15 +476,7 @@ __device__ __forceinline__ void queries_pass(const Maps &maps, const Params &p, 
     prefetch_tensormap(&maps.v128);
     if (DR) prefetch_tensormap(&maps.r128);
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc(&m.tmem, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tm = m.tmem;
-  const SeqTile st = m.tile;
 
   // longest first: the last queries of a sequence see the most keys
   const int x0 = (st.n_tiles - 1 - st.tile) * kX;
@@ -730,26 +695,63 @@ __device__ __forceinline__ void queries_pass(const Maps &maps, const Params &p, 
     }
     __syncthreads();
   }
-  if (warp == kMmaWarp) {
-    __syncwarp();
-    tmem_dealloc(tm, 512);
-  }
 }
 
-// Blocks [0, k_tiles * H): the keys pass, then the queries pass.
+// The keys pass's items, then the queries pass's; both longest first (the first keys
+// are seen by the most queries, the last queries see the most keys).
 template <int DR>
 __global__ void __launch_bounds__(kThreads, 1)
 kda_latent_bwd_kernel(const __grid_constant__ Maps maps, const Params p) {
   extern __shared__ __align__(1024) unsigned char tiles[];
-  const uint32_t base = smem_u32(tiles);
-  const int first_q = p.k_tiles * p.H;
-  if ((int)blockIdx.x < first_q)
-    keys_pass<DR>(maps, p, blockIdx.x % p.k_tiles, blockIdx.x / p.k_tiles, base,
-                  *reinterpret_cast<Shared *>(tiles + kSmem - kSharedBytes));
-  else
-    queries_pass<DR>(maps, p, (blockIdx.x - first_q) % p.q_tiles,
-                     (blockIdx.x - first_q) / p.q_tiles, base,
-                     *reinterpret_cast<QShared *>(tiles + kSmem - kSharedBytes));
+  __shared__ SeqTile s_tile;
+  __shared__ int s_head, s_keys;
+  __shared__ uint32_t s_tmem;
+  const int warp = threadIdx.x >> 5;
+  if (warp == kMmaWarp) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+  }
+  if (warp == 0) {
+    SeqTile f;
+    f.seq = -1;
+    int head = 0;
+    const LaneSeqs seqs(p);
+    const int64_t nk = count_tiles(p, seqs, kX, true), nq = count_tiles(p, seqs, kX, false);
+    const int64_t b = blockIdx.x, first_q = nk * p.H;
+    const bool keys = nk >= 0 && b < first_q;
+    if (nk < 0) {
+      if (p.n_q == 0 && b == 0 && threadIdx.x == 0)      // no kernel before this one
+        set_device_status(p.status, KDA_ERR_INVALID_ARG, 1);
+    } else if (keys) {
+      f = place_item(p, seqs, kX, true, nk, b, &head);
+    } else if (b < first_q + nq * p.H) {
+      f = place_item(p, seqs, kX, false, nq, b - first_q, &head);
+    }
+    if (threadIdx.x == 0) {
+      s_tile = f;
+      s_head = head;
+      s_keys = keys;
+    }
+  }
+  pdl_launch_dependents();
+  pdl_wait();                            // the row statistics
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const SeqTile st = s_tile;
+  const uint32_t base = smem_u32(tiles), tm = s_tmem;
+  if (st.seq >= 0) {
+    if (s_keys)
+      keys_pass<DR>(maps, p, st, s_head, base, tm,
+                    *reinterpret_cast<Shared *>(tiles + keys_bytes<DR>()));
+    else
+      queries_pass<DR>(maps, p, st, s_head, base, tm,
+                       *reinterpret_cast<QShared *>(tiles + kSmem - kSharedBytes));
+  }
+  if (warp == kMmaWarp) {                // all warps have passed the pass's last barrier
+    __syncwarp();
+    tmem_dealloc(tm, 512);
+  }
 }
 
 // lse * log2(e) and delta = d_out . out of 64 rows of a head, in the padded layout.
@@ -761,6 +763,7 @@ kda_latent_stat_kernel(const __nv_bfloat16 *__restrict__ out,
                        float *__restrict__ lse2, float *__restrict__ delta, const Params p) {
   __shared__ SeqTile st;
   const int tid = threadIdx.x, head = blockIdx.y;
+  pdl_launch_dependents();
   if (tid < 32) {
     const SeqTile f =
         find_seq_tile(p.cu_q, p.cu_k, p.n_seqs, p.n_q, p.n_k, kY, false, blockIdx.x);
@@ -805,6 +808,7 @@ kda_latent_stat_kernel(const __nv_bfloat16 *__restrict__ out,
 __global__ void kda_latent_rope_kernel(const float *__restrict__ rope, int64_t n, int32_t H,
                                        float scale, const DeviceStatus *status,
                                        __nv_bfloat16 *__restrict__ out) {
+  pdl_wait();
   const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
   if (i >= n || status->code == KDA_ERR_INVALID_ARG) return;
   float4 a = make_float4(0, 0, 0, 0);
@@ -847,8 +851,7 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   Params p;
   p.cu_q = a.cu_q; p.cu_k = a.cu_k; p.n_seqs = a.n_seqs; p.H = a.H; p.n_q = a.n_q; p.n_k = a.n_k;
-  p.k_tiles = a.n_k > 0 ? (int32_t)(a.n_k / kX + a.n_seqs) : 0;
-  p.q_tiles = a.n_q > 0 ? (int32_t)(a.n_q / kX + a.n_seqs) : 0;
+  p.sms = sm_count();
   p.stat_rows = stat_rows(a.n_q, a.n_seqs);
   p.scale = a.scale; p.scale2 = a.scale * kLog2e; p.causal = a.causal;
   p.dq = static_cast<__nv_bfloat16 *>(a.dq); p.dk = static_cast<__nv_bfloat16 *>(a.dk);
@@ -857,7 +860,9 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
   float *lse2 = static_cast<float *>(a.scratch), *delta = lse2 + p.stat_rows * a.H;
   p.lse2 = lse2; p.delta = delta; p.rope = delta + p.stat_rows * a.H;
   p.status = a.status;
-  const int64_t blocks = ((int64_t)p.k_tiles + p.q_tiles) * a.H;
+  // as many items as there can be (one sequence: exactly that many)
+  auto most = [&](int64_t n) { return n == 0 ? 0 : a.n_seqs == 1 ? (n + kX - 1) / kX : n / kX + a.n_seqs; };
+  const int64_t blocks = (most(a.n_k) + most(a.n_q)) * a.H;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   auto kernel = kda_latent_bwd_kernel<DR>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -871,13 +876,28 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  kernel<<<(unsigned)blocks, kThreads, kSmem, stream>>>(mp, p);
-  e = cudaGetLastError();
+  // each kernel starts while the one before ends, and waits for it where it reads its
+  // results
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = a.n_q > 0 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kernel, mp, p);
   if (e != cudaSuccess || !DR || a.n_k == 0) return e;
   const int64_t elems = a.n_k * kLatentRope;
-  kda_latent_rope_kernel<<<(unsigned)((elems / 4 + 255) / 256), 256, 0, stream>>>(
-      p.rope, elems, a.H, a.scale, a.status, static_cast<__nv_bfloat16 *>(a.d_k_rope));
-  return cudaGetLastError();
+  cfg.gridDim = dim3((unsigned)((elems / 4 + 255) / 256));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kda_latent_rope_kernel, (const float *)p.rope, elems, a.H, a.scale,
+                            (const DeviceStatus *)a.status,
+                            static_cast<__nv_bfloat16 *>(a.d_k_rope));
 }
 
 }  // namespace

@@ -84,11 +84,8 @@ constexpr uint32_t smem_bytes() {
 
 constexpr int kMinPart = 4;              // key tiles of a part, at least
 
-struct Params {
-  const int32_t *cu_q, *cu_k;
-  int32_t n_seqs, H, sms;
+struct Params : Packed {
   int32_t split;                         // whether keys may be shared out
-  int64_t n_q, n_k;
   float scale2;
   int causal;
   __nv_bfloat16 *out;
@@ -110,69 +107,6 @@ __device__ __forceinline__ int key_tiles(const SeqTile &st, int row0, int t, int
 // keys, come first.
 __device__ __forceinline__ int first_row(const SeqTile &st) {
   return (st.n_tiles - 1 - st.tile) * kRows;
-}
-
-// Tile `index` of all sequences, by one warp: every sequence's last tile, then every
-// sequence's last but one, and so on (up to 32 sequences; more of them in sequence
-// order, where a sequence is a small part of the whole anyway).
-__device__ inline SeqTile ordered_tile(const Params &p, int64_t index) {
-  const int lane = threadIdx.x & 31;
-  if (p.n_seqs > 32)
-    return find_seq_tile(p.cu_q, p.cu_k, p.n_seqs, p.n_q, p.n_k, kRows, false, index);
-  int q0 = 0, nq = 0, k0 = 0, nk = 0;
-  if (lane < p.n_seqs) {  // checked by the caller's count
-    q0 = cu_at(p.cu_q, lane, p.n_q);
-    nq = cu_at(p.cu_q, lane + 1, p.n_q) - q0;
-    k0 = cu_at(p.cu_k, lane, p.n_k);
-    nk = cu_at(p.cu_k, lane + 1, p.n_k) - k0;
-  }
-  const int tiles = (nq + kRows - 1) / kRows;
-  // the largest level (tiles from the end) with at most `index` tiles before it
-  int lo = 0, hi = __reduce_max_sync(0xffffffffu, tiles);
-  while (lo + 1 < hi) {
-    const int mid = (lo + hi) / 2;
-    if (__reduce_add_sync(0xffffffffu, min(tiles, mid)) <= index) lo = mid;
-    else hi = mid;
-  }
-  const int rank = (int)(index - __reduce_add_sync(0xffffffffu, min(tiles, lo)));
-  const unsigned have = __ballot_sync(0xffffffffu, tiles > lo);
-  const int s = __popc(have) > rank ? (int)__fns(have, 0, rank + 1) : -1;
-  SeqTile r;
-  r.bad = 0;
-  r.seq = s;
-  r.tile = lo;
-  const int from = max(s, 0);
-  r.n_tiles = __shfl_sync(0xffffffffu, tiles, from);
-  r.q0 = __shfl_sync(0xffffffffu, q0, from);
-  r.nq = __shfl_sync(0xffffffffu, nq, from);
-  r.k0 = __shfl_sync(0xffffffffu, k0, from);
-  r.nk = __shfl_sync(0xffffffffu, nk, from);
-  return r;
-}
-
-// All tiles, or -1 for malformed cu_seqlens; by one warp.
-__device__ inline int64_t count_tiles(const Params &p) {
-  const int lane = threadIdx.x & 31;
-  bool bad = cu_at(p.cu_q, 0, p.n_q) != 0 || cu_at(p.cu_k, 0, p.n_k) != 0 ||
-             cu_at(p.cu_q, p.n_seqs, p.n_q) != p.n_q || cu_at(p.cu_k, p.n_seqs, p.n_k) != p.n_k;
-  int mine = 0;
-  for (int s = lane; s < p.n_seqs; s += 32) {
-    const int qa = cu_at(p.cu_q, s, p.n_q), qb = cu_at(p.cu_q, s + 1, p.n_q);
-    const int ka = cu_at(p.cu_k, s, p.n_k), kb = cu_at(p.cu_k, s + 1, p.n_k);
-    bad = bad || qb < qa || kb < ka || qa < 0 || ka < 0 || qb > p.n_q || kb > p.n_k;
-    if (!bad) mine += (qb - qa + kRows - 1) / kRows;
-  }
-  if (__any_sync(0xffffffffu, bad)) return -1;
-  return __reduce_add_sync(0xffffffffu, mine);
-}
-
-// Tile and head of work item `index` among `tiles` * H.
-__device__ inline void place_item(const Params &p, int64_t tiles, int64_t index, Item &it) {
-  const int64_t group = max((int64_t)1, p.sms / tiles);  // heads that run side by side
-  const int64_t g = index / (tiles * group), heads = min(group, p.H - g * group);
-  const int64_t in = index - g * tiles * group;
-  it.head = (int)(g * group + in % heads);
-  it.tile = ordered_tile(p, in / heads);
 }
 
 // Items of whole rounds run undivided, one a block; item `whole` + j of the `rest` in
@@ -198,15 +132,16 @@ __device__ inline Item find_item(const Params &p, int64_t block) {
   it.tile.q0 = it.tile.nq = it.tile.k0 = it.tile.nk = 0;
   it.head = it.part = it.slot = 0;
   it.parts = 1;
-  const int64_t tiles = count_tiles(p);
+  const LaneSeqs seqs(p);
+  const int64_t tiles = count_tiles(p, seqs, kRows, false);
   if (tiles < 0) it.tile.bad = 1;
   if (tiles <= 0) return it;
   const Rounds r(p, tiles * p.H);
   if (block < r.whole) {
-    place_item(p, tiles, block, it);
+    it.tile = place_item(p, seqs, kRows, false, tiles, block, &it.head);
   } else if (block - r.whole < (int64_t)r.rest * r.ways) {
     it.slot = (int)(block - r.whole);
-    place_item(p, tiles, r.whole + it.slot / r.ways, it);
+    it.tile = place_item(p, seqs, kRows, false, tiles, r.whole + it.slot / r.ways, &it.head);
     it.part = it.slot % r.ways;
     it.parts = parts_of(it.tile, r.ways, p.causal);
     if (it.part >= it.parts) it.tile.seq = -1;
@@ -626,12 +561,13 @@ __global__ void __launch_bounds__(256) kda_latent_fwd_join_kernel(const Params p
     it.tile.seq = -1;
     it.parts = 1;
     int ways = 1;
-    const int64_t tiles = count_tiles(p);
+    const LaneSeqs seqs(p);
+    const int64_t tiles = count_tiles(p, seqs, kRows, false);
     if (tiles > 0) {
       const Rounds r(p, tiles * p.H);
       ways = r.ways;
       if ((int)blockIdx.y < r.rest) {
-        place_item(p, tiles, r.whole + blockIdx.y, it);
+        it.tile = place_item(p, seqs, kRows, false, tiles, r.whole + blockIdx.y, &it.head);
         it.parts = parts_of(it.tile, r.ways, p.causal);
       }
     }
