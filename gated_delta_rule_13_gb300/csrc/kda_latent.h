@@ -37,7 +37,7 @@ struct LatentArgs {
 };
 cudaError_t launch_latent_fwd(const LatentArgs &a, cudaStream_t stream);
 cudaError_t launch_latent_bwd(const LatentArgs &a, cudaStream_t stream);
-size_t latent_fwd_scratch_bytes(int64_t n_q, int64_t n_k, int32_t H);
+size_t latent_fwd_scratch_bytes(int32_t n_seqs, int64_t n_q, int64_t n_k, int32_t H);
 size_t latent_bwd_scratch_bytes(int32_t n_seqs, int64_t n_q, int64_t n_k, int32_t H, int32_t dr);
 
 // Absorbed form over a paged cache.
@@ -88,7 +88,7 @@ __device__ __forceinline__ void set_device_status(DeviceStatus *st, int32_t code
   *st = DeviceStatus{code, detail, 0, 0, 0, 0};
 }
 
-// A tile of `rows` packed rows of one sequence: which sequence and which rows.
+// A tile of consecutive rows of one sequence.
 struct SeqTile {
   int32_t seq, tile, n_tiles;      // n_tiles of the sequence; seq < 0: no such tile
   int32_t q0, nq, k0, nk;          // the sequence's queries and keys
@@ -100,70 +100,31 @@ __device__ __forceinline__ int32_t cu_at(const int32_t *__restrict__ cu, int32_t
   return cu ? cu[s] : s == 0 ? 0 : (int32_t)n;
 }
 
-// Tile `index` of the packed sequences, cut into tiles of `rows` queries
-// (by_key: keys), by one whole warp.  Every entry of both arrays is read, so a
-// malformed array is seen by every caller, whatever its tile.
-__device__ inline SeqTile find_seq_tile(const int32_t *__restrict__ cu_q,
-                                        const int32_t *__restrict__ cu_k, int32_t n_seqs,
-                                        int64_t n_q, int64_t n_k, int32_t rows, bool by_key,
-                                        int64_t index) {
-  const int lane = threadIdx.x & 31;
-  SeqTile r;
-  r.seq = -1; r.tile = 0; r.n_tiles = 0; r.q0 = r.nq = r.k0 = r.nk = 0;
-  bool bad = cu_at(cu_q, 0, n_q) != 0 || cu_at(cu_k, 0, n_k) != 0 ||
-             cu_at(cu_q, n_seqs, n_q) != n_q || cu_at(cu_k, n_seqs, n_k) != n_k;
-  int64_t base = 0;
-  for (int32_t s0 = 0; s0 < n_seqs; s0 += 32) {
-    const int32_t s = s0 + lane;
-    int32_t qa = 0, qb = 0, ka = 0, kb = 0;
-    if (s < n_seqs) {
-      qa = cu_at(cu_q, s, n_q); qb = cu_at(cu_q, s + 1, n_q);
-      ka = cu_at(cu_k, s, n_k); kb = cu_at(cu_k, s + 1, n_k);
-    }
-    bad = bad || qb < qa || kb < ka || qa < 0 || ka < 0 || qb > n_q || kb > n_k;
-    bad = __any_sync(0xffffffffu, bad);
-    if (bad) break;
-    const int32_t len = by_key ? kb - ka : qb - qa;
-    const int32_t t = (int32_t)(((int64_t)len + rows - 1) / rows);
-    int32_t inc = t;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    const int64_t lo = base + inc - t;
-    const unsigned hit = __ballot_sync(0xffffffffu, index >= lo && index < lo + t);
-    if (hit) {
-      const int w = __ffs(hit) - 1;
-      r.seq = s0 + w;
-      r.tile = (int32_t)__shfl_sync(0xffffffffu, (int)(index - lo), w);
-      r.n_tiles = __shfl_sync(0xffffffffu, t, w);
-      r.q0 = __shfl_sync(0xffffffffu, qa, w);
-      r.nq = __shfl_sync(0xffffffffu, qb - qa, w);
-      r.k0 = __shfl_sync(0xffffffffu, ka, w);
-      r.nk = __shfl_sync(0xffffffffu, kb - ka, w);
-    }
-    base += __shfl_sync(0xffffffffu, inc, 31);
-  }
-  r.bad = __any_sync(0xffffffffu, bad) ? 1 : 0;
-  if (r.bad) r.seq = -1;
-  return r;
-}
-// The packed sequences of a call, as its kernels need them to find their work.
+// The packed sequences of a call, as its kernels need them to find their work.  Each
+// kind of tile they are cut into (kTileRows) has, for more than kLaneSeqs sequences,
+// the number of tiles before every sequence in memory.
+enum TileKind { kTileA = 0, kTileB = 1, kTileC = 2, kTileKinds = 3 };
+constexpr int kLaneSeqs = 32;
 struct Packed {
   const int32_t *cu_q, *cu_k;
   int32_t n_seqs, H, sms;
   int64_t n_q, n_k;
+  int32_t rows[kTileKinds];        // rows of a tile; 0: no such kind
+  bool by_key[kTileKinds];         // of keys (else of queries)
+  const int32_t *before[kTileKinds];  // [n_seqs + 1], -1 in the last entry: malformed arrays
 };
 
-// Up to 32 sequences, one a lane, loaded once; `bad`: the arrays are malformed.
+// The calling warp's view of the sequences: up to 32 of them are in its lanes, loaded
+// once; more are looked up.
 struct LaneSeqs {
   int32_t q0, nq, k0, nk;
-  bool bad, many;  // many: more than 32, looked up in memory instead
-  __device__ explicit LaneSeqs(const Packed &p) : q0(0), nq(0), k0(0), nk(0), many(p.n_seqs > 32) {
+  bool bad, many;
+  __device__ explicit LaneSeqs(const Packed &p)
+      : q0(0), nq(0), k0(0), nk(0), bad(false), many(p.n_seqs > kLaneSeqs) {
+    if (many) return;
     const int lane = threadIdx.x & 31;
     int32_t qb = 0, kb = 0;
-    if (!many && lane < p.n_seqs) {
+    if (lane < p.n_seqs) {
       q0 = cu_at(p.cu_q, lane, p.n_q);
       qb = cu_at(p.cu_q, lane + 1, p.n_q);
       k0 = cu_at(p.cu_k, lane, p.n_k);
@@ -171,47 +132,55 @@ struct LaneSeqs {
     }
     nq = qb - q0;
     nk = kb - k0;
-    bool wrong = q0 < 0 || k0 < 0 || nq < 0 || nk < 0 || qb > p.n_q || kb > p.n_k;
-    wrong = wrong || (!many && ((lane == 0 && (q0 != 0 || k0 != 0)) ||
-                                (lane == p.n_seqs - 1 && (qb != p.n_q || kb != p.n_k))));
-    bad = __any_sync(0xffffffffu, wrong);
+    bad = __any_sync(0xffffffffu,
+                     q0 < 0 || k0 < 0 || nq < 0 || nk < 0 || qb > p.n_q || kb > p.n_k ||
+                         (lane == 0 && (q0 != 0 || k0 != 0)) ||
+                         (lane == p.n_seqs - 1 && (qb != p.n_q || kb != p.n_k)));
   }
 };
 
-// All tiles (of `rows` queries, by_key: keys), or -1 for malformed arrays; by one warp.
-__device__ inline int64_t count_tiles(const Packed &p, const LaneSeqs &l, int32_t rows,
-                                      bool by_key) {
-  if (!l.many) {
-    if (l.bad) return -1;
-    return __reduce_add_sync(0xffffffffu, ((by_key ? l.nk : l.nq) + rows - 1) / rows);
-  }
-  const int lane = threadIdx.x & 31;
-  bool bad = cu_at(p.cu_q, 0, p.n_q) != 0 || cu_at(p.cu_k, 0, p.n_k) != 0 ||
-             cu_at(p.cu_q, p.n_seqs, p.n_q) != p.n_q || cu_at(p.cu_k, p.n_seqs, p.n_k) != p.n_k;
-  int mine = 0;
-  for (int s = lane; s < p.n_seqs; s += 32) {
-    const int qa = cu_at(p.cu_q, s, p.n_q), qb = cu_at(p.cu_q, s + 1, p.n_q);
-    const int ka = cu_at(p.cu_k, s, p.n_k), kb = cu_at(p.cu_k, s + 1, p.n_k);
-    bad = bad || qb < qa || kb < ka || qa < 0 || ka < 0 || qb > p.n_q || kb > p.n_k;
-    if (!bad) mine += ((by_key ? kb - ka : qb - qa) + rows - 1) / rows;
-  }
-  if (__any_sync(0xffffffffu, bad)) return -1;
-  return __reduce_add_sync(0xffffffffu, mine);
+// All tiles of a kind, or -1 for malformed arrays; by one warp.
+__device__ inline int32_t count_tiles(const Packed &p, const LaneSeqs &l, TileKind kind) {
+  if (l.many) return p.before[kind][p.n_seqs];
+  if (l.bad) return -1;
+  return __reduce_add_sync(
+      0xffffffffu, ((p.by_key[kind] ? l.nk : l.nq) + p.rows[kind] - 1) / p.rows[kind]);
 }
 
 // Tile `index` of all sequences, by one warp: every sequence's tile 0, then every
-// sequence's tile 1, and so on (up to 32 sequences; more of them in sequence order,
-// where a sequence is a small part of the whole anyway).  Callers count tiles from
-// the end of a sequence that has the most work.
-__device__ inline SeqTile ordered_tile(const Packed &p, const LaneSeqs &l, int32_t rows,
-                                       bool by_key, int64_t index) {
-  if (l.many)
-    return find_seq_tile(p.cu_q, p.cu_k, p.n_seqs, p.n_q, p.n_k, rows, by_key, index);
-  const int tiles = ((by_key ? l.nk : l.nq) + rows - 1) / rows;
+// sequence's tile 1, and so on (more than 32 sequences: in sequence order, where a
+// sequence is a small part of the whole anyway).  Callers count tiles from the end
+// of a sequence that has the most work.
+__device__ inline SeqTile ordered_tile(const Packed &p, const LaneSeqs &l, TileKind kind,
+                                       int32_t index) {
+  const int lane = threadIdx.x & 31;
+  SeqTile r;
+  r.bad = 0;
+  if (l.many) {
+    // the last sequence with at most `index` tiles before it, 32 probes a step
+    const int32_t *before = p.before[kind];
+    int32_t lo = 0, hi = p.n_seqs;
+    while (hi - lo > 1) {
+      const int32_t step = (hi - lo + 31) / 32, at = lo + lane * step;
+      const unsigned le =
+          __ballot_sync(0xffffffffu, at < hi && before[at < hi ? at : lo] <= index);
+      lo += (31 - __clz(le)) * step;     // lane 0 always holds
+      hi = lo + step < hi ? lo + step : hi;
+    }
+    r.seq = lo;
+    r.tile = index - before[lo];
+    r.n_tiles = before[lo + 1] - before[lo];
+    r.q0 = cu_at(p.cu_q, lo, p.n_q);
+    r.nq = cu_at(p.cu_q, lo + 1, p.n_q) - r.q0;
+    r.k0 = cu_at(p.cu_k, lo, p.n_k);
+    r.nk = cu_at(p.cu_k, lo + 1, p.n_k) - r.k0;
+    return r;
+  }
+  const int32_t tiles = ((p.by_key[kind] ? l.nk : l.nq) + p.rows[kind] - 1) / p.rows[kind];
   // the largest tile number with at most `index` tiles before it
   int lo = 0, s = 0;
   if (p.n_seqs == 1) {
-    lo = (int)index;
+    lo = index;
   } else {
     int hi = __reduce_max_sync(0xffffffffu, tiles);
     while (lo + 1 < hi) {
@@ -219,12 +188,10 @@ __device__ inline SeqTile ordered_tile(const Packed &p, const LaneSeqs &l, int32
       if (__reduce_add_sync(0xffffffffu, min(tiles, mid)) <= index) lo = mid;
       else hi = mid;
     }
-    const int rank = (int)(index - __reduce_add_sync(0xffffffffu, min(tiles, lo)));
+    const int rank = index - __reduce_add_sync(0xffffffffu, min(tiles, lo));
     const unsigned have = __ballot_sync(0xffffffffu, tiles > lo);
     s = __popc(have) > rank ? (int)__fns(have, 0, rank + 1) : -1;
   }
-  SeqTile r;
-  r.bad = 0;
   r.seq = s;
   r.tile = lo;
   const int from = max(s, 0);
@@ -238,14 +205,21 @@ __device__ inline SeqTile ordered_tile(const Packed &p, const LaneSeqs &l, int32
 
 // Tile and head of work item `index` of `tiles` * H.  Items run in groups of as many
 // heads as fill the SMs once, inside a group tile by tile.
-__device__ inline SeqTile place_item(const Packed &p, const LaneSeqs &l, int32_t rows, bool by_key,
+__device__ inline SeqTile place_item(const Packed &p, const LaneSeqs &l, TileKind kind,
                                      int64_t tiles, int64_t index, int *head) {
   const int64_t fill = p.sms / tiles, group = fill > 1 ? fill : 1;
   const int64_t g = index / (tiles * group), left = p.H - g * group;
   const int64_t heads = group < left ? group : left, in = index - g * tiles * group;
   *head = (int)(g * group + in % heads);
-  return ordered_tile(p, l, rows, by_key, in / heads);
+  return ordered_tile(p, l, kind, (int32_t)(in / heads));
 }
 #endif
+
+#ifdef __CUDACC__
+// Fills the `before` arrays (and the status) of a call with more than kLaneSeqs
+// sequences: one kernel before the others.  `mem`: plan_bytes().
+cudaError_t launch_latent_plan(Packed &p, void *mem, DeviceStatus *status, cudaStream_t stream);
+#endif
+size_t latent_plan_bytes(int32_t n_seqs);
 
 }  // namespace kda

@@ -134,7 +134,7 @@ int kda_latent_fwd_workspace_size(int32_t n_seqs, int64_t n_q, int64_t n_k, int3
   if (!bytes) return KDA_ERR_INVALID_ARG;
   const int d = check_sizes(n_seqs, n_q, n_k, H, dk, dr, dv, dtype);
   if (d != KDA_OK) return d;
-  *bytes = base_bytes(n_seqs) + round_up(kda::latent_fwd_scratch_bytes(n_q, n_k, H), 256);
+  *bytes = base_bytes(n_seqs) + round_up(kda::latent_fwd_scratch_bytes(n_seqs, n_q, n_k, H), 256);
   return KDA_OK;
 }
 
@@ -159,7 +159,7 @@ int kda_latent_fwd(const void *q, const void *k, const void *v, const void *k_ro
                       {k_rope, (size_t)n_k * dr * 2}};
   const Range outs[] = {{out, rows * dv * 2}, {lse, rows * 4}};
   if (any_overlap(in, outs)) return KDA_ERR_INVALID_ARG;
-  const size_t scratch = round_up(kda::latent_fwd_scratch_bytes(n_q, n_k, H), 256);
+  const size_t scratch = round_up(kda::latent_fwd_scratch_bytes(n_seqs, n_q, n_k, H), 256);
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < base_bytes(n_seqs) + scratch)
     return KDA_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -716,16 +716,16 @@ kda_latent_bwd_kernel(const __grid_constant__ Maps maps, const Params p) {
     f.seq = -1;
     int head = 0;
     const LaneSeqs seqs(p);
-    const int64_t nk = count_tiles(p, seqs, kX, true), nq = count_tiles(p, seqs, kX, false);
+    const int64_t nk = count_tiles(p, seqs, kTileB), nq = count_tiles(p, seqs, kTileA);
     const int64_t b = blockIdx.x, first_q = nk * p.H;
     const bool keys = nk >= 0 && b < first_q;
     if (nk < 0) {
       if (p.n_q == 0 && b == 0 && threadIdx.x == 0)      // no kernel before this one
         set_device_status(p.status, KDA_ERR_INVALID_ARG, 1);
     } else if (keys) {
-      f = place_item(p, seqs, kX, true, nk, b, &head);
+      f = place_item(p, seqs, kTileB, nk, b, &head);
     } else if (b < first_q + nq * p.H) {
-      f = place_item(p, seqs, kX, false, nq, b - first_q, &head);
+      f = place_item(p, seqs, kTileA, nq, b - first_q, &head);
     }
     if (threadIdx.x == 0) {
       s_tile = f;
@@ -765,8 +765,12 @@ kda_latent_stat_kernel(const __nv_bfloat16 *__restrict__ out,
   const int tid = threadIdx.x, head = blockIdx.y;
   pdl_launch_dependents();
   if (tid < 32) {
-    const SeqTile f =
-        find_seq_tile(p.cu_q, p.cu_k, p.n_seqs, p.n_q, p.n_k, kY, false, blockIdx.x);
+    const LaneSeqs seqs(p);
+    const int32_t tiles = count_tiles(p, seqs, kTileC);
+    SeqTile f;
+    f.seq = -1;
+    if ((int32_t)blockIdx.x < tiles) f = ordered_tile(p, seqs, kTileC, (int32_t)blockIdx.x);
+    f.bad = tiles < 0;
     if (tid == 0) st = f;
   }
   __syncthreads();
@@ -852,12 +856,19 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
   Params p;
   p.cu_q = a.cu_q; p.cu_k = a.cu_k; p.n_seqs = a.n_seqs; p.H = a.H; p.n_q = a.n_q; p.n_k = a.n_k;
   p.sms = sm_count();
+  p.rows[kTileA] = kX; p.by_key[kTileA] = false;
+  p.rows[kTileB] = kX; p.by_key[kTileB] = true;
+  p.rows[kTileC] = kY; p.by_key[kTileC] = false;
+  cudaError_t e = launch_latent_plan(p, a.scratch, a.status, stream);
+  if (e != cudaSuccess) return e;
   p.stat_rows = stat_rows(a.n_q, a.n_seqs);
   p.scale = a.scale; p.scale2 = a.scale * kLog2e; p.causal = a.causal;
   p.dq = static_cast<__nv_bfloat16 *>(a.dq); p.dk = static_cast<__nv_bfloat16 *>(a.dk);
   p.dv = static_cast<__nv_bfloat16 *>(a.dv);
   p.dk_ts = a.dk_ts; p.dk_hs = a.dk_hs; p.dv_ts = a.dv_ts; p.dv_hs = a.dv_hs;
-  float *lse2 = static_cast<float *>(a.scratch), *delta = lse2 + p.stat_rows * a.H;
+  float *lse2 = reinterpret_cast<float *>(static_cast<unsigned char *>(a.scratch) +
+                                          latent_plan_bytes(a.n_seqs));
+  float *delta = lse2 + p.stat_rows * a.H;
   p.lse2 = lse2; p.delta = delta; p.rope = delta + p.stat_rows * a.H;
   p.status = a.status;
   // as many items as there can be (one sequence: exactly that many)
@@ -865,8 +876,7 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
   const int64_t blocks = (most(a.n_k) + most(a.n_q)) * a.H;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   auto kernel = kda_latent_bwd_kernel<DR>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kSmem);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   if (a.n_q > 0) {
     const dim3 grid((unsigned)(a.n_q / kY + a.n_seqs), (unsigned)a.H);
@@ -903,7 +913,7 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
 }  // namespace
 
 size_t latent_bwd_scratch_bytes(int32_t n_seqs, int64_t n_q, int64_t n_k, int32_t H, int32_t dr) {
-  return (size_t)H * sizeof(float) * (2 * (size_t)stat_rows(n_q, n_seqs) + (size_t)n_k * dr);
+  return latent_plan_bytes(n_seqs) + (size_t)H * sizeof(float) * (2 * (size_t)stat_rows(n_q, n_seqs) + (size_t)n_k * dr);
 }
 
 cudaError_t launch_latent_bwd(const LatentArgs &a, cudaStream_t stream) {

@@ -133,15 +133,15 @@ __device__ inline Item find_item(const Params &p, int64_t block) {
   it.head = it.part = it.slot = 0;
   it.parts = 1;
   const LaneSeqs seqs(p);
-  const int64_t tiles = count_tiles(p, seqs, kRows, false);
+  const int64_t tiles = count_tiles(p, seqs, kTileA);
   if (tiles < 0) it.tile.bad = 1;
   if (tiles <= 0) return it;
   const Rounds r(p, tiles * p.H);
   if (block < r.whole) {
-    it.tile = place_item(p, seqs, kRows, false, tiles, block, &it.head);
+    it.tile = place_item(p, seqs, kTileA, tiles, block, &it.head);
   } else if (block - r.whole < (int64_t)r.rest * r.ways) {
     it.slot = (int)(block - r.whole);
-    it.tile = place_item(p, seqs, kRows, false, tiles, r.whole + it.slot / r.ways, &it.head);
+    it.tile = place_item(p, seqs, kTileA, tiles, r.whole + it.slot / r.ways, &it.head);
     it.part = it.slot % r.ways;
     it.parts = parts_of(it.tile, r.ways, p.causal);
     if (it.part >= it.parts) it.tile.seq = -1;
@@ -206,8 +206,8 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = m.tmem;
-  const Item item = m.item;
-  const SeqTile st = item.tile;
+  const Item &item = m.item;             // read where needed, not kept in registers
+  const SeqTile &st = item.tile;
   const int head = item.head;
   // every block sees a malformed array; block 0 says so, or clears the status (a
   // wait that gives up does so seconds later)
@@ -562,12 +562,12 @@ __global__ void __launch_bounds__(256) kda_latent_fwd_join_kernel(const Params p
     it.parts = 1;
     int ways = 1;
     const LaneSeqs seqs(p);
-    const int64_t tiles = count_tiles(p, seqs, kRows, false);
+    const int64_t tiles = count_tiles(p, seqs, kTileA);
     if (tiles > 0) {
       const Rounds r(p, tiles * p.H);
       ways = r.ways;
       if ((int)blockIdx.y < r.rest) {
-        it.tile = place_item(p, seqs, kRows, false, tiles, r.whole + blockIdx.y, &it.head);
+        it.tile = place_item(p, seqs, kTileA, tiles, r.whole + blockIdx.y, &it.head);
         it.parts = parts_of(it.tile, r.ways, p.causal);
       }
     }
@@ -652,10 +652,17 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
   Params p;
   p.cu_q = a.cu_q; p.cu_k = a.cu_k; p.n_seqs = a.n_seqs; p.H = a.H;
   p.sms = max(1, sm_count());
+  p.rows[kTileA] = kRows;
+  p.by_key[kTileA] = false;
+  p.rows[kTileB] = p.rows[kTileC] = 0;
+  p.n_q = a.n_q; p.n_k = a.n_k;
+  e = launch_latent_plan(p, a.scratch, a.status, stream);
+  if (e != cudaSuccess) return e;
+  unsigned char *parts = static_cast<unsigned char *>(a.scratch) + latent_plan_bytes(a.n_seqs);
   p.split = may_split(a.n_k) && p.sms > 1;
-  p.part_ml = static_cast<float *>(a.scratch);
+  p.part_ml = reinterpret_cast<float *>(parts);
   p.part_o = p.part_ml + (int64_t)p.sms * 2 * 256;
-  p.n_q = a.n_q; p.n_k = a.n_k; p.scale2 = a.scale * kLog2e; p.causal = a.causal;
+  p.scale2 = a.scale * kLog2e; p.causal = a.causal;
   p.out = static_cast<__nv_bfloat16 *>(a.out); p.lse = a.lse; p.status = a.status;
   // as many items as there can be (one sequence: exactly that many), and the parts
   const int64_t tiles = a.n_seqs == 1 ? (a.n_q + kRows - 1) / kRows : a.n_q / kRows + a.n_seqs;
@@ -678,11 +685,12 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
 
 }  // namespace
 
-size_t latent_fwd_scratch_bytes(int64_t n_q, int64_t n_k, int32_t H) {
+size_t latent_fwd_scratch_bytes(int32_t n_seqs, int64_t n_q, int64_t n_k, int32_t H) {
   (void)H;
-  if (n_q == 0 || !may_split(n_k)) return 0;
+  const size_t plan = latent_plan_bytes(n_seqs);
+  if (n_q == 0 || !may_split(n_k)) return plan;
   const int sms = sm_count();
-  return (size_t)(sms > 1 ? sms : 1) * 2 * (256 + 128 * kLatentD) * sizeof(float);
+  return plan + (size_t)(sms > 1 ? sms : 1) * 2 * (256 + 128 * kLatentD) * sizeof(float);
 }
 
 cudaError_t launch_latent_fwd(const LatentArgs &a, cudaStream_t stream) {

@@ -93,6 +93,40 @@ def test_long_sequence():
     check_both(_problem([1500], [1700], H=1, dr=64))
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dr", [0, 64])
+@pytest.mark.parametrize("lens", [([3], [5000]), ([300, 1], [2500, 4100]), ([257], [1100])])
+def test_few_queries_over_many_keys(lens, dr, causal):
+    """Few work items: their keys are shared out over several CTAs and joined."""
+    check_both(_problem(*lens, H=2, dr=dr), causal=causal)
+
+
+@pytest.mark.parametrize("n", [31, 32, 33, 700, 2500])
+def test_sequence_counts(n):
+    """Up to 32 sequences are found in a warp's lanes, more through a table."""
+    lens_q = [(5 * i) % 13 for i in range(n)]
+    lens_k = [q + (3 * i) % 7 for i, q in enumerate(lens_q)]
+    lens_q[n // 2], lens_k[n // 2] = 300, 420
+    check_both(_problem(lens_q, lens_k, H=1, dr=64 if n % 2 else 0))
+
+
+def test_graph_of_both_directions():
+    x = _problem([100, 300], [100, 300], H=2, dr=64)
+    d_out = _randn(400, 2, 128, seed=3)
+    want = _fwd(x)
+    want_g = _bwd(x, *want, d_out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = _fwd(x)
+        grads = _bwd(x, out, lse, d_out)
+    for t in (out, lse, *grads):
+        t.zero_()
+    graph.replay()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    for a, b in zip(want_g, grads):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("scale", [0.5, 1e-3, 3.0])
 def test_scales(scale):
     check_both(_problem([130, 200], [130, 400], H=2, dr=64), scale=scale)
@@ -173,6 +207,36 @@ def test_bad_cu_seqlens_are_reported():
     x["cu_q"] = x["cu_q"].cpu()
     with pytest.raises(pkg.KDAError):
         _fwd(x, out=out, workspace=ws)
+
+
+@pytest.mark.parametrize("n", [5, 100])
+@pytest.mark.parametrize("which", ["cu_q", "cu_k"])
+@pytest.mark.parametrize("how", ["first", "order", "last", "past"])
+def test_malformed_cu_seqlens(n, which, how):
+    from gated_delta_rule_13_gb300 import kda
+    x = _problem([7] * n, [7] * n, H=2, dr=64)
+    out, lse = _fwd(x)
+    bad = x[which].clone()
+    if how == "first":
+        bad[0] = 1
+    elif how == "order":
+        bad[3] = 7 * n
+    elif how == "last":
+        bad[n] -= 1
+    else:
+        bad[n // 2] = 1 << 30
+    y = dict(x, **{which: bad})
+    ws = torch.empty(1 << 25, dtype=torch.uint8, device=DEV)
+    keep = torch.full_like(out, 3.0)
+    _fwd(y, out=keep, workspace=ws)
+    assert kda.kda_read_device_status(ws) == kda.KDA_ERR_INVALID_ARG
+    assert bool((keep == 3.0).all())
+    g = torch.full((2, 7 * n, 2, 128), 3.0, device=DEV).bfloat16()
+    _bwd(y, out, lse, out, d_k=g[0], d_v=g[1], workspace=ws)
+    assert kda.kda_read_device_status(ws) == kda.KDA_ERR_INVALID_ARG
+    assert bool((g == 3.0).all())
+    _fwd(x, workspace=ws)
+    assert kda.kda_read_device_status(ws) == kda.KDA_OK
 
 
 def test_keys_past_two_to_the_31_elements():
