@@ -876,8 +876,7 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
   const int64_t blocks = (most(a.n_k) + most(a.n_q)) * a.H;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   auto kernel = kda_latent_bwd_kernel<DR>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
+  if (!kernel_ready<kda_latent_bwd_kernel<DR>>(kSmem, 0)) return cudaErrorNotSupported;
   if (a.n_q > 0) {
     const dim3 grid((unsigned)(a.n_q / kY + a.n_seqs), (unsigned)a.H);
     kda_latent_stat_kernel<<<grid, kStatThreads, 0, stream>>>(

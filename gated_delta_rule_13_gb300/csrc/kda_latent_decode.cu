@@ -772,9 +772,10 @@ kda_latent_join_kernel(const Params p) {
     p.lse[out_row] = l == 0.f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
 }
 
-// Pairs of CTAs the device runs at once (0 without a device), asked once.
+// Pairs of CTAs the device runs at once (0 without a device).
 int resident_pairs() {
-  static const int pairs = [] {
+  static std::atomic<int> cache[kMaxDevices];
+  return per_device(cache, [](int) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(kThreads);
@@ -787,15 +788,13 @@ int resident_pairs() {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaFuncSetAttribute(kda_latent_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmem) != cudaSuccess ||
+    if (!kernel_ready<kda_latent_decode_kernel>(kSmem, 0) ||
         cudaOccupancyMaxActiveClusters(&n, kda_latent_decode_kernel, &cfg) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
     }
     return n;
-  }();
-  return pairs;
+  });
 }
 
 struct Plan {

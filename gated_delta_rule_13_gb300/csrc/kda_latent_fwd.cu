@@ -641,14 +641,9 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
       (DR && !make_bf16_map(&mr, a.n_k > 0 ? a.k_rope : any, 2, rd, rs, br)))
     return cudaErrorInvalidValue;
   auto kernel = kda_latent_fwd_kernel<DR>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       smem_bytes<DR>());
-  if (e != cudaSuccess) return e;
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, kernel);
-  if (e != cudaSuccess) return e;
   // the register split must not exceed what the block is launched with
-  if ((uint32_t)fa.numRegs < kLaunchRegs) return cudaErrorNotSupported;
+  if (!kernel_ready<kda_latent_fwd_kernel<DR>>(smem_bytes<DR>(), kLaunchRegs))
+    return cudaErrorNotSupported;
   Params p;
   p.cu_q = a.cu_q; p.cu_k = a.cu_k; p.n_seqs = a.n_seqs; p.H = a.H;
   p.sms = max(1, sm_count());
@@ -656,7 +651,7 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
   p.by_key[kTileA] = false;
   p.rows[kTileB] = p.rows[kTileC] = 0;
   p.n_q = a.n_q; p.n_k = a.n_k;
-  e = launch_latent_plan(p, a.scratch, a.status, stream);
+  cudaError_t e = launch_latent_plan(p, a.scratch, a.status, stream);
   if (e != cudaSuccess) return e;
   unsigned char *parts = static_cast<unsigned char *>(a.scratch) + latent_plan_bytes(a.n_seqs);
   p.split = may_split(a.n_k) && p.sms > 1;

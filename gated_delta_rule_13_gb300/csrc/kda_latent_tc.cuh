@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/kda.h"
 #include "kda_latent.h"
 #include "kda_sm100.cuh"
@@ -185,14 +187,52 @@ inline bool make_bf16_map(CUtensorMap *map, const void *base, uint32_t rank,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-inline int sm_count() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+// What the host asks of a device is asked once for each (a launch takes a few
+// microseconds, and each of these calls one): value(device) for the current device.
+constexpr int kMaxDevices = 64;
+template <class F>
+inline int per_device(std::atomic<int> (&cache)[kMaxDevices], F value) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
-  return sms;
+  if (dev < 0 || dev >= kMaxDevices) return value(dev);
+  int v = cache[dev].load(std::memory_order_relaxed);
+  if (v == 0) {
+    v = value(dev);
+    cache[dev].store(v, std::memory_order_relaxed);
+  }
+  return v;
+}
+
+inline int sm_count() {
+  static std::atomic<int> cache[kMaxDevices];
+  return per_device(cache, [](int dev) {
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      cudaGetLastError();
+      sms = 0;
+    }
+    return sms;
+  });
+}
+
+// The kernel may use `bytes` of dynamic shared memory and is launched with `regs`
+// registers a thread at least (0: any).
+template <auto kKernel>
+inline bool kernel_ready(int bytes, int regs) {
+  static std::atomic<int> cache[kMaxDevices];
+  return per_device(cache, [=](int) {
+    cudaFuncAttributes fa;
+    if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+            cudaSuccess ||
+        cudaFuncGetAttributes(&fa, kKernel) != cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+    return fa.numRegs >= regs ? 1 : 0;
+  }) == 1;
 }
 
 }  // namespace latent
