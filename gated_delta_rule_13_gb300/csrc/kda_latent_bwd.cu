@@ -5,21 +5,17 @@
 //   delta_i = do_i . o_i
 //   dv_j = sum_i p_ij do_i,  dk_j = scale sum_i ds_ij q_i,  dq_i = scale sum_j ds_ij k_j
 //
-// Two passes of one shape in one launch, each output element owned by one CTA
-// (no atomics, so the result does not depend on the order of execution; the price
-// is that s and dp are computed twice, 1152 multiply-adds a pair at dr = 64
-// instead of 832).  A CTA keeps 128 rows X1, X2 in shared memory and streams
-// tiles of 64 rows Y1, Y2 past them:
+// Two passes in one launch, each output element owned by one CTA (no atomics, so the
+// result does not depend on the order of execution; the price is that s and dp are
+// computed twice, 1,152 multiply-adds a pair at dr = 64 instead of 832).  A CTA keeps
+// 128 rows X1, X2 and streams tiles of rows Y1, Y2 past them:
 //   S  = X1 Y1^T,  dP = X2 Y2^T              (fp32, TMEM)
 //   P  = exp2(S scale log2e - lse log2e),  dS = P (dP - delta)
 //   A1 += dS Y1,   A2 += P Y2                (fp32, TMEM, over all tiles)
-// keys pass:    X = (keys, values), Y = (queries, d_out): A1 = dk, A2 = dv
-// queries pass: X = (queries, d_out), Y = (keys, values): A1 = dq
-// P and dS are bf16 operands in TMEM, over the columns they were computed from.
-// A1 (192 columns) and A2 (128) leave 192 columns: two S buffers and one dP, so the
-// tensor cores run S two tiles ahead and dP one ahead of the elementwise work.
-// A tile costs 1,600 (keys) and 1,344 (queries) cycles of the tensor cores at
-// dr = 64; the elementwise work (64 x 128 exponentials) hides behind it.
+// keys pass:    X = (keys, values), Y = (queries, d_out), 64 rows: A1 = dk, A2 = dv
+// queries pass: X = (queries, d_out), Y = (keys, values), 128 rows: A1 = dq
+// P and dS are rounded to bf16 (half a step, 2^-8 of the value): they are operands of
+// the tensor cores, in TMEM over the columns they were computed from.
 //
 // The rotary key is shared by the heads: every head leaves its fp32 gradient in
 // the workspace and a last kernel adds them in head order.
@@ -43,7 +39,7 @@ constexpr uint32_t kXBlock = 16384, kYBlock = 8192;  // 128 or 64 rows x 64 chan
 
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages], s_full[2];
-  uint64_t x_full, dp_full, ds_ready, clean_req, clean, acc_full, fin;
+  uint64_t x_full, dp_full, p_ready[2], ds_ready, clean_req, clean, acc_full, fin;
   int abort, loaded;
   alignas(16) float lse2[kMaxStages][kY];
   float delta[kMaxStages][kY];
@@ -83,7 +79,7 @@ struct Params : Packed {
 __host__ __device__ inline int64_t stat_tile(int64_t q0, int64_t s) { return q0 / kY + s; }
 
 struct Maps {
-  CUtensorMap q128, q64, g128, g64, k128, k64, v128, v64, r128, r64;
+  CUtensorMap q128, q64, g128, g64, k128, v128, r128;
 };
 
 // The 64 columns at `col` of this warpgroup's 128 accumulator rows, times `mul`, as
@@ -122,10 +118,13 @@ __device__ __forceinline__ void store_cols(uint32_t col, float mul, bool zero,
   __syncwarp();
 }
 
+// The keys pass: X = 128 keys and their values.  A1 (192 columns) and A2 (128) leave 192
+// columns of TMEM: two S buffers and one dP, so the tensor cores run S two tiles ahead
+// and dP one ahead of the elementwise work.  Tiles of 64 queries: with the 80 KB of X,
+// 96 of them fit shared memory only once, and S and dP would need 288 columns.
 template <int DR>
 __device__ __forceinline__ void keys_pass(const Maps &maps, const Params &p, const SeqTile &st, int head,
                                           uint32_t base, uint32_t tm, Shared &m) {
-  constexpr bool kKeys = true;
   constexpr int KB = (kLatentD + DR) / 64, ST = stages<DR>();
   constexpr uint32_t kStage = x_bytes<DR>();
   constexpr int N1 = kLatentD + DR;
@@ -144,6 +143,8 @@ __device__ __forceinline__ void keys_pass(const Maps &maps, const Params &p, con
     mbar_init(&m.s_full[1], 1);
     mbar_init(&m.x_full, 1);
     mbar_init(&m.dp_full, 1);
+    mbar_init(&m.p_ready[0], 8);
+    mbar_init(&m.p_ready[1], 8);
     mbar_init(&m.ds_ready, 8);
     mbar_init(&m.clean_req, 1);
     mbar_init(&m.clean, 1);
@@ -154,42 +155,36 @@ __device__ __forceinline__ void keys_pass(const Maps &maps, const Params &p, con
     fence_mbarrier_init();
   }
   if (warp == kLoadWarp && lane == 0) {
-    prefetch_tensormap(kKeys ? &maps.k128 : &maps.q128);
-    prefetch_tensormap(kKeys ? &maps.v128 : &maps.g128);
-    prefetch_tensormap(kKeys ? &maps.q64 : &maps.k64);
-    prefetch_tensormap(kKeys ? &maps.g64 : &maps.v64);
-    if (DR) prefetch_tensormap(kKeys ? &maps.r128 : &maps.r64);
+    prefetch_tensormap(&maps.k128);
+    prefetch_tensormap(&maps.v128);
+    prefetch_tensormap(&maps.q64);
+    prefetch_tensormap(&maps.g64);
+    if (DR) prefetch_tensormap(&maps.r128);
   }
   __syncthreads();
 
-  // The CTA's rows [x0, x0 + 128) of the sequence, longest first: the first keys are
-  // seen by the most queries, the last queries see the most keys.  It streams
-  // tiles [y_first, y_first + n) of 64.
-  const int x0 = (kKeys ? st.tile : st.n_tiles - 1 - st.tile) * kX;
-  const int nx = kKeys ? st.nk : st.nq, ny = kKeys ? st.nq : st.nk;
+  // The CTA's keys [x0, x0 + 128) of the sequence, longest first: the first keys are
+  // seen by the most queries.  It streams tiles [y_first, y_first + n) of 64 queries.
+  const int x0 = st.tile * kX;
+  const int ny = st.nq;
   const int shift = st.nk - st.nq;       // query i sees keys <= i + shift
-  int y_first = 0, y_end = ny;
-  if (p.causal) {
-    if (kKeys) y_first = max(0, x0 - shift) / kY;
-    else y_end = min(ny, min(x0 + kX, nx) + shift);
-  }
-  int n = y_end > 0 ? (y_end + kY - 1) / kY - y_first : 0;
+  const int y_first = p.causal ? max(0, x0 - shift) / kY : 0;
+  int n = (ny + kY - 1) / kY - y_first;
   if (st.seq < 0 || n < 0) n = 0;
   const int live = min(kY, ny - (y_first + n - 1) * kY);  // rows of the last tile
   const WaitCtx cx{&m.abort, p.status, (int)blockIdx.x};
 
   if (warp == kLoadWarp && lane == 0 && n > 0) {
     // ---- loader
-    const int xr = (kKeys ? st.k0 : st.q0) + x0;
+    const int xr = st.k0 + x0;
     mbar_arrive_expect_tx(&m.x_full, (KB + 2) * kXBlock);
     for (int kb = 0; kb < KB; ++kb) {
       const uint32_t dst = base + kb * kXBlock;
-      if (!kKeys) tma_load_3d_u(dst, &maps.q128, &m.x_full, 64 * kb, head, xr);
-      else if (kb < 2) tma_load_3d_u(dst, &maps.k128, &m.x_full, 64 * kb, head, xr);
+      if (kb < 2) tma_load_3d_u(dst, &maps.k128, &m.x_full, 64 * kb, head, xr);
       else tma_load_2d(dst, &maps.r128, &m.x_full, 0, xr);
     }
     for (int c = 0; c < 2; ++c)
-      tma_load_3d_u(base + (KB + c) * kXBlock, kKeys ? &maps.v128 : &maps.g128, &m.x_full, 64 * c,
+      tma_load_3d_u(base + (KB + c) * kXBlock, &maps.v128, &m.x_full, 64 * c,
                     head, xr);
     bool ok = true;
     int i = 0;
@@ -197,22 +192,17 @@ __device__ __forceinline__ void keys_pass(const Maps &maps, const Params &p, con
       const int s = i % ST;
       if (i >= ST) ok = wait_or_abort(cx, &m.empty[s], (i / ST - 1) & 1, 10, i);
       if (!ok) break;
-      const int yr = (kKeys ? st.q0 : st.k0) + (y_first + i) * kY;
+      const int yr = st.q0 + (y_first + i) * kY;
       const uint32_t dst = base + kStage + s * stage_bytes<DR>();
-      mbar_arrive_expect_tx(&m.full[s], stage_bytes<DR>() + (kKeys ? 2 * kY * 4 : 0));
-      for (int kb = 0; kb < KB; ++kb) {
-        if (kKeys) tma_load_3d_u(dst + kb * kYBlock, &maps.q64, &m.full[s], 64 * kb, head, yr);
-        else if (kb < 2) tma_load_3d_u(dst + kb * kYBlock, &maps.k64, &m.full[s], 64 * kb, head, yr);
-        else tma_load_2d(dst + kb * kYBlock, &maps.r64, &m.full[s], 0, yr);
-      }
+      mbar_arrive_expect_tx(&m.full[s], stage_bytes<DR>() + 2 * kY * 4);
+      for (int kb = 0; kb < KB; ++kb)
+        tma_load_3d_u(dst + kb * kYBlock, &maps.q64, &m.full[s], 64 * kb, head, yr);
       for (int c = 0; c < 2; ++c)
-        tma_load_3d_u(dst + (KB + c) * kYBlock, kKeys ? &maps.g64 : &maps.v64, &m.full[s], 64 * c,
+        tma_load_3d_u(dst + (KB + c) * kYBlock, &maps.g64, &m.full[s], 64 * c,
                       head, yr);
-      if (kKeys) {
-        const int64_t at = head * p.stat_rows + (stat_tile(st.q0, st.seq) + y_first + i) * kY;
-        bulk_load(smem_u32(m.lse2[s]), p.lse2 + at, kY * 4, &m.full[s]);
-        bulk_load(smem_u32(m.delta[s]), p.delta + at, kY * 4, &m.full[s]);
-      }
+      const int64_t at = head * p.stat_rows + (stat_tile(st.q0, st.seq) + y_first + i) * kY;
+      bulk_load(smem_u32(m.lse2[s]), p.lse2 + at, kY * 4, &m.full[s]);
+      bulk_load(smem_u32(m.delta[s]), p.delta + at, kY * 4, &m.full[s]);
     }
     if (ok) mbar_arrive(&m.clean_req);
     m.loaded = i;
@@ -243,18 +233,24 @@ __device__ __forceinline__ void keys_pass(const Maps &maps, const Params &p, con
     int s0 = 0;                          // stage of tile i
     for (int i = 0; ok && i < n; ++i) {
       const int s1 = s0 + 1 == ST ? 0 : s0 + 1, s2 = s1 + 1 == ST ? 0 : s1 + 1;
-      ok = wait_or_abort(cx, &m.ds_ready, i & 1, 22, i);
+      // P Y2 while the elementwise warps are still at dS, which needs dP.  (P of the
+      // tile after the next may be ready before this wait: a barrier for each parity.)
+      ok = wait_or_abort(cx, &m.p_ready[i & 1], (i >> 1) & 1, 24, i);
       if (ok && i + 1 == n && live < kY) ok = wait_or_abort(cx, &m.clean, 0, 23, i);
       if (!ok) break;
       tc_fence_after();
       const uint32_t sb = tm + TM_S + 64 * (i & 1);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {  // bf16 columns: rows 0 .. 31 at +0, 32 .. 63 at +32
-        const uint32_t a = (k >> 1) * 32 + (k & 1) * 8;
-        if (kKeys)
-          umma_ts(tm + TM_A2, sb + a, y_a.at(s0 * SB + KB * kYBlock + k * 2048), ID_A2, i + k > 0);
-        umma_ts(tm + TM_A1, tm + TM_DP + a, y_a.at(s0 * SB + k * 2048), ID_A1, i + k > 0);
-      }
+      for (int k = 0; k < 4; ++k)  // bf16 columns: rows 0 .. 31 at +0, 32 .. 63 at +32
+        umma_ts(tm + TM_A2, sb + (k >> 1) * 32 + (k & 1) * 8,
+                y_a.at(s0 * SB + KB * kYBlock + k * 2048), ID_A2, i + k > 0);
+      ok = wait_or_abort(cx, &m.ds_ready, i & 1, 22, i);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        umma_ts(tm + TM_A1, tm + TM_DP + (k >> 1) * 32 + (k & 1) * 8, y_a.at(s0 * SB + k * 2048),
+                ID_A1, i + k > 0);
       umma_commit(&m.empty[s0]);
       if (i + 1 < n) issue_dp(s1);
       if (i + 2 < n) issue_s(i + 2, s2);
@@ -282,18 +278,8 @@ __device__ __forceinline__ void keys_pass(const Maps &maps, const Params &p, con
     const int wg = warp >> 2, xr = x0 + (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t col = 32 * wg;
-    float lse2 = 0.f, delta = 0.f;
-    if (!kKeys && st.seq >= 0 && xr < nx) {
-      const int64_t at = head * p.stat_rows + stat_tile(st.q0, st.seq) * kY + xr;
-      lse2 = p.lse2[at];
-      delta = p.delta[at];
-    }
-    // columns [lo, hi) of the streamed rows pair with this row
-    int lo = 0, hi = ny;
-    if (p.causal) {
-      if (kKeys) lo = max(0, xr - shift);
-      else hi = min(ny, xr + shift + 1);
-    }
+    // queries [lo, ny) see this row's key
+    const int lo = p.causal ? max(0, xr - shift) : 0;
     bool ok = true;
     for (int i = 0; ok && i < n; ++i) {
       ok = warp_wait(cx, &m.s_full[i & 1], (i >> 1) & 1, 40, i);
@@ -304,59 +290,49 @@ __device__ __forceinline__ void keys_pass(const Maps &maps, const Params &p, con
       tmem_ld32(ts, r);
       tmem_ld_wait(r);
       const int y0 = (y_first + i) * kY + (int)col;
-      const bool edge = __any_sync(0xffffffffu, y0 < lo || y0 + 32 > hi);
+      const bool edge = __any_sync(0xffffffffu, y0 < lo || y0 + 32 > ny);
       float pr[32];
-      if constexpr (kKeys) {
-        const uint32_t sl = smem_u32(&m.lse2[i % ST][col]);
+      const uint32_t sl = smem_u32(&m.lse2[i % ST][col]);
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 l = ld_shared_f32x4(sl + 4 * j);
-          pr[j] = ex2(fmaf(__uint_as_float(r[j]), p.scale2, -l.x));
-          pr[j + 1] = ex2(fmaf(__uint_as_float(r[j + 1]), p.scale2, -l.y));
-          pr[j + 2] = ex2(fmaf(__uint_as_float(r[j + 2]), p.scale2, -l.z));
-          pr[j + 3] = ex2(fmaf(__uint_as_float(r[j + 3]), p.scale2, -l.w));
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) pr[j] = ex2(fmaf(__uint_as_float(r[j]), p.scale2, -lse2));
+      for (int j = 0; j < 32; j += 4) {
+        const float4 l = ld_shared_f32x4(sl + 4 * j);
+        pr[j] = ex2(fmaf(__uint_as_float(r[j]), p.scale2, -l.x));
+        pr[j + 1] = ex2(fmaf(__uint_as_float(r[j + 1]), p.scale2, -l.y));
+        pr[j + 2] = ex2(fmaf(__uint_as_float(r[j + 2]), p.scale2, -l.z));
+        pr[j + 3] = ex2(fmaf(__uint_as_float(r[j + 3]), p.scale2, -l.w));
       }
       if (edge) {
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          if (y0 + j < lo || y0 + j >= hi) pr[j] = 0.f;
+          if (y0 + j < lo || y0 + j >= ny) pr[j] = 0.f;
       }
-      if constexpr (kKeys) {
-        uint32_t pk[16];
+      uint32_t pk[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(pr[2 * j], pr[2 * j + 1]);
-        tmem_st16(ts, pk);
-      }
+      for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(pr[2 * j], pr[2 * j + 1]);
+      tmem_st16(ts, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.p_ready[i & 1]);
       ok = warp_wait(cx, &m.dp_full, i & 1, 41, i);
       if (!ok) break;
       tc_fence_after();
       tmem_ld32(td, r);
       tmem_ld_wait(r);
-      if constexpr (kKeys) {
-        const uint32_t sd = smem_u32(&m.delta[i % ST][col]);
+      const uint32_t sd = smem_u32(&m.delta[i % ST][col]);
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 d = ld_shared_f32x4(sd + 4 * j);
-          r[j] = __float_as_uint(pr[j] * (__uint_as_float(r[j]) - d.x));
-          r[j + 1] = __float_as_uint(pr[j + 1] * (__uint_as_float(r[j + 1]) - d.y));
-          r[j + 2] = __float_as_uint(pr[j + 2] * (__uint_as_float(r[j + 2]) - d.z));
-          r[j + 3] = __float_as_uint(pr[j + 3] * (__uint_as_float(r[j + 3]) - d.w));
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          r[j] = __float_as_uint(pr[j] * (__uint_as_float(r[j]) - delta));
+      for (int j = 0; j < 32; j += 4) {
+        const float4 d = ld_shared_f32x4(sd + 4 * j);
+        r[j] = __float_as_uint(pr[j] * (__uint_as_float(r[j]) - d.x));
+        r[j + 1] = __float_as_uint(pr[j + 1] * (__uint_as_float(r[j + 1]) - d.y));
+        r[j + 2] = __float_as_uint(pr[j + 2] * (__uint_as_float(r[j + 2]) - d.z));
+        r[j + 3] = __float_as_uint(pr[j + 3] * (__uint_as_float(r[j + 3]) - d.w));
       }
       if (edge) {  // dP of a pair outside may be anything
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          if (y0 + j < lo || y0 + j >= hi) r[j] = 0;
+          if (y0 + j < lo || y0 + j >= ny) r[j] = 0;
       }
-      uint32_t pk[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j)
         pk[j] = pack_bf16x2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
@@ -374,41 +350,34 @@ __device__ __forceinline__ void keys_pass(const Maps &maps, const Params &p, con
     if (ok && st.seq >= 0) {
       const bool zero = n == 0;
       const uint32_t buf = base + warp * 8192, acc = tm + lanes;
-      const int rows = nx - x0, w4 = warp & 3;
-      if constexpr (kKeys) {
-        const int64_t kr = st.k0 + x0;
-        store_cols(acc + TM_A2 + 64 * wg, 1.f, zero, p.dv + kr * p.dv_ts + head * p.dv_hs + 64 * wg,
-                   p.dv_ts, rows, buf, w4, lane);
-        store_cols(acc + TM_A1 + 64 * wg, p.scale, zero,
-                   p.dk + kr * p.dk_ts + head * p.dk_hs + 64 * wg, p.dk_ts, rows, buf, w4, lane);
-        if (DR) {  // fp32, 32 columns a warpgroup
-          uint32_t o[32];
-          if (zero) {
+      const int rows = st.nk - x0, w4 = warp & 3;
+      const int64_t kr = st.k0 + x0;
+      store_cols(acc + TM_A2 + 64 * wg, 1.f, zero, p.dv + kr * p.dv_ts + head * p.dv_hs + 64 * wg,
+                 p.dv_ts, rows, buf, w4, lane);
+      store_cols(acc + TM_A1 + 64 * wg, p.scale, zero,
+                 p.dk + kr * p.dk_ts + head * p.dk_hs + 64 * wg, p.dk_ts, rows, buf, w4, lane);
+      if (DR) {  // fp32, 32 columns a warpgroup
+        uint32_t o[32];
+        if (zero) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0;
-          } else {
-            tmem_ld32(acc + TM_A1 + kLatentD + 32 * wg, o);
-            tmem_ld_wait(o);
-          }
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            st_shared_v4(buf + lane * 128 + ((q ^ (lane & 7)) << 4), o[4 * q], o[4 * q + 1],
-                         o[4 * q + 2], o[4 * q + 3]);
-          __syncwarp();
-          float *dst = p.rope + ((int64_t)head * p.n_k + kr + w4 * 32) * kLatentRope + 32 * wg;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int rr = 4 * k + (lane >> 3), piece = lane & 7;
-            const uint4 v = ld_shared_v4(buf + rr * 128 + ((piece ^ (rr & 7)) << 4));
-            if (w4 * 32 + rr < rows)
-              *reinterpret_cast<uint4 *>(dst + rr * kLatentRope + 4 * piece) = v;
-          }
+          for (int j = 0; j < 32; ++j) o[j] = 0;
+        } else {
+          tmem_ld32(acc + TM_A1 + kLatentD + 32 * wg, o);
+          tmem_ld_wait(o);
         }
-      } else {
-        const int64_t qr = st.q0 + x0;
-        for (int c = wg; c < KB; c += 2)
-          store_cols(acc + TM_A1 + 64 * c, p.scale, zero, p.dq + (qr * p.H + head) * N1 + 64 * c,
-                     (int64_t)p.H * N1, rows, buf, w4, lane);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          st_shared_v4(buf + lane * 128 + ((q ^ (lane & 7)) << 4), o[4 * q], o[4 * q + 1],
+                       o[4 * q + 2], o[4 * q + 3]);
+        __syncwarp();
+        float *dst = p.rope + ((int64_t)head * p.n_k + kr + w4 * 32) * kLatentRope + 32 * wg;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int rr = 4 * k + (lane >> 3), piece = lane & 7;
+          const uint4 v = ld_shared_v4(buf + rr * 128 + ((piece ^ (rr & 7)) << 4));
+          if (w4 * 32 + rr < rows)
+            *reinterpret_cast<uint4 *>(dst + rr * kLatentRope + 4 * piece) = v;
+        }
       }
     }
   }
@@ -845,13 +814,12 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
   const cuuint64_t vs[2] = {(cuuint64_t)a.v_hs * 2, (cuuint64_t)a.v_ts * 2};
   const cuuint64_t rd[2] = {64, nk}, rs[1] = {128};
   const cuuint32_t b128[3] = {64, 1, 128}, b64[3] = {64, 1, 64};
-  const cuuint32_t r128[2] = {64, 128}, r64[2] = {64, 64};
+  const cuuint32_t r128[2] = {64, 128};
   if (!make_bf16_map(&mp.q128, q, 3, qd, qs, b128) || !make_bf16_map(&mp.q64, q, 3, qd, qs, b64) ||
       !make_bf16_map(&mp.g128, g, 3, gd, gs, b128) || !make_bf16_map(&mp.g64, g, 3, gd, gs, b64) ||
-      !make_bf16_map(&mp.k128, k, 3, kd, ks, b128) || !make_bf16_map(&mp.k64, k, 3, kd, ks, b64) ||
-      !make_bf16_map(&mp.v128, v, 3, kd, vs, b128) || !make_bf16_map(&mp.v64, v, 3, kd, vs, b64) ||
-      (DR && (!make_bf16_map(&mp.r128, r, 2, rd, rs, r128) ||
-              !make_bf16_map(&mp.r64, r, 2, rd, rs, r64))))
+      !make_bf16_map(&mp.k128, k, 3, kd, ks, b128) ||
+      !make_bf16_map(&mp.v128, v, 3, kd, vs, b128) ||
+      (DR && !make_bf16_map(&mp.r128, r, 2, rd, rs, r128)))
     return cudaErrorInvalidValue;
   Params p;
   p.cu_q = a.cu_q; p.cu_k = a.cu_k; p.n_seqs = a.n_seqs; p.H = a.H; p.n_q = a.n_q; p.n_k = a.n_k;
