@@ -40,8 +40,8 @@ namespace {
 using namespace latent;
 
 constexpr int kRows = 256, kKeys = 128;
-constexpr int kThreads = 384;            // two softmax warpgroups; loader, MMA, cleaner, spare
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
+constexpr int kThreads = 384;            // two softmax warpgroups; loader, MMA, cleaner, items
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kCleanWarp = 10, kItemWarp = 11;
 constexpr uint32_t kSlotBytes = 16384;
 constexpr uint32_t kSmemMax = 232448;
 constexpr float kSlack = 8.f;            // log2 units a score may exceed its reference by
@@ -52,22 +52,27 @@ constexpr int kMaxSlots = 10;
 // A unit of the ring is a key tile (KB slots) or a value tile (2 slots); units are
 // loaded, used and released in the order K0 V0 K1 V1 .., so the barriers of eight
 // consecutive units are enough (at most five are resident).
-constexpr int kUnits = 8;
+constexpr uint32_t kUnits = 8;
+constexpr int kItemUsers = 11;           // loader, MMA, cleaner, eight softmax warps
 
 // What a block works on: a tile of a sequence, a head, and part `part` of `parts` of
 // its keys; seq < 0: nothing.
 struct Item {
   SeqTile tile;
   int head, part, parts, slot;           // slot: of its partial results
+  int i0, n_iter, nt[2];                 // key tiles [i0, i0 + n_iter); of each query tile
+  int row0, last_live;                   // first query; keys of the last tile
 };
 
 struct Shared {
   uint64_t full[kUnits], empty[kUnits];
-  uint64_t q_full[2], s_full[2], p_ready[2][2], o_full[2], clean_req, clean, fin;
+  uint64_t q_full[2], q_free[2], s_full[2], p_ready[2][2], o_full[2], clean_req[2], clean[2];
+  uint64_t item_full[2], item_free[2], want, taken, fin;
+  alignas(16) uint32_t answer[4];
   uint32_t tmem;
-  int loaded;                              // units loaded
+  uint32_t loaded, loaded_q[2];                // units loaded, tiles of queries loaded
   int abort;
-  Item item;
+  Item item[2];
 };
 
 template <int DR>
@@ -82,6 +87,7 @@ constexpr uint32_t smem_bytes() {
   return 1024 + q_bytes<DR>() + slots<DR>() * kSlotBytes + sizeof(Shared);
 }
 
+constexpr int kAhead = 4;                // key tiles before an item's last, the next one is asked for
 constexpr int kMinPart = 4;              // key tiles of a part, at least
 
 struct Params : Packed {
@@ -146,6 +152,18 @@ __device__ inline Item find_item(const Params &p, int64_t block) {
     it.parts = parts_of(it.tile, r.ways, p.causal);
     if (it.part >= it.parts) it.tile.seq = -1;
   }
+  it.row0 = first_row(it.tile);
+  // Key tiles [i0, i0 + n_iter) of this part, and those of the two query tiles among
+  // them (the second never has fewer, unless it has no queries).
+  const int all0 = key_tiles(it.tile, it.row0, 0, p.causal);
+  const int all1 = key_tiles(it.tile, it.row0, 1, p.causal);
+  const int n_all = max(all0, all1);
+  it.i0 = (int)((int64_t)n_all * it.part / it.parts);
+  const int i1 = (int)((int64_t)n_all * (it.part + 1) / it.parts);
+  it.nt[0] = max(0, min(all0, i1) - it.i0);
+  it.nt[1] = max(0, min(all1, i1) - it.i0);
+  it.n_iter = i1 - it.i0;
+  it.last_live = min(kKeys, it.tile.nk - (i1 - 1) * kKeys);
   return it;
 }
 
@@ -169,27 +187,28 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
   Shared &m = *reinterpret_cast<Shared *>(tiles + kRing + S * kSlotBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  if (warp == kCleanWarp) {
-    const Item f = find_item(p, blockIdx.x);
-    if (lane == 0) m.item = f;
-  }
   if (tid == 0) {
-    for (int i = 0; i < kUnits; ++i) {
+    for (uint32_t i = 0; i < kUnits; ++i) {
       mbar_init(&m.full[i], 1);
       mbar_init(&m.empty[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&m.q_full[t], 1);
+      mbar_init(&m.q_free[t], 1);
       mbar_init(&m.s_full[t], 1);
       mbar_init(&m.p_ready[t][0], 4);
       mbar_init(&m.p_ready[t][1], 4);
       mbar_init(&m.o_full[t], 1);
+      mbar_init(&m.clean_req[t], 1);
+      mbar_init(&m.clean[t], 1);
+      mbar_init(&m.item_full[t], 1);
+      mbar_init(&m.item_free[t], kItemUsers);
     }
-    mbar_init(&m.clean_req, 1);
-    mbar_init(&m.clean, 1);
+    mbar_init(&m.want, 1);
+    mbar_init(&m.taken, 1);
     mbar_init(&m.fin, 1);
     m.abort = 0;
-    m.loaded = 0;
+    m.loaded = m.loaded_q[0] = m.loaded_q[1] = 0;
     fence_mbarrier_init();
   }
   if (warp == kLoadWarp && lane == 0) {
@@ -206,46 +225,66 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = m.tmem;
-  const Item &item = m.item;             // read where needed, not kept in registers
-  const SeqTile &st = item.tile;
-  const int head = item.head;
-  // every block sees a malformed array; block 0 says so, or clears the status (a
-  // wait that gives up does so seconds later)
-  if (blockIdx.x == 0 && tid == 0)
-    set_device_status(p.status, st.bad ? KDA_ERR_INVALID_ARG : KDA_OK, st.bad);
-  pdl_launch_dependents();
-
-  const int row0 = first_row(st);
-  // Key tiles [i0, i1) of this part, and those of the two query tiles among them (the
-  // second never has fewer).
-  const int all0 = key_tiles(st, row0, 0, p.causal), all1 = key_tiles(st, row0, 1, p.causal);
-  const int n_all = max(all0, all1);
-  const int i0 = (int)((int64_t)n_all * item.part / item.parts);
-  const int i1 = (int)((int64_t)n_all * (item.part + 1) / item.parts);
-  const int nt[2] = {max(0, min(all0, i1) - i0), max(0, min(all1, i1) - i0)};
-  const int n_iter = i1 - i0;
-  const int last_live = min(kKeys, st.nk - (i1 - 1) * kKeys);  // keys of the last tile
-  const int halves_last = last_live > 64 ? 2 : 1;
   const WaitCtx cx{&m.abort, p.status, (int)blockIdx.x};
+  pdl_launch_dependents();
 
   if (warp >= 8) {
     setmaxnreg_dec<kIssueRegs>();
-    if (warp == kLoadWarp && lane == 0 && n_iter > 0) {
+    if (warp == kItemWarp) {
+      // ---- items: finds what a block of the grid works on, and takes over the next
+      // block when the loader is about to be through with this one
+      int64_t block = blockIdx.x;
+      int asked = 0, k = 0;
+      for (bool ok = true; ok;) {
+        Item it;
+        it.tile.seq = -1;
+        if (block >= 0) {
+          it = find_item(p, block);
+          // every block sees a malformed array; block 0 says so, or clears the status
+          // (a wait that gives up does so seconds later)
+          if (block == 0 && lane == 0)
+            set_device_status(p.status, it.tile.bad ? KDA_ERR_INVALID_ARG : KDA_OK, it.tile.bad);
+        }
+        if (block < 0 || it.tile.seq >= 0) {
+          if (k >= 2) ok = warp_wait_idle(cx, &m.item_free[k & 1], ((k >> 1) - 1) & 1, 50, k);
+          if (!ok) break;
+          if (lane == 0) {
+            m.item[k & 1] = it;
+            mbar_arrive(&m.item_full[k & 1]);
+          }
+          if (block < 0) break;
+          ok = warp_wait_idle(cx, &m.want, k & 1, 51, k);
+          ++k;
+          if (!ok) break;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&m.taken, 16);
+          take_block(smem_u32(m.answer), &m.taken);
+        }
+        __syncwarp();
+        // the answer is waited for whatever else fails: it is written to this block
+        ok = __all_sync(0xffffffffu, mbar_wait(&m.taken, asked & 1, kWaitNs));
+        ++asked;
+        if (!ok) {
+          if (lane == 0) record_device_status(p.status, KDA_ERR_TIMEOUT, 52, (int)blockIdx.x, k);
+          *(volatile int *)&m.abort = 1;
+          break;
+        }
+        block = taken_block(smem_u32(m.answer));
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+    } else if (warp == kLoadWarp && lane == 0) {
       // ---- loader
-      auto load_q = [&](int t) {
-        mbar_arrive_expect_tx(&m.q_full[t], KB * kQTile);
-        for (int kb = 0; kb < KB; ++kb)
-          tma_load_3d_u(base + (t * KB + kb) * kQTile, &map_q, &m.q_full[t], 64 * kb, head,
-                        st.q0 + row0 + 128 * t);
-      };
       // Slots [at, at + PER) hold key tile i and its values; before a unit is loaded,
       // the last unit that had one of its slots has been released.
       bool ok = true;
       uint32_t at = 0;
-      int u = 0;
+      uint32_t u = 0, cleans = 0;
+      uint32_t q_loads[2] = {0, 0};
       auto before = [&](int count) {  // slots `at` .. `at + count` of unit u
         // unit of slot position end - S, where positions run on without wrapping
-        const int end = (u >> 1) * PER + (u & 1) * KB + count - 1 - S;
+        const int end = (int)(u >> 1) * PER + (int)(u & 1) * KB + count - 1 - S;
         if (end < 0) return;
         const int v = end / PER * 2 + (end % PER >= KB ? 1 : 0);
         ok = wait_or_abort(cx, &m.empty[v % kUnits], (v / kUnits) & 1, 10, u);
@@ -255,115 +294,173 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
         at = at + 1 == S ? 0 : at + 1;
         return dst;
       };
-      if (nt[0] > 0) load_q(0);
-      for (int i = 0; i < n_iter; ++i) {
-        const int key = st.k0 + (i0 + i) * kKeys;
-        before(KB);
+      for (int k = 0; ok; ++k) {
+        ok = wait_or_abort(cx, &m.item_full[k & 1], (k >> 1) & 1, 11, k);
         if (!ok) break;
-        uint64_t *bar = &m.full[u % kUnits];
-        mbar_arrive_expect_tx(bar, KB * kSlotBytes);
-        for (int kb = 0; kb < KB; ++kb) {
-          if (kb < 2) tma_load_3d_u(next(), &map_k, bar, 64 * kb, head, key);
-          else tma_load_2d(next(), &map_r, bar, 64 * (kb - 2), key);
+        const Item &item = m.item[k & 1];
+        const int seq = item.tile.seq, head = item.head, n_iter = item.n_iter;
+        if (seq < 0) break;
+        const int halves_last = item.last_live > 64 ? 2 : 1;
+        const int nt1 = item.nt[1], nt0 = item.nt[0], q_row = item.tile.q0 + item.row0;
+        const int key0 = item.tile.k0 + item.i0 * kKeys;
+        const bool clean = (item.last_live & 63) != 0;
+        auto load_q = [&](int t) {
+          // the item before has read its queries
+          if (q_loads[t] > 0) ok = wait_or_abort(cx, &m.q_free[t], (q_loads[t] - 1) & 1, 12, k);
+          if (!ok) return;
+          ++q_loads[t];
+          mbar_arrive_expect_tx(&m.q_full[t], KB * kQTile);
+          for (int kb = 0; kb < KB; ++kb)
+            tma_load_3d_u(base + (t * KB + kb) * kQTile, &map_q, &m.q_full[t], 64 * kb, head,
+                          q_row + 128 * t);
+        };
+        if (nt0 > 0) load_q(0);
+        if (n_iter == 0) mbar_arrive(&m.want);
+        for (int i = 0; ok && i < n_iter; ++i) {
+          // early enough for the next item's queries to follow this one's last keys
+          if (i == max(0, n_iter - kAhead)) mbar_arrive(&m.want);
+          const int key = key0 + i * kKeys;
+          before(KB);
+          if (!ok) break;
+          uint64_t *bar = &m.full[u % kUnits];
+          mbar_arrive_expect_tx(bar, KB * kSlotBytes);
+          for (int kb = 0; kb < KB; ++kb) {
+            if (kb < 2) tma_load_3d_u(next(), &map_k, bar, 64 * kb, head, key);
+            else tma_load_2d(next(), &map_r, bar, 64 * (kb - 2), key);
+          }
+          ++u;
+          if (i == 0 && nt1 > 0) load_q(1);
+          if (ok) before(2);
+          if (!ok) break;
+          const int halves = i + 1 < n_iter ? 2 : halves_last;
+          bar = &m.full[u % kUnits];
+          mbar_arrive_expect_tx(bar, halves * kSlotBytes);
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint32_t dst = next();
+            if (hf >= halves) continue;
+            tma_load_3d_u(dst, &map_v, bar, 0, head, key + 64 * hf);
+            tma_load_3d_u(dst + 8192, &map_v, bar, 64, head, key + 64 * hf);
+          }
+          ++u;
         }
-        ++u;
-        if (i == 0 && nt[1] > 0) load_q(1);
-        const int halves = i + 1 < n_iter ? 2 : halves_last;
-        before(2);
-        if (!ok) break;
-        bar = &m.full[u % kUnits];
-        mbar_arrive_expect_tx(bar, halves * kSlotBytes);
-        for (int hf = 0; hf < halves; ++hf) {
-          const uint32_t dst = next();
-          tma_load_3d_u(dst, &map_v, bar, 0, head, key + 64 * hf);
-          tma_load_3d_u(dst + 8192, &map_v, bar, 64, head, key + 64 * hf);
-        }
-        ++u;
+        if (ok && n_iter > 0 && clean) mbar_arrive(&m.clean_req[cleans++ & 1]);
+        mbar_arrive(&m.item_free[k & 1]);
       }
-      if (ok) mbar_arrive(&m.clean_req);
       m.loaded = u;
-    } else if (warp == kMmaWarp && n_iter > 0 && elect_one()) {
+      m.loaded_q[0] = q_loads[0];
+      m.loaded_q[1] = q_loads[1];
+    } else if (warp == kMmaWarp && elect_one()) {
       // ---- MMA issue, by the elected lane (elect.sync lets the compiler keep the
       // descriptors in uniform registers: 270 us against 441 under lane == 0 with
       // descriptors built for each product, and 311 with the warp converged and a
       // branch per product; 4 x 4096 tokens, 16 heads)
       bool ok = true;
-      const int last_user = nt[1] > 0 ? 1 : 0;   // releases the units
       const Desc ring_k(base + kRing, 16), ring_v(base + kRing, 8192);
-      auto issue_s = [&](int t, int i, uint32_t at) {  // at: first slot of key tile i
-        const Desc a(base + t * KB * kQTile, 16);
-        ok = wait_or_abort(cx, &m.full[(2 * i) % kUnits], (2 * i / kUnits) & 1, 20, i);
-        if (!ok) return;
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          const uint32_t off = at * kSlotBytes;
-          at = at + 1 == S ? 0 : at + 1;
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma_ss(tm + 128 * t, a.at(kb * kQTile + ks * 32), ring_k.at(off + ks * 32), ID_S,
-                    kb + ks > 0);
-        }
-        if (t == last_user) umma_commit(&m.empty[(2 * i) % kUnits]);
-        umma_commit(&m.s_full[t]);
-      };
-      auto issue_pv = [&](int t, int i, uint32_t at) {  // at: first slot of value tile i
-        const int u = 2 * i + 1;
-        const bool last = i + 1 == n_iter;
-        ok = wait_or_abort(cx, &m.full[u % kUnits], (u / kUnits) & 1, 21, i);
-        // the last tile's rows past the sequence have been zeroed
-        if (ok && last && (last_live & 63) != 0) ok = wait_or_abort(cx, &m.clean, 0, 22, i);
-        ok = ok && wait_or_abort(cx, &m.p_ready[t][0], i & 1, 23, i);
-        if (!ok) return;
-        tc_fence_after();
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          umma_ts(tm + 256 + 128 * t, tm + 128 * t + 8 * ks, ring_v.at(at * kSlotBytes + ks * 2048),
-                  ID_PV, i + ks > 0);
-        at = at + 1 == S ? 0 : at + 1;
-        ok = wait_or_abort(cx, &m.p_ready[t][1], i & 1, 24, i);
-        if (!ok) return;
-        tc_fence_after();
-        if (!last || halves_last == 2) {
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma_ts(tm + 256 + 128 * t, tm + 128 * t + 32 + 8 * ks,
-                    ring_v.at(at * kSlotBytes + ks * 2048), ID_PV, 1);
-        }
-        if (t == last_user) umma_commit(&m.empty[u % kUnits]);
-      };
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (ok && nt[t] > 0) {
-          ok = wait_or_abort(cx, &m.q_full[t], 0, 25, t);
-          if (ok) issue_s(t, 0, 0);
-        }
+      uint32_t u0 = 0, cleans = 0;               // units and cleaned tiles of items before
+      int seen[2] = {0, 0}, q_seen[2] = {0, 0};  // key tiles and queries of items before
       uint32_t at = 0;                           // first slot of key tile i
-      for (int i = 0; ok && i < n_iter; ++i) {
-        const uint32_t at_v = at + KB >= S ? at + KB - S : at + KB;
-        const uint32_t at_n = at + PER >= S ? at + PER - S : at + PER;
+      for (int k = 0; ok; ++k) {
+        ok = wait_or_abort(cx, &m.item_full[k & 1], (k >> 1) & 1, 26, k);
+        if (!ok || m.item[k & 1].tile.seq < 0) break;
+        const int n_iter = m.item[k & 1].n_iter, last_live = m.item[k & 1].last_live;
+        const int nt[2] = {m.item[k & 1].nt[0], m.item[k & 1].nt[1]};
+        mbar_arrive(&m.item_free[k & 1]);
+        const bool last_half = last_live > 64, clean = (last_live & 63) != 0;
+        const int last_user = nt[1] > 0 ? 1 : 0;   // releases the units
+        auto issue_s = [&](int t, int i, uint32_t at) {  // at: first slot of key tile i
+          const Desc a(base + t * KB * kQTile, 16);
+          const uint32_t u = u0 + 2 * i;
+          ok = wait_or_abort(cx, &m.full[u % kUnits], (u / kUnits) & 1, 20, i);
+          if (!ok) return;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || i >= nt[t]) continue;
-          issue_pv(t, i, at_v);
-          if (!ok) continue;
-          if (i + 1 < nt[t]) {
-            issue_s(t, i + 1, at_n);
-          } else {
-            umma_commit(&m.o_full[t]);
+          for (int kb = 0; kb < KB; ++kb) {
+            const uint32_t off = at * kSlotBytes;
+            at = at + 1 == S ? 0 : at + 1;
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              umma_ss(tm + 128 * t, a.at(kb * kQTile + ks * 32), ring_k.at(off + ks * 32), ID_S,
+                      kb + ks > 0);
           }
+          if (t == last_user) umma_commit(&m.empty[u % kUnits]);
+          umma_commit(&m.s_full[t]);
+          if (i + 1 == nt[t]) umma_commit(&m.q_free[t]);
+        };
+        auto issue_pv = [&](int t, int i, uint32_t at) {  // at: first slot of value tile i
+          const uint32_t u = u0 + 2 * i + 1;
+          const bool last = i + 1 == n_iter;
+          ok = wait_or_abort(cx, &m.full[u % kUnits], (u / kUnits) & 1, 21, i);
+          // the last tile's rows past the sequence have been zeroed
+          if (ok && last && clean)
+            ok = wait_or_abort(cx, &m.clean[cleans & 1], (cleans >> 1) & 1, 22, i);
+          ok = ok && wait_or_abort(cx, &m.p_ready[t][0], (seen[t] + i) & 1, 23, i);
+          if (!ok) return;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_ts(tm + 256 + 128 * t, tm + 128 * t + 8 * ks,
+                    ring_v.at(at * kSlotBytes + ks * 2048), ID_PV, i + ks > 0);
+          at = at + 1 == S ? 0 : at + 1;
+          ok = wait_or_abort(cx, &m.p_ready[t][1], (seen[t] + i) & 1, 24, i);
+          if (!ok) return;
+          tc_fence_after();
+          if (!last || last_half) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              umma_ts(tm + 256 + 128 * t, tm + 128 * t + 32 + 8 * ks,
+                      ring_v.at(at * kSlotBytes + ks * 2048), ID_PV, 1);
+          }
+          if (t == last_user) umma_commit(&m.empty[u % kUnits]);
+        };
+        // S of the first tiles follows the item before's last products, which are read
+        // out of O while it runs
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (ok && nt[t] > 0) {
+            ok = wait_or_abort(cx, &m.q_full[t], q_seen[t]++ & 1, 25, t);
+            if (ok) issue_s(t, 0, at);
+          }
+        for (int i = 0; ok && i < n_iter; ++i) {
+          const uint32_t at_v = at + KB >= S ? at + KB - S : at + KB;
+          const uint32_t at_n = at + PER >= S ? at + PER - S : at + PER;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!ok || i >= nt[t]) continue;
+            issue_pv(t, i, at_v);
+            if (!ok) continue;
+            if (i + 1 < nt[t]) {
+              issue_s(t, i + 1, at_n);
+            } else {
+              umma_commit(&m.o_full[t]);
+            }
+          }
+          at = at_n;
         }
-        at = at_n;
+        u0 += 2 * n_iter;
+        seen[0] += nt[0];
+        seen[1] += nt[1];
+        if (n_iter > 0 && clean) ++cleans;
       }
-    } else if (warp == kCleanWarp && n_iter > 0 && (last_live & 63) != 0) {
+    } else if (warp == kCleanWarp) {
       // ---- cleaner: value rows past the sequence's end are another sequence's, and
       // may hold anything; zero them (0 * NaN would reach the sum).  The loader asks
-      // once the copies of the last tile are under way.
-      const int u = 2 * n_iter - 1;
-      bool ok = warp_wait(cx, &m.clean_req, 0, 30, n_iter);
-      ok = ok && warp_wait(cx, &m.full[u % kUnits], (u / kUnits) & 1, 31, n_iter);
-      if (ok) {
+      // once the copies of the last tile are under way.  It may ask for the next item
+      // too before this one's tile is used, but no further: two barriers each.
+      int tiles_before = 0, cleans = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        ok = warp_wait_idle(cx, &m.item_full[k & 1], (k >> 1) & 1, 32, k);
+        if (!ok || m.item[k & 1].tile.seq < 0) break;
+        const int n_iter = m.item[k & 1].n_iter, last_live = m.item[k & 1].last_live;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m.item_free[k & 1]);
+        tiles_before += n_iter;
         const int from = last_live & 63;
-        const uint32_t s = ((uint32_t)(n_iter - 1) * PER + KB + halves_last - 1) % S;
+        if (n_iter == 0 || from == 0) continue;
+        const int u = 2 * tiles_before - 1, halves_last = last_live > 64 ? 2 : 1;
+        ok = warp_wait_idle(cx, &m.clean_req[cleans & 1], (cleans >> 1) & 1, 30, n_iter);
+        ok = ok && warp_wait(cx, &m.full[u % kUnits], (u / kUnits) & 1, 31, n_iter);
+        if (!ok) break;
+        const uint32_t s = ((uint32_t)(tiles_before - 1) * PER + KB + halves_last - 1) % S;
         const uint32_t dst = base + kRing + s * kSlotBytes + from * 128;
         for (int j = lane; j < (64 - from) * 8; j += 32) {
           st_shared_v4(dst + j * 16, 0, 0, 0, 0);
@@ -371,7 +468,8 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&m.clean);
+        if (lane == 0) mbar_arrive(&m.clean[cleans & 1]);
+        ++cleans;
       }
     }
   } else {
@@ -380,14 +478,22 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     const int t = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t tm_s = tm + lanes + 128 * t, tm_o = tm + lanes + 256 + 128 * t;
-    const int row = row0 + 128 * t + r;                  // of the sequence
-    // keys this row sees
+    int done = 0, outs = 0;                              // key tiles and outputs of items before
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+    ok = warp_wait(cx, &m.item_full[k & 1], (k >> 1) & 1, 42, k);
+    const Item &item = m.item[k & 1];                    // read where needed: few registers
+    const SeqTile &st = item.tile;
+    if (!ok || st.seq < 0) break;
+    const int row = item.row0 + 128 * t + r;             // of the sequence
+    const int n_t = item.nt[t];
+    // keys this row sees, counted from the first of the part
     int limit = st.nk;
     if (p.causal) limit = min(limit, row + st.nk - st.nq + 1);
+    limit -= item.i0 * kKeys;
     float ref = kNoRef, l = 0.f;
-    bool ok = true;
-    for (int i = 0; ok && i < nt[t]; ++i) {
-      ok = warp_wait(cx, &m.s_full[t], i & 1, 40, i);
+    for (int i = 0; i < n_t; ++i) {
+      ok = warp_wait(cx, &m.s_full[t], (done + i) & 1, 40, i);
       if (!ok) break;
       tc_fence_after();
       uint32_t x[4][32];
@@ -395,7 +501,7 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       for (int c = 0; c < 4; ++c) tmem_ld32(tm_s + 32 * c, x[c]);
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld_wait(x[c]);
-      const int seen = limit - (i0 + i) * kKeys;         // columns below it are allowed
+      const int seen = limit - i * kKeys;                // columns below it are allowed
       if (__any_sync(0xffffffffu, seen < kKeys)) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -450,80 +556,53 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       }
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
-    // ---- output: O / l through this warp's rows of its own query tile's buffer
-    // (all products with Q are done), so that rows leave whole
-    const bool live = st.seq >= 0 && row0 + 128 * t < st.nq;
-    if (ok && nt[t] > 0)
-      ok = warp_wait(cx, &m.o_full[t], 0, 41, n_iter);
-    if (ok && live) {
-      if (nt[t] > 0) tc_fence_after();
-      if (item.parts > 1) {
-        // four channels of the 32 rows beside one another
-        const int64_t at = (int64_t)item.slot * 2 + t;
-        p.part_ml[at * 256 + r] = ref;
-        p.part_ml[at * 256 + 128 + r] = l;
-        uint4 *to = reinterpret_cast<uint4 *>(p.part_o) + at * (kLatentD / 4) * 128 + r;
+    // ---- output
+    if (ok && n_t > 0) ok = warp_wait(cx, &m.o_full[t], outs & 1, 41, n_t);
+    if (!ok) break;
+    if (n_t > 0) tc_fence_after();
+    done += n_t;
+    outs += n_t > 0;
+    const bool live = row < st.nq;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t at = (int64_t)item.slot * 2 + t;       // of a part
+    const int64_t to = (st.q0 + row) * (int64_t)p.H + item.head;
+    if (item.parts > 1) {
+      p.part_ml[at * 256 + r] = ref;
+      p.part_ml[at * 256 + 128 + r] = l;
+    } else if (live) {
+      p.lse[to] = l == 0.f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
+    }
+    const bool parts = item.parts > 1;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
-          if (nt[t] > 0) {
-            tmem_ld32(tm_o + 32 * c, o);
-            tmem_ld_wait(o);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0;
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            to[(8 * c + j) * 128] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-        }
+    for (int c = 0; c < 4; ++c) {
+      uint32_t o[32];
+      if (n_t > 0) {
+        tmem_ld32(tm_o + 32 * c, o);
+        tmem_ld_wait(o);
       } else {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const uint32_t buf = base + t * KB * kQTile + (warp & 3) * 32 * 256;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
-          if (nt[t] > 0) {
-            tmem_ld32(tm_o + 32 * c, o);
-            tmem_ld_wait(o);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0;
-          }
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {   // 16-byte pieces, rotated by the row
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              w[j] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * j]) * inv,
-                                 __uint_as_float(o[8 * q + 2 * j + 1]) * inv);
-            st_shared_v4(buf + lane * 256 + (((4 * c + q) ^ (lane & 15)) << 4), w[0], w[1], w[2],
-                         w[3]);
-          }
-        }
-        __syncwarp();
-        const int64_t first = st.q0 + row0 + 128 * t + (warp & 3) * 32;
-#pragma unroll
-        for (int k0 = 0; k0 < 16; k0 += 8) {
-          uint4 v[8];
-          const int piece = lane & 15;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int rr = 2 * (k0 + k) + (lane >> 4);
-            v[k] = ld_shared_v4(buf + rr * 256 + ((piece ^ (rr & 15)) << 4));
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int rr = 2 * (k0 + k) + (lane >> 4);
-            if (row - lane + rr < st.nq)
-              *reinterpret_cast<uint4 *>(p.out + ((first + rr) * p.H + head) * kLatentD +
-                                         8 * piece) = v[k];
-          }
-        }
-        if (row < st.nq)
-          p.lse[(st.q0 + row) * (int64_t)p.H + head] =
-              l == 0.f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
+        for (int j = 0; j < 32; ++j) o[j] = 0;
       }
+      if (parts) {  // four channels of the 32 rows beside one another
+        uint4 *w = reinterpret_cast<uint4 *>(p.part_o) + (at * (kLatentD / 4) + 8 * c) * 128 + r;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          w[j * 128] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+      } else if (live) {
+        uint4 *w = reinterpret_cast<uint4 *>(p.out + to * kLatentD) + 4 * c;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t b[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            b[j] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * j]) * inv,
+                               __uint_as_float(o[8 * q + 2 * j + 1]) * inv);
+          w[q] = make_uint4(b[0], b[1], b[2], b[3]);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&m.item_free[k & 1]);
     }
   }
 
@@ -531,11 +610,11 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
   __syncthreads();
   if (m.abort) {  // nothing in flight outlives the CTA
     if (tid == 32 * kLoadWarp) {
-      const int u = m.loaded;
-      for (int v = max(0, u - kUnits); v < u; ++v)
+      const uint32_t u = m.loaded;
+      for (uint32_t v = u > kUnits ? u - kUnits : 0; v < u; ++v)
         mbar_wait(&m.full[v % kUnits], (v / kUnits) & 1, kWaitNs);
       for (int t = 0; t < 2; ++t)
-        if (nt[t] > 0) mbar_wait(&m.q_full[t], 0, kWaitNs);
+        if (m.loaded_q[t] > 0) mbar_wait(&m.q_full[t], (m.loaded_q[t] - 1) & 1, kWaitNs);
     }
     if (tid == 32 * kMmaWarp) {
       umma_commit(&m.fin);

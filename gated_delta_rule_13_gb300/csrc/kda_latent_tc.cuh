@@ -1,5 +1,5 @@
 // What the tensor-core kernels of latent attention share: bounded waits with an
-// abort flag, tiled copies, block reductions and tensor maps.
+// abort flag, tiled copies, clusters, taking over blocks and tensor maps.
 #pragma once
 
 #include <cuda.h>
@@ -57,6 +57,30 @@ __device__ __forceinline__ void cluster_sync_all() {
       "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
           : "memory");
 }
+// Work for a block that is done: a block of this grid that has not started is taken
+// out of the launch.  take_block asks (16 bytes at dst, counted by the barrier);
+// taken_block reads the answer, -1 when no block was left, after which there is no
+// asking again.
+__device__ __forceinline__ void take_block(uint32_t dst, uint64_t *bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+      "[%0], [%1];" ::"r"(dst),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ int64_t taken_block(uint32_t src) {
+  uint32_t any, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\tld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(any), "=r"(x)
+      : "r"(src)
+      : "memory");
+  return any ? (int64_t)x : -1;
+}
+
 // Where a wait gave up: the abort flag in shared memory ends every other wait of
 // the block, so that each role leaves its loop.
 struct WaitCtx {
@@ -88,16 +112,21 @@ __device__ __forceinline__ bool warp_wait(const WaitCtx &cx, uint64_t *bar, uint
   return __all_sync(0xffffffffu, wait_or_abort(cx, bar, parity, where, step)) != 0;
 }
 
-// Barrier `id` over nthreads (a multiple of 32); returns whether any of them passed true.
-__device__ __forceinline__ bool bar_any(uint32_t id, uint32_t nthreads, bool pred) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
-      "barrier.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(nthreads), "r"((uint32_t)pred)
-      : "memory");
-  return r != 0;
+// For waits as long as a work item takes, by a warp that is in no hurry: it sleeps
+// between looks, and leaves it to those it waits for to give up first.
+__device__ __forceinline__ bool warp_wait_idle(const WaitCtx &cx, uint64_t *bar, uint32_t parity,
+                                               int where, int step) {
+  const uint64_t t0 = global_timer_ns();
+  while (!__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) {
+    if (__any_sync(0xffffffffu, *cx.abort)) return false;
+    if (__any_sync(0xffffffffu, global_timer_ns() - t0 > 32 * kWaitNs)) {
+      record_device_status(cx.status, KDA_ERR_TIMEOUT, where, cx.chain, step);
+      *cx.abort = 1;
+      return false;
+    }
+    __nanosleep(200);
+  }
+  return true;
 }
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, uint64_t *bar,
@@ -150,15 +179,6 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t round_up_1k(uint32_t x) { return (x + 1023u) & ~1023u; }
-
-// A float as an integer of the same order (NaN with a clear sign above +inf).
-__device__ __forceinline__ int ordered(float x) {
-  const int b = __float_as_int(x);
-  return b >= 0 ? b : b ^ 0x7fffffff;
-}
-__device__ __forceinline__ float unordered(int b) {
-  return __int_as_float(b >= 0 ? b : b ^ 0x7fffffff);
-}
 
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
