@@ -190,7 +190,9 @@ __device__ inline SeqTile ordered_tile(const Packed &p, const LaneSeqs &l, TileK
     }
     const int rank = index - __reduce_add_sync(0xffffffffu, min(tiles, lo));
     const unsigned have = __ballot_sync(0xffffffffu, tiles > lo);
-    s = __popc(have) > rank ? (int)__fns(have, 0, rank + 1) : -1;
+    // the sequence that `rank` others with such a tile come before
+    const bool it = tiles > lo && __popc(have & ((1u << lane) - 1)) == rank;
+    s = __ffs(__ballot_sync(0xffffffffu, it)) - 1;
   }
   r.seq = s;
   r.tile = lo;
@@ -203,13 +205,13 @@ __device__ inline SeqTile ordered_tile(const Packed &p, const LaneSeqs &l, TileK
   return r;
 }
 
-// Tile and head of work item `index` of `tiles` * H.  Items run in groups of as many
-// heads as fill the SMs once, inside a group tile by tile.
+// Tile and head of work item `index` of `tiles` * H (a grid's blocks: below 2^31).
+// Items run in groups of as many heads as fill the SMs once, inside a group tile by tile.
 __device__ inline SeqTile place_item(const Packed &p, const LaneSeqs &l, TileKind kind,
-                                     int64_t tiles, int64_t index, int *head) {
-  const int64_t fill = p.sms / tiles, group = fill > 1 ? fill : 1;
-  const int64_t g = index / (tiles * group), left = p.H - g * group;
-  const int64_t heads = group < left ? group : left, in = index - g * tiles * group;
+                                     uint32_t tiles, uint32_t index, int *head) {
+  const uint32_t fill = (uint32_t)p.sms / tiles, group = fill > 1 ? fill : 1;
+  const uint32_t g = index / (tiles * group), left = (uint32_t)p.H - g * group;
+  const uint32_t heads = group < left ? group : left, in = index - g * tiles * group;
   *head = (int)(g * group + in % heads);
   return ordered_tile(p, l, kind, (int32_t)(in / heads));
 }

@@ -144,10 +144,11 @@ __device__ inline Item find_item(const Params &p, int64_t block) {
   if (tiles <= 0) return it;
   const Rounds r(p, tiles * p.H);
   if (block < r.whole) {
-    it.tile = place_item(p, seqs, kTileA, tiles, block, &it.head);
+    it.tile = place_item(p, seqs, kTileA, (uint32_t)tiles, (uint32_t)block, &it.head);
   } else if (block - r.whole < (int64_t)r.rest * r.ways) {
     it.slot = (int)(block - r.whole);
-    it.tile = place_item(p, seqs, kTileA, tiles, r.whole + it.slot / r.ways, &it.head);
+    it.tile = place_item(p, seqs, kTileA, (uint32_t)tiles, (uint32_t)(r.whole + it.slot / r.ways),
+                         &it.head);
     it.part = it.slot % r.ways;
     it.parts = parts_of(it.tile, r.ways, p.causal);
     if (it.part >= it.parts) it.tile.seq = -1;
@@ -646,7 +647,8 @@ __global__ void __launch_bounds__(256) kda_latent_fwd_join_kernel(const Params p
       const Rounds r(p, tiles * p.H);
       ways = r.ways;
       if ((int)blockIdx.y < r.rest) {
-        it.tile = place_item(p, seqs, kTileA, tiles, r.whole + blockIdx.y, &it.head);
+        it.tile = place_item(p, seqs, kTileA, (uint32_t)tiles, (uint32_t)(r.whole + blockIdx.y),
+                             &it.head);
         it.parts = parts_of(it.tile, r.ways, p.causal);
       }
     }

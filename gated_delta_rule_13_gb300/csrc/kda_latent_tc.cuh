@@ -81,6 +81,10 @@ __device__ __forceinline__ int64_t taken_block(uint32_t src) {
   return any ? (int64_t)x : -1;
 }
 
+__device__ __forceinline__ void mbar_inval(uint64_t *bar) {
+  asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // Where a wait gave up: the abort flag in shared memory ends every other wait of
 // the block, so that each role leaves its loop.
 struct WaitCtx {
@@ -171,6 +175,37 @@ struct Desc {
     return d;
   }
 };
+
+// A lane holds 64 bytes of row `lane` of 32 rows; they are stored at dst + row * stride
+// (bytes), rows >= n_rows left out.  Four lanes exchange their pieces first, so that a
+// store covers 64 consecutive bytes of eight rows and not 16 of each of the 32.
+__device__ __forceinline__ uint4 shfl_xor(uint4 v, int mask) {
+  v.x = __shfl_xor_sync(0xffffffffu, v.x, mask);
+  v.y = __shfl_xor_sync(0xffffffffu, v.y, mask);
+  v.z = __shfl_xor_sync(0xffffffffu, v.z, mask);
+  v.w = __shfl_xor_sync(0xffffffffu, v.w, mask);
+  return v;
+}
+__device__ __forceinline__ void store_rows(uint4 (&v)[4], void *dst, int64_t stride, int n_rows,
+                                           int lane) {
+#pragma unroll
+  for (int b = 1; b < 4; b *= 2) {
+    const bool high = lane & b;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j & b) continue;
+      const uint4 got = shfl_xor(high ? v[j] : v[j + b], b);
+      if (high) v[j] = got;
+      else v[j + b] = got;
+    }
+  }
+  unsigned char *to = static_cast<unsigned char *>(dst) + 16 * (lane & 3);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int row = (lane & ~3) + j;
+    if (row < n_rows) *reinterpret_cast<uint4 *>(to + row * stride) = v[j];
+  }
+}
 
 // Programmatic launch: the next kernel's blocks may start; wait for the previous grid.
 __device__ __forceinline__ void pdl_launch_dependents() {
