@@ -958,8 +958,9 @@ kda_latent_stat_kernel(const __nv_bfloat16 *__restrict__ out,
 #pragma unroll
   for (int k = 0; k < kY * 16 / kStatThreads; ++k) {  // 16 lanes a row, 8 channels each
     const int r = (k * kStatThreads + tid) >> 4, c = tid & 15, row = st.tile * kY + r;
-    float sum = 0.f;
+    float sum = 0.f, l = -CUDART_INF_F;
     if (row < st.nq) {
+      if (c == 0) l = lse[((int64_t)st.q0 + row) * p.H + head];
       const int64_t e = (((int64_t)st.q0 + row) * p.H + head) * kLatentD + 8 * c;
       const uint4 a = *reinterpret_cast<const uint4 *>(out + e);
       const uint4 b = *reinterpret_cast<const uint4 *>(d_out + e);
@@ -974,12 +975,7 @@ kda_latent_stat_kernel(const __nv_bfloat16 *__restrict__ out,
 #pragma unroll
     for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (c == 0) {
-      float l = CUDART_INF_F;
-      if (row < st.nq) {
-        l = lse[((int64_t)st.q0 + row) * p.H + head];
-        l = l == -CUDART_INF_F ? CUDART_INF_F : l * kLog2e;
-      }
-      lse2[at + r] = l;
+      lse2[at + r] = l == -CUDART_INF_F ? CUDART_INF_F : l * kLog2e;
       delta[at + r] = sum;
     }
   }
