@@ -90,8 +90,7 @@ struct Params {
   float *lse;
   DeviceStatus *status;
   DeviceStatus *errors; // [CTAs]
-  int2 *begins;         // [G] sequence and tile a pair begins with
-  int32_t *total;       // all tiles
+  int4 *joins;          // [G] of the border before a pair: sequence, parts (0: none), slot
   float *part_o;        // [row tiles][G][2][512 / 4][128 rows][4]
   float *part_ml;       // [row tiles][G][2][2][128]
 };
@@ -252,8 +251,14 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
   pdl_launch_dependents();
   const uint32_t tm = m.tmem;
   if (rt == 0 && rank == 0 && tid == 0) {  // for the kernel that joins the parts
-    p.begins[slice] = make_int2(m.seq0, m.tile0);
-    if (slice == 0) *p.total = m.total;
+    // The first border inside a sequence joins its parts, from the pair before it to the
+    // pair of its last tile.  A pair's first segment is in slot 0, its last in slot 1.
+    const int at = pair_begin(slice, p.G, m.total), start = at - m.tile0;
+    const int before = slice > 0 ? pair_begin(slice - 1, p.G, m.total) : 0;
+    int parts = 0;
+    if (slice > 0 && m.tile0 > 0 && before <= start)
+      parts = pair_of(start + key_tiles(seq_len(p, m.seq0)) - 1, p.G, m.total) - slice + 2;
+    p.joins[slice] = make_int4(m.seq0, parts, 2 * (slice - 1) + (before < start ? 1 : 0), 0);
   }
   const int begin = pair_begin(slice, p.G, m.total);
   const int mine = pair_begin(slice + 1, p.G, m.total) - begin;
@@ -681,49 +686,65 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
 }
 
 // Joins the parts of sequences that several pairs shared, in the list's order.
-// Block (x: 32 rows and 16 channels, y: a border between two pairs): the first border
-// inside a sequence joins it.  A lane is a row; the eight warps take the parts in
-// turn, so that a long list is read by all of them, and their sums are added in
-// warp order.  The first block also sets the call's status: the first error of any
-// CTA, or none.
+// Block (x: 32 rows and some channels, y: the y-th border that joins a sequence; the
+// last y: the call's status, which is the first error of any CTA, or none).  A lane is
+// a row.  With few sequences there are many parts to each: a block has 16 channels, its
+// warps take the parts in turn, and their sums are added in warp order.  With many
+// there are few: a block has 128 channels, 16 a warp, and every warp takes all parts.
+// Whole calls, first form against second, 96 rows: 1 x 3000 keys 20.5 / 48.4 us, 8 x
+// 4000 30.6 / 35.0, 12 x 4000 (six parts and a half each) 37.0 / 37.7, 19 x 4000 49.2 /
+// 45.2, 64 x 2000 85.9 / 61.5.  Both wait for memory: a border, its parts, their sum.
 constexpr int kJoinWarps = 8, kJoinCh = 16;
+template <bool kMany>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 kda_latent_join_kernel(const Params p) {
-  __shared__ float s_o[kJoinWarps][kJoinCh][32], s_ref[kJoinWarps][32], s_l[kJoinWarps][32];
+  constexpr int kStep = kMany ? kJoinWarps : 1;         // warps that share the parts
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
+  if (blockIdx.y + 1 == gridDim.y) {
+    if (blockIdx.x > 0 || warp > 0) return;
     int at = 0x7fffffff;
     const int ctas = p.G * p.row_tiles * 2;
+#pragma unroll 8
     for (int i = lane; i < ctas; i += 32)
-      if (p.errors[i].code != 0) { at = i; break; }
+      if (p.errors[i].code != 0) at = min(at, i);
     at = __reduce_min_sync(0xffffffffu, at);
     if (lane == 0) {
       DeviceStatus st{0, 0, 0, 0, 0, 0};
       if (at < ctas) st = p.errors[at];
       *p.status = st;
     }
+    return;
   }
-  const int border = blockIdx.y + 1;
-  if (border >= p.G) return;
-  const int2 at = p.begins[border];
-  if (at.y == 0) return;                 // a sequence begins with the pair
-  const int all = *p.total, start = pair_begin(border, p.G, all) - at.y, first = border - 1;
-  if (pair_begin(first, p.G, all) > start) return;  // an earlier border joins it
-  const int last = pair_of(start + key_tiles(seq_len(p, at.x)) - 1, p.G, all);
+  int4 join = make_int4(0, 0, 0, 0);
+  int skip = blockIdx.y;                 // joining borders still to be passed over
+#pragma unroll 3
+  for (int i = lane; i - lane < p.G; i += 32) {
+    const int4 v = i < p.G ? p.joins[i] : make_int4(0, 0, 0, 0);
+    const unsigned have = __ballot_sync(0xffffffffu, v.y > 0);
+    const int src =
+        __ffs(__ballot_sync(0xffffffffu,
+                            v.y > 0 && __popc(have & ((1u << lane) - 1)) == skip)) - 1;
+    if (src >= 0) {
+      join.x = __shfl_sync(0xffffffffu, v.x, src);
+      join.y = __shfl_sync(0xffffffffu, v.y, src);
+      join.z = __shfl_sync(0xffffffffu, v.z, src);
+    }
+    skip -= __popc(have);                // below 0 once found, and never 0 again
+  }
+  const int parts = join.y;
+  if (parts == 0) return;
   const int groups = (p.R + 31) / 32;
-  const int group = blockIdx.x % groups, ch = blockIdx.x / groups * kJoinCh;
+  const int group = blockIdx.x % groups;
+  const int ch = (blockIdx.x / groups * (kMany ? 1 : kJoinWarps) + (kMany ? 0 : warp)) * kJoinCh;
   const int rt = group / 4, r = (group & 3) * 32 + lane, row = group * 32 + lane;
-  // a pair's first segment is in slot 0, its last in slot 1
-  const int64_t slot0 = ((int64_t)rt * p.G + first) * 2;
-  const int late = pair_begin(first, p.G, all) < start ? 1 : 0;
-  const int parts = last - first + 1;
+  const int64_t slot0 = (int64_t)rt * p.G * 2 + join.z;
   float ref = kNoRef, l = 0.f, o[kJoinCh];
 #pragma unroll
   for (int c = 0; c < kJoinCh; ++c) o[c] = 0.f;
-#pragma unroll 2
-  for (int i = warp; i < parts; i += kJoinWarps) {
-    const int64_t slot = slot0 + 2 * i + (i == 0 ? late : 0);
+#pragma unroll 4
+  for (int i = kMany ? warp : 0; i < parts; i += kStep) {
+    const int64_t slot = i == 0 ? slot0 : (slot0 & ~(int64_t)1) + 2 * i;
     const float4 *x = reinterpret_cast<const float4 *>(p.part_o) +
                       (slot * (kLatentC / 4) + ch / 4) * kRows + r;
     float4 v[kJoinCh / 4];
@@ -742,6 +763,21 @@ kda_latent_join_kernel(const Params p) {
       o[4 * c + 3] = o[4 * c + 3] * a + v[c].w * b;
     }
   }
+  const int64_t out_row = (int64_t)join.x * p.R + row;
+  if (!kMany) {
+    if (row >= p.R) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint32_t w[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) w[c] = pack_bf16x2(o[2 * c] * inv, o[2 * c + 1] * inv);
+    uint4 *to = reinterpret_cast<uint4 *>(p.out + out_row * kLatentC + ch);
+    to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    if (p.lse && ch == 0)
+      p.lse[out_row] = l == 0.f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
+    return;
+  }
+  __shared__ float s_o[kJoinWarps][kJoinCh][32], s_ref[kJoinWarps][32], s_l[kJoinWarps][32];
   s_ref[warp][lane] = ref;
   s_l[warp][lane] = l;
 #pragma unroll
@@ -765,7 +801,6 @@ kda_latent_join_kernel(const Params p) {
   }
   if (row >= p.R) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t out_row = (int64_t)at.x * p.R + row;
   *reinterpret_cast<uint32_t *>(p.out + out_row * kLatentC + ch + 2 * warp) =
       pack_bf16x2(u * inv, v * inv);
   if (p.lse && ch == 0 && warp == 0)
@@ -799,7 +834,7 @@ int resident_pairs() {
 
 struct Plan {
   int row_tiles, G;
-  size_t begins, errors, ml, o;          // bytes of the workspace's pieces
+  size_t joins, errors, ml, o;          // bytes of the workspace's pieces
 };
 Plan make_plan(int T, int H) {
   Plan pl;
@@ -810,7 +845,7 @@ Plan make_plan(int T, int H) {
   auto round = [](size_t x) { return (x + 255) / 256 * 256; };
   // partial results: none when one pair has all keys of its rows
   const size_t parts = pl.G > 1 ? (size_t)pl.row_tiles * pl.G * 2 : 0;
-  pl.begins = round((size_t)pl.G * sizeof(int2)) + 256;  // and the total
+  pl.joins = round((size_t)pl.G * sizeof(int4));
   pl.errors = round((size_t)pl.row_tiles * pl.G * 2 * sizeof(DeviceStatus));
   pl.ml = parts * 2 * kRows * sizeof(float);
   pl.o = parts * kRows * kLatentC * sizeof(float);
@@ -823,7 +858,7 @@ size_t latent_decode_scratch_bytes(int32_t B, int32_t T, int32_t H, int32_t dr) 
   (void)B;
   (void)dr;
   const Plan pl = make_plan(T, H);
-  return pl.begins + pl.errors + pl.ml + pl.o;
+  return pl.joins + pl.errors + pl.ml + pl.o;
 }
 
 cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t stream) {
@@ -863,17 +898,18 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t stream)
   p.scale2 = a.scale * kLog2e;
   p.out = static_cast<__nv_bfloat16 *>(a.out); p.lse = a.lse; p.status = a.status;
   unsigned char *ws = static_cast<unsigned char *>(a.scratch);
-  p.begins = reinterpret_cast<int2 *>(ws);
-  p.total = reinterpret_cast<int32_t *>(ws + pl.begins - 256);
-  p.errors = reinterpret_cast<DeviceStatus *>(ws + pl.begins);
-  p.part_ml = reinterpret_cast<float *>(ws + pl.begins + pl.errors);
-  p.part_o = reinterpret_cast<float *>(ws + pl.begins + pl.errors + pl.ml);
+  p.joins = reinterpret_cast<int4 *>(ws);
+  p.errors = reinterpret_cast<DeviceStatus *>(ws + pl.joins);
+  p.part_ml = reinterpret_cast<float *>(ws + pl.joins + pl.errors);
+  p.part_o = reinterpret_cast<float *>(ws + pl.joins + pl.errors + pl.ml);
   kda_latent_decode_kernel<<<2 * pl.G * pl.row_tiles, kThreads, kSmem, stream>>>(mq, mc, p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((R + 31) / 32 * (kLatentC / kJoinCh)),
-                     (unsigned)(pl.G > 2 ? pl.G - 1 : 1));
+  const bool many = pl.G > 7 * (int64_t)a.B;           // parts of a sequence
+  const int borders = pl.G - 1 < a.B ? pl.G - 1 : a.B;  // a sequence is joined at one
+  cfg.gridDim = dim3((unsigned)((R + 31) / 32 * (kLatentC / kJoinCh / (many ? 1 : kJoinWarps))),
+                     (unsigned)(borders + 1));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -881,7 +917,8 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t stream)
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kda_latent_join_kernel, p);
+  return cudaLaunchKernelEx(
+      &cfg, many ? kda_latent_join_kernel<true> : kda_latent_join_kernel<false>, p);
 }
 
 }  // namespace kda

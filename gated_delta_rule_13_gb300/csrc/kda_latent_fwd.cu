@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(256) kda_latent_fwd_join_kernel(const Params p
   float ref = kNoRef, l = 0.f, o[16];
 #pragma unroll
   for (int c = 0; c < 16; ++c) o[c] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
   for (int i = 0; i < it.parts; ++i) {
     const int64_t at = (slot0 + i) * 2 + t;
     const float4 *x =
