@@ -27,7 +27,7 @@ __device__ __forceinline__ int64_t row_of(const int32_t *__restrict__ table, int
 }
 
 constexpr int kWriteThreads = 128;
-constexpr int kWriteBatch = 8;   // rows in flight per thread
+constexpr int kWriteBatch = 4;   // rows in flight per thread
 
 // Block (x: 16-byte columns, y: sequence, z: layer).  The sequence's row moves
 // (source row, destination row) are worked out once per block, in shared memory,
@@ -35,10 +35,16 @@ constexpr int kWriteBatch = 8;   // rows in flight per thread
 //
 // Compaction moves row start + path[i] to row start + i inside the pool.  With a
 // strictly increasing path, path[i] >= i, and a thread reads its column of rows
-// i .. i + 7 before it writes them: a later read path[j] >= j > i + 7 never meets
+// i .. i + 3 before it writes them: a later read path[j] >= j > i + 3 never meets
 // a row already written, and no other thread touches the column.  So no second
 // buffer and no barrier between reads and writes is needed.  A path that is not
 // increasing is refused for its sequence (status).
+//
+// Bound by latency (three dependent reads: start, block table, row), then by HBM: one
+// row of 1,152 bytes for each of 64 sequences 4.3 us on the device, 7.8 with the call;
+// the accepted rows of 16 drafts, 256 sequences, 24 layers at once, 12.3 us with the
+// pool's rows in L2, 15.7 without.  With 1, 4, 8 and 16 rows in flight a thread: 12.4,
+// 12.3, 12.8, 20.6 us (one row at a time: 5.8 us for the first).
 template <bool kCompact>
 __global__ void __launch_bounds__(kWriteThreads)
 kda_cache_write_kernel(CacheWriteArgs a) {
@@ -94,7 +100,9 @@ constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 4;   // 16-byte loads in flight per thread
 
 // Block (x: piece of a page, y: layer, z: pair).  A pair out of range, or a page
-// copied onto itself, moves nothing.
+// copied onto itself, moves nothing.  Each byte is read and written once, past the
+// caches: 16 states of 3 layers, 604 MB both ways, 89.6 us, 6.7 TB/s, the rate of a
+// plain copy; one page of 24 layers 5.9 us, the launch.
 __global__ void __launch_bounds__(kCopyThreads)
 kda_cache_copy_pages_kernel(unsigned char *pool, const int32_t *__restrict__ src,
                             const int32_t *__restrict__ dst, int32_t n_pages, int64_t page_bytes,

@@ -12,7 +12,8 @@ namespace {
 
 constexpr int kThreads = 1024;
 
-// One block; sequence by sequence in rounds of 1024, the sum carried along.
+// One block; sequence by sequence in rounds of 1024, the sum carried along.  Bound by
+// latency: 5.3 us for 64 sequences, 9 for 4096.
 __global__ void __launch_bounds__(kThreads)
 kda_latent_plan_kernel(const Packed p, int32_t *mem, int64_t stride, DeviceStatus *status) {
   __shared__ int32_t warp_sum[kThreads / 32];

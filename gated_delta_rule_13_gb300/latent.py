@@ -197,18 +197,22 @@ def kda_latent_bwd(q, k, v, k_rope, out, lse, d_out, cu_seqlens_q=None, cu_seqle
     _tensor("lse", lse, _F32, (n_q, H), dev)
     _tensor("d_out", d_out, _BF16, (n_q, H, HEAD_DIM), dev)
     dq = _new(stream, q.shape, _BF16, dev)
+    k_strides = v_strides = (H * HEAD_DIM, HEAD_DIM)
     if d_k is None:
         d_k = _new(stream, (n_k, H, HEAD_DIM), _BF16, dev)
+    else:
+        k_strides = _view("d_k", d_k, n_k, H, dev)
     if d_v is None:
         d_v = _new(stream, (n_k, H, HEAD_DIM), _BF16, dev)
-    strides = _view("d_k", d_k, n_k, H, dev) + _view("d_v", d_v, n_k, H, dev)
+    else:
+        v_strides = _view("d_v", d_v, n_k, H, dev)
     d_rope = _new(stream, (n_k, dr), _BF16, dev) if dr else None
     ws = _workspace(workspace, kda_latent_bwd_workspace_size(n_seqs, n_q, n_k, H, dr=dr), dev,
                     stream)
     _check(library().kda_latent_bwd(*head, 1 if causal else 0, out.data_ptr(), lse.data_ptr(),
                                     d_out.data_ptr(), dq.data_ptr(), d_k.data_ptr(),
-                                    d_v.data_ptr(), d_rope.data_ptr() if dr else None, *strides,
-                                    ws.data_ptr(), ws.nbytes, _stream(stream, dev)),
+                                    d_v.data_ptr(), d_rope.data_ptr() if dr else None,
+                                    *k_strides, *v_strides, ws.data_ptr(), ws.nbytes, _stream(stream, dev)),
            "kda_latent_bwd")
     return dq, d_k, d_v, d_rope
 
