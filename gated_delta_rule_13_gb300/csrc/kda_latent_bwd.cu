@@ -80,7 +80,9 @@ struct Shared {
 };
 enum { kNoPass, kKeysPass, kQueriesPass };
 constexpr int kItemUsers = 11;           // loader, MMA, cleaner, eight elementwise warps
-constexpr int kAhead = 4;                // tiles before an item's last, the next is asked for
+// Tiles before an item's last, the next is asked for: finding it takes about 2 us.
+// (4 x 4096 tokens: 871 us; 874 with 2, 878 with 1.)
+constexpr int kAhead = 4;
 // What a role has behind it in a pass: streamed tiles, items that streamed any, and
 // those of them whose last tile was cleaned.
 struct Behind {
@@ -173,8 +175,8 @@ __device__ __forceinline__ void store_cols(uint32_t col, float mul, bool zero, _
 // Zeroes rows [from, n) of the `blocks` 64-channel blocks of a streamed tile: they are
 // another sequence's and may hold anything, and as operands of the sums 0 * NaN would
 // reach the result.
-__device__ __forceinline__ void clean_rows(uint32_t tile, int blocks, uint32_t block_bytes, int from,
-                                           int n, int lane) {
+__device__ __forceinline__ void clean_rows(uint32_t tile, int blocks, uint32_t block_bytes,
+                                           int from, int n, int lane) {
   for (int b = 0; b < blocks; ++b)
     for (int j = lane; j < (n - from) * 8; j += 32)
       st_shared_v4(tile + b * block_bytes + from * 128 + j * 16, 0, 0, 0, 0);
@@ -186,8 +188,9 @@ __device__ __forceinline__ void clean_rows(uint32_t tile, int blocks, uint32_t b
 // columns of TMEM: two S buffers and one dP, so the tensor cores run S two tiles ahead
 // and dP one ahead of the elementwise work.  Tiles of 64 queries: with the 80 KB of X,
 // 96 of them fit shared memory only once, and S and dP would need 288 columns.
-struct Span {                            // of an item
-  int x0, first, n, live;                // rows from x0; n streamed tiles from `first`; rows of the last
+// Of an item: its rows from x0, n streamed tiles from `first` on, `live` rows of the last.
+struct Span {
+  int x0, first, n, live;
 };
 // Longest first: the first keys are seen by the most queries.
 __device__ __forceinline__ Span keys_span(const SeqTile &st, int causal) {
@@ -1057,7 +1060,9 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
   p.lse2 = lse2; p.delta = delta; p.rope = delta + p.stat_rows * a.H;
   p.status = a.status;
   // as many items as there can be (one sequence: exactly that many)
-  auto most = [&](int64_t n) { return n == 0 ? 0 : a.n_seqs == 1 ? (n + kX - 1) / kX : n / kX + a.n_seqs; };
+  auto most = [&](int64_t n) {
+    return n == 0 ? 0 : a.n_seqs == 1 ? (n + kX - 1) / kX : n / kX + a.n_seqs;
+  };
   const int64_t blocks = (most(a.n_k) + most(a.n_q)) * a.H;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   auto kernel = kda_latent_bwd_kernel<DR>;
@@ -1072,7 +1077,8 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
   }
   // starts while the statistics' kernel ends, and waits for it before it reads them.
   // (The kernel after this one starts in the usual way: launched early it makes this one
-  // slower, 67 against 64 us for all three on 1,847 tokens in five sequences, 16 heads.)
+  // slower: all three, replayed from a graph, take 67 us and not 64 on 1,847 tokens in
+  // five sequences, 16 heads.)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kThreads);

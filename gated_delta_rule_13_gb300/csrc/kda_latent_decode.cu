@@ -81,7 +81,7 @@ struct Shared {
   float ref[2][kRows];                   // reference after a tile, by its parity
   float2 part[kRows];                    // the last but one tile's warpgroup: its sum, and of what
 };
-constexpr uint32_t kSharedBytes = 3072;
+constexpr uint32_t kSharedBytes = 3 * 1024;
 static_assert(sizeof(Shared) <= kSharedBytes, "fits beside the tiles");
 
 struct Params {

@@ -101,7 +101,9 @@ constexpr uint32_t smem_bytes() {
   return 1024 + q_bytes<DR>() + slots<DR>() * kSlotBytes + sizeof(Shared);
 }
 
-constexpr int kAhead = 4;                // key tiles before an item's last, the next one is asked for
+// Key tiles before an item's last, the next item is asked for: finding it takes about
+// 2 us.  (4 x 4096 tokens: 240 us; 242 with 2, 244 with 1.)
+constexpr int kAhead = 4;
 constexpr int kMinPart = 4;              // key tiles of a part, at least
 
 struct Params : Packed {
@@ -496,128 +498,128 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
     int done = 0, outs = 0;                              // key tiles and outputs of items before
     bool ok = true;
     for (int k = 0; ok; ++k) {
-    ok = warp_wait(cx, &m.item_full[k & 1], (k >> 1) & 1, 42, k);
-    const Item &item = m.item[k & 1];                    // read where needed: few registers
-    const SeqTile &st = item.tile;
-    if (!ok || st.seq < 0) break;
-    const int row = item.row0 + 128 * t + r;             // of the sequence
-    const int n_t = item.nt[t];
-    // keys this row sees, counted from the first of the part
-    int limit = st.nk;
-    if (p.causal) limit = min(limit, row + st.nk - st.nq + 1);
-    limit -= item.i0 * kKeys;
-    float ref = kNoRef, l = 0.f;
-    for (int i = 0; i < n_t; ++i) {
-      ok = warp_wait(cx, &m.s_full[t], (done + i) & 1, 40, i);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t x[4][32];
+      ok = warp_wait(cx, &m.item_full[k & 1], (k >> 1) & 1, 42, k);
+      const Item &item = m.item[k & 1];                    // read where needed: few registers
+      const SeqTile &st = item.tile;
+      if (!ok || st.seq < 0) break;
+      const int row = item.row0 + 128 * t + r;             // of the sequence
+      const int n_t = item.nt[t];
+      // keys this row sees, counted from the first of the part
+      int limit = st.nk;
+      if (p.causal) limit = min(limit, row + st.nk - st.nq + 1);
+      limit -= item.i0 * kKeys;
+      float ref = kNoRef, l = 0.f;
+      for (int i = 0; i < n_t; ++i) {
+        ok = warp_wait(cx, &m.s_full[t], (done + i) & 1, 40, i);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t x[4][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(tm_s + 32 * c, x[c]);
+        for (int c = 0; c < 4; ++c) tmem_ld32(tm_s + 32 * c, x[c]);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld_wait(x[c]);
-      const int seen = limit - i * kKeys;                // columns below it are allowed
-      if (__any_sync(0xffffffffu, seen < kKeys)) {
+        for (int c = 0; c < 4; ++c) tmem_ld_wait(x[c]);
+        const int seen = limit - i * kKeys;                // columns below it are allowed
+        if (__any_sync(0xffffffffu, seen < kKeys)) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (32 * c + j >= seen) x[c][j] = __float_as_uint(-CUDART_INF_F);
+            for (int j = 0; j < 32; ++j)
+              if (32 * c + j >= seen) x[c][j] = __float_as_uint(-CUDART_INF_F);
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = __uint_as_float(x[c][0]);
+#pragma unroll
+          for (int j = 1; j < 32; ++j) mx[c] = fmaxf(mx[c], __uint_as_float(x[c][j]));
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale2;
+        if (__any_sync(0xffffffffu, top > ref + kSlack)) {
+          const float now = fmaxf(ref, top), f = ex2(ref - now);
+          ref = now;
+          l *= f;
+          if (i > 0) {
+            // S of this tile was issued after the product of the tile before, so its
+            // completion covers that product
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tm_o + 32 * c, o);
+              tmem_ld_wait(o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st32(tm_o + 32 * c, o);
+            }
+          }
+        }
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float a = ex2(fmaf(__uint_as_float(x[c][j]), p.scale2, -ref));
+            const float b = ex2(fmaf(__uint_as_float(x[c][j + 1]), p.scale2, -ref));
+            sum[(j >> 1) & 3] += a + b;
+            pk[j / 2] = pack_bf16x2(a, b);
+          }
+          tmem_st16(tm_s + 16 * c, pk);
+          if (c & 1) {  // 64 keys are ready for their product
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m.p_ready[t][c >> 1]);
+          }
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       }
-      float mx[4];
+      // ---- output
+      if (ok && n_t > 0) ok = warp_wait(cx, &m.o_full[t], outs & 1, 41, n_t);
+      if (!ok) break;
+      if (n_t > 0) tc_fence_after();
+      done += n_t;
+      outs += n_t > 0;
+      const bool live = row < st.nq;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int64_t at = (int64_t)item.slot * 2 + t;       // of a part
+      const int64_t to = (st.q0 + row) * (int64_t)p.H + item.head;
+      if (item.parts > 1) {
+        p.part_ml[at * 256 + r] = ref;
+        p.part_ml[at * 256 + 128 + r] = l;
+      } else if (live) {
+        p.lse[to] = l == 0.f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
+      }
+      const bool parts = item.parts > 1;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        mx[c] = __uint_as_float(x[c][0]);
+        uint32_t o[32];
+        if (n_t > 0) {
+          tmem_ld32(tm_o + 32 * c, o);
+          tmem_ld_wait(o);
+        } else {
 #pragma unroll
-        for (int j = 1; j < 32; ++j) mx[c] = fmaxf(mx[c], __uint_as_float(x[c][j]));
-      }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale2;
-      if (__any_sync(0xffffffffu, top > ref + kSlack)) {
-        const float now = fmaxf(ref, top), f = ex2(ref - now);
-        ref = now;
-        l *= f;
-        if (i > 0) {
-          // S of this tile was issued after the product of the tile before, so its
-          // completion covers that product
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tm_o + 32 * c, o);
-            tmem_ld_wait(o);
+          for (int j = 0; j < 32; ++j) o[j] = 0;
+        }
+        if (parts) {  // four channels of the 32 rows beside one another
+          uint4 *w = reinterpret_cast<uint4 *>(p.part_o) + (at * (kLatentD / 4) + 8 * c) * 128 + r;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-            tmem_st32(tm_o + 32 * c, o);
+          for (int j = 0; j < 8; ++j)
+            w[j * 128] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        } else if (live) {
+          uint4 *w = reinterpret_cast<uint4 *>(p.out + to * kLatentD) + 4 * c;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t b[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              b[j] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * j]) * inv,
+                                 __uint_as_float(o[8 * q + 2 * j + 1]) * inv);
+            w[q] = make_uint4(b[0], b[1], b[2], b[3]);
           }
         }
       }
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const float a = ex2(fmaf(__uint_as_float(x[c][j]), p.scale2, -ref));
-          const float b = ex2(fmaf(__uint_as_float(x[c][j + 1]), p.scale2, -ref));
-          sum[(j >> 1) & 3] += a + b;
-          pk[j / 2] = pack_bf16x2(a, b);
-        }
-        tmem_st16(tm_s + 16 * c, pk);
-        if (c & 1) {  // 64 keys are ready for their product
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&m.p_ready[t][c >> 1]);
-        }
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-    }
-    // ---- output
-    if (ok && n_t > 0) ok = warp_wait(cx, &m.o_full[t], outs & 1, 41, n_t);
-    if (!ok) break;
-    if (n_t > 0) tc_fence_after();
-    done += n_t;
-    outs += n_t > 0;
-    const bool live = row < st.nq;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t at = (int64_t)item.slot * 2 + t;       // of a part
-    const int64_t to = (st.q0 + row) * (int64_t)p.H + item.head;
-    if (item.parts > 1) {
-      p.part_ml[at * 256 + r] = ref;
-      p.part_ml[at * 256 + 128 + r] = l;
-    } else if (live) {
-      p.lse[to] = l == 0.f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
-    }
-    const bool parts = item.parts > 1;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t o[32];
-      if (n_t > 0) {
-        tmem_ld32(tm_o + 32 * c, o);
-        tmem_ld_wait(o);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = 0;
-      }
-      if (parts) {  // four channels of the 32 rows beside one another
-        uint4 *w = reinterpret_cast<uint4 *>(p.part_o) + (at * (kLatentD / 4) + 8 * c) * 128 + r;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          w[j * 128] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-      } else if (live) {
-        uint4 *w = reinterpret_cast<uint4 *>(p.out + to * kLatentD) + 4 * c;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t b[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            b[j] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * j]) * inv,
-                               __uint_as_float(o[8 * q + 2 * j + 1]) * inv);
-          w[q] = make_uint4(b[0], b[1], b[2], b[3]);
-        }
-      }
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&m.item_free[k & 1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.item_free[k & 1]);
     }
   }
 

@@ -7,7 +7,8 @@ import torch
 
 import gated_delta_rule_13_gb300 as pkg
 from gated_delta_rule_13_gb300 import kda
-from test_gpu_latent import DEV, _bwd, _decode_problem, _fwd, _problem, _randn
+from test_gpu_latent import (DEV, _bwd, _decode_problem, _fwd, _problem, _randn, check_both,
+                             check_decode)
 
 pytestmark = pytest.mark.gpu
 REPEATS = 100
@@ -45,3 +46,21 @@ def test_decode(lens, T, H):
                      dtype=torch.uint8, device=DEV)
     _same(lambda: [pkg.kda_latent_decode(x["q"], x["cache"], x["table"], x["lens"],
                                          workspace=ws)], ws)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dr", [0, 64])
+@pytest.mark.parametrize("lens_q,lens_k,H", [
+    ([0, 300, 0, 1, 700, 0], [900, 300, 128, 3000, 700, 64], 24),   # keys nobody queries
+    ([1] * 40 + [129], [1] * 20 + [0] * 20 + [129], 40),            # items of one tile, rows without keys
+    ([513], [513], 96),
+])
+def test_many_items_a_block(lens_q, lens_k, H, dr, causal):
+    """A block works through many items of different lengths, some of them empty."""
+    check_both(_problem(lens_q, lens_k, H, dr), causal=causal)
+
+
+@pytest.mark.parametrize("B", [1, 2, 9, 10, 11, 12, 40])
+def test_joined_sequences(B):
+    """Few sequences have many parts to join, many sequences have few."""
+    check_decode(_decode_problem([1500 + 7 * b for b in range(B)], 1, 40, 64, 64))
