@@ -76,9 +76,16 @@ def _new(stream, shape, dtype, device):
 
 
 def _stream(stream, device):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    """The raw stream of a call.  The kernels launch on the current device, and what is
+    asked of a device (its SMs, whether a kernel fits) is asked of that one."""
+    if torch.cuda.current_device() != device.index:
+        raise ValueError(f"the tensors are on {device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()} (torch.cuda.set_device)")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+    return stream.cuda_stream
 
 
 def _scale(scale, dim):
@@ -134,9 +141,15 @@ def _workspace(workspace, size, device, stream):
     return workspace
 
 
+def _device():
+    """Index of the current device; without one in use, a number of its own."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+
+
 @functools.lru_cache(maxsize=1024)
-def _size(fn, *args):
-    """A workspace size: it follows from the sizes and the device's SM count alone."""
+def _size(fn, device, *args):
+    """A workspace size: it follows from the sizes and the SM count of the current
+    device, whose index is ``device``."""
     out = ctypes.c_size_t(0)
     _check(getattr(library(), fn)(*args, ctypes.byref(out)), fn)
     return out.value
@@ -144,16 +157,18 @@ def _size(fn, *args):
 
 def kda_latent_fwd_workspace_size(n_seqs, n_q, n_k, H, dk=HEAD_DIM, dr=0, dv=HEAD_DIM,
                                   dtype=KDA_BF16) -> int:
-    return _size("kda_latent_fwd_workspace_size", n_seqs, n_q, n_k, H, dk, dr, dv, dtype)
+    return _size("kda_latent_fwd_workspace_size", _device(), n_seqs, n_q, n_k, H, dk, dr, dv,
+                 dtype)
 
 
 def kda_latent_bwd_workspace_size(n_seqs, n_q, n_k, H, dk=HEAD_DIM, dr=0, dv=HEAD_DIM,
                                   dtype=KDA_BF16) -> int:
-    return _size("kda_latent_bwd_workspace_size", n_seqs, n_q, n_k, H, dk, dr, dv, dtype)
+    return _size("kda_latent_bwd_workspace_size", _device(), n_seqs, n_q, n_k, H, dk, dr, dv,
+                 dtype)
 
 
 def kda_latent_decode_workspace_size(B, T, H, dc=LATENT_DIM, dr=0, dtype=KDA_BF16) -> int:
-    return _size("kda_latent_decode_workspace_size", B, T, H, dc, dr, dtype)
+    return _size("kda_latent_decode_workspace_size", _device(), B, T, H, dc, dr, dtype)
 
 
 def kda_latent_fwd(q, k, v, k_rope=None, cu_seqlens_q=None, cu_seqlens_k=None, *, causal=True,
@@ -169,6 +184,7 @@ def kda_latent_fwd(q, k, v, k_rope=None, cu_seqlens_q=None, cu_seqlens_k=None, *
     defaults to 1 / sqrt(128 + dr).  Returns ``(out [n_q, H, 128], lse [n_q, H])``."""
     head, sizes, dev = _expanded(q, k, v, k_rope, cu_seqlens_q, cu_seqlens_k, scale)
     n_seqs, n_q, n_k, H, dr = sizes
+    raw = _stream(stream, dev)
     if out is None:
         out = _new(stream, (n_q, H, HEAD_DIM), _BF16, dev)
     else:
@@ -180,7 +196,7 @@ def kda_latent_fwd(q, k, v, k_rope=None, cu_seqlens_q=None, cu_seqlens_k=None, *
     ws = _workspace(workspace, kda_latent_fwd_workspace_size(n_seqs, n_q, n_k, H, dr=dr), dev,
                     stream)
     _check(library().kda_latent_fwd(*head, 1 if causal else 0, out.data_ptr(), lse.data_ptr(),
-                                    ws.data_ptr(), ws.nbytes, _stream(stream, dev)),
+                                    ws.data_ptr(), ws.nbytes, raw),
            "kda_latent_fwd")
     return out, lse
 
@@ -193,6 +209,7 @@ def kda_latent_bwd(q, k, v, k_rope, out, lse, d_out, cu_seqlens_q=None, cu_seqle
     ``d_v`` may be given as strided views, as k and v may."""
     head, sizes, dev = _expanded(q, k, v, k_rope, cu_seqlens_q, cu_seqlens_k, scale)
     n_seqs, n_q, n_k, H, dr = sizes
+    raw = _stream(stream, dev)
     _tensor("out", out, _BF16, (n_q, H, HEAD_DIM), dev)
     _tensor("lse", lse, _F32, (n_q, H), dev)
     _tensor("d_out", d_out, _BF16, (n_q, H, HEAD_DIM), dev)
@@ -212,7 +229,7 @@ def kda_latent_bwd(q, k, v, k_rope, out, lse, d_out, cu_seqlens_q=None, cu_seqle
     _check(library().kda_latent_bwd(*head, 1 if causal else 0, out.data_ptr(), lse.data_ptr(),
                                     d_out.data_ptr(), dq.data_ptr(), d_k.data_ptr(),
                                     d_v.data_ptr(), d_rope.data_ptr() if dr else None,
-                                    *k_strides, *v_strides, ws.data_ptr(), ws.nbytes, _stream(stream, dev)),
+                                    *k_strides, *v_strides, ws.data_ptr(), ws.nbytes, raw),
            "kda_latent_bwd")
     return dq, d_k, d_v, d_rope
 
@@ -232,6 +249,7 @@ def kda_latent_decode(q, cache, block_table, seq_lens, *, tree_mask=None, scale=
     if not isinstance(q, torch.Tensor) or not q.is_cuda:
         raise TypeError("q must be a CUDA tensor")
     dev = q.device
+    raw = _stream(stream, dev)
     _tensor("q", q, _BF16, None, dev)
     if q.dim() != 4 or q.shape[3] not in (LATENT_DIM, LATENT_DIM + ROPE_DIM):
         raise ValueError(f"q must be [B, T, H, 512] or [B, T, H, 576], got {tuple(q.shape)}")
@@ -258,7 +276,7 @@ def kda_latent_decode(q, cache, block_table, seq_lens, *, tree_mask=None, scale=
         None if tree_mask is None else tree_mask.data_ptr(), B, T, H, LATENT_DIM, dr,
         cache.shape[0], cache.shape[1], block_table.shape[1], KDA_BF16,
         _scale(scale, HEAD_DIM + dr), out.data_ptr(), None if lse is None else lse.data_ptr(),
-        ws.data_ptr(), ws.nbytes, _stream(stream, dev)), "kda_latent_decode")
+        ws.data_ptr(), ws.nbytes, raw), "kda_latent_decode")
     return out
 
 
@@ -284,6 +302,7 @@ def kda_cache_write(cache, rows, block_table, start, *, path=None, n_write=None,
     if not isinstance(cache, torch.Tensor) or not cache.is_cuda:
         raise TypeError("cache must be a CUDA tensor")
     dev, dtype = cache.device, cache.dtype
+    raw = _stream(stream, dev)
     _tensor("cache", cache, dtype, None, dev)
     layered = cache.dim() == 4
     if not layered and cache.dim() != 3:
@@ -334,7 +353,7 @@ def kda_cache_write(cache, rows, block_table, start, *, path=None, n_write=None,
         return cache
     _check(library().kda_cache_write(
         cache.data_ptr(), at_rows, ls, bs, ts, block_table.data_ptr(), start.data_ptr(), at_path,
-        at_n, L, n_pages, page, W * esz, B, T, max_pages, at_status, _stream(stream, dev)),
+        at_n, L, n_pages, page, W * esz, B, T, max_pages, at_status, raw),
         "kda_cache_write")
     return cache
 
@@ -347,6 +366,7 @@ def kda_cache_copy_pages(cache, src, dst, *, status=None, stream=None):
     if not isinstance(cache, torch.Tensor) or not cache.is_cuda:
         raise TypeError("cache must be a CUDA tensor")
     dev = cache.device
+    raw = _stream(stream, dev)
     _tensor("cache", cache, cache.dtype, None, dev)
     if cache.dim() < 3:
         raise ValueError("cache must be [L, n_pages, ...]")
@@ -361,6 +381,6 @@ def kda_cache_copy_pages(cache, src, dst, *, status=None, stream=None):
         return cache
     page_bytes = math.prod(cache.shape[2:]) * cache.element_size()
     _check(library().kda_cache_copy_pages(cache.data_ptr(), src.data_ptr(), dst.data_ptr(), n, L,
-                                          n_pages, page_bytes, at_status, _stream(stream, dev)),
+                                          n_pages, page_bytes, at_status, raw),
            "kda_cache_copy_pages")
     return cache
