@@ -42,6 +42,9 @@ struct TestControl {
 static_assert(sizeof(DeviceStatus) <= kTestControlOffset, "status block layout");
 static_assert(kTestControlOffset + sizeof(TestControl) <= kStatusBytes, "status block layout");
 
+// n host numbers to device memory, in stream order; src is read before the return.
+cudaError_t put_ints(int32_t *dst, const int32_t *src, int64_t n, cudaStream_t stream);
+
 // Helper CTAs of the tensor-core prefill.  When a call has fewer chains than the
 // GPU has SMs, the idle SMs run "helpers" that compute the state-independent
 // half of chunks ahead of the chain CTAs: the operand build, the Gram matrix,

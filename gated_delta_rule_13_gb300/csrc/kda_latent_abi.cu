@@ -65,7 +65,14 @@ size_t span_bytes(int64_t ts, int64_t hs, int32_t H, int64_t n) {
   return n == 0 ? 0 : (size_t)((n - 1) * ts + (int64_t)(H - 1) * hs + kda::kLatentD) * 2;
 }
 
-// Host arrays are validated and copied to `dst`; device arrays are used as they are.
+int cuda_result(cudaError_t e) {
+  if (e == cudaSuccess) return KDA_OK;
+  cudaGetLastError();
+  return e == cudaErrorNotSupported ? KDA_ERR_UNSUPPORTED : KDA_ERR_CUDA;
+}
+
+// Host arrays are validated and taken to `dst` (the caller may write or free them after
+// the call, also between replays of a captured one); device arrays are used as they are.
 int resolve_cu(const int32_t *cu, int32_t n_seqs, int64_t n, void *dst, cudaStream_t st,
                const int32_t **dev) {
   *dev = nullptr;
@@ -81,19 +88,9 @@ int resolve_cu(const int32_t *cu, int32_t n_seqs, int64_t n, void *dst, cudaStre
   if (cu[0] != 0 || cu[n_seqs] != n) return KDA_ERR_INVALID_ARG;
   for (int32_t s = 0; s < n_seqs; ++s)
     if (cu[s + 1] < cu[s]) return KDA_ERR_INVALID_ARG;
-  *dev = static_cast<const int32_t *>(dst);
-  if (cudaMemcpyAsync(dst, cu, sizeof(int32_t) * ((size_t)n_seqs + 1), cudaMemcpyHostToDevice,
-                      st) != cudaSuccess) {
-    cudaGetLastError();
-    return KDA_ERR_CUDA;
-  }
-  return KDA_OK;
-}
-
-int cuda_result(cudaError_t e) {
-  if (e == cudaSuccess) return KDA_OK;
-  cudaGetLastError();
-  return e == cudaErrorNotSupported ? KDA_ERR_UNSUPPORTED : KDA_ERR_CUDA;
+  int32_t *to = static_cast<int32_t *>(dst);
+  *dev = to;
+  return cuda_result(kda::put_ints(to, cu, (int64_t)n_seqs + 1, st));
 }
 
 // Fields, checks and device cu_seqlens shared by both directions.

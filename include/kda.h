@@ -587,7 +587,9 @@ int kda_latent_fwd_workspace_size(int32_t n_seqs, int64_t n_q, int64_t n_k, int3
  *   k_rope  [n_k, dr] bf16, NULL if and only if dr = 0
  *   cu_seqlens_q, cu_seqlens_k  [n_seqs + 1] int32, prefix sums of the query
  *           and key counts, each host or device memory (rules as kda_chunk_fwd:
- *           host arrays are validated here; device arrays in the kernel, which
+ *           host arrays are validated here and read before the return, so that
+ *           the caller may write or free them, also where the call is captured;
+ *           device arrays are validated in the kernel, which
  *           then writes nothing and records KDA_ERR_INVALID_ARG in the status).
  *           NULL, if n_seqs = 1: one sequence of all the rows
  *   causal  non-zero: query i of a sequence with nq queries and nk keys sees
