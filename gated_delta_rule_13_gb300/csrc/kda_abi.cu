@@ -238,8 +238,7 @@ int kda_chunk_bwd_sched(const void *q, const void *k, const void *v, const float
     for (int32_t s = 0; s < n_seqs; ++s)
       if (cu_seqlens[s + 1] < cu_seqlens[s]) return KDA_ERR_INVALID_ARG;
     int32_t *dst = reinterpret_cast<int32_t *>(ws + lay.cu);
-    if (cudaMemcpyAsync(dst, cu_seqlens, sizeof(int32_t) * ((size_t)n_seqs + 1),
-                        cudaMemcpyHostToDevice, st) != cudaSuccess) {
+    if (kda::put_ints(dst, cu_seqlens, (int64_t)n_seqs + 1, st) != cudaSuccess) {
       cudaGetLastError();
       return KDA_ERR_CUDA;
     }
@@ -355,13 +354,13 @@ int kda_chunk_fwd_sched(const void *q, const void *k, const void *v, const float
   const int32_t *cu_dev = cu_seqlens;
   unsigned char *ws = static_cast<unsigned char *>(workspace);
   if (!cu_on_device) {
-    // Host array: validate it here, then stage a device copy in the workspace.
+    // Host array: validate it here, then take it to the workspace (read before the return:
+    // the caller may write or free it, also between replays of a captured call).
     if (cu_seqlens[0] != 0 || cu_seqlens[n_seqs] != n_tokens) return KDA_ERR_INVALID_ARG;
     for (int32_t s = 0; s < n_seqs; ++s)
       if (cu_seqlens[s + 1] < cu_seqlens[s]) return KDA_ERR_INVALID_ARG;
     int32_t *dst = reinterpret_cast<int32_t *>(ws + kStatusBytes);
-    if (cudaMemcpyAsync(dst, cu_seqlens, sizeof(int32_t) * ((size_t)n_seqs + 1),
-                        cudaMemcpyHostToDevice, st) != cudaSuccess) {
+    if (kda::put_ints(dst, cu_seqlens, (int64_t)n_seqs + 1, st) != cudaSuccess) {
       cudaGetLastError();
       return KDA_ERR_CUDA;
     }
@@ -507,8 +506,7 @@ int kda_chunk_fwd_transitions(const void *q, const void *k, const void *v,
     for (int32_t s = 0; s < n_seqs; ++s)
       if (cu_seqlens[s + 1] < cu_seqlens[s]) return KDA_ERR_INVALID_ARG;
     int32_t *dst = reinterpret_cast<int32_t *>(ws + kStatusBytes);
-    if (cudaMemcpyAsync(dst, cu_seqlens, sizeof(int32_t) * ((size_t)n_seqs + 1),
-                        cudaMemcpyHostToDevice, st) != cudaSuccess) {
+    if (kda::put_ints(dst, cu_seqlens, (int64_t)n_seqs + 1, st) != cudaSuccess) {
       cudaGetLastError();
       return KDA_ERR_CUDA;
     }

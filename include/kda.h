@@ -124,8 +124,10 @@ int kda_chunk_fwd_workspace_size(int32_t n_seqs, int64_t n_tokens, int32_t H, in
  *              copied, not advanced in place: same page, section 7.4).
  *   cu_seqlens [S + 1] int32, cu_seqlens[0] = 0, non-decreasing,
  *              cu_seqlens[S] = N.  May be host or device memory: a host array
- *              is validated here (KDA_ERR_INVALID_ARG on failure) and copied
- *              into the workspace; a device array is validated by the kernel,
+ *              is validated here (KDA_ERR_INVALID_ARG on failure) and taken
+ *              into the workspace before the return (the caller may write or
+ *              free it, also where the call is captured); a device array is
+ *              validated by the kernel,
  *              which then writes nothing and records KDA_ERR_INVALID_ARG in
  *              the device status.
  *   dtype      KDA_F32 (fp32 CUDA-core path) or KDA_BF16 (tcgen05 tensor-core
