@@ -74,7 +74,7 @@ struct Shared {
   uint32_t tmem;
   int abort;
   int seq0, tile0, total;                // the pair's first sequence and tile, all tiles
-  int warp_sum[kThreads / 32];
+  int64_t warp_sum[kThreads / 32];
   uint32_t load_pos;                     // tiles loaded, segments begun (loader)
   int load_seg;
   DeviceStatus error;                    // the CTA's first error
@@ -109,7 +109,8 @@ __device__ __forceinline__ int seq_len(const Params &p, int b) {
   const int n = p.lens[b];
   return n < 0 || n > (int64_t)p.max_pages * p.page_size ? 0 : n;
 }
-__device__ __forceinline__ int key_tiles(int n) { return (n + kTile - 1) / kTile; }
+// (n reaches 2^31 - 1: nothing may be added to it)
+__device__ __forceinline__ int key_tiles(int n) { return n / kTile + (n % kTile != 0); }
 
 // First tile of pair c of G when the list has `total` tiles: the first total % G
 // pairs take one more than the others.
@@ -218,30 +219,34 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
   {  // the pair's share of the tile list
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = tid * per, b1 = min(p.B, b0 + per);
-    int mine = 0;
+    int64_t mine = 0;                    // sequences may share pages: no pool bounds the sum
     bool bad = false;
     for (int b = b0; b < b1; ++b) {
       const int n = p.lens[b];
       if (n < 0 || n > (int64_t)p.max_pages * p.page_size) bad = true;
       else mine += key_tiles(n);
     }
-    int inc = mine;
+    int64_t inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
     if (lane == 31) m.warp_sum[warp] = inc;
     __syncthreads();
     if (bad) record_device_status(&m.error, KDA_ERR_INVALID_ARG, 1, b0, 0);
-    int before = inc - mine, total = 0;
+    int64_t before = inc - mine, all = 0;
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) before += m.warp_sum[w];
-      total += m.warp_sum[w];
+      all += m.warp_sum[w];
     }
+    // tiles are counted in 32 bits from here on; a list that is longer is refused
+    const int total = all > 0x7fffffff ? 0 : (int)all;
+    if (all > 0x7fffffff && tid == 0)
+      record_device_status(&m.error, KDA_ERR_INVALID_ARG, 3, 0, 0);
     const int begin = pair_begin(slice, p.G, total);
-    if (begin >= before && begin < before + mine) {
-      int at = before;
+    if (total > 0 && begin >= before && begin < before + mine) {
+      int at = (int)before;
       for (int b = b0; b < b1; ++b) {
         const int k = key_tiles(seq_len(p, b));
         if (begin < at + k) {
@@ -287,8 +292,9 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
       const int n = walk.n;
       // pool row of this lane's box of tile t, -1: nothing to load
       auto box_row = [&](int t) {
+        if (piece >= pieces || t >= walk.tb) return -1;
         const int at = t * kTile + piece * p.box_rows;
-        if (piece >= pieces || at >= n || t >= walk.tb) return -1;
+        if (at >= n) return -1;
         const int page = at / p.page_size;
         const int32_t id = p.table[(int64_t)b * p.max_pages + page];
         if (id < 0 || id >= p.n_pages) {
@@ -413,7 +419,7 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
       const int live = walk.n - (walk.tb - 1) * kTile;
       if (live >= kTile) continue;
       const int s = (pos - 1) % NS;
-      ok = warp_wait(cx, &m.clean_req[s], asked >> s & 1, 30, walk.tb) &&
+      ok = warp_wait<kLongWaits>(cx, &m.clean_req[s], asked >> s & 1, 30, walk.tb) &&
            warp_wait(cx, &m.full[s], ((pos - 1) / NS) & 1, 31, walk.tb);
       if (!ok) break;
       asked ^= 1u << s;
@@ -508,7 +514,7 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
             x[c][4 * j + 2] = __float_as_uint(__uint_as_float(x[c][4 * j + 2]) + y.z);
             x[c][4 * j + 3] = __float_as_uint(__uint_as_float(x[c][4 * j + 3]) + y.w);
           }
-        if ((t + 1) * kTile > t_draft) {                // the drafts' own tiles and the end
+        if (t * kTile > t_draft - kTile) {              // the drafts' own tiles and the end
           const int live = min(kTile, n - t * kTile), d0 = t_draft - t * kTile;
           // bit j: this row sees key j of the tile
           uint64_t see = live >= 64 ? ~0ull : (1ull << live) - 1;

@@ -92,6 +92,10 @@ struct WaitCtx {
   DeviceStatus *status;
   int chain;
 };
+// kTimes: limits it waits.  A wait as long as a work item takes (kLongWaits) leaves it to
+// those it waits for to give up first.
+constexpr int kLongWaits = 32;
+template <int kTimes = 1>
 __device__ __forceinline__ bool wait_or_abort(const WaitCtx &cx, uint64_t *bar, uint32_t parity,
                                               int where, int step) {
   if (mbar_test_wait(bar, parity)) return true;
@@ -101,7 +105,7 @@ __device__ __forceinline__ bool wait_or_abort(const WaitCtx &cx, uint64_t *bar, 
     for (int i = 0; i < 16; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*cx.abort) return false;
-    if (global_timer_ns() - t0 > kWaitNs) {
+    if (global_timer_ns() - t0 > kTimes * kWaitNs) {
       record_device_status(cx.status, KDA_ERR_TIMEOUT, where, cx.chain, step);
       *cx.abort = 1;
       return false;
@@ -110,20 +114,21 @@ __device__ __forceinline__ bool wait_or_abort(const WaitCtx &cx, uint64_t *bar, 
 }
 
 // The same by a converged warp, whose lanes leave together.
+template <int kTimes = 1>
 __device__ __forceinline__ bool warp_wait(const WaitCtx &cx, uint64_t *bar, uint32_t parity,
                                           int where, int step) {
   if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
-  return __all_sync(0xffffffffu, wait_or_abort(cx, bar, parity, where, step)) != 0;
+  return __all_sync(0xffffffffu, wait_or_abort<kTimes>(cx, bar, parity, where, step)) != 0;
 }
 
 // For waits as long as a work item takes, by a warp that is in no hurry: it sleeps
-// between looks, and leaves it to those it waits for to give up first.
+// between looks.
 __device__ __forceinline__ bool warp_wait_idle(const WaitCtx &cx, uint64_t *bar, uint32_t parity,
                                                int where, int step) {
   const uint64_t t0 = global_timer_ns();
   while (!__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) {
     if (__any_sync(0xffffffffu, *cx.abort)) return false;
-    if (__any_sync(0xffffffffu, global_timer_ns() - t0 > 32 * kWaitNs)) {
+    if (__any_sync(0xffffffffu, global_timer_ns() - t0 > kLongWaits * kWaitNs)) {
       record_device_status(cx.status, KDA_ERR_TIMEOUT, where, cx.chain, step);
       *cx.abort = 1;
       return false;

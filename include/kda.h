@@ -669,6 +669,8 @@ int kda_latent_decode_workspace_size(int32_t B, int32_t T, int32_t H, int32_t dc
  * A sequence length that is negative or beyond max_pages * page_size, or a page
  * id outside [0, n_pages), records KDA_ERR_INVALID_ARG in the status; nothing
  * outside the pool is read, and that sequence's output is undefined.
+ * All sequences together have at most 2^31 - 1 tiles of 64 rows; more record
+ * KDA_ERR_INVALID_ARG, and no output but the empty sequences' is written.
  * Alignment: q, cache, out 16 bytes; block_table, seq_lens, lse 4; tree_mask 8.
  * Errors as kda_latent_fwd (B at most 65535, T * H at most 2^24,
  * n_pages * page_size and max_pages * page_size at most 2^31 - 1).
