@@ -78,9 +78,10 @@ def _new(stream, shape, dtype, device):
 def _stream(stream, device):
     """The raw stream of a call.  The kernels launch on the current device, and what is
     asked of a device (its SMs, whether a kernel fits) is asked of that one."""
-    if torch.cuda.current_device() != device.index:
+    current = torch._C._cuda_getDevice()   # the tensors exist: CUDA is initialised
+    if current != device.index:
         raise ValueError(f"the tensors are on {device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()} (torch.cuda.set_device)")
+                         f"cuda:{current} (torch.cuda.set_device)")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device.index)
     if stream.device != device:
@@ -143,7 +144,7 @@ def _workspace(workspace, size, device, stream):
 
 def _device():
     """Index of the current device; without one in use, a number of its own."""
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
 
 
 @functools.lru_cache(maxsize=1024)
@@ -193,8 +194,8 @@ def kda_latent_fwd(q, k, v, k_rope=None, cu_seqlens_q=None, cu_seqlens_k=None, *
         lse = _new(stream, (n_q, H), _F32, dev)
     else:
         _tensor("lse", lse, _F32, (n_q, H), dev)
-    ws = _workspace(workspace, kda_latent_fwd_workspace_size(n_seqs, n_q, n_k, H, dr=dr), dev,
-                    stream)
+    ws = _workspace(workspace, _size("kda_latent_fwd_workspace_size", dev.index, n_seqs, n_q, n_k,
+                                     H, HEAD_DIM, dr, HEAD_DIM, KDA_BF16), dev, stream)
     _check(library().kda_latent_fwd(*head, 1 if causal else 0, out.data_ptr(), lse.data_ptr(),
                                     ws.data_ptr(), ws.nbytes, raw),
            "kda_latent_fwd")
@@ -224,8 +225,8 @@ def kda_latent_bwd(q, k, v, k_rope, out, lse, d_out, cu_seqlens_q=None, cu_seqle
     else:
         v_strides = _view("d_v", d_v, n_k, H, dev)
     d_rope = _new(stream, (n_k, dr), _BF16, dev) if dr else None
-    ws = _workspace(workspace, kda_latent_bwd_workspace_size(n_seqs, n_q, n_k, H, dr=dr), dev,
-                    stream)
+    ws = _workspace(workspace, _size("kda_latent_bwd_workspace_size", dev.index, n_seqs, n_q, n_k,
+                                     H, HEAD_DIM, dr, HEAD_DIM, KDA_BF16), dev, stream)
     _check(library().kda_latent_bwd(*head, 1 if causal else 0, out.data_ptr(), lse.data_ptr(),
                                     d_out.data_ptr(), dq.data_ptr(), d_k.data_ptr(),
                                     d_v.data_ptr(), d_rope.data_ptr() if dr else None,
@@ -270,7 +271,8 @@ def kda_latent_decode(q, cache, block_table, seq_lens, *, tree_mask=None, scale=
         _tensor("out", out, _BF16, (B, T, H, LATENT_DIM), dev)
     if lse is not None:
         _tensor("lse", lse, _F32, (B, T, H), dev)
-    ws = _workspace(workspace, kda_latent_decode_workspace_size(B, T, H, dr=dr), dev, stream)
+    ws = _workspace(workspace, _size("kda_latent_decode_workspace_size", dev.index, B, T, H,
+                                     LATENT_DIM, dr, KDA_BF16), dev, stream)
     _check(library().kda_latent_decode(
         q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
         None if tree_mask is None else tree_mask.data_ptr(), B, T, H, LATENT_DIM, dr,

@@ -17,7 +17,7 @@ DEV = torch.device("cuda:0")
 def current(monkeypatch):
     """Sets what the binding takes for the current device."""
     def set_to(index):
-        monkeypatch.setattr(torch.cuda, "current_device", lambda: index)
+        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: index, raising=False)
         monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
     return set_to
 
@@ -48,8 +48,8 @@ def test_workspace_sizes_are_kept_by_device(current, monkeypatch):
     class Library:
         def __getattr__(self, name):
             def size(*args):
-                asked.append(torch.cuda.current_device())
-                args[-1]._obj.value = 1000 * (1 + torch.cuda.current_device())
+                asked.append(torch._C._cuda_getDevice())
+                args[-1]._obj.value = 1000 * (1 + torch._C._cuda_getDevice())
                 return 0
             return size
 
