@@ -14,6 +14,14 @@ constexpr int kLatentC = 512;    // latent channels of a cached row
 constexpr int kLatentRope = 64;  // rotary channels (or none)
 constexpr int kTreeMax = 64;     // drafts a tree mask can describe
 
+// The bound on any wait in these kernels and, for a test, a block (none: -1) whose loader
+// withholds tile `tile` of its first item, so that the waits for that tile run out.
+struct WaitTest {
+  uint64_t wait_ns;
+  int32_t block, tile;
+};
+constexpr uint64_t kWaitNs = 2000000000ull;
+
 // Expanded form: packed sequences, keys and values per head.
 struct LatentArgs {
   const void *q;       // [n_q, H, 128 + dr]
@@ -34,6 +42,7 @@ struct LatentArgs {
   void *dq, *dk, *dv, *d_k_rope;
   int64_t dk_ts, dk_hs, dv_ts, dv_hs;
   void *scratch;       // latent_fwd_scratch_bytes() or latent_bwd_scratch_bytes()
+  WaitTest test;
 };
 cudaError_t launch_latent_fwd(const LatentArgs &a, cudaStream_t stream);
 cudaError_t launch_latent_bwd(const LatentArgs &a, cudaStream_t stream);
@@ -53,6 +62,7 @@ struct LatentDecodeArgs {
   float *lse;                 // [B, T, H] or nullptr
   DeviceStatus *status;
   void *scratch;              // latent_decode_scratch_bytes()
+  WaitTest test;
 };
 cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t stream);
 size_t latent_decode_scratch_bytes(int32_t B, int32_t T, int32_t H, int32_t dr);

@@ -5,6 +5,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "../../include/kda.h"
 #include "kda_latent.h"
 
@@ -93,6 +95,17 @@ int resolve_cu(const int32_t *cu, int32_t n_seqs, int64_t n, void *dst, cudaStre
   return cuda_result(kda::put_ints(to, cu, (int64_t)n_seqs + 1, st));
 }
 
+// Test control of the waits: armed for one workspace, taken by the next call with it.
+std::atomic<const void *> g_test_workspace{nullptr};
+kda::WaitTest g_test;
+kda::WaitTest take_test(const void *workspace) {
+  const void *mine = workspace;
+  if (g_test_workspace.load(std::memory_order_relaxed) == workspace &&
+      g_test_workspace.compare_exchange_strong(mine, nullptr))
+    return g_test;
+  return {kda::kWaitNs, -1, -1};
+}
+
 // Fields, checks and device cu_seqlens shared by both directions.
 int prepare(kda::LatentArgs &a, int32_t dk, int32_t dv, int dtype, const int32_t *cu_q,
             const int32_t *cu_k, const float *lse) {
@@ -164,6 +177,7 @@ int kda_latent_fwd(const void *q, const void *k, const void *v, const void *k_ro
   const int r = begin(a, cu_seqlens_q, cu_seqlens_k, ws, st);
   if (r != KDA_OK) return r;
   a.scratch = ws + base_bytes(n_seqs);
+  a.test = take_test(workspace);
   return cuda_result(kda::launch_latent_fwd(a, st));
 }
 
@@ -229,6 +243,7 @@ int kda_latent_bwd(const void *q, const void *k, const void *v, const void *k_ro
   const int r = begin(a, cu_seqlens_q, cu_seqlens_k, ws, st);
   if (r != KDA_OK) return r;
   a.scratch = ws + base_bytes(n_seqs);
+  a.test = take_test(workspace);
   return cuda_result(kda::launch_latent_bwd(a, st));
 }
 
@@ -285,7 +300,18 @@ int kda_latent_decode(const void *q, const void *cache, const int32_t *block_tab
   a.page_size = page_size; a.max_pages = max_pages; a.scale = scale; a.out = out; a.lse = lse;
   a.status = reinterpret_cast<kda::DeviceStatus *>(ws);
   a.scratch = ws + kStatusBytes;
+  a.test = take_test(workspace);
   return cuda_result(kda::launch_latent_decode(a, st));
+}
+
+int kda_latent_test_timeout(const void *workspace, int32_t block, int32_t tile, uint32_t wait_us) {
+  if (!workspace || (block >= 0 && (tile < 0 || wait_us < 1 || wait_us > 2000000)))
+    return KDA_ERR_INVALID_ARG;
+  g_test_workspace.store(nullptr);
+  if (block < 0) return KDA_OK;
+  g_test = {1000ull * wait_us, block, tile};
+  g_test_workspace.store(workspace);
+  return KDA_OK;
 }
 
 int kda_cache_write(void *cache, const void *rows, int64_t rows_layer_stride,

@@ -131,7 +131,13 @@ struct Params : Packed {
   const float *lse2, *delta;             // [H][stat_rows]
   float *rope;                           // [H][n_k][64]
   DeviceStatus *status;
+  WaitTest test;
 };
+
+// A test lets the waits for tile i of the block's item k run out.
+__device__ __forceinline__ bool withheld(const Params &p, int k, int i) {
+  return k == 0 && i == p.test.tile && p.test.block == (int)blockIdx.x;
+}
 
 // Row statistics are kept per head in tiles of 64 that no two sequences share:
 // the first tile of sequence s is floor(q0 / 64) + s.
@@ -246,6 +252,8 @@ __device__ __forceinline__ void keys_pass(const Maps &maps, const Params &p, Sha
         tma_load_3d_u(base + (KB + c) * kXBlock, &maps.v128, &m.x_full, 64 * c, head, xr);
       ++did.items;
       for (int i = 0; i < sp.n; ++i) {
+        if (withheld(p, k, i)) ok = false;
+        if (!ok) break;
         if (i == max(0, sp.n - kAhead)) mbar_arrive(&sh.want);
         const uint32_t g = did.tiles, s = g % ST;
         if (g >= ST) ok = wait_or_abort(cx, &m.empty[s], (g / ST - 1) & 1, 10, i);
@@ -533,6 +541,8 @@ __device__ __forceinline__ void queries_pass(const Maps &maps, const Params &p, 
         tma_load_3d_u(base + kb * kXBlock, &maps.q128, &m.x_full, 64 * kb, head, xr);
       const uint32_t x2 = did.items++ & 1;       // phase of this item's d_out
       for (int i = 0; i < sp.n; ++i) {
+        if (withheld(p, k, i)) ok = false;
+        if (!ok) break;
         if (i == max(0, sp.n - kAhead)) mbar_arrive(&sh.want);
         const int yr = st.k0 + i * 128;
         const uint32_t g = did.tiles, sk = g % KT, sv = g % VT;
@@ -844,7 +854,7 @@ kda_latent_bwd_kernel(const __grid_constant__ Maps maps, const Params p) {
     __syncthreads();
     tc_fence_after();
   };
-  const WaitCtx cx{&sh.abort, p.status, (int)blockIdx.x};
+  const WaitCtx cx{&sh.abort, p.status, (int)blockIdx.x, p.test.wait_ns};
 
   if (warp == kItemWarp) {
     // ---- items: publishes this block's, and takes over the next one when the loader
@@ -1059,6 +1069,7 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t stream) {
   float *delta = lse2 + p.stat_rows * a.H;
   p.lse2 = lse2; p.delta = delta; p.rope = delta + p.stat_rows * a.H;
   p.status = a.status;
+  p.test = a.test;
   // as many items as there can be (one sequence: exactly that many)
   auto most = [&](int64_t n) {
     return n == 0 ? 0 : a.n_seqs == 1 ? (n + kX - 1) / kX : n / kX + a.n_seqs;

@@ -102,6 +102,7 @@ struct Params {
   int4 *joins;          // [G] of the border before a pair: sequence, parts (0: none), slot
   float *part_o;        // [row tiles][G][2][512 / 4][128 rows][4]
   float *part_ml;       // [row tiles][G][2][2][128]
+  WaitTest test;
 };
 
 // Length of sequence b, 0 when it is out of range.
@@ -276,7 +277,7 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
   }
   const int begin = pair_begin(slice, p.G, m.total);
   const int mine = pair_begin(slice + 1, p.G, m.total) - begin;
-  const WaitCtx cx{&m.abort, &m.error, (int)blockIdx.x};
+  const WaitCtx cx{&m.abort, &m.error, (int)blockIdx.x, p.test.wait_ns};
   Walk walk(p, m.seq0, m.tile0, mine);
   int b;
 
@@ -315,6 +316,10 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
       }
       ++seg;
       for (int t = walk.ta; t < walk.tb; ++t) {
+        if ((int)pos == p.test.tile && p.test.block == (int)blockIdx.x) {
+          ok = false;                    // a test: the waits for this tile run out
+          break;
+        }
         const int row_next = box_row(t + 1);
         if (pos >= NS) ok = warp_wait(cx, &m.empty[s], (pos / NS - 1) & 1, 11, t);
         if (ok && rope && pos >= NR) ok = warp_wait(cx, &m.rope_free[sr], (pos / NR - 1) & 1, 12, t);
@@ -399,7 +404,7 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
         if (*cx.abort) break;
         const uint64_t now = global_timer_ns();
         if (idle == 0) idle = now;
-        if (now - idle > kWaitNs) {
+        if (now - idle > cx.wait_ns) {
           record_device_status(cx.status, KDA_ERR_TIMEOUT, 20, cx.chain, (int)pos);
           *cx.abort = 1;
           break;
@@ -684,7 +689,7 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
         mbar_wait(&m.full[k % NS], (k / NS) & 1, kWaitNs);
       if (m.load_seg > 0) mbar_wait(&m.q_full, (m.load_seg - 1) & 1, kWaitNs);
     }
-    if (tid == 32 * kMmaWarp) {
+    if (warp == kMmaWarp && elect_one()) {  // of the lane that issued the products
       umma_commit(&m.fin);
       mbar_wait(&m.fin, 0, kWaitNs);
       const uint64_t t0 = global_timer_ns();
@@ -917,6 +922,7 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t stream)
   p.errors = reinterpret_cast<DeviceStatus *>(ws + pl.joins);
   p.part_ml = reinterpret_cast<float *>(ws + pl.joins + pl.errors);
   p.part_o = reinterpret_cast<float *>(ws + pl.joins + pl.errors + pl.ml);
+  p.test = a.test;
   kda_latent_decode_kernel<<<2 * pl.G * pl.row_tiles, kThreads, kSmem, stream>>>(mq, mc, p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;

@@ -18,7 +18,6 @@ namespace latent {
 
 using namespace sm100;
 
-constexpr uint64_t kWaitNs = 2000000000ull;  // limit of any wait in these kernels
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Reference of a softmax row that has met no key yet: finite, so that masked
@@ -91,6 +90,7 @@ struct WaitCtx {
   volatile int *abort;
   DeviceStatus *status;
   int chain;
+  uint64_t wait_ns;
 };
 // kTimes: limits it waits.  A wait as long as a work item takes (kLongWaits) leaves it to
 // those it waits for to give up first.
@@ -105,7 +105,7 @@ __device__ __forceinline__ bool wait_or_abort(const WaitCtx &cx, uint64_t *bar, 
     for (int i = 0; i < 16; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (*cx.abort) return false;
-    if (global_timer_ns() - t0 > kTimes * kWaitNs) {
+    if (global_timer_ns() - t0 > kTimes * cx.wait_ns) {
       record_device_status(cx.status, KDA_ERR_TIMEOUT, where, cx.chain, step);
       *cx.abort = 1;
       return false;
@@ -128,7 +128,7 @@ __device__ __forceinline__ bool warp_wait_idle(const WaitCtx &cx, uint64_t *bar,
   const uint64_t t0 = global_timer_ns();
   while (!__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) {
     if (__any_sync(0xffffffffu, *cx.abort)) return false;
-    if (__any_sync(0xffffffffu, global_timer_ns() - t0 > kLongWaits * kWaitNs)) {
+    if (__any_sync(0xffffffffu, global_timer_ns() - t0 > kLongWaits * cx.wait_ns)) {
       record_device_status(cx.status, KDA_ERR_TIMEOUT, where, cx.chain, step);
       *cx.abort = 1;
       return false;

@@ -37,7 +37,8 @@ EXPORTED = ("kda_status_string", "kda_version", "kda_chunk_fwd_workspace_size",
             "kda_chunk_bwd_workspace_size_sched",
             "kda_latent_fwd", "kda_latent_fwd_workspace_size", "kda_latent_bwd",
             "kda_latent_bwd_workspace_size", "kda_latent_decode",
-            "kda_latent_decode_workspace_size", "kda_cache_write", "kda_cache_copy_pages")
+            "kda_latent_decode_workspace_size", "kda_latent_test_timeout", "kda_cache_write",
+            "kda_cache_copy_pages")
 
 _lib = None
 
@@ -140,6 +141,8 @@ def library() -> ctypes.CDLL:
         lib.kda_latent_decode.restype = ci
         lib.kda_latent_decode.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32,
                                           i32, ci, f32, vp, vp, vp, sz, vp]
+        lib.kda_latent_test_timeout.restype = ci
+        lib.kda_latent_test_timeout.argtypes = [vp, i32, i32, ctypes.c_uint32]
         lib.kda_cache_write.restype = ci
         lib.kda_cache_write.argtypes = [vp, vp, i64, i64, i64, vp, vp, vp, vp, i32, i32, i32, i64,
                                         i32, i32, i32, vp, vp]

@@ -282,6 +282,15 @@ def kda_latent_decode(q, cache, block_table, seq_lens, *, tree_mask=None, scale=
     return out
 
 
+def kda_latent_test_timeout(workspace, block: int, tile: int = 0, wait_us: int = 1000):
+    """Test control of the bounded waits (see include/kda.h): the next latent-attention
+    call with ``workspace`` waits at most ``wait_us`` for anything, and block ``block``
+    withholds tile ``tile``; ``block < 0`` disarms."""
+    _need_cuda("workspace", workspace)
+    _check(library().kda_latent_test_timeout(workspace.data_ptr(), int(block), int(tile),
+                                             int(wait_us)), "kda_latent_test_timeout")
+
+
 def _status(status, device):
     if status is None:
         return None

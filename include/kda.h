@@ -682,6 +682,22 @@ int kda_latent_decode(const void *q, const void *cache, const int32_t *block_tab
                       void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * TEST CONTROL of the bounded waits of latent attention (fault-handling tests only).
+ * Arms the next kda_latent_fwd, kda_latent_bwd or kda_latent_decode call with this
+ * `workspace`: every wait of its kernels is bounded by `wait_us` microseconds (of work
+ * items: 32 times that), and the loader of block `block` withholds tile `tile` of its
+ * first work item.  The waits for that tile give up: the block records KDA_ERR_TIMEOUT
+ * with its number in the status (as the chain), waits for its copies and products,
+ * frees its tensor memory and returns, leaving the item's outputs, and those of the
+ * blocks it exchanges data with, undefined.  Nothing traps or waits without bound.  A
+ * number of a block or tile that the call has not changes the waits' bound alone;
+ * block < 0 disarms.  The call is on the host: nothing is launched.
+ * Errors: KDA_ERR_INVALID_ARG (NULL workspace; when arming, tile < 0 or wait_us outside
+ * [1, 2000000]).
+ */
+int kda_latent_test_timeout(const void *workspace, int32_t block, int32_t tile, uint32_t wait_us);
+
+/*
  * Rows of a paged cache [L, n_pages, page_size, row_bytes] (any element type),
  * all L layers in one call.  For every sequence b, with n = n_write[b] clamped
  * to [0, T] (n_write NULL: n = T), rows i = 0 .. n - 1 go to positions
