@@ -687,7 +687,7 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
       const uint32_t pos = m.load_pos;
       for (uint32_t k = pos > (uint32_t)NS ? pos - NS : 0; k < pos; ++k)
         mbar_wait(&m.full[k % NS], (k / NS) & 1, kWaitNs);
-      if (m.load_seg > 0) mbar_wait(&m.q_full, (m.load_seg - 1) & 1, kWaitNs);
+      if (rope && m.load_seg > 0) mbar_wait(&m.q_full, (m.load_seg - 1) & 1, kWaitNs);
     }
     if (warp == kMmaWarp && elect_one()) {  // of the lane that issued the products
       umma_commit(&m.fin);

@@ -100,6 +100,23 @@ def test_decode(block, tile, dr):
     _gave_up(run, ws, want, block, tile, [block & ~1, block | 1])
 
 
+@pytest.mark.parametrize("dr", [0, 64])
+@pytest.mark.parametrize("block", [0, 1])
+def test_decode_gives_up_in_time(block, dr):
+    """What is in flight is waited for, and nothing else: only one CTA of a pair, and only
+    with a rotary part, copies queries.  (The limit of those waits is two seconds.)"""
+    x = _decode_problem([3000, 5000], 1, 16, dr, 64)
+    ws = torch.empty(pkg.kda_latent_decode_workspace_size(2, 1, 16, dr=dr), dtype=torch.uint8,
+                     device=DEV)
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    latent.kda_latent_test_timeout(ws, block, 0, WAIT_US)
+    begin.record()
+    pkg.kda_latent_decode(x["q"], x["cache"], x["table"], x["lens"], workspace=ws)
+    end.record()
+    assert _status(ws)[0] == kda.KDA_ERR_TIMEOUT
+    assert begin.elapsed_time(end) < 1000
+
+
 def test_a_control_that_meets_nothing():
     x = _problem([100], [100], H=1, dr=0)
     ws = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
