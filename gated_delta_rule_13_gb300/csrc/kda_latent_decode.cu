@@ -110,8 +110,9 @@ __device__ __forceinline__ int seq_len(const Params &p, int b) {
   const int n = p.lens[b];
   return n < 0 || n > (int64_t)p.max_pages * p.page_size ? 0 : n;
 }
-// (n reaches 2^31 - 1: nothing may be added to it)
-__device__ __forceinline__ int key_tiles(int n) { return n / kTile + (n % kTile != 0); }
+static_assert(kTile == 64, "tiles are counted with shifts");
+// (n reaches 2^31 - 1: nothing may be added to it.)
+__device__ __forceinline__ int key_tiles(int n) { return (n >> 6) + ((n & 63) != 0); }
 
 // First tile of pair c of G when the list has `total` tiles: the first total % G
 // pairs take one more than the others.
@@ -519,7 +520,7 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
             x[c][4 * j + 2] = __float_as_uint(__uint_as_float(x[c][4 * j + 2]) + y.z);
             x[c][4 * j + 3] = __float_as_uint(__uint_as_float(x[c][4 * j + 3]) + y.w);
           }
-        if (t * kTile > t_draft - kTile) {              // the drafts' own tiles and the end
+        if (t_draft - t * kTile < kTile) {              // the drafts' own tiles and the end
           const int live = min(kTile, n - t * kTile), d0 = t_draft - t * kTile;
           // bit j: this row sees key j of the tile
           uint64_t see = live >= 64 ? ~0ull : (1ull << live) - 1;
