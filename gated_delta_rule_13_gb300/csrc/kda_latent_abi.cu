@@ -73,6 +73,31 @@ int cuda_result(cudaError_t e) {
   return e == cudaErrorNotSupported ? KDA_ERR_UNSUPPORTED : KDA_ERR_CUDA;
 }
 
+// Whether two such views of equal strides have an element in common: whether their
+// distance is, but for less than a row, a number of tokens plus a number of heads that
+// both lie within a view.  One stride spans all rows of the other (strides_ok), so that
+// two numbers of the longer and, for each, two of the shorter come into question.
+bool views_overlap(const void *a, const void *b, int64_t ts, int64_t hs, int32_t H, int64_t n) {
+  if (n == 0) return false;
+  const int64_t far = (int64_t)1 << 62, d = kda::kLatentD;
+  const int64_t dist = (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a)) / 2;
+  struct Dim {
+    int64_t stride, count;
+  } x = {n > 1 ? ts : far, n}, y = {H > 1 ? hs : far, H};
+  const Dim big = x.stride >= y.stride ? x : y, small = x.stride >= y.stride ? y : x;
+  auto down = [](int64_t v, int64_t by) { return v / by - (v % by < 0); };
+  for (int64_t i = down(dist, big.stride), i1 = i + 1; i <= i1; ++i) {
+    if (i <= -big.count || i >= big.count) continue;
+    const int64_t left = dist - i * big.stride;
+    for (int64_t j = down(left, small.stride), j1 = j + 1; j <= j1; ++j) {
+      if (j <= -small.count || j >= small.count) continue;
+      const int64_t off = left - j * small.stride;
+      if (off > -d && off < d) return true;
+    }
+  }
+  return false;
+}
+
 // Host arrays are validated and taken to `dst` (the caller may write or free them after
 // the call, also between replays of a captured one); device arrays are used as they are.
 int resolve_cu(const int32_t *cu, int32_t n_seqs, int64_t n, void *dst, cudaStream_t st,
@@ -227,13 +252,16 @@ int kda_latent_bwd(const void *q, const void *k, const void *v, const void *k_ro
                       {out, rows * dv * 2},
                       {lse, rows * 4},
                       {d_out, rows * dv * 2}};
-  // d_k and d_v may be two interleaved views of one tensor: their spans are
-  // checked against everything but each other.
+  // d_k and d_v may be two interleaved views of one tensor: their spans are checked
+  // against everything but each other, their rows against each other's where the
+  // strides are equal, as those of such views are.
   const Range o1[] = {{dq, rows * (dk + dr) * 2}, {d_k_rope, (size_t)n_k * dr * 2},
                       {d_k, span_bytes(a.dk_ts, a.dk_hs, H, n_k)}};
   const Range o2[] = {{dq, rows * (dk + dr) * 2}, {d_k_rope, (size_t)n_k * dr * 2},
                       {d_v, span_bytes(a.dv_ts, a.dv_hs, H, n_k)}};
-  if (any_overlap(in, o1) || any_overlap(in, o2) || (n_k > 0 && d_k == d_v))
+  const bool alike = (n_k <= 1 || a.dk_ts == a.dv_ts) && (H <= 1 || a.dk_hs == a.dv_hs);
+  if (any_overlap(in, o1) || any_overlap(in, o2) || (n_k > 0 && d_k == d_v) ||
+      (alike && views_overlap(d_k, d_v, a.dk_ts, a.dk_hs, H, n_k)))
     return KDA_ERR_INVALID_ARG;
   const size_t scratch = round_up(kda::latent_bwd_scratch_bytes(n_seqs, n_q, n_k, H, dr), 256);
   if (!workspace || !aligned(workspace, 16) || workspace_bytes < base_bytes(n_seqs) + scratch)

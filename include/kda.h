@@ -631,7 +631,8 @@ int kda_latent_bwd_workspace_size(int32_t n_seqs, int64_t n_q, int64_t n_k, int3
  *   one tensor).
  * Every element of every gradient is written exactly once, by one thread, from
  * sums in a fixed order: results do not vary between calls.  Other rules as
- * kda_latent_fwd; no output may overlap an input or another output.
+ * kda_latent_fwd; no output may overlap an input or another output (refused, but for
+ * rows of d_k and d_v that meet although their strides differ).
  */
 int kda_latent_bwd(const void *q, const void *k, const void *v, const void *k_rope,
                    int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
