@@ -19,15 +19,20 @@
 //
 // A block works through items, taking over blocks of the grid that have not started;
 // the next item's rows and first tiles arrive beside this one's last products and its
-// output, which leaves from registers because the buffers are the next item's by then.
+// output, which leaves from registers because the buffers are the next item's by then
+// (none of this holds across the change of pass, where the pipeline runs empty: with
+// under four items a block that costs more than it gains).
 // 4 x 4096 tokens, 16 heads: 920 us with a block for each item, 855 so; 32 x 512: 350 and
 // 288; five sequences of 1,847 tokens together, at under four items a block, 59 and 64.
 //
-// Measured (dr = 64, 16 heads): 4 x 4096 tokens 855 us, of it statistics 27, both passes
-// 813, rotary sums 14: 1.05 PFLOP/s of the formulas, 1.4 of what the two passes
-// compute, whose products alone are 2,624 tensor-core cycles for 64 x 128 pairs (S and
-// dP of the keys pass have 64 columns, which the tensor cores take at two thirds of
-// their rate).  Bound by these products and by the way S -> P -> dP -> dS between them.
+// Measured (16 heads, dr = 64): 4 x 4096 tokens 855 us (L2 warm, replayed), of it
+// statistics 27, both passes 813, rotary sums 14: 1.05 PFLOP/s of the formulas, 1.4 of
+// what the two passes compute, whose products alone are 2,624 tensor-core cycles for
+// 64 x 128 pairs (S and dP of the keys pass have 64 columns, which the tensor cores take
+// at two thirds of their rate).  The whole call on cold inputs: 917 us, 0.97 PFLOP/s.
+// 4 x 2048 tokens, the passes: 250 us with the tensor cores busy 54 % of the time and
+// DRAM 22 %; dr = 0: 215 us, 49 % and 21 %.  Bound by the products and by the way
+// S -> P -> dP -> dS between them.
 //
 // The rotary key is shared by the heads: every head leaves its fp32 gradient in
 // the workspace and a last kernel adds them in head order.

@@ -26,21 +26,27 @@
 // of O), O 256, S 64.  The rotary blocks of the tiles have a ring of their own,
 // because they are done with S.  A thread owns a row of every other tile; exponents
 // are taken against a reference per row, handed from tile to tile, that moves only
-// when a score exceeds it by more than 8 (log2), and only then O is rescaled.
+// when a score exceeds it by more than 8 (log2), and only then O is rescaled.  P is
+// rounded to bf16 (half a step, 2^-8 of the value) as an operand of the tensor cores;
+// the exchanged scores, sums, references and O are fp32.
 //
 // The 64-key tiles of all sequences form one list, cut evenly over the pairs
 // whatever the lengths.  A pair's first and last sequence may be shared with its
 // neighbours: it leaves (reference, sum, O) in the workspace and a second small
-// kernel joins the parts in the list's order.
+// kernel joins the parts in the list's order.  Every tile of 128 query rows has
+// pairs / row tiles pairs, rounded down: with 76 pairs 12 row tiles use 72 of them, 20
+// use 60, 39 use 39, and 77 take a second round for one.
 //
-// Measured (96 heads, dr = 64): one token of 128 sequences of up to 16384 rows, 1.2 GB,
-// 296 us, 4.2 TB/s (DRAM 55 % busy, tensor cores 42 %); trees of 16 drafts, 32
-// sequences, 1,107 us, 0.92 PFLOP/s; one token over 3001 rows, dr = 0, 20.5 us, all of
-// it start, one tile's way and the join.  The bound is that way: 24 KB are exchanged in
-// each direction at the 22 bytes a cycle that distributed shared memory gives (1,100
-// cycles), the products take 1,200 and HBM 0.84 us a tile; these overlap, but shared
-// memory has room for only four or five tiles at a time.  The copies alone, in the same
-// ring, run at 7.3 TB/s.
+// Measured (96 heads, dr = 64; whole calls, cold inputs): one token of 128 sequences of
+// up to 16384 rows, 1.2 GB, 297 us, 4.1 TB/s (DRAM 55 % busy, tensor cores 42 %); trees
+// of 16 drafts, 32 sequences, 1,114 us, 0.91 PFLOP/s (DRAM 5 %, tensor cores 37 %); one
+// token over 3001 rows, dr = 0, 20.5 us (replayed), all of it start, one tile's way and
+// the join.  A pair takes about 2,750 cycles a tile at 96 rows and 2,850 at 128, though
+// it then exchanges 32 KB and not 24 in each direction (1,490 and 1,100 cycles at the 22
+// bytes a cycle that distributed shared memory gave by itself).  The products take
+// 1,200, the copies at 96 rows 1,740 (by themselves, in the same ring, 7.3 TB/s).  So
+// none of them is the bound alone; what is left is a tile's way, of which two at most
+// overlap.  How its steps share the time has not been measured.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>

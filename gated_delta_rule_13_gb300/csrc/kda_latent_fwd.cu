@@ -12,10 +12,13 @@
 //   S_t = Q_t K^T     (shared-memory operands, 128 x 128 fp32 in TMEM)
 //   P_t               bf16, written by the softmax over S_t's own columns
 //   O_t += P_t V      (P_t from TMEM)
-// so TMEM holds exactly S_0, S_1, O_0, O_1.  A thread owns a query row.  Its
-// exponents are taken against a reference that only moves when a score exceeds it
-// by more than 8 (log2): O_t is then rescaled in TMEM, which after the first
-// tiles hardly ever happens.
+// so TMEM holds exactly S_0, S_1, O_0, O_1.  A thread owns a query row.  The softmax is
+// the one-pass form of Milakov and Gimelshein ("Online normalizer calculation for
+// softmax", 2018), with a reference that need not be the maximum: it only moves when a
+// score exceeds it by more than 8 (log2).  O_t is then rescaled in TMEM, which after
+// the first tiles hardly ever happens.  P is rounded to bf16 (half a step, 2^-8 of the
+// value) because it is an operand of the tensor cores; its sum, the reference and O
+// are fp32.
 //
 // Work items are (256 queries, head).  They run in groups of as many heads as fill the
 // SMs once, inside a group longest first: a group's keys are read by its tiles at
@@ -34,11 +37,14 @@
 // computed, beside the last products and the output.  4 x 4096 tokens, 16 heads: 247
 // us with a block for each item, 237 so.
 //
-// Measured (2,070 MHz, L2 warm; cold, as a layer finds it, 5 % more): 4 x 4096 tokens,
-// 16 heads, dr = 64: 237 us, 1.45 PFLOP/s, tensor cores busy 63 % of the time, DRAM
-// 15 %.  2048 queries over 32768 keys, 96 heads, dr = 0: 1,950 us, 1.65 PFLOP/s.  What
-// bounds it are the products with their waits: without the softmax (time only) it
-// takes 217 and 1,650 us, without the copies of keys and values 227 and 1,876.
+// Measured (2,070 MHz, L2 warm, replayed): 4 x 4096 tokens, 16 heads, dr = 64: 237 us,
+// 1.45 PFLOP/s, tensor cores busy 63 % of the time, DRAM 15 %.  2048 queries over 32768
+// keys, 96 heads, dr = 0: 1,950 us, 1.64 PFLOP/s.  Whole calls on cold inputs, as a
+// layer finds them: 254 and 2,077 us, 1.35 and 1.54 PFLOP/s.  What bounds it are the
+// products with their waits: without the softmax (time only, warm) it takes 217 and
+// 1,650 us, without the copies of keys and values 227 and 1,876.  A step of 256 x 128
+// pairs at dr = 64 moves about 345 KB through shared memory (operands of the products
+// and copies), 2,690 cycles at 128 bytes a cycle beside 2,560 of matrix work.
 // Handing P over in quarters (253 us), exponentials before the maximum is known (247)
 // and an issuing warp for each query tile (243; 2,150 for the second) were slower.
 #include <cuda_bf16.h>
@@ -468,7 +474,8 @@ kda_latent_fwd_kernel(const __grid_constant__ CUtensorMap map_q,
       // ---- cleaner: value rows past the sequence's end are another sequence's, and
       // may hold anything; zero them (0 * NaN would reach the sum).  The loader asks
       // once the copies of the last tile are under way.  It may ask for the next item
-      // too before this one's tile is used, but no further: two barriers each.
+      // too before this one's tile is used, but no further (the item after that is only
+      // published when all softmax warps are through with this one): two barriers each.
       int tiles_before = 0, cleans = 0;
       bool ok = true;
       for (int k = 0; ok; ++k) {

@@ -566,7 +566,9 @@ int kda_post_fwd(const void *o, const void *g, const float *gamma, int64_t n_tok
  * ds, are rounded to bf16 as operands of their matrix products).  A row that may
  * see no key gets o = 0 and lse = -inf.  Rows and keys outside a sequence never
  * reach its result, whatever they hold; inside a sequence all keys must be
- * finite (a masked key enters its product with a zero weight).
+ * finite (a masked key enters its product with a zero weight), and in the
+ * gradient so must queries and d_out.  Every call launches on the current device,
+ * which must be that of its memory and stream.
  */
 
 /*
@@ -615,8 +617,9 @@ int kda_latent_fwd(const void *q, const void *k, const void *v, const void *k_ro
                    int32_t dv, int dtype, float scale, int causal, void *out, float *lse,
                    void *workspace, size_t workspace_bytes, void *stream);
 
-/* Workspace of kda_latent_bwd (status, cu_seqlens copies, per-row statistics,
- * per-head gradients of the shared rotary key).  Errors as above. */
+/* Workspace of kda_latent_bwd (status, cu_seqlens copies, per-row statistics, 8 bytes a
+ * query and head, and with dr = 64 the per-head gradients of the shared rotary key, 256
+ * bytes a key and head: 3.2 GB for 96 heads and 131,072 keys).  Errors as above. */
 int kda_latent_bwd_workspace_size(int32_t n_seqs, int64_t n_q, int64_t n_k, int32_t H, int32_t dk,
                                   int32_t dr, int32_t dv, int dtype, size_t *bytes);
 
