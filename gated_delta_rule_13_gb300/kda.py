@@ -173,15 +173,25 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _need_current(what, device):
+    """The kernels launch on the current device: all they use has to be there."""
+    if device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"{what} is on {device}, but the current device is "
+                         f"cuda:{torch._C._cuda_getDevice()} (torch.cuda.set_device)")
+
+
 def _stream_handle(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
+    else:
+        _need_current("stream", stream.device)
     return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _need_cuda(name, t, dtype=None, shape=None):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
+    _need_current(name, t.device)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
