@@ -20,6 +20,8 @@ struct WaitTest {
   uint64_t wait_ns;
   int32_t block, tile;
 };
+// What kda_latent_test_timeout armed for this workspace, or the usual bounds.
+WaitTest take_wait_test(const void *workspace);
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // Expanded form: packed sequences, keys and values per head.

@@ -120,17 +120,6 @@ int resolve_cu(const int32_t *cu, int32_t n_seqs, int64_t n, void *dst, cudaStre
   return cuda_result(kda::put_ints(to, cu, (int64_t)n_seqs + 1, st));
 }
 
-// Test control of the waits: armed for one workspace, taken by the next call with it.
-std::atomic<const void *> g_test_workspace{nullptr};
-kda::WaitTest g_test;
-kda::WaitTest take_test(const void *workspace) {
-  const void *mine = workspace;
-  if (g_test_workspace.load(std::memory_order_relaxed) == workspace &&
-      g_test_workspace.compare_exchange_strong(mine, nullptr))
-    return g_test;
-  return {kda::kWaitNs, -1, -1};
-}
-
 // Fields, checks and device cu_seqlens shared by both directions.
 int prepare(kda::LatentArgs &a, int32_t dk, int32_t dv, int dtype, const int32_t *cu_q,
             const int32_t *cu_k, const float *lse) {
@@ -161,6 +150,17 @@ int begin(kda::LatentArgs &a, const int32_t *cu_q, const int32_t *cu_k, unsigned
 }
 
 }  // namespace
+
+// Test control of the waits: armed for one workspace, taken by the next call with it.
+static std::atomic<const void *> g_test_workspace{nullptr};
+static kda::WaitTest g_test;
+kda::WaitTest kda::take_wait_test(const void *workspace) {
+  const void *mine = workspace;
+  if (g_test_workspace.load(std::memory_order_relaxed) == workspace &&
+      g_test_workspace.compare_exchange_strong(mine, nullptr))
+    return g_test;
+  return {kda::kWaitNs, -1, -1};
+}
 
 extern "C" {
 
@@ -202,7 +202,7 @@ int kda_latent_fwd(const void *q, const void *k, const void *v, const void *k_ro
   const int r = begin(a, cu_seqlens_q, cu_seqlens_k, ws, st);
   if (r != KDA_OK) return r;
   a.scratch = ws + base_bytes(n_seqs);
-  a.test = take_test(workspace);
+  a.test = kda::take_wait_test(workspace);
   return cuda_result(kda::launch_latent_fwd(a, st));
 }
 
@@ -271,7 +271,7 @@ int kda_latent_bwd(const void *q, const void *k, const void *v, const void *k_ro
   const int r = begin(a, cu_seqlens_q, cu_seqlens_k, ws, st);
   if (r != KDA_OK) return r;
   a.scratch = ws + base_bytes(n_seqs);
-  a.test = take_test(workspace);
+  a.test = kda::take_wait_test(workspace);
   return cuda_result(kda::launch_latent_bwd(a, st));
 }
 
@@ -328,7 +328,7 @@ int kda_latent_decode(const void *q, const void *cache, const int32_t *block_tab
   a.page_size = page_size; a.max_pages = max_pages; a.scale = scale; a.out = out; a.lse = lse;
   a.status = reinterpret_cast<kda::DeviceStatus *>(ws);
   a.scratch = ws + kStatusBytes;
-  a.test = take_test(workspace);
+  a.test = kda::take_wait_test(workspace);
   return cuda_result(kda::launch_latent_decode(a, st));
 }
 

@@ -38,7 +38,10 @@ EXPORTED = ("kda_status_string", "kda_version", "kda_chunk_fwd_workspace_size",
             "kda_latent_fwd", "kda_latent_fwd_workspace_size", "kda_latent_bwd",
             "kda_latent_bwd_workspace_size", "kda_latent_decode",
             "kda_latent_decode_workspace_size", "kda_latent_test_timeout", "kda_cache_write",
-            "kda_cache_copy_pages")
+            "kda_cache_copy_pages", "kda_rope", "kda_norm_fwd", "kda_norm_bwd",
+            "kda_norm_bwd_workspace_size", "kda_latent_weights",
+            "kda_latent_weights_workspace_size", "kda_cache_evict",
+            "kda_cache_evict_workspace_size")
 
 _lib = None
 
@@ -148,6 +151,27 @@ def library() -> ctypes.CDLL:
                                         i32, i32, i32, vp, vp]
         lib.kda_cache_copy_pages.restype = ci
         lib.kda_cache_copy_pages.argtypes = [vp, vp, vp, i32, i32, i32, i64, vp, vp]
+        lib.kda_rope.restype = ci
+        lib.kda_rope.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, vp, vp, i64, i32,
+                                 i32, ci, f32, ci, ci, vp]
+        lib.kda_norm_fwd.restype = ci
+        lib.kda_norm_fwd.argtypes = [vp, i64, vp, vp, i64, i32, ci, ci, f32, vp, i64, vp, vp, vp]
+        lib.kda_norm_bwd_workspace_size.restype = ci
+        lib.kda_norm_bwd_workspace_size.argtypes = [i64, i32, ci, ctypes.POINTER(sz)]
+        lib.kda_norm_bwd.restype = ci
+        lib.kda_norm_bwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, i64, i32, ci, vp, i64, vp, vp,
+                                     vp, sz, vp]
+        lib.kda_latent_weights_workspace_size.restype = ci
+        lib.kda_latent_weights_workspace_size.argtypes = [i32, i32, i32, i32, i32, ci,
+                                                          ctypes.POINTER(sz)]
+        lib.kda_latent_weights.restype = ci
+        lib.kda_latent_weights.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32,
+                                           i32, i32, ci, f32, f32, vp, vp, sz, vp]
+        lib.kda_cache_evict_workspace_size.restype = ci
+        lib.kda_cache_evict_workspace_size.argtypes = [i32, i32, i32, ctypes.POINTER(sz)]
+        lib.kda_cache_evict.restype = ci
+        lib.kda_cache_evict.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i64, i32, i32, i32,
+                                        i32, i32, vp, vp, vp, sz, vp, vp]
         _lib = lib
     return _lib
 

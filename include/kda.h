@@ -742,6 +742,156 @@ int kda_cache_write(void *cache, const void *rows, int64_t rows_layer_stride,
 int kda_cache_copy_pages(void *cache, const int32_t *src, const int32_t *dst, int32_t n, int32_t L,
                          int32_t n_pages, int64_t page_bytes, int32_t *status, void *stream);
 
+/* ------------------------------------------------------------------ around a cached row
+ *
+ * What happens to a latent row before it is cached and while it is: the norm before a
+ * projection and of the latent itself, the rotation of the rotary channels of queries and
+ * rows, the attention weight a row has been given, and the eviction of those that were
+ * given least when the cache has a budget ("Kimi K3: 架构、训练与系统全景解析", section 2:
+ * the latent-attention layers of the hybrid stack).  dtype is KDA_F32 or KDA_BF16; every
+ * sum, statistic and angle is fp32 or wider, and a result is rounded once.
+ * An output may be its input itself (same address and strides: in place) where that is
+ * said; otherwise no output may overlap an input or another output.  Of views whose spans
+ * meet, those with equal token strides (and, both with several heads, equal head strides)
+ * are told apart exactly, others are refused.
+ */
+
+/*
+ * Rotary positions: with t = positions[n] * inv_freq[i], the pair i of channels (a, b)
+ * of a row becomes
+ *     scale (a cos t - b sin t, b cos t + a sin t);
+ * with transpose non-zero t counts negative: the gradient of the call without it.
+ * Pair i is channels (2 i, 2 i + 1) where interleaved is non-zero, else (i, i + dr / 2).
+ *   x, out     [n_tokens, H, dr] dtype with token and head strides (elements, >= 0): the
+ *              rotary channels of wider heads are a view of them
+ *   k, k_out   [n_tokens, dr] with token strides, or both NULL: the key all heads share,
+ *              turned in the same launch
+ *   positions  [n_tokens] int32 (any value), DEVICE
+ *   inv_freq   [dr / 2] fp64, DEVICE: angle per position; scaling for longer contexts goes
+ *              into these and into scale (finite)
+ * An angle is off by at most 2^-24 of a turn whatever the position.
+ * out may be x, k_out may be k (in place).  dr even, at most 512.  Alignment: of an
+ * element; rows that start on 16 bytes (address and strides) and whose halves, or pairs,
+ * fill 16-byte pieces move in these.
+ * Errors: KDA_ERR_INVALID_ARG (NULL, sizes, alignment, negative strides, rows of an output
+ * that meet, overlap, one of k and k_out), KDA_ERR_UNSUPPORTED (dr above 512, dtype),
+ * KDA_ERR_CUDA.
+ */
+int kda_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, void *out,
+             int64_t out_token_stride, int64_t out_head_stride, const void *k,
+             int64_t k_token_stride, void *k_out, int64_t k_out_token_stride,
+             const int32_t *positions, const double *inv_freq, int64_t n_tokens, int32_t H,
+             int32_t dr, int interleaved, float scale, int transpose, int dtype, void *stream);
+
+/*
+ * Norm over the W channels of each row:
+ *     m = mean x (center non-zero; else 0),  r = 1 / sqrt(mean (x - m)^2 + eps),
+ *     out = (x - m) r weight + bias
+ *   x, out       [n, W] dtype, rows x_row_stride / out_row_stride elements apart (>= 0)
+ *   weight, bias [W] fp32 or NULL (1, 0)
+ *   mean, rstd   [n] fp32 or NULL (not written; mean NULL if center is zero): m and r,
+ *                as kda_norm_bwd takes them
+ * eps > 0.  out may be x.  W at most 16384.  Alignment: of an element (16 bytes, address
+ * and stride, lets rows move in 16-byte pieces).
+ * Errors as kda_rope.
+ */
+int kda_norm_fwd(const void *x, int64_t x_row_stride, const float *weight, const float *bias,
+                 int64_t n, int32_t W, int dtype, int center, float eps, void *out,
+                 int64_t out_row_stride, float *mean, float *rstd, void *stream);
+
+/* Workspace of kda_norm_bwd: 8 W bytes for each of its blocks (at most two an SM).  A call
+ * with neither d_weight nor d_bias needs none. */
+int kda_norm_bwd_workspace_size(int64_t n, int32_t W, int dtype, size_t *bytes);
+
+/*
+ * The gradient of kda_norm_fwd for the gradient d_out of its output; mean (NULL: a norm
+ * without its mean) and rstd are what the forward pass left.  With z = (x - m) r:
+ *     d_x = r (weight d_out - mean(weight d_out) - z mean(weight d_out z))
+ *     d_weight = sum over rows of d_out z,  d_bias = sum over rows of d_out
+ * (without its mean: no second term).
+ *   d_out, d_x   [n, W] dtype with row strides like x; d_x may be d_out or x
+ *   d_weight, d_bias  [W] fp32 or NULL (not computed); zeros for n = 0
+ *   workspace    kda_norm_bwd_workspace_size() bytes, 16-byte aligned
+ * Sums over rows are taken in a fixed order: results do not vary between calls.
+ * Errors as kda_norm_fwd, KDA_ERR_WORKSPACE.
+ */
+int kda_norm_bwd(const void *d_out, int64_t d_out_row_stride, const void *x, int64_t x_row_stride,
+                 const float *weight, const float *mean, const float *rstd, int64_t n, int32_t W,
+                 int dtype, void *d_x, int64_t d_x_row_stride, float *d_weight, float *d_bias,
+                 void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace of kda_latent_weights: the status word and an error word a block.  Errors as
+ * kda_latent_decode_workspace_size. */
+int kda_latent_weights_workspace_size(int32_t B, int32_t T, int32_t H, int32_t dc, int32_t dr,
+                                      int dtype, size_t *bytes);
+
+/*
+ * The attention weight that the last T tokens of each sequence have given its cached
+ * rows, added up over tokens and heads:
+ *     weights[b, j] <- decay weights[b, j] + sum over t, h that see j of
+ *                      exp(scale q[b, t, h] . cache row j - lse[b, t, h])
+ * for the positions j < seq_lens[b].  q, cache, block_table, seq_lens, tree_mask and scale
+ * as in kda_latent_decode, whose lse [B, T, H] fp32 of the same call makes the terms its
+ * probabilities.  A row whose lse is infinite gives nothing: -inf is that of a token that
+ * sees no key, +inf leaves a token out (a rejected draft).
+ *   weights  [B, max_pages * page_size] fp32, in place; places from seq_lens[b] on stay
+ *            as they are, and those that a new row takes should hold 0
+ *   decay    finite and >= 0; with 0 the old weights are not read
+ * A sequence whose length is out of range, or with a page id outside [0, n_pages), records
+ * KDA_ERR_INVALID_ARG in the status; its weights stay as they are where the length is out
+ * of range, and are undefined where a page is.
+ * Results do not vary between calls.  Queries must be finite; a cached row that is not
+ * makes its own weight so and no other.
+ * Workspace: kda_latent_weights_workspace_size() bytes, 16-byte aligned; the status word is
+ * set by the call (kda_read_device_status), and kda_latent_test_timeout arms its waits too.
+ * Alignment: q, cache 16 bytes; tree_mask 8; the others 4.  Limits and errors as
+ * kda_latent_decode, but for max_pages * page_size at most 2^30.
+ */
+int kda_latent_weights(const void *q, const void *cache, const int32_t *block_table,
+                       const int32_t *seq_lens, const int64_t *tree_mask, const float *lse,
+                       int32_t B, int32_t T, int32_t H, int32_t dc, int32_t dr, int32_t n_pages,
+                       int32_t page_size, int32_t max_pages, int dtype, float scale, float decay,
+                       float *weights, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace of kda_cache_evict: the moves, 8 bytes a kept row and layer.  Errors:
+ * KDA_ERR_INVALID_ARG. */
+int kda_cache_evict_workspace_size(int32_t L, int32_t B, int32_t budget, size_t *bytes);
+
+/*
+ * Sequences of more than `budget` cached rows cut to it, in every layer of a paged cache
+ * [L, n_pages, page_size, row_bytes] (any element type) by that layer's weights.  Of
+ * n = seq_lens[b] > budget rows these stay: the first `first`, the last `recent`, and of
+ * those between the budget - first - recent of the greatest weight (of equal weights the
+ * earlier row; a weight that is no number counts as the least).  The rows lie at
+ * 0 .. budget - 1 afterwards:
+ *   - kept rows in front of budget - recent stay where they are;
+ *   - places there that fall free take, in order, the kept rows from behind, in order;
+ *   - the last `recent` rows follow, in order.
+ * So the order of rows changes (attention over a cache has none but the last tokens') and
+ * as few of them move as can.  Sequences of at most budget rows stay as they are.
+ *   weights      [L, B, max_pages * page_size] fp32
+ *   weights_out  the same shape, or weights itself: the kept rows' weights at their new
+ *                places, and 0 from the new length on
+ *   new_lens     [B] int32: min(n, budget)
+ *   origin       [L, B, budget] int32: the former position of the row now at each place,
+ *                -1 from the new length on
+ * block_table [B, max_pages], seq_lens [B]: int32, DEVICE; first + recent <= budget.
+ * A sequence whose length is out of range, or with a page id outside [0, n_pages), has
+ * nothing moved (weights_out: its weights, origin: -1, new_lens: its length), and
+ * KDA_ERR_INVALID_ARG is recorded in *status (DEVICE int32 or NULL; not cleared by the
+ * call).  No two sequences may share a page of which rows are moved.
+ *   workspace  kda_cache_evict_workspace_size() bytes, 16-byte aligned
+ * row_bytes is a multiple of 16, cache 16-byte aligned; max_pages * page_size and budget
+ * at most 2^30.
+ * Errors (before any launch): KDA_ERR_INVALID_ARG, KDA_ERR_WORKSPACE, KDA_ERR_CUDA.
+ */
+int kda_cache_evict(void *cache, const int32_t *block_table, const int32_t *seq_lens,
+                    const float *weights, float *weights_out, int32_t L, int32_t n_pages,
+                    int32_t page_size, int64_t row_bytes, int32_t B, int32_t max_pages,
+                    int32_t budget, int32_t first, int32_t recent, int32_t *new_lens,
+                    int32_t *origin, void *workspace, size_t workspace_bytes, int32_t *status,
+                    void *stream);
+
 #ifdef __cplusplus
 }
 #endif

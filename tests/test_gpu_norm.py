@@ -1,0 +1,215 @@
+"""The norm over a row's channels and its gradient against their 64-bit forms."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import gated_delta_rule_13_gb300 as kda
+import rows_util as ru
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+WIDTHS = [1, 2, 7, 64, 100, 512, 513, 1024, 1025, 2047, 3584, 4100, 7168, 8192, 9001, 16384]
+
+
+def _in(shape, dtype, seed=0, std=1.0, mean=0.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device=DEV) * std + mean).to(dtype)
+
+
+def _vec(W, seed, mean=0.0):
+    return _in((W,), F32, seed, 0.3, mean)
+
+
+def _within(got, want, tol, what):
+    err = (got.double() - want).abs()
+    assert (err <= tol).all(), f"{what}: worst {(err / tol).max().item():.3g} of the bound"
+
+
+def _check_fwd(got, x, w, b, center, eps):
+    y, mean, rstd = got
+    want = ru.norm_ref(x, w, b, center, eps)
+    tol = ru.norm_bounds(x, w, b, center, eps, x.dtype)
+    _within(y, want[0], tol[0], "out")
+    assert (mean is None) == (not center)
+    if center:
+        _within(mean, want[1], tol[1], "mean")
+    _within(rstd, want[2], tol[2], "rstd")
+
+
+def _check_bwd(got, g, x, w, mean, rstd):
+    want = ru.norm_grad_ref(g, x, w, mean, rstd)
+    tol = ru.norm_grad_bounds(g, x, w, mean, rstd, x.dtype)
+    for name, a, b, t in zip(("d_x", "d_weight", "d_bias"), got, want, tol):
+        if a is not None:
+            _within(a, b, t, name)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("center", [True, False])
+@pytest.mark.parametrize("W", WIDTHS)
+def test_against_64_bits(dtype, center, W):
+    for n, affine in ((1, True), (5, False), (260, True)):
+        x, g = _in((n, W), dtype, 1, 1.5, 0.3), _in((n, W), dtype, 2)
+        w, b = (_vec(W, 3, 1.0), _vec(W, 4)) if affine else (None, None)
+        got = kda.kda_norm_fwd(x, w, b, center=center)
+        _check_fwd(got, x, w, b, center, 1e-5)
+        _, mean, rstd = got
+        back = kda.kda_norm_bwd(g, x, w, mean, rstd, bias=affine)
+        assert (back[1] is None) == (back[2] is None) == (not affine)
+        _check_bwd(back, g, x, w, mean, rstd)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("off,stride", [(0, 576), (1, 577), (3, 600), (64, 576)])
+def test_views(dtype, off, stride):
+    """Channels of wider rows, starting on 16 bytes and not; in place; nothing around
+    them changes."""
+    n, W = 70, 512
+    base, gbase = _in((n, stride), dtype, 1), _in((n, stride), dtype, 2)
+    x, g = base[:, off:off + W], gbase[:, off:off + W]
+    w = _vec(W, 3, 1.0)
+    got = kda.kda_norm_fwd(x, w, None, center=False)
+    _check_fwd(got, x, w, None, False, 1e-5)
+    to = _in((n, stride), dtype, 5)
+    around = to.clone()
+    kda.kda_norm_fwd(x, w, None, center=False, out=to[:, off:off + W])
+    assert torch.equal(to[:, off:off + W], got[0])
+    to[:, off:off + W] = around[:, off:off + W]
+    assert torch.equal(to, around)
+    back = kda.kda_norm_bwd(g, x, w, None, got[2], d_x=to[:, off:off + W])
+    _check_bwd(back, g, x, w, None, got[2])
+    want = [t.clone() for t in back[:2]]
+    into = gbase.clone()
+    same = kda.kda_norm_bwd(into[:, off:off + W], x, w, None, got[2], d_x=into[:, off:off + W])
+    assert torch.equal(same[0], want[0]) and torch.equal(same[1], want[1])
+    copy = base.clone()
+    kda.kda_norm_fwd(copy[:, off:off + W], w, None, center=False, out=copy[:, off:off + W])
+    assert torch.equal(copy[:, off:off + W], got[0])
+    assert torch.equal(copy[:, :off], base[:, :off])
+
+
+def test_a_mean_far_from_zero():
+    x = _in((40, 7168), F32, 1, 1.0, 300.0)
+    _check_fwd(kda.kda_norm_fwd(x, None, None), x, None, None, True, 1e-5)
+
+
+def test_constant_and_zero_rows():
+    x = torch.full((3, 200), 2.5, dtype=F32, device=DEV)
+    x[1] = 0
+    y, mean, rstd = kda.kda_norm_fwd(x, None, None)
+    assert torch.equal(y, torch.zeros_like(y))
+    assert torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5), rtol=1e-6)
+    y, _, rstd = kda.kda_norm_fwd(x, None, None, center=False)
+    assert torch.equal(y[1], torch.zeros_like(y[1]))
+
+
+def test_rows_of_more_dimensions_and_none():
+    x = _in((4, 6, 5, 64), BF)[:, :, :3]
+    with pytest.raises(ValueError, match="evenly"):
+        kda.kda_norm_fwd(x)
+    x = _in((4, 6, 64), BF)
+    y, mean, rstd = kda.kda_norm_fwd(x)
+    assert y.shape == x.shape and mean.shape == rstd.shape == (4, 6)
+    _check_fwd((y, mean, rstd), x, None, None, True, 1e-5)
+    w = _vec(64, 1)
+    y, mean, rstd = kda.kda_norm_fwd(x[:0], w)
+    d = kda.kda_norm_bwd(x[:0], x[:0], w, mean, rstd, bias=True)
+    assert d[0].shape == (0, 6, 64)
+    assert torch.equal(d[1], torch.zeros_like(w)) and torch.equal(d[2], torch.zeros_like(w))
+    y, mean, rstd = kda.kda_norm_fwd(x, w, stats=False)
+    assert mean is None and rstd is None
+
+
+def test_not_a_number_stays_in_its_row():
+    x, g = _in((20, 700), BF, 1), _in((20, 700), BF, 2)
+    x[3, 5] = float("nan")
+    x[7, 1] = float("inf")
+    y, mean, rstd = kda.kda_norm_fwd(x, None, None)
+    good = [i for i in range(20) if i not in (3, 7)]
+    assert torch.isfinite(y[good]).all() and torch.isnan(y[3]).all()
+    d = kda.kda_norm_bwd(g, x, None, mean, rstd)[0]
+    assert torch.isfinite(d[good]).all()
+
+
+@pytest.mark.parametrize("n,W,dtype", [(5000, 512, F32), (3001, 7168, BF), (20000, 40, BF)])
+def test_many_rows_and_the_same_bits(n, W, dtype):
+    x, g = _in((n, W), dtype, 1, 1.2, 0.1), _in((n, W), dtype, 2)
+    w = _vec(W, 3, 1.0)
+    got = kda.kda_norm_fwd(x, w, None)
+    back = kda.kda_norm_bwd(g, x, w, got[1], got[2], bias=True)
+    _check_bwd(back, g, x, w, got[1], got[2])
+    again = kda.kda_norm_bwd(g, x, w, got[1], got[2], bias=True)
+    for a, b in zip(back, again):
+        assert torch.equal(a, b)
+
+
+def test_gradient_against_differences():
+    """f = <g, y>: f(x + h v) - f(x - h v) is the gradient along the step, but for the
+    bounds of the values, those of the gradient, and what a central difference leaves, which
+    is taken from the 64-bit form."""
+    x, g, v = _in((4, 64), F32, 1), _in((4, 64), F32, 2), _in((4, 64), F32, 3)
+    w, b = _vec(64, 4, 1.0), _vec(64, 5)
+    h = 2.0 ** -6
+    for center in (True, False):
+        f = lambda t: (g.double() * kda.kda_norm_fwd(t, w, b, center=center)[0].double()).sum()  # noqa: E731
+        f64 = lambda t: (g.double() * ru.norm_ref(t, w, b, center, 1e-5)[0]).sum()  # noqa: E731
+        xp, xm = x + h * v, x - h * v                    # as the kernel gets them
+        tol = sum((g.double().abs() * ru.norm_bounds(t, w, b, center, 1e-5, F32)[0]).sum()
+                  for t in (xp, xm))
+        step = (xp.double() - xm.double())
+        _, mean, rstd = kda.kda_norm_fwd(x, w, b, center=center)
+        d = kda.kda_norm_bwd(g, x, w, mean, rstd)[0].double()
+        exact_grad = ru.norm_grad_ref(g, x, w, *(t if t is None else t.double() for t in
+                                                 (mean, rstd)))[0]
+        curve = abs(f64(xp.double()) - f64(xm.double()) - (exact_grad * step).sum())
+        slack = (ru.norm_grad_bounds(g, x, w, mean, rstd, F32)[0] * step.abs()).sum()
+        assert abs(f(xp) - f(xm) - (d * step).sum()) <= tol + slack + curve
+        assert curve < 0.05 * abs((exact_grad * step).sum()) + 0.02
+
+
+def test_streams_and_graphs():
+    x, g, w = _in((300, 512), BF, 1), _in((300, 512), BF, 2), _vec(512, 3, 1.0)
+    want = kda.kda_norm_fwd(x, w, w)
+    grad = kda.kda_norm_bwd(g, x, w, want[1], want[2], bias=True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = kda.kda_norm_fwd(x, w, w, stream=s)
+    back = kda.kda_norm_bwd(g, x, w, got[1], got[2], bias=True, stream=s)
+    s.synchronize()
+    for a, b in zip((*got, *back), (*want, *grad)):
+        assert torch.equal(a, b)
+    ws = torch.empty(kda.kda_norm_bwd_workspace_size(300, 512), dtype=torch.uint8, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, mean, rstd = kda.kda_norm_fwd(x, w, w)
+        d = kda.kda_norm_bwd(g, x, w, mean, rstd, bias=True, workspace=ws)
+    x.mul_(0.5)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    _check_fwd((y, mean, rstd), x, w, w, True, 1e-5)
+    _check_bwd(d, g, x, w, mean, rstd)
+
+
+def test_refusals():
+    x, w = _in((8, 64), BF), _vec(64, 1)
+    _, mean, rstd = kda.kda_norm_fwd(x, w)
+    for call in (lambda: kda.kda_norm_fwd(x.half()), lambda: kda.kda_norm_fwd(x.cpu()),
+                 lambda: kda.kda_norm_fwd(x, w.bfloat16()), lambda: kda.kda_norm_fwd(x, w[:32]),
+                 lambda: kda.kda_norm_fwd(x, eps=0.0), lambda: kda.kda_norm_fwd(x[:, ::2]),
+                 lambda: kda.kda_norm_fwd(x, out=x.float()), lambda: kda.kda_norm_fwd(x, out=x[:4]),
+                 lambda: kda.kda_norm_bwd(x[:4], x, w, mean, rstd),
+                 lambda: kda.kda_norm_bwd(x, x, w, mean[:4], rstd),
+                 lambda: kda.kda_norm_bwd(x, x, w, mean, rstd.double()),
+                 lambda: kda.kda_norm_bwd(x.float(), x, w, mean, rstd)):
+        with pytest.raises((TypeError, ValueError)):
+            call()
+    wide = _in((8, 100), BF)
+    with pytest.raises(kda.KDAError):
+        kda.kda_norm_fwd(wide[:, :64], out=wide[:, 1:65])
+    with pytest.raises(kda.KDAError):
+        kda.kda_norm_fwd(_in((2, 16385), BF))
+    with pytest.raises(kda.KDAError):
+        kda.kda_norm_bwd(x, x, w, mean, rstd, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
