@@ -1,11 +1,30 @@
-// The attention weight that cached rows have been given (kda_latent_weights).
+// The attention weight that cached rows have been given (kda_latent_weights), tcgen05 /
+// TMEM / TMA, sm_103a.
 //
 //   w_j <- decay w_j + sum over tokens t and heads h that see j of exp(scale q_th . c_j - lse_th)
 //
-// One thread block per 32 cached rows of a sequence, held in shared memory; a warp takes
-// every eighth query row, a lane is a cached row.
+// Scores once more, but transposed: S [keys x query rows] = C Q^T, so that a thread of the
+// epilogue has a key, and its sum over the R = T * H query rows is a sum along its own row
+// of the accumulator, in registers, in a fixed order, whatever R is.  No key is touched by
+// two CTAs: nothing is joined and nothing depends on the order of CTAs.  With lse from the
+// decode pass every term is final, and there is no maximum to follow.
+//
+// A cached row is 2 W = 1,024 or 1,152 bytes against 2 R W operations: at R = 96 the card's
+// 289 operations a byte leave it bound by HBM, from R = 145 on by the matrix work.  So there
+// are two forms, by what stays in shared memory while the other operand streams past it, in
+// blocks of 64 channels:
+//   R <= 128  the queries of a sequence stay (at most 147 KB), 128-key tiles stream: every
+//             cached row is read once, 64 to 190 KB of copies in flight an SM.
+//   R > 128   a 256-key tile stays, half in each CTA of a pair, and the query rows stream
+//             from L2, 256 at a time, half to each CTA; cta_group::2 products (256 keys x
+//             256 rows) read both halves.  One CTA by itself would have to stream 64 bytes
+//             of queries a cycle from L2 to keep its tensor cores busy; a pair 32 a CTA.
+// Steps (one accumulator each) are double-buffered in TMEM: the products of one run beside
+// the exponentials of the other.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <math_constants.h>
+#include <string.h>
 
 #include "kda_latent_tc.cuh"
 #include "kda_rows.h"
@@ -13,69 +32,586 @@
 namespace kda {
 namespace {
 
-constexpr int kRows = 32, kWarps = 8;
+using namespace latent;
 
-__global__ void __launch_bounds__(32 * kWarps) kda_latent_weights_kernel(const LatentWeightsArgs a) {
-  extern __shared__ uint32_t tile[];       // [32][W / 2 + 1]
-  __shared__ float part[kWarps][kRows];
-  __shared__ int bad;
-  const int b = blockIdx.y, W = kLatentC + a.dr, words = W / 2, R = a.T * a.H;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int cap = a.max_pages * a.page_size;
-  const int n = a.seq_lens[b];
-  if (threadIdx.x == 0) bad = n < 0 || n > cap;
-  __syncthreads();
-  const int32_t *table = a.block_table + (int64_t)b * a.max_pages;
-  if (!bad) {
-    bool wrong = false;
-    for (int i = threadIdx.x; i < (n + a.page_size - 1) / a.page_size; i += 32 * kWarps)
-      wrong = wrong || table[i] < 0 || table[i] >= a.n_pages;
-    if (wrong) bad = 2;
-  }
-  __syncthreads();
-  if (bad) {
-    if (threadIdx.x == 0 && blockIdx.x == 0)
-      record_device_status(a.status, KDA_ERR_INVALID_ARG, bad, b, 0);
-    return;
-  }
-  for (int64_t j0 = (int64_t)blockIdx.x * kRows; j0 < n; j0 += (int64_t)gridDim.x * kRows) {
-    const int live = (int)min((int64_t)kRows, n - j0);
-    __syncthreads();
-    for (int i = threadIdx.x; i < live * words; i += 32 * kWarps) {
-      const int r = i / words, c = i - r * words;
-      const int pos = (int)j0 + r, pg = pos / a.page_size;
-      const uint32_t *row = static_cast<const uint32_t *>(a.cache) +
-                            ((int64_t)table[pg] * a.page_size + (pos - pg * a.page_size)) * words;
-      tile[r * (words + 1) + c] = row[c];
+constexpr int kThreads = 384;            // 2 x 4 epilogue warps, loader, MMA, lse, spare
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kLseWarp = 10;
+constexpr uint32_t kBlock = 16384;       // 128 rows x 64 channels
+constexpr uint32_t kSmem = 232448;
+constexpr int kMaxSlots = 12, kMaxBlocks = 9;
+
+template <bool kPair>
+constexpr int kKeysLog = kPair ? 8 : 7;  // keys of a tile
+template <bool kPair>
+constexpr int kCols = kPair ? 256 : 128; // query rows of a step at most
+
+template <bool kPair>
+struct Shared {
+  // Of a pair, the barriers that the products wait for are rank 0's.
+  uint64_t full[kMaxSlots], empty[kMaxSlots], kept_full[kMaxBlocks], kept_free[kMaxBlocks];
+  uint64_t s_full[2], s_free[2], lse_full[2], lse_free[2], part_ready[4][2], part_free[4][2], fin;
+  uint32_t tmem;
+  int abort;
+  int seq0, tile0, total;                // the CTA's (pair's) first sequence and tile, all tiles
+  int64_t warp_sum[kThreads / 32];
+  DeviceStatus error;
+  uint32_t load_ring, load_kept;         // blocks the loader asked for
+  alignas(16) float lse[2][kCols<kPair>];            // times log2(e); +inf where a row gives nothing
+  float part[2][128];                    // the second warpgroup's sums
+};
+template <bool kPair>
+constexpr uint32_t kSharedBytes = kPair ? 4096 : 3072;
+static_assert(sizeof(Shared<false>) <= kSharedBytes<false>, "fits beside the tiles");
+static_assert(sizeof(Shared<true>) <= kSharedBytes<true>, "fits beside the tiles");
+
+struct Params {
+  const int32_t *table, *lens;
+  const int64_t *mask;
+  const float *lse;
+  int32_t B, T, H, R, n_pages, page_size, max_pages, box_rows;
+  int32_t blocks;       // of 64 channels
+  int32_t cols;         // query rows of a step, a multiple of 16
+  int32_t row_steps;    // steps for all of them (1 where they stay)
+  int32_t slots;        // of the ring
+  int32_t groups;       // CTAs, or pairs of them
+  uint32_t kept_bytes;  // a kept block's place
+  float scale2, decay;  // scale * log2(e)
+  float *weights;
+  DeviceStatus *status;
+  WaitTest test;
+};
+
+// Length of sequence b, 0 when it is out of range.
+__device__ __forceinline__ int seq_len(const Params &p, int b) {
+  const int n = p.lens[b];
+  return n < 0 || n > (int64_t)p.max_pages * p.page_size ? 0 : n;
+}
+template <bool kPair>
+__device__ __forceinline__ int key_tiles(int n) {
+  return (n >> kKeysLog<kPair>)+((n & ((1 << kKeysLog<kPair>)-1)) != 0);
+}
+
+// First tile of group c of G when the list has `total`: the first total % G take one more.
+__device__ __forceinline__ int group_begin(int c, int G, int total) {
+  const int each = total / G, more = total - each * G;
+  return c * each + min(c, more);
+}
+
+// Walks the group's steps; every role does so by itself.
+template <bool kPair>
+struct Steps {
+  const Params &p;
+  int next_b, next_t, left;       // next sequence, its next tile, tiles left
+  int b = 0, n = 0, ta = 0, tb = 0, t = 0, rs = 0;   // current: sequence, tiles [ta, tb), tile, row step
+  __device__ Steps(const Params &p_, int b_, int t_, int left_)
+      : p(p_), next_b(b_), next_t(t_), left(left_) {}
+  __device__ bool next() {
+    if (kPair && tb > 0 && rs + 1 < p.row_steps) {
+      ++rs;
+      return true;
     }
-    __syncthreads();
-    const int j = (int)j0 + lane, draft = j - (n - a.T);
-    float sum = 0.f;
-    for (int r = warp; r < R; r += kWarps) {
-      const int t = r / a.H;
-      const float lse = a.lse[(int64_t)b * R + r];
-      bool seen = lane < live && !isinf(lse);
-      if (draft >= 0)
-        seen = seen && (a.tree_mask ? (a.tree_mask[(int64_t)b * a.T + t] >> draft & 1) != 0 : draft <= t);
-      const uint32_t *q = static_cast<const uint32_t *>(a.q) + ((int64_t)b * R + r) * words;
-      float s = 0.f;
-      for (int c = 0; c < words; ++c) {
-        const float2 x = sm100::unpack_bf16x2(q[c]);
-        const float2 y = sm100::unpack_bf16x2(tile[(lane < live ? lane : 0) * (words + 1) + c]);
-        s = fmaf(x.x, y.x, s);
-        s = fmaf(x.y, y.y, s);
+    rs = 0;
+    if (t + 1 < tb) {
+      ++t;
+      return true;
+    }
+    if (left <= 0) return false;
+    for (; next_b < p.B; ++next_b, next_t = 0) {
+      n = seq_len(p, next_b);
+      const int k = key_tiles<kPair>(n);
+      if (next_t >= k) continue;
+      b = next_b;
+      t = ta = next_t;
+      tb = k - ta <= left ? k : ta + left;
+      left -= tb - ta;
+      next_t = tb;                // at the end of the sequence the loop passes on
+      return true;
+    }
+    return false;
+  }
+  // of what stays in shared memory
+  __device__ bool first() const { return kPair ? rs == 0 : t == ta; }
+  __device__ bool last() const { return kPair ? rs + 1 == p.row_steps : t + 1 == tb; }
+  // of a tile of keys
+  __device__ bool tile_begins() const { return !kPair || rs == 0; }
+  __device__ bool tile_ends() const { return !kPair || rs + 1 == p.row_steps; }
+};
+
+// What differs between one CTA and a pair: the products and who hears of their end.
+template <bool kPair>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  if constexpr (!kPair) {
+    umma_ss(d, a, b, idesc, add);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+  }
+}
+template <bool kPair>
+__device__ __forceinline__ void commit(uint64_t *bar) {
+  if constexpr (!kPair) {
+    umma_commit(bar);
+  } else {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  }
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_get(uint32_t *dst) {
+  if constexpr (!kPair) {
+    tmem_alloc(dst, 256);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(dst))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <bool kPair>
+__device__ __forceinline__ void tmem_give(uint32_t addr) {
+  if constexpr (!kPair) tmem_dealloc(addr, 256);
+  else asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(addr) : "memory");
+}
+// Copies counted by barrier `bar` (an address of the cluster's shared memory).
+template <bool kPair>
+__device__ __forceinline__ void copy_2d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t c0,
+                                        int32_t c1) {
+  if constexpr (!kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+template <bool kPair>
+__device__ __forceinline__ void copy_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t c0,
+                                        int32_t c1, int32_t c2) {
+  if constexpr (!kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+// The call's status is cleared by a kernel of its own, beside which the next one starts.
+__global__ void kda_latent_weights_begin_kernel(DeviceStatus *status) {
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) set_device_status(status, KDA_OK, 0);
+}
+
+template <bool kPair>
+__device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUtensorMap &map_c,
+                                             const Params &p) {
+  using Sh = Shared<kPair>;
+  constexpr int kN = kCols<kPair>;
+  extern __shared__ __align__(1024) unsigned char tiles[];
+  const uint32_t base = smem_u32(tiles);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = kPair ? cluster_rank() : 0;
+  const int group = kPair ? blockIdx.x >> 1 : blockIdx.x;
+  const int NB = p.blocks, NS = p.slots;
+  const uint32_t sm_kept = base, sm_ring = base + NB * p.kept_bytes;
+  Sh &m = *reinterpret_cast<Sh *>(tiles + (kSmem - kSharedBytes<kPair>));
+
+  if (tid == 0) {
+    for (int i = 0; i < kMaxSlots; ++i) {
+      mbar_init(&m.full[i], 1);
+      mbar_init(&m.empty[i], 1);
+    }
+    for (int i = 0; i < kMaxBlocks; ++i) {
+      mbar_init(&m.kept_full[i], 1);
+      mbar_init(&m.kept_free[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&m.s_full[i], 1);
+      mbar_init(&m.s_free[i], kPair ? 16 : 8);
+      mbar_init(&m.lse_full[i], 1);
+      mbar_init(&m.lse_free[i], 8);
+      for (int w = 0; w < 4; ++w) {
+        mbar_init(&m.part_ready[w][i], 1);
+        mbar_init(&m.part_free[w][i], 1);
       }
-      if (seen) sum += exp2f((s * a.scale - lse) * latent::kLog2e);
     }
-    part[warp][lane] = sum;
+    mbar_init(&m.fin, 1);
+    m.abort = 0;
+    m.seq0 = p.B;
+    m.tile0 = 0;
+    m.error = DeviceStatus{0, 0, 0, 0, 0, 0};
+    fence_mbarrier_init();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    prefetch_tensormap(&map_q);
+    prefetch_tensormap(&map_c);
+  }
+  if (warp == kMmaWarp) tmem_get<kPair>(&m.tmem);
+  {  // the group's share of the tile list
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = tid * per, b1 = min(p.B, b0 + per);
+    int64_t mine = 0;                    // sequences may share pages: no pool bounds the sum
+    bool bad = false;
+    for (int b = b0; b < b1; ++b) {
+      const int n = p.lens[b];
+      if (n < 0 || n > (int64_t)p.max_pages * p.page_size) bad = true;
+      else mine += key_tiles<kPair>(n);
+    }
+    int64_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) m.warp_sum[warp] = inc;
     __syncthreads();
-    if (warp == 0 && lane < live) {
-      float all = 0.f;
-      for (int k = 0; k < kWarps; ++k) all += part[k][lane];
-      float *to = a.weights + (int64_t)b * cap + j;
-      *to = a.decay == 0.f ? all : fmaf(*to, a.decay, all);
+    if (bad) record_device_status(&m.error, KDA_ERR_INVALID_ARG, 1, b0, 0);
+    int64_t before = inc - mine, all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += m.warp_sum[w];
+      all += m.warp_sum[w];
+    }
+    // tiles are counted in 32 bits from here on; a list that is longer is refused
+    const int total = all > 0x7fffffff ? 0 : (int)all;
+    if (all > 0x7fffffff && tid == 0)
+      record_device_status(&m.error, KDA_ERR_INVALID_ARG, 3, 0, 0);
+    const int begin = group_begin(group, p.groups, total);
+    if (total > 0 && begin >= before && begin < before + mine) {
+      int at = (int)before;
+      for (int b = b0; b < b1; ++b) {
+        const int k = key_tiles<kPair>(seq_len(p, b));
+        if (begin < at + k) {
+          m.seq0 = b;
+          m.tile0 = begin - at;
+          break;
+        }
+        at += k;
+      }
+    }
+    if (tid == 0) m.total = total;
+  }
+  tc_fence_before();
+  if constexpr (kPair) cluster_sync_all();  // barriers of both CTAs are ready
+  else __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = m.tmem;
+  const int begin = group_begin(group, p.groups, m.total);
+  const int mine = group_begin(group + 1, p.groups, m.total) - begin;
+  const WaitCtx cx{&m.abort, &m.error, (int)blockIdx.x, p.test.wait_ns};
+  Steps<kPair> st(p, m.seq0, m.tile0, mine);
+
+  if (warp == kLoadWarp) {
+    // ---- loader: a lane has a piece of the tile's keys (the rows of one page); lane 0 the
+    // queries too
+    const int pieces = 128 / p.box_rows;
+    const uint32_t piece_bytes = p.box_rows * 128;
+    uint32_t ring = 0, kept = 0, outer = 0;  // blocks asked for; changes of what is kept
+    int s = 0;
+    const auto lead = [&](uint64_t *bar) { return kPair ? map_rank(smem_u32(bar), 0) : smem_u32(bar); };
+    int row = -1, have = 0;                  // this lane's pool row, pieces of the group
+    bool ok = true;
+    while (ok && st.next()) {
+      if (st.tile_begins()) {
+        const int at0 = st.t << kKeysLog<kPair>, at = at0 + (int)rank * 128 + lane * p.box_rows;
+        row = -1;
+        if (lane < pieces && at < st.n) {
+          const int page = at / p.page_size;
+          const int32_t id = p.table[(int64_t)st.b * p.max_pages + page];
+          if (id < 0 || id >= p.n_pages) {
+            record_device_status(&m.error, KDA_ERR_INVALID_ARG, 2, st.b, at);
+            row = p.n_pages * p.page_size;   // past the pool: reads zeros
+          } else {
+            row = id * p.page_size + at - page * p.page_size;
+          }
+        }
+        const int live = min(st.n - at0, 1 << kKeysLog<kPair>);
+        have = (live + p.box_rows - 1) / p.box_rows;
+      }
+      if (p.test.block == (int)blockIdx.x && p.test.tile == st.t - st.ta) break;  // a test
+      const uint32_t key_bytes = have * piece_bytes, query_bytes = p.cols * 128;
+      const auto keys = [&](uint32_t dst, uint64_t *bar, int c) {
+        if (row >= 0) copy_2d<kPair>(dst + lane * piece_bytes, &map_c, lead(bar), c * 64, row);
+      };
+      const auto queries = [&](uint32_t dst, uint64_t *bar, int c) {
+        if (lane == 0)
+          copy_3d<kPair>(dst, &map_q, lead(bar), c * 64, st.rs * kN + (int)rank * 128, st.b);
+      };
+      for (int c = 0; c < NB; ++c) {
+        if (st.first()) {                    // what stays: the queries, or a pair's keys
+          if (outer > 0) ok = warp_wait<2>(cx, &m.kept_free[c], (outer - 1) & 1, 10, st.t);
+          if (!ok) break;
+          if (lane == 0 && rank == 0)
+            mbar_arrive_expect_tx(&m.kept_full[c], kPair ? key_bytes : query_bytes);
+          __syncwarp();
+          if constexpr (kPair) keys(sm_kept + c * kBlock, &m.kept_full[c], c);
+          else queries(sm_kept + c * p.kept_bytes, &m.kept_full[c], c);
+          ++kept;
+        }
+        if (ring >= (uint32_t)NS) ok = warp_wait(cx, &m.empty[s], (ring / NS - 1) & 1, 11, st.t);
+        if (!ok) break;
+        if (lane == 0 && rank == 0)
+          mbar_arrive_expect_tx(&m.full[s], kPair ? query_bytes : key_bytes);
+        __syncwarp();
+        if constexpr (kPair) queries(sm_ring + s * kBlock, &m.full[s], c);
+        else keys(sm_ring + s * kBlock, &m.full[s], c);
+        ++ring;
+        s = s + 1 == NS ? 0 : s + 1;
+      }
+      outer += st.first();
+    }
+    if (lane == 0) {
+      m.load_ring = ring;
+      m.load_kept = kept;
+    }
+  } else if (warp == kMmaWarp) {
+    // ---- products: one lane of rank 0
+    if (rank == 0 && elect_one()) {
+      const uint32_t idesc = idesc_bf16(kPair ? 256 : 128, p.cols, false, false);
+      const Desc d_kept(sm_kept, 16), d_ring(sm_ring, 16);
+      uint32_t ring = 0, step = 0, outer = 0;
+      int s = 0;
+      bool ok = true;
+      while (ok && st.next()) {
+        const uint32_t buf = step & 1;
+        if (step > 1) ok = wait_or_abort(cx, &m.s_free[buf], ((step >> 1) - 1) & 1, 20, st.t);
+        if (!ok) break;
+        tc_fence_after();
+        for (int c = 0; c < NB; ++c) {
+          if (st.first()) ok = wait_or_abort(cx, &m.kept_full[c], outer & 1, 21, st.t);
+          ok = ok && wait_or_abort(cx, &m.full[s], (ring / NS) & 1, 22, st.t);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t k_at = kPair ? c * kBlock : s * kBlock;
+          const uint32_t q_at = kPair ? s * kBlock : c * p.kept_bytes;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t a = kPair ? d_kept.at(k_at + k * 32) : d_ring.at(k_at + k * 32);
+            const uint64_t q = kPair ? d_ring.at(q_at + k * 32) : d_kept.at(q_at + k * 32);
+            mma<kPair>(tm + buf * kN, a, q, idesc, c > 0 || k > 0);
+          }
+          commit<kPair>(&m.empty[s]);
+          if (st.last()) commit<kPair>(&m.kept_free[c]);
+          ++ring;
+          s = s + 1 == NS ? 0 : s + 1;
+        }
+        if (!ok) break;
+        commit<kPair>(&m.s_full[buf]);
+        outer += st.last();
+        ++step;
+      }
+    }
+  } else if (warp == kLseWarp) {
+    // ---- lse of a step's rows (where the queries stay: of a sequence's)
+    uint32_t item = 0;
+    bool ok = true;
+    while (ok && st.next()) {
+      if (!kPair && !st.first()) continue;
+      const uint32_t i = item & 1;
+      if (item > 1) ok = warp_wait<2>(cx, &m.lse_free[i], ((item >> 1) - 1) & 1, 30, st.t);
+      if (!ok) break;
+      const float *src = p.lse + (int64_t)st.b * p.R;
+      for (int c = lane; c < p.cols; c += 32) {
+        const int r = st.rs * kN + c;
+        const float v = r < p.R ? src[r] : CUDART_INF_F;
+        m.lse[i][c] = isinf(v) ? CUDART_INF_F : v * kLog2e;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.lse_full[i]);
+      ++item;
+    }
+  } else if (warp < 8) {
+    // ---- sums: thread = key; the warpgroups take 16 of the step's rows in turn
+    const int wg = warp >> 2, w4 = warp & 3, key = w4 * 32 + lane;
+    const uint32_t ts = tm + ((uint32_t)w4 << 21);
+    const int chunks = p.cols / 16;
+    const uint32_t credit0 = kPair ? map_rank(smem_u32(&m.s_free[0]), 0) : 0;
+    uint32_t step = 0, item = 0, tile = 0;
+    float sum = 0.f, old = 0.f;
+    bool ok = true;
+    while (ok && st.next()) {
+      const uint32_t buf = step & 1, par = (step >> 1) & 1;
+      const int j = (st.t << kKeysLog<kPair>)+(int)rank * 128 + key;
+      float *to = p.weights + (int64_t)st.b * p.max_pages * p.page_size + j;
+      if (st.tile_begins()) {
+        sum = 0.f;
+        if (wg == 0 && p.decay != 0.f && j < st.n) old = *to;
+      }
+      if (kPair || st.first()) {
+        ok = warp_wait<2>(cx, &m.lse_full[item & 1], (item >> 1) & 1, 40, st.t);
+        if (!ok) break;
+      }
+      const float *lse = m.lse[item & 1];
+      ok = warp_wait<2>(cx, &m.s_full[buf], par, 41, st.t);
+      if (!ok) break;
+      tc_fence_after();
+      // drafts: which of the step's rows see this key
+      const int draft = j - (st.n - p.T);
+      const bool masked = (p.T > 1 || p.mask) && ((st.t + 1) << kKeysLog<kPair>) > st.n - p.T;
+      constexpr int kBatch = 4;              // chunks of 16 in registers
+#pragma unroll 1
+      for (int c0 = wg; c0 < chunks; c0 += 2 * kBatch) {
+        uint32_t x[kBatch][16];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (c0 + 2 * i < chunks) tmem_ld16(ts + buf * kN + 16 * (c0 + 2 * i), x[i]);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (c0 + 2 * i < chunks) tmem_ld_wait(x[i]);
+        if (c0 + 2 * kBatch >= chunks) {     // the accumulator has been read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (kPair) remote_arrive_relaxed(credit0 + 8 * buf);
+            else mbar_arrive(&m.s_free[buf]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int c = 16 * (c0 + 2 * i);
+          if (c >= p.cols) continue;
+          if (masked) {
+            int tok = (st.rs * kN + c) / p.H, head = st.rs * kN + c - tok * p.H;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              bool see = draft < 0;
+              if (!see && tok < p.T)
+                see = p.mask ? (p.mask[(int64_t)st.b * p.T + tok] >> (draft & 63) & 1) != 0
+                             : draft <= tok;
+              if (!see) x[i][k] = __float_as_uint(-CUDART_INF_F);
+              if (++head == p.H) {
+                head = 0;
+                ++tok;
+              }
+            }
+          }
+          const float4 *l4 = reinterpret_cast<const float4 *>(lse + c);
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 l = l4[k];
+            part[0] += ex2(fmaf(__uint_as_float(x[i][4 * k]), p.scale2, -l.x));
+            part[1] += ex2(fmaf(__uint_as_float(x[i][4 * k + 1]), p.scale2, -l.y));
+            part[2] += ex2(fmaf(__uint_as_float(x[i][4 * k + 2]), p.scale2, -l.z));
+            part[3] += ex2(fmaf(__uint_as_float(x[i][4 * k + 3]), p.scale2, -l.w));
+          }
+          sum += (part[0] + part[1]) + (part[2] + part[3]);
+        }
+      }
+      if (wg >= chunks) {                    // nothing for this warpgroup: it has read it all
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m.s_free[buf]);
+      }
+      if (kPair || st.last()) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m.lse_free[item & 1]);
+        ++item;
+      }
+      ++step;
+      if (!st.tile_ends()) continue;
+      const uint32_t h = tile & 1, hp = (tile >> 1) & 1;
+      if (wg == 1) {
+        if (tile > 1) ok = warp_wait(cx, &m.part_free[w4][h], hp ^ 1, 42, st.t);
+        if (!ok) break;
+        m.part[h][key] = sum;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m.part_ready[w4][h]);
+      } else {
+        ok = warp_wait(cx, &m.part_ready[w4][h], hp, 43, st.t);
+        if (!ok) break;
+        const float all = sum + m.part[h][key];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m.part_free[w4][h]);
+        if (j < st.n) *to = p.decay == 0.f ? all : fmaf(old, p.decay, all);
+      }
+      ++tile;
     }
   }
+
+  __syncwarp();
+  __syncthreads();
+  if (m.abort) {
+    // Nothing in flight outlives the block: the last copies, whose barriers tell rank 0 so,
+    // and the products; then time for the copies of a pair's other CTA.
+    if (tid == 32 * kLoadWarp && rank == 0) {
+      const uint32_t ring = m.load_ring, kept = m.load_kept;
+      for (uint32_t k = ring > (uint32_t)NS ? ring - NS : 0; k < ring; ++k)
+        mbar_wait(&m.full[k % NS], (k / NS) & 1, 1000000);
+      for (uint32_t k = kept > (uint32_t)NB ? kept - NB : 0; k < kept; ++k)
+        mbar_wait(&m.kept_full[k % NB], (k / NB) & 1, 1000000);
+    }
+    if (warp == kMmaWarp && rank == 0 && elect_one()) {  // of the lane that issued them
+      commit<kPair>(&m.fin);
+      mbar_wait(&m.fin, 0, kWaitNs);
+    }
+    const uint64_t t0 = global_timer_ns();
+    while (kPair && global_timer_ns() - t0 < 200000) {}
+    __syncthreads();
+  }
+  tc_fence_before();
+  if constexpr (kPair) cluster_sync_all();  // what one CTA signals in the other has arrived
+  else __syncthreads();
+  tc_fence_after();
+  if (tid == 0) {
+    pdl_wait();                // the status has been cleared
+    if (m.error.code != 0)
+      record_device_status(p.status, m.error.code, m.error.detail, m.error.chain, m.error.chunk);
+  }
+  if (warp == kMmaWarp) tmem_give<kPair>(tm);
+  if constexpr (kPair) cluster_sync_all();
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+kda_latent_weights_kernel(const __grid_constant__ CUtensorMap map_q,
+                          const __grid_constant__ CUtensorMap map_c, const Params p) {
+  weights_body<false>(map_q, map_c, p);
+}
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+kda_latent_weights_pair_kernel(const __grid_constant__ CUtensorMap map_q,
+                               const __grid_constant__ CUtensorMap map_c, const Params p) {
+  weights_body<true>(map_q, map_c, p);
+}
+
+// Pairs of CTAs the device runs at once (0 without a device).
+int resident_pairs() {
+  static std::atomic<int> cache[kMaxDevices];
+  return per_device(cache, [](int) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (!kernel_ready<kda_latent_weights_pair_kernel>(kSmem, 0) ||
+        cudaOccupancyMaxActiveClusters(&n, kda_latent_weights_pair_kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    return n;
+  });
 }
 
 }  // namespace
@@ -83,13 +619,53 @@ __global__ void __launch_bounds__(32 * kWarps) kda_latent_weights_kernel(const L
 size_t latent_weights_scratch_bytes(int32_t, int32_t, int32_t, int32_t) { return 0; }
 
 cudaError_t launch_latent_weights(const LatentWeightsArgs &a, cudaStream_t stream) {
-  const cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(DeviceStatus), stream);
-  if (e != cudaSuccess || a.B == 0) return e;
-  const size_t smem = (size_t)kRows * ((kLatentC + a.dr) / 2 + 1) * 4;
-  int64_t tiles = ((int64_t)a.max_pages * a.page_size + kRows - 1) / kRows;
-  if (tiles > 4096) tiles = 4096;
-  kda_latent_weights_kernel<<<dim3((unsigned)tiles, (unsigned)a.B), 32 * kWarps, smem, stream>>>(a);
-  return cudaGetLastError();
+  if (a.B == 0) return cudaMemsetAsync(a.status, 0, sizeof(DeviceStatus), stream);
+  const int W = kLatentC + a.dr, R = a.T * a.H;
+  const bool pair = R > 128;
+  if (!latent::encode_tiled() || (pair ? resident_pairs() : sm_count()) < 1 ||
+      !kernel_ready<kda_latent_weights_kernel>(kSmem, 0))
+    return cudaErrorNotSupported;
+  Params p;
+  p.table = a.block_table; p.lens = a.seq_lens; p.mask = a.tree_mask; p.lse = a.lse;
+  p.B = a.B; p.T = a.T; p.H = a.H; p.R = R; p.n_pages = a.n_pages; p.page_size = a.page_size;
+  p.max_pages = a.max_pages;
+  p.box_rows = 128;                      // rows of a copied box: as many as lie in one page
+  while (a.page_size % p.box_rows) p.box_rows >>= 1;
+  p.blocks = W / 64;
+  p.cols = pair ? 256 : (R + 15) / 16 * 16;
+  p.row_steps = pair ? (R + 255) / 256 : 1;
+  p.kept_bytes = pair ? kBlock : (uint32_t)p.cols * 128;  // whole 1,024s
+  const uint32_t space = kSmem - (pair ? kSharedBytes<true> : kSharedBytes<false>) - p.blocks * p.kept_bytes;
+  p.slots = (int)(space / kBlock);
+  if (p.slots > kMaxSlots) p.slots = kMaxSlots;
+  p.groups = pair ? resident_pairs() : sm_count();
+  p.scale2 = a.scale * kLog2e; p.decay = a.decay; p.weights = a.weights; p.status = a.status;
+  p.test = a.test;
+  CUtensorMap mq, mc;
+  const cuuint64_t qd[3] = {(cuuint64_t)W, (cuuint64_t)R, (cuuint64_t)a.B};
+  const cuuint64_t qs[2] = {(cuuint64_t)W * 2, (cuuint64_t)W * 2 * R};
+  const cuuint32_t qb[3] = {64, (cuuint32_t)(pair ? 128 : p.cols), 1};
+  const cuuint64_t cd[2] = {(cuuint64_t)W, (cuuint64_t)a.n_pages * a.page_size};
+  const cuuint64_t cs[1] = {(cuuint64_t)W * 2};
+  const cuuint32_t cb[2] = {64, (cuuint32_t)p.box_rows};
+  if (!latent::make_bf16_map(&mq, a.q, 3, qd, qs, qb) ||
+      !latent::make_bf16_map(&mc, a.cache, 2, cd, cs, cb))
+    return cudaErrorInvalidValue;
+  kda_latent_weights_begin_kernel<<<1, 32, 0, stream>>>(a.status);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(pair ? 2 * p.groups : p.groups));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return pair ? cudaLaunchKernelEx(&cfg, kda_latent_weights_pair_kernel, mq, mc, p)
+              : cudaLaunchKernelEx(&cfg, kda_latent_weights_kernel, mq, mc, p);
 }
 
 }  // namespace kda
