@@ -38,32 +38,26 @@ def _like(name, t, x, shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _rows(name, t, lead):
-    """Stride between the rows of a view whose first ``lead`` dimensions are one
-    dimension of rows, as of a slice of a contiguous tensor."""
-    shape, stride = t.shape, t.stride()
+def _step(name, shape, stride, lead):
+    """Stride between the rows of a view whose first ``lead`` dimensions are one dimension
+    of rows, as of a slice of a contiguous tensor; its rows must be contiguous."""
+    if stride[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if lead == 1 and shape[0] > 1:
+        return stride[0]
     step = None
     for i in range(lead - 1, -1, -1):
+        if shape[i] == 0:
+            return shape[-1]
         if shape[i] == 1:                   # torch leaves its stride open
             continue
         if step is None:
-            first, step, n = stride[i], stride[i], shape[i]
+            first = stride[i]
         elif stride[i] != step * n:
             raise ValueError(f"{name}: rows of {tuple(shape)} must be evenly spaced, "
                              f"got strides {stride}")
-        else:
-            step, n = stride[i], shape[i]
+        step, n = stride[i], shape[i]
     return math.prod(shape[lead:]) if step is None else first
-
-
-def _heads(name, t, lead, heads):
-    """Token and head strides of ``[*tokens, H, dr]`` (or ``[*tokens, dr]``)."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    if t.numel() == 0:
-        return t.shape[-1], t.shape[-1]
-    return (_rows(name, t, lead),
-            t.stride(-2) if heads and t.shape[-2] > 1 else t.shape[-1])
 
 
 def kda_rope_inv_freq(dim, base=10000.0, *, scaling=None, factor=1.0, original=None,
@@ -119,15 +113,15 @@ def kda_rope(x, positions, inv_freq, *, k=None, interleaved=True, scale=1.0, tra
     the gradient of the call without it.  ``out`` and ``k_out`` may be views, and x and
     k themselves (in place).  Returns ``out``, with ``k`` ``(out, k_out)``."""
     code = _code("x", x)
-    dev = x.device
+    dev, shape = x.device, x.shape
     raw = _stream(stream, dev)
     _tensor("positions", positions, _I32, None, dev)
-    lead = positions.dim()
-    if x.dim() not in (lead + 1, lead + 2) or x.shape[:lead] != positions.shape:
+    lead, tokens = positions.dim(), positions.shape
+    heads = len(shape) == lead + 2
+    if shape[:lead] != tokens or not (heads or len(shape) == lead + 1):
         raise ValueError(f"x must be [*tokens, H, dr] or [*tokens, dr] with positions "
-                         f"{tuple(positions.shape)}, got {tuple(x.shape)}")
-    heads = x.dim() == lead + 2
-    H, dr = x.shape[-2] if heads else 1, x.shape[-1]
+                         f"{tuple(tokens)}, got {tuple(shape)}")
+    H, dr = shape[-2] if heads else 1, shape[-1]
     _tensor("inv_freq", inv_freq, _F64, None, dev)
     if dr % 2 or dr == 0 or inv_freq.shape != (dr // 2,):
         raise ValueError(f"x has {dr} rotary channels: inv_freq must be [{dr // 2}] and "
@@ -136,41 +130,35 @@ def kda_rope(x, positions, inv_freq, *, k=None, interleaved=True, scale=1.0, tra
     if not math.isfinite(scale):
         raise ValueError(f"scale must be finite, got {scale}")
     if out is None:
-        out = _new(stream, x.shape, x.dtype, dev)
+        out = _new(stream, shape, x.dtype, dev)
     else:
-        _like("out", out, x, x.shape)
-    n = positions.numel()
+        _like("out", out, x, shape)
+    x_st, o_st = x.stride(), out.stride()
+    x_ts, o_ts = _step("x", shape, x_st, lead), _step("out", shape, o_st, lead)
+    x_hs, o_hs = (x_st[-2], o_st[-2]) if heads and H > 1 else (dr, dr)
     at_k = at_ko = None
     k_ts = ko_ts = dr
     if k is not None:
-        _like("k", k, x, (*positions.shape, dr))
+        k_shape = (*tokens, dr)
+        _like("k", k, x, k_shape)
         if k_out is None:
-            k_out = _new(stream, k.shape, k.dtype, dev)
+            k_out = _new(stream, k_shape, x.dtype, dev)
         else:
-            _like("k_out", k_out, x, k.shape)
-        k_ts, _ = _heads("k", k, lead, False)
-        ko_ts, _ = _heads("k_out", k_out, lead, False)
+            _like("k_out", k_out, x, k_shape)
+            ko_ts = _step("k_out", k_shape, k_out.stride(), lead)
+        k_ts = _step("k", k_shape, k.stride(), lead)
         at_k, at_ko = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out is given without k")
-    x_ts, x_hs = _heads("x", x, lead, heads)
-    o_ts, o_hs = _heads("out", out, lead, heads)
+    n = positions.numel()
     if n > 0 and H > 0:
         _check(library().kda_rope(
             x.data_ptr(), x_ts, x_hs, out.data_ptr(), o_ts, o_hs, at_k, k_ts, at_ko, ko_ts,
-            positions.data_ptr(), inv_freq.data_ptr(), n, H, dr, 1 if interleaved else 0, scale,
-            1 if transpose else 0, code, raw), "kda_rope")
+            positions.data_ptr(), inv_freq.data_ptr(), n, H, dr, interleaved, scale, transpose,
+            code, raw), "kda_rope")
     elif n > 0 and k is not None:
         raise ValueError("x has no heads")
     return out if k is None else (out, k_out)
-
-
-def _norm_rows(name, t):
-    if t.dim() < 1:
-        raise ValueError(f"{name} must be [*rows, W]")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    return t.shape[-1] if t.numel() == 0 else _rows(name, t, t.dim() - 1)
 
 
 def kda_norm_fwd(x, weight=None, bias=None, *, center=True, eps=1e-5, out=None, stats=True,
@@ -181,27 +169,31 @@ def kda_norm_fwd(x, weight=None, bias=None, *, center=True, eps=1e-5, out=None, 
     Returns ``(out, mean, rstd)``: fp32 ``[*rows]`` for ``kda_norm_bwd``, mean None without
     ``center``, both None without ``stats``."""
     code = _code("x", x)
-    dev = x.device
+    dev, shape = x.device, x.shape
     raw = _stream(stream, dev)
-    x_rs = _norm_rows("x", x)
-    W, lead = x.shape[-1], x.shape[:-1]
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            _tensor(name, t, _F32, (W,), dev)
+    lead = len(shape) - 1
+    if lead < 0:
+        raise ValueError("x must be [*rows, W]")
+    W, rows = shape[-1], shape[:-1]
+    n = rows[0] if lead == 1 else math.prod(rows)
+    x_rs = _step("x", shape, x.stride(), lead)
+    if weight is not None:
+        _tensor("weight", weight, _F32, (W,), dev)
+    if bias is not None:
+        _tensor("bias", bias, _F32, (W,), dev)
     eps = float(eps)
     if not (eps > 0.0 and math.isfinite(eps)):
         raise ValueError(f"eps must be finite and positive, got {eps}")
     if out is None:
-        out = _new(stream, x.shape, x.dtype, dev)
+        out, out_rs = _new(stream, shape, x.dtype, dev), W
     else:
-        _like("out", out, x, x.shape)
-    out_rs = _norm_rows("out", out)
-    mean = _new(stream, lead, _F32, dev) if stats and center else None
-    rstd = _new(stream, lead, _F32, dev) if stats else None
-    n = math.prod(lead)
+        _like("out", out, x, shape)
+        out_rs = _step("out", shape, out.stride(), lead)
+    mean = _new(stream, rows, _F32, dev) if stats and center else None
+    rstd = _new(stream, rows, _F32, dev) if stats else None
     _check(library().kda_norm_fwd(
         x.data_ptr(), x_rs, None if weight is None else weight.data_ptr(),
-        None if bias is None else bias.data_ptr(), n, W, code, 1 if center else 0, eps,
+        None if bias is None else bias.data_ptr(), n, W, code, center, eps,
         out.data_ptr(), out_rs, None if mean is None else mean.data_ptr(),
         None if rstd is None else rstd.data_ptr(), raw), "kda_norm_fwd")
     return out, mean, rstd
@@ -218,25 +210,28 @@ def kda_norm_bwd(d_out, x, weight, mean, rstd, *, bias=False, d_x=None, workspac
     d_bias)``, the sums in fp32, d_weight None without ``weight``, d_bias None without
     ``bias``.  ``d_x`` may be given as a view, and be d_out or x itself."""
     code = _code("x", x)
-    dev = x.device
+    dev, shape = x.device, x.shape
     raw = _stream(stream, dev)
-    x_rs = _norm_rows("x", x)
-    W, lead = x.shape[-1], x.shape[:-1]
-    _like("d_out", d_out, x, x.shape)
-    g_rs = _norm_rows("d_out", d_out)
+    lead = len(shape) - 1
+    if lead < 0:
+        raise ValueError("x must be [*rows, W]")
+    W, rows = shape[-1], shape[:-1]
+    n = rows[0] if lead == 1 else math.prod(rows)
+    x_rs = _step("x", shape, x.stride(), lead)
+    _like("d_out", d_out, x, shape)
+    g_rs = _step("d_out", shape, d_out.stride(), lead)
     if weight is not None:
         _tensor("weight", weight, _F32, (W,), dev)
     if mean is not None:
-        _tensor("mean", mean, _F32, lead, dev)
-    _tensor("rstd", rstd, _F32, lead, dev)
+        _tensor("mean", mean, _F32, rows, dev)
+    _tensor("rstd", rstd, _F32, rows, dev)
     if d_x is None:
-        d_x = _new(stream, x.shape, x.dtype, dev)
+        d_x, dx_rs = _new(stream, shape, x.dtype, dev), W
     else:
-        _like("d_x", d_x, x, x.shape)
-    dx_rs = _norm_rows("d_x", d_x)
+        _like("d_x", d_x, x, shape)
+        dx_rs = _step("d_x", shape, d_x.stride(), lead)
     d_weight = _new(stream, (W,), _F32, dev) if weight is not None else None
     d_bias = _new(stream, (W,), _F32, dev) if bias else None
-    n = math.prod(lead)
     at_ws, ws_bytes = None, 0
     if weight is not None or bias:
         ws = _workspace(workspace, _size("kda_norm_bwd_workspace_size", dev.index, n, W, code),

@@ -178,18 +178,23 @@ def test_evict_of_no_sequences_launches_nothing(lib):
 
 def test_rows_of_a_view_are_evenly_spaced():
     from gated_delta_rule_13_gb300 import rows
+    step = lambda t, lead: rows._step("x", t.shape, t.stride(), lead)  # noqa: E731
     x = torch.zeros(4, 6, 3, 64)
-    assert rows._rows("x", x, 2) == 192
-    assert rows._rows("x", x[:, :, :, 8:40], 2) == 192
-    assert rows._rows("x", x[:, 2:3], 2) == 6 * 192
-    assert rows._rows("x", x[1:2, 2:3], 2) == 192
-    assert rows._rows("x", x[:, ::2], 2) == 384
-    assert rows._rows("x", x[0, :, 0].expand(6, 64), 1) == 192
-    assert rows._rows("x", x[0, 0, 0].expand(5, 64), 1) == 0
+    assert step(x, 2) == 192
+    assert step(x[:, :, :, 8:40], 2) == 192
+    assert step(x[:, 2:3], 2) == 6 * 192
+    assert step(x[1:2, 2:3], 2) == 192
+    assert step(x[:, ::2], 2) == 384
+    assert step(x[0, :, 0].expand(6, 64), 1) == 192
+    assert step(x[0, 0, 0].expand(5, 64), 1) == 0
+    assert step(x[:0], 2) == step(x[:, :0], 2) == 64
+    assert step(x[0, 0, 0], 0) == 64
     with pytest.raises(ValueError, match="evenly"):
-        rows._rows("x", x[:, :5], 2)
+        step(x[:, :5], 2)
     with pytest.raises(ValueError, match="evenly"):
-        rows._rows("x", x.transpose(0, 1), 2)
+        step(x.transpose(0, 1), 2)
+    with pytest.raises(ValueError, match="contiguous"):
+        step(x[..., ::2], 2)
 
 
 def test_inv_freq():
