@@ -20,17 +20,29 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kGroup = 4;          // pieces in flight per thread
+constexpr int kThreads = 256, kSmThreads = 1024;   // of a block at most, of an SM
+template <bool kInterleaved>
+constexpr int kGroup = kInterleaved ? 6 : 3;   // pieces in flight per thread: 96 bytes
 constexpr int kMaxAngles = 2048;   // of a block
 
-// Turns per position, 2^64 to the turn, of an angle per position in radians: the product
-// with 1 / (2 pi), held as the sum of two doubles.
+// Turns per position, 2^64 to the turn and modulo a turn, of an angle per position in radians,
+// |f| < 2^118: the significand times 2^130 / (2 pi), shifted by what the exponent leaves.  In
+// integers, because the 64-bit floating-point pipe is narrow here: off by one at most.
 __device__ __forceinline__ uint64_t turns_of(double f) {
-  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
-  const double hi = f * kHi, lo = fma(f, kHi, -hi) + f * kLo;
-  const double frac = hi - floor(hi);                    // exact
-  return (uint64_t)(frac * 0x1p64) + (uint64_t)(int64_t)(lo * 0x1p64);
+  constexpr uint64_t kHi = 0xa2f9836e4e441529ull, kLo = 0xfc2757d1f534ddc1ull;  // 2^130 / (2 pi)
+  const uint64_t bits = (uint64_t)__double_as_longlong(f);
+  const int exponent = (int)(bits >> 52 & 2047);
+  const uint64_t m = (bits & 0xfffffffffffffull) | (exponent ? 1ull << 52 : 0);
+  uint64_t w0 = m * kLo, w1 = __umul64hi(m, kLo), w2 = __umul64hi(m, kHi);
+  const uint64_t mid = m * kHi;
+  w1 += mid;
+  w2 += w1 < mid;
+  const int shift = 1141 - exponent, bit = shift & 63;
+  if (shift < 0 || shift >= 192) return 0;
+  const uint64_t lo = shift < 64 ? w0 : shift < 128 ? w1 : w2;
+  const uint64_t hi = shift < 64 ? w1 : shift < 128 ? w2 : 0;
+  const uint64_t t = bit ? lo >> bit | hi << (64 - bit) : lo;
+  return bits >> 63 ? 0 - t : t;
 }
 
 template <typename T>
@@ -128,111 +140,101 @@ struct Piece {
 };
 
 struct Shape {
-  int unit_bits, head_bits;   // lanes of a block: pieces of a row, heads, the rest tokens
-  int tokens;                 // of a block
-  int heads;                  // of a block (the key counts as head H)
+  int unit_bits;    // lanes of a block: pieces of a row, the rest rows
+  int tokens;       // of a block
+  int heads;        // of a block (the key counts as head H)
+  uint32_t magic;   // 2^32 / heads, rounded up
 };
 
-// Block (x: tokens, y: heads).  Its angles' cosines and sines are worked out once, in
-// shared memory, while its first pieces are on their way.
+// Block (x: tokens, y: heads); its rows, a token's heads beside one another, go over the lanes in
+// turn.  The cosines and sines of its angles are worked out once, in shared memory, while its
+// first pieces are on their way.
 template <typename T, bool kInterleaved, bool kVector>
-__global__ void __launch_bounds__(kThreads) kda_rope_kernel(const RopeArgs a, const Shape sh) {
+__global__ void __launch_bounds__(kThreads, kSmThreads / kThreads) kda_rope_kernel(const RopeArgs a, const Shape sh) {
   using P = Piece<T, kInterleaved, kVector>;
   extern __shared__ float2 cs[];                         // [tokens][pairs]
-  __shared__ uint64_t step[kRopeMax / 2];
   const int half = a.dr / 2, tid = threadIdx.x;
-  const int units = half / P::kPairs;
-  const int unit = tid & ((1 << sh.unit_bits) - 1);
-  const int hl = (tid >> sh.unit_bits) & ((1 << sh.head_bits) - 1);
-  const int tl = tid >> (sh.unit_bits + sh.head_bits);
-  const int hp = 1 << sh.head_bits, tp = kThreads >> (sh.unit_bits + sh.head_bits);
+  const int unit = tid & ((1 << sh.unit_bits) - 1), step = blockDim.x >> sh.unit_bits;
+  const int pair = unit * P::kPairs;
   const int64_t t0 = (int64_t)blockIdx.x * sh.tokens;
   const int nt = (int)min((int64_t)sh.tokens, a.n - t0);
-  const int h0 = blockIdx.y * sh.heads;
-  const int h1 = min(h0 + sh.heads, a.H + (a.k != nullptr));
-  const int pair = unit * P::kPairs;
-  // Pieces of this thread: heads h0 + hl + i hp of tokens tl + j tp, heads first.
-  int t = unit < units && h0 + hl < h1 ? tl : nt, h = h0 + hl;
-  P piece[kGroup];
-  T *to[kGroup];
-  int at[kGroup];                                        // token of the block, -1: none
+  const int h0 = blockIdx.y * sh.heads, heads = min(sh.heads, a.H + (a.k != nullptr) - h0);
+  const int rows = pair < half ? nt * sh.heads : 0;      // of the last heads some are none
+  int r = tid >> sh.unit_bits;
+  constexpr int G = kGroup<kInterleaved>;
+  P piece[G];
+  T *to[G];
+  int at[G];                                        // token of the block, -1: none
   const auto load = [&] {
 #pragma unroll
-    for (int i = 0; i < kGroup; ++i) {
+    for (int i = 0; i < G; ++i) {
       at[i] = -1;
-      if (t < nt) {
+      const int t = sh.heads == 1 ? r : (int)__umulhi((uint32_t)r, sh.magic), h = r - t * sh.heads;
+      if (r < rows && h < heads) {
         const int64_t tok = t0 + t;
         const T *from;
-        if (h < a.H) {
-          from = static_cast<const T *>(a.x) + tok * a.x_ts + h * a.x_hs;
-          to[i] = static_cast<T *>(a.out) + tok * a.o_ts + h * a.o_hs;
+        if (h0 + h < a.H) {
+          from = static_cast<const T *>(a.x) + tok * a.x_ts + (h0 + h) * a.x_hs;
+          to[i] = static_cast<T *>(a.out) + tok * a.o_ts + (h0 + h) * a.o_hs;
         } else {
           from = static_cast<const T *>(a.k) + tok * a.k_ts;
           to[i] = static_cast<T *>(a.k_out) + tok * a.ko_ts;
         }
         piece[i].load(from, pair, half);
         at[i] = t;
-        h += hp;
-        if (h >= h1) {
-          h = h0 + hl;
-          t += tp;
-        }
       }
+      r += step;
     }
   };
   load();
-  for (int i = tid; i < half; i += kThreads) step[i] = turns_of(a.inv_freq[i]);
-  __syncthreads();
-  for (int i = tid; i < nt * half; i += kThreads) {
+  for (int i = tid; i < nt * half; i += blockDim.x) {
     const int tok = i / half, p = i - tok * half;
-    const uint64_t turns = (uint64_t)(int64_t)a.positions[t0 + tok] * step[p];
+    const uint64_t turns = (uint64_t)(int64_t)a.positions[t0 + tok] * turns_of(a.inv_freq[p]);
     float s, c;
     sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);
     cs[i] = make_float2(c * a.scale, (a.transpose ? -s : s) * a.scale);
   }
   __syncthreads();
-  while (at[0] >= 0) {
+  for (;;) {
 #pragma unroll
-    for (int i = 0; i < kGroup; ++i)
+    for (int i = 0; i < G; ++i)
       if (at[i] >= 0) piece[i].turn_store(to[i], pair, half, cs + at[i] * half + pair);
+    if (r >= rows) break;
     load();
   }
-}
-
-int bits_for(int n) {
-  int b = 0;
-  while ((1 << b) < n) ++b;
-  return b;
 }
 
 template <typename T, bool kInterleaved, bool kVector>
 cudaError_t launch(const RopeArgs &a, cudaStream_t stream) {
   using P = Piece<T, kInterleaved, kVector>;
   const int half = a.dr / 2, units = half / P::kPairs, heads = a.H + (a.k != nullptr);
+  const int64_t sms = latent::sm_count() > 0 ? latent::sm_count() : 1;
   Shape sh;
-  sh.unit_bits = bits_for(units);
-  sh.head_bits = bits_for(heads);
-  if (sh.unit_bits + sh.head_bits > 8) sh.head_bits = 8 - sh.unit_bits;
-  // the key beside a full set of heads takes a turn of its own rather than twice the lanes
-  if (sh.head_bits > 0 && (1 << (sh.head_bits - 1)) == a.H) --sh.head_bits;
-  const int tp = kThreads >> (sh.unit_bits + sh.head_bits), hp = 1 << sh.head_bits;
-  const int sms = latent::sm_count() > 0 ? latent::sm_count() : 1;
-  // Tokens of a block: about 8 pieces a thread, as far as the grid keeps four blocks an SM.
-  int turns = (heads + hp - 1) / hp;                     // of a thread, for one token
-  sh.tokens = tp;
-  while (turns * (sh.tokens / tp) < 8 && sh.tokens * 2 * half <= kMaxAngles &&
-         (a.n + sh.tokens * 2 - 1) / (sh.tokens * 2) >= 4 * sms)
-    sh.tokens *= 2;
-  while (sh.tokens * half > kMaxAngles) sh.tokens /= 2;
-  // Few tokens: their heads over several blocks.
+  sh.unit_bits = 0;
+  while ((1 << sh.unit_bits) < units) ++sh.unit_bits;
+  // Blocks are small, 128 threads, unless a token's heads are more than these have in flight.
+  constexpr int G = kGroup<kInterleaved>;
+  const int threads = (kThreads / 2 >> sh.unit_bits) * G >= heads && units <= kThreads / 2
+                          ? kThreads / 2 : kThreads;
+  const int64_t blocks_sm = kSmThreads / threads, lanes = threads >> sh.unit_bits;  // rows at a time
+  // A block's rows: what its lanes have in flight, or all heads of a token, whose angles are then
+  // worked out once, where tokens are enough to fill the SMs; fewer where SMs would have none.
+  int64_t rows = lanes * G;
+  if (heads > rows && a.n >= blocks_sm * sms) rows = heads < 16 * lanes ? heads : 16 * lanes;
+  while (rows > lanes && a.n * heads < rows * blocks_sm * sms) rows /= 2;
   sh.heads = heads;
+  if (heads > rows) {                                    // one token over several blocks
+    const int64_t split = (heads + rows - 1) / rows;
+    sh.heads = (int)((heads + split - 1) / split);
+  }
+  sh.tokens = (int)(rows / sh.heads);
+  if (sh.tokens > kMaxAngles / half) sh.tokens = kMaxAngles / half;
+  if (sh.tokens < 1) sh.tokens = 1;
+  sh.magic = (uint32_t)(((1ull << 32) + sh.heads - 1) / sh.heads);   // 0 for one head: not used
   const int64_t blocks = (a.n + sh.tokens - 1) / sh.tokens;
-  while (sh.heads > hp && blocks * ((heads + sh.heads - 1) / sh.heads) < sms)
-    sh.heads = (sh.heads / 2 + hp - 1) / hp * hp;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)blocks, (unsigned)((heads + sh.heads - 1) / sh.heads));
   kda_rope_kernel<T, kInterleaved, kVector>
-      <<<grid, kThreads, (size_t)sh.tokens * half * sizeof(float2), stream>>>(a, sh);
+      <<<grid, threads, (size_t)sh.tokens * half * sizeof(float2), stream>>>(a, sh);
   return cudaGetLastError();
 }
 
