@@ -8,12 +8,18 @@
 // as many movers as holes, they come from [last, n - recent) and go to [first, last), and
 // the cache's rows have no order but the last ones.
 //
-// Selection: one block a (layer, sequence).  A weight becomes an unsigned number of the
-// same order; its bytes are fixed one after another, from the top, by counting the
-// candidates that share the bytes before (a radix selection), which leaves the last kept
-// value and how many of its equals are kept.  Each warp then walks its own stretch of the
-// candidates in order with the counts of the stretches before it, so that ranks need no
-// sorting.  The moves follow in a second kernel.
+// Selection, one block a (layer, sequence): a weight becomes an unsigned number of the same
+// order.  Counts by its upper 11 bits (four bins an octave) tell in which bin the last kept one
+// is; the few in that bin are ranked against each other.  Where they are not few, the bits that
+// are left are fixed some at a time by counts in the same way (a radix selection), and equal
+// weights by their order.  Each warp then walks its own stretch of the candidates in order and,
+// with the counts of the stretches before it, lists holes and movers in the workspace.
+//
+// Moves, in a second kernel that starts beside the first.  The last rows take places that movers
+// leave, and where n - budget < recent also one another's.  Where they do not, a place and all
+// that goes through it are one warp's: first the mover leaves, then the last row comes.  Where
+// they do (and then there are few movers), a block has some columns of all rows and takes the
+// movers first.  No block waits for another.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -24,14 +30,22 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kKeep = 16384;               // candidates in shared memory
+constexpr int kBins = 2048, kLow = 21;     // of the first count; bits below it
+constexpr int kFew = 1024;                 // ranked directly
+static_assert(kBins % kThreads == 0 && kBins <= 4 * kThreads, "a thread has four bins at most");
 
-// Scratch of a (layer, sequence): [0] moves, [1] rows that move up, [2], [3] unused, then
-// `budget` destinations and `budget` sources.
+// Scratch of a (layer, sequence): what to move, then as many numbers as the budget each of
+// destinations and sources of movers (the moves), then where the row at each of the last
+// `recent` places goes, -1: nowhere.
+struct Moves {
+  int32_t movers, near, recent, n;         // near: movers from places that the last rows take
+};
 constexpr int kHead = 4;
-__host__ __device__ inline int64_t scratch_ints(int32_t budget) {
-  return kHead + 2 * (int64_t)((budget + 3) / 4 * 4);
-}
+static_assert(sizeof(Moves) == kHead * sizeof(int32_t), "head of the scratch");
+__host__ __device__ inline int64_t list_ints(int32_t budget) { return ((int64_t)budget + 3) / 4 * 4; }
+__host__ __device__ inline int64_t scratch_ints(int32_t budget) { return kHead + 3 * list_ints(budget); }
 
 // In the order of the weights; one that is no number is below all others.
 __device__ __forceinline__ uint32_t order_of(float w) {
@@ -40,8 +54,10 @@ __device__ __forceinline__ uint32_t order_of(float w) {
   return u >> 31 ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheEvictArgs a) {
-  __shared__ int hist[256], counts[3][kWarps], pick[2], bad;
+__global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheEvictArgs a, const int32_t room) {
+  extern __shared__ uint32_t keys[];       // [room] candidates, as numbers
+  __shared__ int hist[kBins], counts[2][kWarps], pick[3], bad, gathered;
+  __shared__ uint2 few[kFew];              // value, position
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t lb = blockIdx.x;
   const int b = (int)(lb % a.B);
@@ -50,30 +66,36 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
   const float *w = a.weights + lb * cap;
   float *to = a.weights_out + lb * cap;
   int32_t *origin = a.origin + lb * a.budget;
-  int32_t *moves = a.moves + lb * scratch_ints(a.budget);
-  int32_t *dst = moves + kHead, *src = dst + (a.budget + 3) / 4 * 4;
+  int32_t *scratch = a.moves + lb * scratch_ints(a.budget);
+  int32_t *dst = scratch + kHead, *src = dst + list_ints(a.budget), *via = src + list_ints(a.budget);
+  const int32_t *table = a.block_table + (int64_t)b * a.max_pages;
   const bool same = w == to;
+  // candidates [lo, hi), a stretch a warp; `keep` of them stay
+  const int lo = a.first, hi = (n < 0 || n > cap ? 0 : n) - a.recent, last = a.budget - a.recent;
+  const int stretch = ((max(hi - lo, 0) + kWarps - 1) / kWarps + 31) / 32 * 32;
+  const int s0 = min(lo + warp * stretch, hi), s1 = min(s0 + stretch, hi);
   latent::pdl_launch_dependents();
 
   if (tid == 0) bad = n < 0 || n > cap;
   __syncthreads();
+  const bool here = hi - lo <= room;
   if (!bad) {
     const int pages = (n + a.page_size - 1) / a.page_size;
     bool wrong = false;
-    for (int i = tid; i < pages; i += kThreads) {
-      const int32_t id = a.block_table[(int64_t)b * a.max_pages + i];
-      wrong = wrong || id < 0 || id >= a.n_pages;
-    }
+    if (here && n > a.budget)              // each its own ones
+#pragma unroll 4
+      for (int i = s0 + lane; i < s1; i += 32) keys[i - lo] = order_of(w[i]);
+    for (int i = tid; i < pages; i += kThreads) wrong = wrong || table[i] < 0 || table[i] >= a.n_pages;
     if (wrong) bad = 1;
   }
   __syncthreads();
   const bool refused = bad != 0;
   if (tid == 0) {
-    moves[0] = moves[1] = 0;
     if (refused && a.status) atomicCAS(a.status, 0, (int32_t)KDA_ERR_INVALID_ARG);
     if (lb < a.B) a.new_lens[b] = refused ? n : min(n, a.budget);
   }
   if (refused || n <= a.budget) {          // all rows stay
+    if (tid == 0) *reinterpret_cast<Moves *>(scratch) = Moves{0, 0, 0, 0};
     for (int i = tid; i < a.budget; i += kThreads) origin[i] = !refused && i < n ? i : -1;
     const int live = refused ? cap : n;
     if (!same)
@@ -82,112 +104,181 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
     return;
   }
 
-  // candidates [lo, hi), `keep` of them stay
-  const int lo = a.first, hi = n - a.recent, last = a.budget - a.recent;
-  const int keep = last - lo;
-  uint32_t prefix = 0, known = 0;          // the last kept value's upper bytes
-  int left = keep;                         // kept ones among those that share them
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kThreads) hist[i] = 0;
-    __syncthreads();
-    for (int i = lo + tid; i < hi; i += kThreads) {
-      const uint32_t u = order_of(w[i]);
-      if ((u & known) == prefix) atomicAdd(&hist[u >> shift & 255], 1);
+  // f(position, value), the warp together, in order; positions >= s1 are none
+  const auto each = [&](auto f) {
+    if (here) {
+#pragma unroll 2
+      for (int i0 = s0; i0 < s1; i0 += 32) f(i0 + lane, i0 + lane < s1 ? keys[i0 + lane - lo] : 0);
+    } else {
+#pragma unroll 1
+      for (int i0 = s0; i0 < s1; i0 += 32) f(i0 + lane, i0 + lane < s1 ? order_of(w[i0 + lane]) : 0);
     }
-    __syncthreads();
-    if (warp == 0) {                       // the byte of the left-th from the top
-      int mine[8], sum = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) sum += mine[k] = hist[255 - (8 * lane + k)];
-      int upto = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
-      }
-      int above = upto - sum;
-      if (above < left && upto >= left)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (above < left && above + mine[k] >= left) {
-            pick[0] = 255 - (8 * lane + k);
-            pick[1] = left - above;
-          }
-          above += mine[k];
-        }
-      if (left == 0 && lane == 0) {        // none is kept: above every value there is
-        pick[0] = 255;
-        pick[1] = 0;
-      }
-    }
-    __syncthreads();
-    prefix |= (uint32_t)pick[0] << shift;
-    known |= 255u << shift;
-    left = pick[1];
-    __syncthreads();
-  }
-  // kept: above `prefix`, and the first `left` of its equals.  (With none to keep, prefix is
-  // all ones, which no weight becomes, and left is 0.)
-  const int stretch = ((hi - lo + kWarps - 1) / kWarps + 31) / 32 * 32;
-  const int s0 = min(lo + warp * stretch, hi), s1 = min(s0 + stretch, hi);
-  int equal = 0;
-  for (int i = s0 + lane; i < s1; i += 32) equal += order_of(w[i]) == prefix;
-  equal = __reduce_add_sync(0xffffffffu, equal);
-  if (lane == 0) counts[0][warp] = equal;
-  __syncthreads();
-  const auto before = [&](const int *c) {
-    return __reduce_add_sync(0xffffffffu, lane < warp ? c[lane] : 0);
   };
-  const int equal0 = before(counts[0]);
-  // Two walks over the stretch: holes and movers are counted, then listed.
-  int hole0 = 0, mover0 = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    int eq = equal0, holes = 0, movers = 0;
-    for (int i0 = s0; i0 < s1; i0 += 32) {
-      const int i = i0 + lane;
-      const uint32_t u = i < s1 ? order_of(w[i]) : 0;
-      const unsigned same_value = __ballot_sync(0xffffffffu, i < s1 && u == prefix);
-      const unsigned under = (1u << lane) - 1;
-      const bool kept = i < s1 && (u > prefix || (u == prefix && eq + __popc(same_value & under) < left));
-      eq += __popc(same_value);
-      const bool hole = i < s1 && !kept && i < last, mover = kept && i >= last;
-      const unsigned hs = __ballot_sync(0xffffffffu, hole), ms = __ballot_sync(0xffffffffu, mover);
-      if (pass == 1) {
-        if (hole) dst[hole0 + holes + __popc(hs & under)] = i;
-        if (mover) src[mover0 + movers + __popc(ms & under)] = i;
-        if (i < last && kept) origin[i] = i;
-        if (i < last && kept && !same) to[i] = w[i];
-      }
-      holes += __popc(hs);
-      movers += __popc(ms);
+  // Of counts in hist[0 .. bins), the bin of the `left`-th from the top: pick = bin, what is
+  // left of it there, its count.
+  const auto find = [&](int bins, int left) {
+    constexpr int kPer = kBins / kThreads;
+    int c[kPer], sum = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int at = bins - 1 - (kPer * tid + k);
+      sum += c[k] = at >= 0 ? hist[at] : 0;
     }
-    if (pass == 0) {
-      if (lane == 0) {
-        counts[1][warp] = holes;
-        counts[2][warp] = movers;
+    int upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    if (lane == 31) counts[0][warp] = upto;
+    __syncthreads();
+    upto += __reduce_add_sync(0xffffffffu, lane < warp ? counts[0][lane] : 0);
+    int above = upto - sum;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      if (above < left && above + c[k] >= left) {
+        pick[0] = bins - 1 - (kPer * tid + k);
+        pick[1] = left - above;
+        pick[2] = c[k];
+      }
+      above += c[k];
+    }
+    __syncthreads();
+  };
+  // Kept: what is above `value`, and of its equals those up to `place`.
+  uint32_t value = ~0u;
+  int place = -1;
+  if (last > lo) {
+    for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
+    if (tid == 0) gathered = 0;
+    __syncthreads();
+    each([&](int i, uint32_t u) {
+      if (i < s1) atomicAdd(&hist[u >> kLow], 1);
+    });
+    __syncthreads();
+    find(kBins, last - lo);
+    value = (uint32_t)pick[0] << kLow;
+    int left = pick[1];
+    const int inside = pick[2];
+    place = 0x7fffffff;                    // all of the bin, if they are as many as are left
+    if (left < inside && inside <= kFew) {
+      each([&](int i, uint32_t u) {
+        if (i < s1 && u >> kLow == value >> kLow)
+          few[atomicAdd(&gathered, 1)] = make_uint2(u, (uint32_t)i);
+      });
+      __syncthreads();
+      for (int k = tid; k < inside; k += kThreads) {
+        const uint2 me = few[k];
+        int rank = 0;
+#pragma unroll 4
+        for (int l = 0; l < inside; ++l) {
+          const uint2 x = few[l];
+          rank += x.x > me.x || (x.x == me.x && x.y < me.y);
+        }
+        if (rank == left - 1) {
+          pick[0] = (int)me.x;
+          pick[1] = (int)me.y;
+        }
       }
       __syncthreads();
-      hole0 = before(counts[1]);
-      mover0 = before(counts[2]);
+      value = (uint32_t)pick[0];
+      place = pick[1];
+    } else if (left < inside) {
+      uint32_t known = ~0u << kLow;
+      for (int shift = kLow; shift > 0;) {
+        const int bits = min(shift, 8);
+        shift -= bits;
+        for (int i = tid; i < 256; i += kThreads) hist[i] = 0;
+        __syncthreads();
+        each([&](int i, uint32_t u) {      // equal ones are counted by one lane
+          const bool in = i < s1 && (u & known) == value;
+          const int digit = u >> shift & ((1 << bits) - 1);
+          const unsigned peers = __match_any_sync(0xffffffffu, in ? digit : 256);
+          if (in && lane == __ffs(peers) - 1) atomicAdd(&hist[digit], __popc(peers));
+        });
+        __syncthreads();
+        find(1 << bits, left);
+        value |= (uint32_t)pick[0] << shift;
+        known |= ((1u << bits) - 1) << shift;
+        left = pick[1];
+        __syncthreads();
+      }
+      // the place of the left-th of those equal to it
+      int equal = 0;
+      each([&](int i, uint32_t u) { equal += __popc(__ballot_sync(0xffffffffu, i < s1 && u == value)); });
+      if (lane == 0) counts[0][warp] = equal;
+      __syncthreads();
+      int seen = __reduce_add_sync(0xffffffffu, lane < warp ? counts[0][lane] : 0);
+      each([&](int i, uint32_t u) {
+        const unsigned alike = __ballot_sync(0xffffffffu, i < s1 && u == value);
+        if (alike >> lane & 1 && seen + __popc(alike & ((1u << lane) - 1)) == left - 1) pick[0] = i;
+        seen += __popc(alike);
+      });
+      __syncthreads();
+      place = pick[0];
     }
   }
-  __syncthreads();
-  int total = 0;
-  for (int k = 0; k < kWarps; ++k) total += counts[1][k];
-  if (tid == 0) {
-    moves[0] = total;
-    moves[1] = a.recent;
+  __syncthreads();                         // counts are free
+
+  // ---- holes and movers, counted and listed
+  const auto kept = [&](int i, uint32_t u) {
+    return i < s1 && (u > value || (u == value && i <= place));
+  };
+  int holes = 0, movers = 0;
+  each([&](int i, uint32_t u) {
+    const bool yes = kept(i, u);
+    holes += i < s1 && !yes && i < last;
+    movers += yes && i >= last;
+  });
+  holes = __reduce_add_sync(0xffffffffu, holes);
+  movers = __reduce_add_sync(0xffffffffu, movers);
+  if (lane == 0) {
+    counts[0][warp] = holes;
+    counts[1][warp] = movers;
   }
+  for (int i = tid; i < a.recent; i += kThreads) via[i] = -1;
+  __syncthreads();
+  int hole = __reduce_add_sync(0xffffffffu, lane < warp ? counts[0][lane] : 0);
+  int mover = __reduce_add_sync(0xffffffffu, lane < warp ? counts[1][lane] : 0);
+  const int total = __reduce_add_sync(0xffffffffu, lane < kWarps ? counts[0][lane] : 0);
+  const unsigned under = (1u << lane) - 1;
+  each([&](int i, uint32_t u) {
+    const bool yes = kept(i, u), h = i < s1 && !yes && i < last, m = yes && i >= last;
+    const unsigned hs = __ballot_sync(0xffffffffu, h), ms = __ballot_sync(0xffffffffu, m);
+    if (h) dst[hole + __popc(hs & under)] = i;
+    if (m) src[mover + __popc(ms & under)] = i;
+    hole += __popc(hs);
+    mover += __popc(ms);
+    if (yes && i < last) {
+      origin[i] = i;
+      if (!same) to[i] = w[i];
+    }
+  });
   for (int i = tid; i < lo; i += kThreads) {
     origin[i] = i;
     if (!same) to[i] = w[i];
   }
+  __syncthreads();                         // the lists; and no weight is looked at again
+
+  // ---- weights of movers and of the last rows (chunks in order, read before written)
+  int near = 0;
   for (int i = tid; i < total; i += kThreads) {
-    origin[dst[i]] = src[i];
-    to[dst[i]] = w[src[i]];
+    const int s = src[i], d = dst[i];
+    origin[d] = s;
+    to[d] = w[s];
+    if (s < a.budget) {
+      via[s - last] = d;
+      ++near;
+    }
   }
+  near = __reduce_add_sync(0xffffffffu, near);
+  if (lane == 0) counts[0][warp] = near;
   __syncthreads();
-  // The last rows move up by n - budget: chunks in order, a chunk read before it is written.
+  if (tid == 0) {
+    int sum = 0;
+    for (int k = 0; k < kWarps; ++k) sum += counts[0][k];
+    *reinterpret_cast<Moves *>(scratch) = Moves{total, sum, a.recent, n};
+  }
   for (int i0 = 0; i0 < a.recent; i0 += kThreads) {
     const int i = i0 + tid;
     float v = 0.f;
@@ -202,96 +293,104 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
   for (int i = a.budget + tid; i < cap; i += kThreads) to[i] = 0.f;
 }
 
-constexpr int kMoveThreads = 256;
-constexpr int kSlice = 8;                  // 16-byte columns of a block
-constexpr int kMoveRows = kMoveThreads / kSlice;
-constexpr int kMoveBatch = 8;              // rows in flight per thread
+constexpr int kMoveThreads = 256, kMoveWarps = kMoveThreads / 32;
+constexpr int kSlots = 5;                  // 16-byte pieces in flight per thread
 
-// Block (x: 128-byte column slice and piece of the moves, y: layer and sequence).  Movers'
-// places and holes have no row in common, so they move in any order.  The last rows may
-// take movers' old places, and one another's: they move after the movers (within the
-// block, or in a launch of its own), chunks in order, a chunk read before it is written.
-template <bool kMoves, bool kUp>
-__global__ void __launch_bounds__(kMoveThreads)
-kda_evict_move_kernel(const CacheEvictArgs a, const int32_t slices, const int32_t pieces,
-                      const int64_t lb0) {
+// Block (x: one of `pieces`, y: layer and sequence).
+__global__ void __launch_bounds__(kMoveThreads, 4)
+kda_evict_move_kernel(const CacheEvictArgs a, const int32_t pieces, const int64_t lb0) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t lb = lb0 + blockIdx.y;
-  const int b = (int)(lb % a.B);
-  const int64_t layer = lb / a.B;
-  const int slice = blockIdx.x % slices, piece = blockIdx.x / slices;
-  const int row = threadIdx.x / kSlice;
-  const int64_t col = ((int64_t)slice * kSlice + threadIdx.x % kSlice) * 16;
-  const bool live = col < a.row_bytes;
+  const int32_t *table = a.block_table + (int64_t)(lb % a.B) * a.max_pages;
+  const int32_t *scratch = a.moves + lb * scratch_ints(a.budget);
+  const int32_t *dst = scratch + kHead, *src = dst + list_ints(a.budget), *via = src + list_ints(a.budget);
   unsigned char *pool = static_cast<unsigned char *>(a.cache) +
-                        layer * a.n_pages * a.page_size * a.row_bytes + col;
-  const int32_t *table = a.block_table + (int64_t)b * a.max_pages;
-  const int32_t *moves = a.moves + lb * scratch_ints(a.budget);
-  const int32_t *dst = moves + kHead, *src = dst + (a.budget + 3) / 4 * 4;
-  const auto at = [&](int pos) {
+                        lb / a.B * a.n_pages * a.page_size * a.row_bytes;
+  const int vecs = (int)(a.row_bytes / 16);
+  const auto pool_row = [&](int pos) {
     const int pg = pos / a.page_size;
-    return reinterpret_cast<uint4 *>(
-        pool + ((int64_t)table[pg] * a.page_size + (pos - pg * a.page_size)) * a.row_bytes);
+    return table[pg] * a.page_size + (pos - pg * a.page_size);
+  };
+  const auto piece_at = [&](int row, int col) {
+    return reinterpret_cast<uint4 *>(pool + row * a.row_bytes + (int64_t)col * 16);
   };
   latent::pdl_wait();
-  if (kMoves && live) {
-    const int n = moves[0];
-    constexpr int kStep = kMoveRows * kMoveBatch;
-    for (int i0 = piece * kStep; i0 < n; i0 += pieces * kStep) {
-      uint4 x[kMoveBatch];
-#pragma unroll
-      for (int j = 0; j < kMoveBatch; ++j) {
-        const int i = i0 + j * kMoveRows + row;
-        if (i < n) x[j] = *at(src[i]);
-      }
-#pragma unroll
-      for (int j = 0; j < kMoveBatch; ++j) {
-        const int i = i0 + j * kMoveRows + row;
-        if (i < n) *at(dst[i]) = x[j];
-      }
-    }
-  }
-  if (kUp) {
-    const int n = moves[1];
-    if (n == 0) return;
-    if (kMoves) __syncthreads();           // the movers have been read
-    const int hi = a.seq_lens[b] - n, last = a.budget - n;
-    constexpr int kStep = kMoveRows * kMoveBatch;
-    for (int i0 = 0; i0 < n; i0 += kStep) {
-      uint4 x[kMoveBatch];
-#pragma unroll
-      for (int j = 0; j < kMoveBatch; ++j) {
-        const int i = i0 + j * kMoveRows + row;
-        if (live && i < n) x[j] = *at(hi + i);
-      }
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < kMoveBatch; ++j) {
-        const int i = i0 + j * kMoveRows + row;
-        if (live && i < n) *at(last + i) = x[j];
-      }
-    }
-  }
-}
+  const Moves m = *reinterpret_cast<const Moves *>(scratch);
+  if (m.movers == 0 && m.recent == 0) return;
+  const int hi = m.n - m.recent, last = a.budget - m.recent;
 
-template <bool kMoves, bool kUp>
-cudaError_t launch_moves(const CacheEvictArgs &a, int32_t slices, int32_t pieces, bool overlap,
-                         cudaStream_t stream) {
-  const int64_t all = (int64_t)a.L * a.B;
-  for (int64_t lb = 0; lb < all; lb += 65535) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(slices * pieces), (unsigned)(all - lb < 65535 ? all - lb : 65535));
-    cfg.blockDim = dim3(kMoveThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = overlap && lb == 0 ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kda_evict_move_kernel<kMoves, kUp>, a, slices,
-                                             pieces, lb);
-    if (e != cudaSuccess) return e;
+  if (m.n - a.budget >= m.recent) {
+    // ---- whole rows, some at a time for each warp: the places of the last rows, then the
+    // movers from behind these
+    const int wide = min(vecs, 32 * kSlots);             // pieces of a row at a time
+    const int group = min(32, 32 * kSlots / wide);       // rows at a time
+    int place[kSlots];                                   // row of the group, piece
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      const int v = lane + 32 * j, r = v / wide;
+      place[j] = r < group ? r << 16 | (v - r * wide) : -1;
+    }
+    // rows s to rows d, each by the lane that has that row of the group; -1: none
+    const auto copy = [&](int s, int d) {
+      for (int c0 = 0; c0 < vecs; c0 += wide) {
+        uint4 x[kSlots];
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+          const int row = __shfl_sync(0xffffffffu, s, place[j] < 0 ? 0 : place[j] >> 16);
+          const int col = c0 + (place[j] & 0xffff);
+          if (place[j] >= 0 && row >= 0 && col < vecs) x[j] = *piece_at(row, col);
+        }
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+          const int row = __shfl_sync(0xffffffffu, d, place[j] < 0 ? 0 : place[j] >> 16);
+          const int col = c0 + (place[j] & 0xffff);
+          if (place[j] >= 0 && row >= 0 && col < vecs) *piece_at(row, col) = x[j];
+        }
+      }
+    };
+    const int far = m.movers - m.near, all = m.recent + far;
+    for (int i0 = (blockIdx.x * kMoveWarps + warp) * group; i0 < all; i0 += pieces * kMoveWarps * group) {
+      const int i = i0 + lane;
+      int s = -1, d = -1, out = -1;
+      if (lane < group && i < all) {
+        if (i < m.recent) {
+          s = pool_row(hi + i);
+          d = pool_row(last + i);
+          out = via[i] >= 0 ? pool_row(via[i]) : -1;
+        } else {
+          s = pool_row(src[m.near + i - m.recent]);
+          d = pool_row(dst[m.near + i - m.recent]);
+        }
+      }
+      if (__any_sync(0xffffffffu, out >= 0)) copy(out >= 0 ? d : -1, out);   // the same lanes, in order
+      copy(s, d);
+    }
+    return;
   }
-  return cudaSuccess;
+
+  // ---- some columns of all rows, chunks in order, a chunk read before it is written
+  const int per = (vecs + pieces - 1) / pieces, c0 = blockIdx.x * per, c1 = min(c0 + per, vecs);
+  for (int cc = c0; cc < c1; cc += kMoveThreads) {
+    const int width = min(c1 - cc, kMoveThreads), lanes = kMoveThreads / width;
+    const int col = cc + tid % width, r = tid / width;
+    for (int kind = 0; kind < 2; ++kind) {               // movers, then the last rows
+      const int rows = kind ? m.recent : m.movers;
+      for (int i0 = 0; i0 < rows; i0 += lanes * kSlots) {
+        uint4 x[kSlots];
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+          const int i = i0 + j * lanes + r;
+          if (r < lanes && i < rows) x[j] = *piece_at(pool_row(kind ? hi + i : src[i]), col);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+          const int i = i0 + j * lanes + r;
+          if (r < lanes && i < rows) *piece_at(pool_row(kind ? last + i : dst[i]), col) = x[j];
+        }
+      }
+    }
+  }
 }
 
 }  // namespace
@@ -303,23 +402,27 @@ size_t cache_evict_scratch_bytes(int32_t L, int32_t B, int32_t budget) {
 cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
   const int64_t all = (int64_t)a.L * a.B;
   if (all == 0) return cudaSuccess;
-  kda_evict_select_kernel<<<(unsigned)all, kThreads, 0, stream>>>(a);
+  const int64_t cap = (int64_t)a.max_pages * a.page_size;
+  const int32_t room = (int32_t)(cap < kKeep ? cap : kKeep);
+  if (!latent::kernel_ready<kda_evict_select_kernel>(kKeep * 4, 0)) return cudaErrorNotSupported;
+  kda_evict_select_kernel<<<(unsigned)all, kThreads, (size_t)room * 4, stream>>>(a, room);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int64_t cols = a.row_bytes / 16;
-  const int32_t slices = (int32_t)((cols + kSlice - 1) / kSlice);
-  const int sms = latent::sm_count() > 0 ? latent::sm_count() : 1;
-  const int64_t blocks = all * slices;
-  // Blocks enough that each may have its columns of all rows: one launch.  Else the moves
-  // are shared out, and the last rows follow by themselves.
-  if (blocks >= sms / 2) return launch_moves<true, true>(a, slices, 1, true, stream);
-  const int64_t most = (a.budget - a.first + kMoveRows * kMoveBatch - 1) / (kMoveRows * kMoveBatch);
-  int64_t pieces = 2 * sms / blocks;
-  if (pieces > most) pieces = most;
-  if (pieces < 1) pieces = 1;
-  e = launch_moves<true, false>(a, slices, (int32_t)pieces, true, stream);
-  if (e != cudaSuccess) return e;
-  return a.recent > 0 ? launch_moves<false, true>(a, slices, 1, false, stream) : cudaSuccess;
+  const int64_t sms = latent::sm_count() > 0 ? latent::sm_count() : 1;
+  const int64_t want = 4 * sms / all;      // blocks of a (layer, sequence)
+  const int32_t pieces = (int32_t)(want < 8 ? 8 : want > 64 ? 64 : want);
+  for (int64_t lb = 0; lb < all && e == cudaSuccess; lb += 65535) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)pieces, (unsigned)(all - lb < 65535 ? all - lb : 65535));
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = lb == 0 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, kda_evict_move_kernel, a, pieces, lb);
+  }
+  return e;
 }
 
 }  // namespace kda

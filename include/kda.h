@@ -853,7 +853,7 @@ int kda_latent_weights(const void *q, const void *cache, const int32_t *block_ta
                        int32_t page_size, int32_t max_pages, int dtype, float scale, float decay,
                        float *weights, void *workspace, size_t workspace_bytes, void *stream);
 
-/* Workspace of kda_cache_evict: the moves, 8 bytes a kept row and layer.  Errors:
+/* Workspace of kda_cache_evict: the moves, 12 bytes a kept row and layer.  Errors:
  * KDA_ERR_INVALID_ARG. */
 int kda_cache_evict_workspace_size(int32_t L, int32_t B, int32_t budget, size_t *bytes);
 
