@@ -81,11 +81,13 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
   const bool here = hi - lo <= room;
   if (!bad) {
     const int pages = (n + a.page_size - 1) / a.page_size;
-    bool wrong = false;
+    const int32_t id0 = tid < pages ? table[tid] : 0;
     if (here && n > a.budget)              // each its own ones
 #pragma unroll 4
       for (int i = s0 + lane; i < s1; i += 32) keys[i - lo] = order_of(w[i]);
-    for (int i = tid; i < pages; i += kThreads) wrong = wrong || table[i] < 0 || table[i] >= a.n_pages;
+    bool wrong = id0 < 0 || id0 >= a.n_pages;
+    for (int i = tid + kThreads; i < pages; i += kThreads)
+      wrong = wrong || table[i] < 0 || table[i] >= a.n_pages;
     if (wrong) bad = 1;
   }
   __syncthreads();
@@ -103,6 +105,8 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
     for (int i = live + tid; i < cap; i += kThreads) to[i] = 0.f;
     return;
   }
+
+  const float recent0 = tid < a.recent ? w[hi + tid] : 0.f;   // needed at the end
 
   // f(position, value), the warp together, in order; positions >= s1 are none
   const auto each = [&](auto f) {
@@ -167,15 +171,18 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
           few[atomicAdd(&gathered, 1)] = make_uint2(u, (uint32_t)i);
       });
       __syncthreads();
-      for (int k = tid; k < inside; k += kThreads) {
-        const uint2 me = few[k];
+      for (int k0 = 0; k0 < inside; k0 += kThreads / 4) {   // four threads each
+        const int k = k0 + tid / 4;
+        const uint2 me = few[min(k, inside - 1)];
         int rank = 0;
 #pragma unroll 4
-        for (int l = 0; l < inside; ++l) {
+        for (int l = tid % 4; l < inside; l += 4) {
           const uint2 x = few[l];
           rank += x.x > me.x || (x.x == me.x && x.y < me.y);
         }
-        if (rank == left - 1) {
+        rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+        rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+        if (k < inside && rank == left - 1) {
           pick[0] = (int)me.x;
           pick[1] = (int)me.y;
         }
@@ -262,14 +269,28 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
 
   // ---- weights of movers and of the last rows (chunks in order, read before written)
   int near = 0;
-  for (int i = tid; i < total; i += kThreads) {
-    const int s = src[i], d = dst[i];
-    origin[d] = s;
-    to[d] = w[s];
-    if (s < a.budget) {
-      via[s - last] = d;
-      ++near;
+  constexpr int kBatch = 4;                // moves in flight per thread
+  for (int i0 = tid; i0 < total; i0 += kBatch * kThreads) {
+    int from[kBatch], at[kBatch];
+    float v[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = min(i0 + k * kThreads, total - 1);
+      from[k] = src[i];
+      at[k] = dst[i];
     }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) v[k] = w[from[k]];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (i0 + k * kThreads < total) {
+        origin[at[k]] = from[k];
+        to[at[k]] = v[k];
+        if (from[k] < a.budget) {
+          via[from[k] - last] = at[k];
+          ++near;
+        }
+      }
   }
   near = __reduce_add_sync(0xffffffffu, near);
   if (lane == 0) counts[0][warp] = near;
@@ -281,9 +302,9 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
   }
   for (int i0 = 0; i0 < a.recent; i0 += kThreads) {
     const int i = i0 + tid;
-    float v = 0.f;
+    float v = recent0;
     if (i < a.recent) {
-      v = w[hi + i];
+      if (i0 > 0) v = w[hi + i];
       origin[last + i] = hi + i;
     }
     __syncthreads();
@@ -294,10 +315,10 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
 }
 
 constexpr int kMoveThreads = 256, kMoveWarps = kMoveThreads / 32;
-constexpr int kSlots = 5;                  // 16-byte pieces in flight per thread
+constexpr int kSlots = 9, kColSlots = 5;   // 16-byte pieces in flight per thread: rows, columns
 
 // Block (x: one of `pieces`, y: layer and sequence).
-__global__ void __launch_bounds__(kMoveThreads, 4)
+__global__ void __launch_bounds__(kMoveThreads, 2)
 kda_evict_move_kernel(const CacheEvictArgs a, const int32_t pieces, const int64_t lb0) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t lb = lb0 + blockIdx.y;
@@ -375,16 +396,16 @@ kda_evict_move_kernel(const CacheEvictArgs a, const int32_t pieces, const int64_
     const int col = cc + tid % width, r = tid / width;
     for (int kind = 0; kind < 2; ++kind) {               // movers, then the last rows
       const int rows = kind ? m.recent : m.movers;
-      for (int i0 = 0; i0 < rows; i0 += lanes * kSlots) {
-        uint4 x[kSlots];
+      for (int i0 = 0; i0 < rows; i0 += lanes * kColSlots) {
+        uint4 x[kColSlots];
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j) {
+        for (int j = 0; j < kColSlots; ++j) {
           const int i = i0 + j * lanes + r;
           if (r < lanes && i < rows) x[j] = *piece_at(pool_row(kind ? hi + i : src[i]), col);
         }
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j) {
+        for (int j = 0; j < kColSlots; ++j) {
           const int i = i0 + j * lanes + r;
           if (r < lanes && i < rows) *piece_at(pool_row(kind ? last + i : dst[i]), col) = x[j];
         }
@@ -408,7 +429,7 @@ cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
   kda_evict_select_kernel<<<(unsigned)all, kThreads, (size_t)room * 4, stream>>>(a, room);
   cudaError_t e = cudaGetLastError();
   const int64_t sms = latent::sm_count() > 0 ? latent::sm_count() : 1;
-  const int64_t want = 4 * sms / all;      // blocks of a (layer, sequence)
+  const int64_t want = 2 * sms / all;      // blocks of a (layer, sequence)
   const int32_t pieces = (int32_t)(want < 8 ? 8 : want > 64 ? 64 : want);
   for (int64_t lb = 0; lb < all && e == cudaSuccess; lb += 65535) {
     cudaLaunchConfig_t cfg = {};
