@@ -38,7 +38,7 @@ constexpr int kThreads = 384;            // 2 x 4 epilogue warps, loader, MMA, l
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kLseWarp = 10;
 constexpr uint32_t kBlock = 16384;       // 128 rows x 64 channels
 constexpr uint32_t kSmem = 232448;
-constexpr int kMaxSlots = 12, kMaxBlocks = 9;
+constexpr int kMaxBlocks = 9;
 
 template <bool kPair>
 constexpr int kKeysLog = kPair ? 8 : 7;  // keys of a tile
@@ -46,23 +46,26 @@ template <bool kPair>
 constexpr int kCols = kPair ? 256 : 128; // query rows of a step at most
 
 template <bool kPair>
+constexpr int kMaxSlots = kPair ? 6 : 12;
+template <bool kPair>
 struct Shared {
   // Of a pair, the barriers that the products wait for are rank 0's.
-  uint64_t full[kMaxSlots], empty[kMaxSlots], kept_full[kMaxBlocks], kept_free[kMaxBlocks];
-  uint64_t s_full[2], s_free[2], lse_full[2], lse_free[2], part_ready[4][2], part_free[4][2], fin;
+  uint64_t full[kMaxSlots<kPair>], empty[kMaxSlots<kPair>], kept_full[kMaxBlocks], kept_free[kMaxBlocks];
+  uint64_t s_full[2], s_free[2], lse_full[2], lse_free[2], part_ready[4], part_free[4], fin;
   uint32_t tmem;
   int abort;
   int seq0, tile0, total;                // the CTA's (pair's) first sequence and tile, all tiles
-  int64_t warp_sum[kThreads / 32];
   DeviceStatus error;
   uint32_t load_ring, load_kept;         // blocks the loader asked for
   alignas(16) float lse[2][kCols<kPair>];            // times log2(e); +inf where a row gives nothing
-  float part[2][128];                    // the second warpgroup's sums
+  union {
+    float part[128];                     // the second warpgroup's sums
+    int64_t warp_sum[kThreads / 32];     // at the start
+  };
 };
-template <bool kPair>
-constexpr uint32_t kSharedBytes = kPair ? 4096 : 3072;
-static_assert(sizeof(Shared<false>) <= kSharedBytes<false>, "fits beside the tiles");
-static_assert(sizeof(Shared<true>) <= kSharedBytes<true>, "fits beside the tiles");
+constexpr uint32_t kSharedBytes = 3072;
+static_assert(sizeof(Shared<false>) <= kSharedBytes, "fits beside the tiles");
+static_assert(sizeof(Shared<true>) <= kSharedBytes, "fits beside the tiles");
 
 struct Params {
   const int32_t *table, *lens;
@@ -231,10 +234,10 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
   const int group = kPair ? blockIdx.x >> 1 : blockIdx.x;
   const int NB = p.blocks, NS = p.slots;
   const uint32_t sm_kept = base, sm_ring = base + NB * p.kept_bytes;
-  Sh &m = *reinterpret_cast<Sh *>(tiles + (kSmem - kSharedBytes<kPair>));
+  Sh &m = *reinterpret_cast<Sh *>(tiles + (kSmem - kSharedBytes));
 
   if (tid == 0) {
-    for (int i = 0; i < kMaxSlots; ++i) {
+    for (int i = 0; i < kMaxSlots<kPair>; ++i) {
       mbar_init(&m.full[i], 1);
       mbar_init(&m.empty[i], 1);
     }
@@ -247,10 +250,10 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
       mbar_init(&m.s_free[i], kPair ? 16 : 8);
       mbar_init(&m.lse_full[i], 1);
       mbar_init(&m.lse_free[i], 8);
-      for (int w = 0; w < 4; ++w) {
-        mbar_init(&m.part_ready[w][i], 1);
-        mbar_init(&m.part_free[w][i], 1);
-      }
+    }
+    for (int w = 0; w < 4; ++w) {
+      mbar_init(&m.part_ready[w], 1);
+      mbar_init(&m.part_free[w], 1);
     }
     mbar_init(&m.fin, 1);
     m.abort = 0;
@@ -526,19 +529,19 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
       }
       ++step;
       if (!st.tile_ends()) continue;
-      const uint32_t h = tile & 1, hp = (tile >> 1) & 1;
+      const uint32_t turn = tile & 1;
       if (wg == 1) {
-        if (tile > 1) ok = warp_wait(cx, &m.part_free[w4][h], hp ^ 1, 42, st.t);
+        if (tile > 0) ok = warp_wait<2>(cx, &m.part_free[w4], turn ^ 1, 42, st.t);
         if (!ok) break;
-        m.part[h][key] = sum;
+        m.part[key] = sum;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&m.part_ready[w4][h]);
+        if (lane == 0) mbar_arrive(&m.part_ready[w4]);
       } else {
-        ok = warp_wait(cx, &m.part_ready[w4][h], hp, 43, st.t);
+        ok = warp_wait<2>(cx, &m.part_ready[w4], turn, 43, st.t);
         if (!ok) break;
-        const float all = sum + m.part[h][key];
+        const float all = sum + m.part[key];
         __syncwarp();
-        if (lane == 0) mbar_arrive(&m.part_free[w4][h]);
+        if (lane == 0) mbar_arrive(&m.part_free[w4]);
         if (j < st.n) *to = p.decay == 0.f ? all : fmaf(old, p.decay, all);
       }
       ++tile;
@@ -635,9 +638,10 @@ cudaError_t launch_latent_weights(const LatentWeightsArgs &a, cudaStream_t strea
   p.cols = pair ? 256 : (R + 15) / 16 * 16;
   p.row_steps = pair ? (R + 255) / 256 : 1;
   p.kept_bytes = pair ? kBlock : (uint32_t)p.cols * 128;  // whole 1,024s
-  const uint32_t space = kSmem - (pair ? kSharedBytes<true> : kSharedBytes<false>) - p.blocks * p.kept_bytes;
+  const uint32_t space = kSmem - kSharedBytes - p.blocks * p.kept_bytes;
   p.slots = (int)(space / kBlock);
-  if (p.slots > kMaxSlots) p.slots = kMaxSlots;
+  const int most = pair ? kMaxSlots<true> : kMaxSlots<false>;
+  if (p.slots > most) p.slots = most;
   p.groups = pair ? resident_pairs() : sm_count();
   p.scale2 = a.scale * kLog2e; p.decay = a.decay; p.weights = a.weights; p.status = a.status;
   p.test = a.test;
