@@ -327,6 +327,7 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
     const uint32_t piece_bytes = p.box_rows * 128;
     uint32_t ring = 0, kept = 0, outer = 0;  // blocks asked for; changes of what is kept
     int s = 0;
+    uint32_t round = 0;                      // parity of the ring's rounds
     const auto lead = [&](uint64_t *bar) { return kPair ? map_rank(smem_u32(bar), 0) : smem_u32(bar); };
     int row = -1, have = 0;                  // this lane's pool row, pieces of the group
     bool ok = true;
@@ -367,7 +368,7 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
           else queries(sm_kept + c * p.kept_bytes, &m.kept_full[c], c);
           ++kept;
         }
-        if (ring >= (uint32_t)NS) ok = warp_wait(cx, &m.empty[s], (ring / NS - 1) & 1, 11, st.t);
+        if (ring >= (uint32_t)NS) ok = warp_wait(cx, &m.empty[s], round ^ 1, 11, st.t);
         if (!ok) break;
         if (lane == 0 && rank == 0)
           mbar_arrive_expect_tx(&m.full[s], kPair ? query_bytes : key_bytes);
@@ -375,7 +376,10 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
         if constexpr (kPair) queries(sm_ring + s * kBlock, &m.full[s], c);
         else keys(sm_ring + s * kBlock, &m.full[s], c);
         ++ring;
-        s = s + 1 == NS ? 0 : s + 1;
+        if (++s == NS) {
+          s = 0;
+          round ^= 1;
+        }
       }
       outer += st.first();
     }
@@ -388,7 +392,7 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
     if (rank == 0 && elect_one()) {
       const uint32_t idesc = idesc_bf16(kPair ? 256 : 128, p.cols, false, false);
       const Desc d_kept(sm_kept, 16), d_ring(sm_ring, 16);
-      uint32_t ring = 0, step = 0, outer = 0;
+      uint32_t round = 0, step = 0, outer = 0;
       int s = 0;
       bool ok = true;
       while (ok && st.next()) {
@@ -398,7 +402,7 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
         tc_fence_after();
         for (int c = 0; c < NB; ++c) {
           if (st.first()) ok = wait_or_abort(cx, &m.kept_full[c], outer & 1, 21, st.t);
-          ok = ok && wait_or_abort(cx, &m.full[s], (ring / NS) & 1, 22, st.t);
+          ok = ok && wait_or_abort(cx, &m.full[s], round, 22, st.t);
           if (!ok) break;
           tc_fence_after();
           const uint32_t k_at = kPair ? c * kBlock : s * kBlock;
@@ -411,8 +415,10 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
           }
           commit<kPair>(&m.empty[s]);
           if (st.last()) commit<kPair>(&m.kept_free[c]);
-          ++ring;
-          s = s + 1 == NS ? 0 : s + 1;
+          if (++s == NS) {
+            s = 0;
+            round ^= 1;
+          }
         }
         if (!ok) break;
         commit<kPair>(&m.s_full[buf]);
