@@ -34,8 +34,8 @@ namespace {
 
 using namespace latent;
 
-constexpr int kThreads = 384;            // 2 x 4 epilogue warps, loader, MMA, lse, spare
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kLseWarp = 10;
+constexpr int kThreads = 384;            // 2 x 4 epilogue warps, two loaders, MMA, lse
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kLseWarp = 10, kKeepWarp = 11;
 constexpr uint32_t kBlock = 16384;       // 128 rows x 64 channels
 constexpr uint32_t kSmem = 232448;
 constexpr int kMaxBlocks = 9;
@@ -320,19 +320,20 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
   const WaitCtx cx{&m.abort, &m.error, (int)blockIdx.x, p.test.wait_ns};
   Steps<kPair> st(p, m.seq0, m.tile0, mine);
 
-  if (warp == kLoadWarp) {
-    // ---- loader: a lane has a piece of the tile's keys (the rows of one page); lane 0 the
-    // queries too
+  if (warp == kLoadWarp || warp == kKeepWarp) {
+    // ---- loaders, of what streams and of what stays: each is as far ahead as its places are
+    // free.  A lane has a piece of the tile's keys (the rows of one page), lane 0 the queries.
+    const bool streams = warp == kLoadWarp, keys = streams != kPair;
     const int pieces = 128 / p.box_rows;
     const uint32_t piece_bytes = p.box_rows * 128;
-    uint32_t ring = 0, kept = 0, outer = 0;  // blocks asked for; changes of what is kept
-    int s = 0;
-    uint32_t round = 0;                      // parity of the ring's rounds
     const auto lead = [&](uint64_t *bar) { return kPair ? map_rank(smem_u32(bar), 0) : smem_u32(bar); };
-    int row = -1, have = 0;                  // this lane's pool row, pieces of the group
+    uint32_t count = 0, round = 0;           // blocks asked for, parity of the places' rounds
+    int s = 0, row = -1;                     // place; this lane's pool row
+    uint32_t bytes = p.cols * 128;           // of a block, in both CTAs
     bool ok = true;
     while (ok && st.next()) {
-      if (st.tile_begins()) {
+      if (!streams && !st.first()) continue;
+      if (keys) {
         const int at0 = st.t << kKeysLog<kPair>, at = at0 + (int)rank * 128 + lane * p.box_rows;
         row = -1;
         if (lane < pieces && at < st.n) {
@@ -346,47 +347,31 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
           }
         }
         const int live = min(st.n - at0, 1 << kKeysLog<kPair>);
-        have = (live + p.box_rows - 1) / p.box_rows;
+        bytes = (live + p.box_rows - 1) / p.box_rows * piece_bytes;
       }
       if (p.test.block == (int)blockIdx.x && p.test.tile == st.t - st.ta) break;  // a test
-      const uint32_t key_bytes = have * piece_bytes, query_bytes = p.cols * 128;
-      const auto keys = [&](uint32_t dst, uint64_t *bar, int c) {
-        if (row >= 0) copy_2d<kPair>(dst + lane * piece_bytes, &map_c, lead(bar), c * 64, row);
-      };
-      const auto queries = [&](uint32_t dst, uint64_t *bar, int c) {
-        if (lane == 0)
-          copy_3d<kPair>(dst, &map_q, lead(bar), c * 64, st.rs * kN + (int)rank * 128, st.b);
-      };
+      const int places = streams ? NS : NB;
+      uint64_t *full = streams ? m.full : m.kept_full, *empty = streams ? m.empty : m.kept_free;
+      const uint32_t base_at = streams ? sm_ring : sm_kept, place_bytes = streams ? kBlock : p.kept_bytes;
       for (int c = 0; c < NB; ++c) {
-        if (st.first()) {                    // what stays: the queries, or a pair's keys
-          if (outer > 0) ok = warp_wait<2>(cx, &m.kept_free[c], (outer - 1) & 1, 10, st.t);
-          if (!ok) break;
-          if (lane == 0 && rank == 0)
-            mbar_arrive_expect_tx(&m.kept_full[c], kPair ? key_bytes : query_bytes);
-          __syncwarp();
-          if constexpr (kPair) keys(sm_kept + c * kBlock, &m.kept_full[c], c);
-          else queries(sm_kept + c * p.kept_bytes, &m.kept_full[c], c);
-          ++kept;
-        }
-        if (ring >= (uint32_t)NS) ok = warp_wait(cx, &m.empty[s], round ^ 1, 11, st.t);
+        if (count >= (uint32_t)places) ok = warp_wait<2>(cx, &empty[s], round ^ 1, streams ? 11 : 10, st.t);
         if (!ok) break;
-        if (lane == 0 && rank == 0)
-          mbar_arrive_expect_tx(&m.full[s], kPair ? query_bytes : key_bytes);
+        if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
         __syncwarp();
-        if constexpr (kPair) queries(sm_ring + s * kBlock, &m.full[s], c);
-        else keys(sm_ring + s * kBlock, &m.full[s], c);
-        ++ring;
-        if (++s == NS) {
+        const uint32_t dst = base_at + s * place_bytes;
+        if (keys) {
+          if (row >= 0) copy_2d<kPair>(dst + lane * piece_bytes, &map_c, lead(&full[s]), c * 64, row);
+        } else if (lane == 0) {
+          copy_3d<kPair>(dst, &map_q, lead(&full[s]), c * 64, st.rs * kN + (int)rank * 128, st.b);
+        }
+        ++count;
+        if (++s == places) {
           s = 0;
           round ^= 1;
         }
       }
-      outer += st.first();
     }
-    if (lane == 0) {
-      m.load_ring = ring;
-      m.load_kept = kept;
-    }
+    if (lane == 0) (streams ? m.load_ring : m.load_kept) = count;
   } else if (warp == kMmaWarp) {
     // ---- products: one lane of rank 0
     if (rank == 0 && elect_one()) {
