@@ -46,7 +46,7 @@ template <bool kPair>
 constexpr int kCols = kPair ? 256 : 128; // query rows of a step at most
 
 template <bool kPair>
-constexpr int kMaxSlots = kPair ? 6 : 12;
+constexpr int kMaxSlots = kPair ? 5 : 12;
 template <bool kPair>
 struct Shared {
   // Of a pair, the barriers that the products wait for are rank 0's.
@@ -54,8 +54,11 @@ struct Shared {
   uint64_t s_full[2], s_free[2], lse_full[2], lse_free[2], part_ready[4], part_free[4], fin;
   uint32_t tmem;
   int abort;
-  int seq0, tile0, total;                // the CTA's (pair's) first sequence and tile, all tiles
+  int seq0, tile0, total;                // the CTA's first sequence and tile; all tiles
   DeviceStatus error;
+  // Of a pair: the tiles it takes, one ahead (sequence, -1: no more; tile; length).
+  uint64_t unit_full[2], unit_free[2];
+  int4 unit[2];
   uint32_t load_ring, load_kept;         // blocks the loader asked for
   alignas(16) float lse[2][kCols<kPair>];            // times log2(e); +inf where a row gives nothing
   union {
@@ -81,6 +84,7 @@ struct Params {
   float scale2, decay;  // scale * log2(e)
   float *weights;
   DeviceStatus *status;
+  int32_t *taken;       // tiles that pairs have taken beyond their first
   WaitTest test;
 };
 
@@ -100,20 +104,16 @@ __device__ __forceinline__ int group_begin(int c, int G, int total) {
   return c * each + min(c, more);
 }
 
-// Walks the group's steps; every role does so by itself.
-template <bool kPair>
-struct Steps {
+// The steps of one CTA, which has consecutive tiles; every role walks over them by itself.
+struct OneSteps {
   const Params &p;
   int next_b, next_t, left;       // next sequence, its next tile, tiles left
-  int b = 0, n = 0, ta = 0, tb = 0, t = 0, rs = 0;   // current: sequence, tiles [ta, tb), tile, row step
-  __device__ Steps(const Params &p_, int b_, int t_, int left_)
+  int b = 0, n = 0, ta = 0, tb = 0, t = 0;   // current: sequence, its length, tiles [ta, tb), tile
+  static constexpr int rs = 0;
+  __device__ OneSteps(const Params &p_, int b_, int t_, int left_)
       : p(p_), next_b(b_), next_t(t_), left(left_) {}
+  template <bool kLane>
   __device__ bool next() {
-    if (kPair && tb > 0 && rs + 1 < p.row_steps) {
-      ++rs;
-      return true;
-    }
-    rs = 0;
     if (t + 1 < tb) {
       ++t;
       return true;
@@ -121,7 +121,7 @@ struct Steps {
     if (left <= 0) return false;
     for (; next_b < p.B; ++next_b, next_t = 0) {
       n = seq_len(p, next_b);
-      const int k = key_tiles<kPair>(n);
+      const int k = key_tiles<false>(n);
       if (next_t >= k) continue;
       b = next_b;
       t = ta = next_t;
@@ -132,12 +132,82 @@ struct Steps {
     }
     return false;
   }
-  // of what stays in shared memory
-  __device__ bool first() const { return kPair ? rs == 0 : t == ta; }
-  __device__ bool last() const { return kPair ? rs + 1 == p.row_steps : t + 1 == tb; }
-  // of a tile of keys
-  __device__ bool tile_begins() const { return !kPair || rs == 0; }
-  __device__ bool tile_ends() const { return !kPair || rs + 1 == p.row_steps; }
+  // of what stays in shared memory; of a tile of keys
+  __device__ bool first() const { return t == ta; }
+  __device__ bool last() const { return t + 1 == tb; }
+  __device__ bool tile_begins() const { return true; }
+  __device__ bool tile_ends() const { return true; }
+  __device__ int number() const { return t - ta; }
+};
+// The steps of a pair.  Pairs are not equally fast (by 20 % in the same work), so that each takes
+// a tile when it needs one: rank 0 counts them up and tells both CTAs, one ahead.
+struct PairSteps {
+  const Params &p;
+  Shared<true> &m;
+  const WaitCtx &cx;
+  const uint32_t rank;
+  uint32_t taken = 0;
+  int b = 0, n = 0, t = 0, rs = 0;           // current: sequence, its length, tile, row step
+  __device__ PairSteps(const Params &p_, Shared<true> &m_, const WaitCtx &cx_, uint32_t rank_)
+      : p(p_), m(m_), cx(cx_), rank(rank_) {}
+  template <bool kLane>                      // by one lane, or by a converged warp
+  __device__ bool next() {
+    if (taken > 0 && rs + 1 < p.row_steps) {
+      ++rs;
+      return true;
+    }
+    const uint32_t s = taken & 1, par = (taken >> 1) & 1;
+    if (!(kLane ? wait_or_abort<2>(cx, &m.unit_full[s], par, 50, (int)taken)
+                : warp_wait<2>(cx, &m.unit_full[s], par, 50, (int)taken)))
+      return false;
+    const int4 u = m.unit[s];
+    // (the vote has consumed what was read: the place may be written again)
+    const bool more = kLane ? u.x >= 0 : __all_sync(0xffffffffu, u.x >= 0) != 0;
+    if (kLane || (threadIdx.x & 31) == 0) {
+      if (rank == 0) mbar_arrive(&m.unit_free[s]);
+      else remote_arrive_relaxed(map_rank(smem_u32(&m.unit_free[s]), 0));
+    }
+    ++taken;
+    rs = 0;
+    b = u.x;
+    t = u.y;
+    n = u.z;
+    return more;
+  }
+  __device__ bool first() const { return rs == 0; }
+  __device__ bool last() const { return rs + 1 == p.row_steps; }
+  __device__ bool tile_begins() const { return rs == 0; }
+  __device__ bool tile_ends() const { return rs + 1 == p.row_steps; }
+  __device__ int number() const { return (int)taken - 1; }
+};
+constexpr int kUnitReaders = 12 + 11;        // loaders, lse, sums of both CTAs, products
+
+// Sequence, tile and length of the x-th tile of all, x not falling from call to call; by a warp.
+struct Finder {
+  const Params &p;
+  int base = -32, before = 0;                // 32 sequences from `base` on, tiles before them
+  int n = 0, upto = 0;                       // of this lane's: length, tiles with those before it
+  int all = 0;                               // tiles of the 32
+  __device__ explicit Finder(const Params &p_) : p(p_) {}
+  __device__ int4 find(int x) {
+    const int lane = threadIdx.x & 31;
+    while (x >= before + all) {
+      before += all;
+      base += 32;
+      n = base + lane < p.B ? seq_len(p, base + lane) : 0;
+      upto = key_tiles<true>(n);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      all = __shfl_sync(0xffffffffu, upto, 31);
+      if (base >= p.B) return make_int4(-1, 0, 0, 0);
+    }
+    const int at = __ffs(__ballot_sync(0xffffffffu, x - before < upto)) - 1;
+    const int k = __shfl_sync(0xffffffffu, upto, at), len = __shfl_sync(0xffffffffu, n, at);
+    return make_int4(base + at, x - before - (k - key_tiles<true>(len)), len, 0);
+  }
 };
 
 // What differs between one CTA and a pair: the products and who hears of their end.
@@ -216,10 +286,13 @@ __device__ __forceinline__ void copy_3d(uint32_t dst, const CUtensorMap *map, ui
         : "memory");
 }
 
-// The call's status is cleared by a kernel of its own, beside which the next one starts.
-__global__ void kda_latent_weights_begin_kernel(DeviceStatus *status) {
+// The call's status and the count of tiles are cleared by a kernel of its own, beside which the next one starts.
+__global__ void kda_latent_weights_begin_kernel(DeviceStatus *status, int32_t *taken) {
   pdl_launch_dependents();
-  if (threadIdx.x == 0) set_device_status(status, KDA_OK, 0);
+  if (threadIdx.x == 0) {
+    set_device_status(status, KDA_OK, 0);
+    *taken = 0;
+  }
 }
 
 template <bool kPair>
@@ -254,6 +327,10 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
     for (int w = 0; w < 4; ++w) {
       mbar_init(&m.part_ready[w], 1);
       mbar_init(&m.part_free[w], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&m.unit_full[i], 1);
+      mbar_init(&m.unit_free[i], kUnitReaders);
     }
     mbar_init(&m.fin, 1);
     m.abort = 0;
@@ -296,7 +373,7 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
     if (all > 0x7fffffff && tid == 0)
       record_device_status(&m.error, KDA_ERR_INVALID_ARG, 3, 0, 0);
     const int begin = group_begin(group, p.groups, total);
-    if (total > 0 && begin >= before && begin < before + mine) {
+    if (!kPair && total > 0 && begin >= before && begin < before + mine) {
       int at = (int)before;
       for (int b = b0; b < b1; ++b) {
         const int k = key_tiles<kPair>(seq_len(p, b));
@@ -315,10 +392,15 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
   else __syncthreads();
   tc_fence_after();
   const uint32_t tm = m.tmem;
-  const int begin = group_begin(group, p.groups, m.total);
-  const int mine = group_begin(group + 1, p.groups, m.total) - begin;
   const WaitCtx cx{&m.abort, &m.error, (int)blockIdx.x, p.test.wait_ns};
-  Steps<kPair> st(p, m.seq0, m.tile0, mine);
+  auto st = [&] {
+    if constexpr (kPair) {
+      return PairSteps(p, m, cx, rank);
+    } else {
+      const int begin = group_begin(group, p.groups, m.total);
+      return OneSteps(p, m.seq0, m.tile0, group_begin(group + 1, p.groups, m.total) - begin);
+    }
+  }();
 
   if (warp == kLoadWarp || warp == kKeepWarp) {
     // ---- loaders, of what streams and of what stays: each is as far ahead as its places are
@@ -331,7 +413,7 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
     int s = 0, row = -1;                     // place; this lane's pool row
     uint32_t bytes = p.cols * 128;           // of a block, in both CTAs
     bool ok = true;
-    while (ok && st.next()) {
+    while (ok && st.template next<false>()) {
       if (!streams && !st.first()) continue;
       if (keys) {
         const int at0 = st.t << kKeysLog<kPair>, at = at0 + (int)rank * 128 + lane * p.box_rows;
@@ -349,7 +431,7 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
         const int live = min(st.n - at0, 1 << kKeysLog<kPair>);
         bytes = (live + p.box_rows - 1) / p.box_rows * piece_bytes;
       }
-      if (p.test.block == (int)blockIdx.x && p.test.tile == st.t - st.ta) break;  // a test
+      if (p.test.block == (int)blockIdx.x && p.test.tile == st.number()) break;  // a test
       const int places = streams ? NS : NB;
       uint64_t *full = streams ? m.full : m.kept_full, *empty = streams ? m.empty : m.kept_free;
       const uint32_t base_at = streams ? sm_ring : sm_kept, place_bytes = streams ? kBlock : p.kept_bytes;
@@ -380,7 +462,7 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
       uint32_t round = 0, step = 0, outer = 0;
       int s = 0;
       bool ok = true;
-      while (ok && st.next()) {
+      while (ok && st.template next<true>()) {
         const uint32_t buf = step & 1;
         if (step > 1) ok = wait_or_abort(cx, &m.s_free[buf], ((step >> 1) - 1) & 1, 20, st.t);
         if (!ok) break;
@@ -412,11 +494,44 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
       }
     }
   } else if (warp == kLseWarp) {
-    // ---- lse of a step's rows (where the queries stay: of a sequence's)
-    uint32_t item = 0;
-    bool ok = true;
-    while (ok && st.next()) {
-      if (!kPair && !st.first()) continue;
+    // ---- lse of a step's rows (where the queries stay: of a sequence's), and a pair's tiles
+    uint32_t item = 0, told = 0;
+    bool ok = true, ended = false;
+    Finder finder(p);
+    // Tile number `told` of this pair to both CTAs: the first is its own, the others as they come.
+    const auto tell = [&] {
+      const uint32_t s = told & 1;
+      if (rank == 0) {
+        int x = group;
+        if (told > 0) {
+          if (lane == 0) x = p.groups + atomicAdd(p.taken, 1);
+          x = __shfl_sync(0xffffffffu, x, 0);
+        }
+        const int4 u = x < m.total ? finder.find(x) : make_int4(-1, 0, 0, 0);
+        if (told > 1) ok = warp_wait<2>(cx, &m.unit_free[s], ((told >> 1) - 1) & 1, 31, (int)told);
+        if (ok && lane == 0) {
+          st_async_v4(map_rank(smem_u32(&m.unit[s]), 1), (uint32_t)u.x, (uint32_t)u.y, (uint32_t)u.z,
+                      0, map_rank(smem_u32(&m.unit_full[s]), 1));
+          m.unit[s] = u;
+          mbar_arrive(&m.unit_full[s]);
+        }
+        ended = u.x < 0;
+      } else if (lane == 0) {
+        mbar_arrive_expect_tx(&m.unit_full[s], 16);
+      }
+      ++told;
+    };
+    if constexpr (kPair) {
+      pdl_wait();                            // the count has been cleared
+      tell();
+    }
+    while (ok && st.template next<false>()) {
+      if constexpr (kPair) {
+        if (st.first() && !ended) tell();
+        if (!ok) break;
+      } else {
+        if (!st.first()) continue;
+      }
       const uint32_t i = item & 1;
       if (item > 1) ok = warp_wait<2>(cx, &m.lse_free[i], ((item >> 1) - 1) & 1, 30, st.t);
       if (!ok) break;
@@ -439,7 +554,7 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
     uint32_t step = 0, item = 0, tile = 0;
     float sum = 0.f, old = 0.f;
     bool ok = true;
-    while (ok && st.next()) {
+    while (ok && st.template next<false>()) {
       const uint32_t buf = step & 1, par = (step >> 1) & 1;
       const int j = (st.t << kKeysLog<kPair>)+(int)rank * 128 + key;
       float *to = p.weights + (int64_t)st.b * p.max_pages * p.page_size + j;
@@ -610,7 +725,7 @@ int resident_pairs() {
 
 }  // namespace
 
-size_t latent_weights_scratch_bytes(int32_t, int32_t, int32_t, int32_t) { return 0; }
+size_t latent_weights_scratch_bytes(int32_t, int32_t, int32_t, int32_t) { return sizeof(int32_t); }
 
 cudaError_t launch_latent_weights(const LatentWeightsArgs &a, cudaStream_t stream) {
   if (a.B == 0) return cudaMemsetAsync(a.status, 0, sizeof(DeviceStatus), stream);
@@ -635,6 +750,7 @@ cudaError_t launch_latent_weights(const LatentWeightsArgs &a, cudaStream_t strea
   if (p.slots > most) p.slots = most;
   p.groups = pair ? resident_pairs() : sm_count();
   p.scale2 = a.scale * kLog2e; p.decay = a.decay; p.weights = a.weights; p.status = a.status;
+  p.taken = static_cast<int32_t *>(a.scratch);
   p.test = a.test;
   CUtensorMap mq, mc;
   const cuuint64_t qd[3] = {(cuuint64_t)W, (cuuint64_t)R, (cuuint64_t)a.B};
@@ -646,7 +762,7 @@ cudaError_t launch_latent_weights(const LatentWeightsArgs &a, cudaStream_t strea
   if (!latent::make_bf16_map(&mq, a.q, 3, qd, qs, qb) ||
       !latent::make_bf16_map(&mc, a.cache, 2, cd, cs, cb))
     return cudaErrorInvalidValue;
-  kda_latent_weights_begin_kernel<<<1, 32, 0, stream>>>(a.status);
+  kda_latent_weights_begin_kernel<<<1, 32, 0, stream>>>(a.status, p.taken);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
