@@ -83,9 +83,28 @@ def _check(got, d, lse, decay=1.0):
     ([2, 3, 200, 1], 4, 16, 64, 64, False), ([500, 64, 333], 5, 96, 64, 48, False),
     ([1000, 129], 70, 3, 64, 64, False), ([640, 200, 90], 16, 96, 64, 64, True),
     ([300, 24, 150], 24, 40, 0, 128, True), ([64, 65, 200], 64, 8, 64, 16, True),
-    ([257], 2, 129, 64, 64, False), ([1025], 1, 300, 64, 64, False)])
+    ([257], 2, 129, 64, 64, False), ([1025], 1, 300, 64, 64, False),
+    ([300], 70, 128, 64, 64, False), ([255, 256, 257, 0, 512, 1], 2, 96, 0, 16, False),
+    ([40000, 3, 9000], 1, 130, 64, 512, False), ([30000, 0, 700], 1, 96, 64, 64, False)])
 def test_against_64_bits(lens, T, H, dr, page, tree):
     d = _data(lens, T, H, dr, page, tree=tree)
+    lse = _lse(d)
+    _check(_run(d, lse), d, lse)
+
+
+@pytest.mark.parametrize("T,H", [(1, 8), (2, 80)])
+def test_many_short_sequences(T, H):
+    g = torch.Generator().manual_seed(5)
+    lens = torch.randint(0, 300, (500,), generator=g).tolist()
+    d = _data(lens, T, H, 64, 16)
+    lse = _lse(d)
+    _check(_run(d, lse), d, lse)
+
+
+def test_sequences_that_share_pages():
+    """A prefix held once: the same rows, weights of each sequence's own."""
+    d = _data([500, 500, 64], 1, 96, 64, 64)
+    d["table"][1, :6] = d["table"][0, :6]
     lse = _lse(d)
     _check(_run(d, lse), d, lse)
 
