@@ -23,6 +23,8 @@
 namespace kda {
 namespace {
 
+constexpr int kShort = 256;              // channels of a short row
+
 // Two fp32 values at a time: the same roundings in half the instructions.
 struct F2 {
   uint64_t v;
@@ -246,7 +248,7 @@ __device__ __forceinline__ void finish(const NormArgs &a, int64_t row, const R &
 template <int N>
 constexpr int kBlock = N < 256 ? 256 : N;
 template <typename T, int N, int E, bool kVector>
-__global__ void __launch_bounds__(kBlock<N>) kda_norm_fwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kBlock<N>, kVector ? 1 : 1024 / kBlock<N>) kda_norm_fwd_kernel(const NormArgs a) {
   using R = Row<T, N, E, kVector>;
   constexpr int kRows = kBlock<N> / N;
   __shared__ float part[kRows][2 * (N / 32)];
@@ -337,6 +339,7 @@ template <typename T, int N, int E>
 __global__ void __launch_bounds__(kFwdThreads, 1) kda_norm_fwd_ring_kernel(const NormArgs a) {
   using R = Row<T, N, E, true>;
   constexpr int kGroups = kFwdThreads / N, kD = kFwdStages<T, N, E>;
+  static_assert(kD >= 1, "a row ahead");
   constexpr uint32_t kStageBytes = kFwdThreads * E * sizeof(T);
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ float part[kGroups][2 * (N / 32)];
@@ -482,10 +485,12 @@ __device__ __forceinline__ void leave_sums(const NormArgs &a, const float (&v)[E
   __syncthreads();
 }
 
+// Rows whose address or distance is no multiple of 16 bytes, one channel at a time.
+constexpr int kSingleThreads = 1024;
 template <typename T, int N, int E>
-__global__ void __launch_bounds__(kBlock<N>) kda_norm_bwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kSingleThreads, 1) kda_norm_bwd_kernel(const NormArgs a) {
   using R = Row<T, N, E, false>;
-  constexpr int kGroups = kBlock<N> / N;
+  constexpr int kGroups = kSingleThreads / N;
   __shared__ float part[kGroups][2][2 * (N / 32)];
   extern __shared__ float sums[];                        // [kGroups][W], where there are several
   latent::pdl_launch_dependents();
@@ -515,9 +520,10 @@ __global__ void __launch_bounds__(kBlock<N>) kda_norm_bwd_kernel(const NormArgs 
 }
 
 template <typename T, int N, int E>
-__global__ void __launch_bounds__(kBwdThreads, 1) kda_norm_bwd_ring_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kBwdThreads, E * N <= kShort ? 2 : 1) kda_norm_bwd_ring_kernel(const NormArgs a) {
   using R = Row<T, N, E, true>;
   constexpr int kGroups = kBwdThreads / N, kD = kBwdStages<T, N, E>, kV = R::kV;
+  static_assert(kD >= 1, "a row ahead");
   constexpr uint32_t kRowBytes = kBwdThreads * E * sizeof(T);
   extern __shared__ __align__(128) unsigned char ring[];
   __shared__ float part[kGroups][2][2 * (N / 32)];
@@ -685,17 +691,18 @@ kda_norm_join_kernel(const float *__restrict__ partial, int32_t blocks, int32_t 
 
 int sms() { return latent::sm_count() > 0 ? latent::sm_count() : 1; }
 
-// Blocks of the gradient: one an SM, or as many as there are rows for.
+// Blocks of the gradient at most: one an SM, of short rows four, whose sums are short too.
+int64_t most_blocks(int32_t W) { return W <= kShort ? 4 * sms() : sms(); }
 template <int kThreads>
-int bwd_blocks(int64_t n, int N) {
-  const int64_t need = (n + kThreads / N - 1) / (kThreads / N);
-  return (int)(need < sms() ? need : sms());
+int bwd_blocks(int64_t n, int32_t W, int N) {
+  const int64_t need = (n + kThreads / N - 1) / (kThreads / N), most = most_blocks(W);
+  return (int)(need < most ? need : most);
 }
 
 template <typename T, int N, int E, bool kVector>
 cudaError_t fwd(const NormArgs &a, cudaStream_t stream) {
   constexpr int kRows = kBlock<N> / N;
-  if constexpr (kVector && N <= 512) {
+  if constexpr (kVector && kFwdStages<T, N, E> >= 1) {
     constexpr int kGroups = kFwdThreads / N;
     constexpr int kBytes = kFwdStages<T, N, E> * kFwdThreads * E * (int)sizeof(T) + 2 * N * E * 4;
     // Rows enough that every group has some to walk over.
@@ -718,12 +725,12 @@ cudaError_t bwd(const NormArgs &a, cudaStream_t stream) {
     constexpr int kBytes = kBwdStages<T, N, E> * 2 * kBwdThreads * E * (int)sizeof(T) + N * E * 4;
     if (!latent::kernel_ready<kda_norm_bwd_ring_kernel<T, N, E>>(kBytes, 0))
       return cudaErrorNotSupported;
-    blocks = bwd_blocks<kBwdThreads>(a.n, N);
+    blocks = bwd_blocks<kBwdThreads>(a.n, a.W, N);
     kda_norm_bwd_ring_kernel<T, N, E><<<blocks, kBwdThreads, kBytes, stream>>>(a);
   } else {
-    blocks = bwd_blocks<kBlock<N>>(a.n, N);
-    const size_t smem = kBlock<N> / N > 1 ? (size_t)(kBlock<N> / N) * a.W * 4 : 0;
-    kda_norm_bwd_kernel<T, N, E><<<blocks, kBlock<N>, smem, stream>>>(a);
+    blocks = bwd_blocks<kSingleThreads>(a.n, a.W, N);
+    const size_t smem = kSingleThreads / N > 1 ? (size_t)(kSingleThreads / N) * a.W * 4 : 0;
+    kda_norm_bwd_kernel<T, N, E><<<blocks, kSingleThreads, smem, stream>>>(a);
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.partial) return e;
@@ -745,22 +752,37 @@ bool rows_of_16(const void *p, int64_t rs, int esz) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && rs * esz % 16 == 0;
 }
 
-// Threads of a row: the fewest that hold it with 64 bytes of it each, of the longest fp32 rows
-// 128.
+// Threads of a row.  With vectors: a warp for a short one, the fewest that hold it with 64 bytes
+// of it each, of the longest fp32 rows 128.  Single channels: eight each, of the longest 16, which
+// leaves registers for 1024 threads an SM.
 template <typename T, bool kVector, bool kForward>
 cudaError_t pick(const NormArgs &a, cudaStream_t stream) {
-  constexpr int E = 64 / sizeof(T);
   const auto go = [&](auto n, auto e) {
     if constexpr (kForward) return fwd<T, decltype(n)::value, decltype(e)::value, kVector>(a, stream);
     else return bwd<T, decltype(n)::value, decltype(e)::value, kVector>(a, stream);
   };
   using std::integral_constant;
-  constexpr integral_constant<int, E> each{};
-  if (a.W <= 32 * E) return go(integral_constant<int, 32>{}, each);
-  if (a.W <= 128 * E) return go(integral_constant<int, 128>{}, each);
-  if (a.W <= 256 * E) return go(integral_constant<int, 256>{}, each);
-  if (a.W <= 512 * E) return go(integral_constant<int, 512>{}, each);
-  if constexpr (512 * E < kNormMax) return go(integral_constant<int, 512>{}, integral_constant<int, 32>{});
+  constexpr integral_constant<int, 32> warp{};
+  constexpr integral_constant<int, 128> four{};
+  constexpr integral_constant<int, 256> eight{};
+  constexpr integral_constant<int, 512> half{};
+  constexpr integral_constant<int, 1024> all{};
+  constexpr integral_constant<int, 8> least{};
+  static_assert(kShort == 32 * 8, "a short row is a warp's with eight channels each");
+  if (a.W <= kShort) return go(warp, least);
+  if constexpr (kVector) {
+    constexpr integral_constant<int, 64 / sizeof(T)> E{};
+    if (a.W <= 32 * E) return go(warp, E);
+    if (a.W <= 128 * E) return go(four, E);
+    if (a.W <= 256 * E) return go(eight, E);
+    if (a.W <= 512 * E) return go(half, E);
+    if constexpr (512 * E < kNormMax) return go(half, integral_constant<int, kNormMax / 512>{});
+  } else {
+    if (a.W <= 128 * least) return go(four, least);
+    if (a.W <= 512 * least) return go(half, least);
+    if (a.W <= 1024 * least) return go(all, least);
+    return go(all, integral_constant<int, kNormMax / 1024>{});
+  }
   return cudaErrorInvalidValue;
 }
 
@@ -782,9 +804,9 @@ cudaError_t launch_norm_fwd(const NormArgs &a, cudaStream_t stream) {
 }
 
 size_t norm_bwd_scratch_bytes(int64_t n, int32_t W, bool bf16) {
-  (void)W;
   (void)bf16;
-  return (size_t)(n < sms() ? n : sms()) * 2 * W * sizeof(float);
+  const int64_t most = most_blocks(W);
+  return (size_t)(n < most ? n : most) * 2 * W * sizeof(float);
 }
 
 cudaError_t launch_norm_bwd(const NormArgs &a, cudaStream_t stream) {

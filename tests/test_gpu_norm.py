@@ -133,13 +133,22 @@ def test_not_a_number_stays_in_its_row():
     assert torch.isfinite(d[good]).all()
 
 
-@pytest.mark.parametrize("n,W,dtype", [(5000, 512, F32), (3001, 7168, BF), (20000, 40, BF)])
+@pytest.mark.parametrize("n,W,dtype", [
+    (5000, 512, F32), (3001, 7168, BF), (20001, 40, BF), (20001, 256, F32), (20001, 128, BF),
+    (20001, 1024, BF), (10001, 500, F32), (5001, 4096, BF), (5001, 2048, F32), (2501, 4096, F32),
+    (1301, 16384, BF), (1301, 8192, F32), (1301, 16384, F32), (20001, 25, BF), (5001, 513, BF),
+    (3001, 4001, F32), (2001, 7169, BF), (1301, 16383, F32), (1301, 16383, BF)])
 def test_many_rows_and_the_same_bits(n, W, dtype):
     x, g = _in((n, W), dtype, 1, 1.2, 0.1), _in((n, W), dtype, 2)
     w = _vec(W, 3, 1.0)
     got = kda.kda_norm_fwd(x, w, None)
+    _check_fwd(got, x, w, None, True, 1e-5)
     back = kda.kda_norm_bwd(g, x, w, got[1], got[2], bias=True)
     _check_bwd(back, g, x, w, got[1], got[2])
+    got = kda.kda_norm_fwd(x, w, w, center=False)
+    _check_fwd(got, x, w, w, False, 1e-5)
+    _check_bwd(kda.kda_norm_bwd(g, x, w, None, got[2]), g, x, w, None, got[2])
+    got = kda.kda_norm_fwd(x, w, None)
     again = kda.kda_norm_bwd(g, x, w, got[1], got[2], bias=True)
     for a, b in zip(back, again):
         assert torch.equal(a, b)
