@@ -34,6 +34,7 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kKeep = 16384;               // candidates in shared memory
 constexpr int kBins = 2048, kLow = 21;     // of the first count; bits below it
 constexpr int kFew = 1024;                 // ranked directly
+constexpr int kShort = 4096, kLeast = 4;   // one launch: positions at most, blocks at least
 static_assert(kBins % kThreads == 0 && kBins <= 4 * kThreads, "a thread has four bins at most");
 
 // Scratch of a (layer, sequence): what to move, then as many numbers as the budget each of
@@ -54,12 +55,114 @@ __device__ __forceinline__ uint32_t order_of(float w) {
   return u >> 31 ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheEvictArgs a, const int32_t room) {
+constexpr int kMoveThreads = 256;
+constexpr int kSlots = 9, kColSlots = 5;   // 16-byte pieces in flight per thread: rows, columns
+
+// The moves of a (layer, sequence), shared out over `pieces` blocks of kN threads.
+template <int kN>
+__device__ __forceinline__ void move_rows(const CacheEvictArgs &a, const int64_t lb, const Moves m,
+                                          const int32_t *via, const int piece, const int pieces) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int32_t *table = a.block_table + (int64_t)(lb % a.B) * a.max_pages;
+  const int32_t *dst = a.moves + lb * scratch_ints(a.budget) + kHead, *src = dst + list_ints(a.budget);
+  unsigned char *pool = static_cast<unsigned char *>(a.cache) +
+                        lb / a.B * a.n_pages * a.page_size * a.row_bytes;
+  const int vecs = (int)(a.row_bytes / 16);
+  const auto pool_row = [&](int pos) {
+    const int pg = pos / a.page_size;
+    return table[pg] * a.page_size + (pos - pg * a.page_size);
+  };
+  const auto piece_at = [&](int row, int col) {
+    return reinterpret_cast<uint4 *>(pool + row * a.row_bytes + (int64_t)col * 16);
+  };
+  if (m.movers == 0 && m.recent == 0) return;
+  const int hi = m.n - m.recent, last = a.budget - m.recent;
+
+  if (m.n - a.budget >= m.recent) {
+    // ---- whole rows, some at a time for each warp: the places of the last rows, then the
+    // movers from behind these
+    const int wide = min(vecs, 32 * kSlots);             // pieces of a row at a time
+    const int group = min(32, 32 * kSlots / wide);       // rows at a time
+    int place[kSlots];                                   // row of the group, piece
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      const int v = lane + 32 * j, r = v / wide;
+      place[j] = r < group ? r << 16 | (v - r * wide) : -1;
+    }
+    // rows s to rows d, each by the lane that has that row of the group; -1: none
+    const auto copy = [&](int s, int d) {
+      for (int c0 = 0; c0 < vecs; c0 += wide) {
+        uint4 x[kSlots];
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+          const int row = __shfl_sync(0xffffffffu, s, place[j] < 0 ? 0 : place[j] >> 16);
+          const int col = c0 + (place[j] & 0xffff);
+          if (place[j] >= 0 && row >= 0 && col < vecs) x[j] = *piece_at(row, col);
+        }
+#pragma unroll
+        for (int j = 0; j < kSlots; ++j) {
+          const int row = __shfl_sync(0xffffffffu, d, place[j] < 0 ? 0 : place[j] >> 16);
+          const int col = c0 + (place[j] & 0xffff);
+          if (place[j] >= 0 && row >= 0 && col < vecs) *piece_at(row, col) = x[j];
+        }
+      }
+    };
+    const int far = m.movers - m.near, all = m.recent + far;
+    for (int i0 = (piece * (kN / 32) + warp) * group; i0 < all; i0 += pieces * (kN / 32) * group) {
+      const int i = i0 + lane;
+      int s = -1, d = -1, out = -1;
+      if (lane < group && i < all) {
+        if (i < m.recent) {
+          s = pool_row(hi + i);
+          d = pool_row(last + i);
+          out = via[i] >= 0 ? pool_row(via[i]) : -1;
+        } else {
+          s = pool_row(src[m.near + i - m.recent]);
+          d = pool_row(dst[m.near + i - m.recent]);
+        }
+      }
+      if (__any_sync(0xffffffffu, out >= 0)) copy(out >= 0 ? d : -1, out);   // the same lanes, in order
+      copy(s, d);
+    }
+    return;
+  }
+
+  // ---- some columns of all rows, chunks in order, a chunk read before it is written
+  const int per = (vecs + pieces - 1) / pieces, c0 = piece * per, c1 = min(c0 + per, vecs);
+  for (int cc = c0; cc < c1; cc += kN) {
+    const int width = min(c1 - cc, kN), lanes = kN / width;
+    const int col = cc + tid % width, r = tid / width;
+    for (int kind = 0; kind < 2; ++kind) {               // movers, then the last rows
+      const int rows = kind ? m.recent : m.movers;
+      for (int i0 = 0; i0 < rows; i0 += lanes * kColSlots) {
+        uint4 x[kColSlots];
+#pragma unroll
+        for (int j = 0; j < kColSlots; ++j) {
+          const int i = i0 + j * lanes + r;
+          if (r < lanes && i < rows) x[j] = *piece_at(pool_row(kind ? hi + i : src[i]), col);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kColSlots; ++j) {
+          const int i = i0 + j * lanes + r;
+          if (r < lanes && i < rows) *piece_at(pool_row(kind ? last + i : dst[i]), col) = x[j];
+        }
+      }
+    }
+  }
+}
+
+// Where a few sequences are short, one launch: each of `pieces` blocks of a (layer, sequence)
+// selects by itself (they write the same to the lists), and takes its share of the moves.
+template <bool kMove>
+__global__ void __launch_bounds__(kThreads, kMove ? 1 : 2)
+kda_evict_select_kernel(const CacheEvictArgs a, const int32_t room, const int32_t pieces) {
   extern __shared__ uint32_t keys[];       // [room] candidates, as numbers
   __shared__ int hist[kBins], counts[2][kWarps], pick[3], bad, gathered;
   __shared__ uint2 few[kFew];              // value, position
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t lb = blockIdx.x;
+  const int64_t lb = kMove ? blockIdx.x / pieces : blockIdx.x;
+  const int piece = kMove ? (int)(blockIdx.x - lb * pieces) : 0;
   const int b = (int)(lb % a.B);
   const int cap = a.max_pages * a.page_size;
   const int n = a.seq_lens[b];
@@ -67,14 +170,16 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
   float *to = a.weights_out + lb * cap;
   int32_t *origin = a.origin + lb * a.budget;
   int32_t *scratch = a.moves + lb * scratch_ints(a.budget);
-  int32_t *dst = scratch + kHead, *src = dst + list_ints(a.budget), *via = src + list_ints(a.budget);
+  int32_t *dst = scratch + kHead, *src = dst + list_ints(a.budget);
+  // (a block that moves has it to itself: it is not the same at all times)
+  int32_t *via = kMove ? reinterpret_cast<int32_t *>(keys + room) : src + list_ints(a.budget);
   const int32_t *table = a.block_table + (int64_t)b * a.max_pages;
   const bool same = w == to;
   // candidates [lo, hi), a stretch a warp; `keep` of them stay
   const int lo = a.first, hi = (n < 0 || n > cap ? 0 : n) - a.recent, last = a.budget - a.recent;
   const int stretch = ((max(hi - lo, 0) + kWarps - 1) / kWarps + 31) / 32 * 32;
   const int s0 = min(lo + warp * stretch, hi), s1 = min(s0 + stretch, hi);
-  latent::pdl_launch_dependents();
+  if constexpr (!kMove) latent::pdl_launch_dependents();
 
   if (tid == 0) bad = n < 0 || n > cap;
   __syncthreads();
@@ -97,7 +202,8 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
     if (lb < a.B) a.new_lens[b] = refused ? n : min(n, a.budget);
   }
   if (refused || n <= a.budget) {          // all rows stay
-    if (tid == 0) *reinterpret_cast<Moves *>(scratch) = Moves{0, 0, 0, 0};
+    if (piece > 0) return;
+    if (!kMove && tid == 0) *reinterpret_cast<Moves *>(scratch) = Moves{0, 0, 0, 0};
     for (int i = tid; i < a.budget; i += kThreads) origin[i] = !refused && i < n ? i : -1;
     const int live = refused ? cap : n;
     if (!same)
@@ -256,12 +362,12 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
     if (m) src[mover + __popc(ms & under)] = i;
     hole += __popc(hs);
     mover += __popc(ms);
-    if (yes && i < last) {
+    if (yes && i < last && piece == 0) {
       origin[i] = i;
       if (!same) to[i] = w[i];
     }
   });
-  for (int i = tid; i < lo; i += kThreads) {
+  for (int i = tid; i < lo && piece == 0; i += kThreads) {
     origin[i] = i;
     if (!same) to[i] = w[i];
   }
@@ -284,8 +390,10 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
       if (i0 + k * kThreads < total) {
-        origin[at[k]] = from[k];
-        to[at[k]] = v[k];
+        if (piece == 0) {
+          origin[at[k]] = from[k];
+          to[at[k]] = v[k];
+        }
         if (from[k] < a.budget) {
           via[from[k] - last] = at[k];
           ++near;
@@ -295,124 +403,39 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
   near = __reduce_add_sync(0xffffffffu, near);
   if (lane == 0) counts[0][warp] = near;
   __syncthreads();
-  if (tid == 0) {
-    int sum = 0;
-    for (int k = 0; k < kWarps; ++k) sum += counts[0][k];
-    *reinterpret_cast<Moves *>(scratch) = Moves{total, sum, a.recent, n};
-  }
-  for (int i0 = 0; i0 < a.recent; i0 += kThreads) {
-    const int i = i0 + tid;
-    float v = recent0;
-    if (i < a.recent) {
-      if (i0 > 0) v = w[hi + i];
-      origin[last + i] = hi + i;
+  near = __reduce_add_sync(0xffffffffu, lane < kWarps ? counts[0][lane] : 0);
+  const Moves moves{total, near, a.recent, n};
+  if (!kMove && tid == 0) *reinterpret_cast<Moves *>(scratch) = moves;
+  if (piece == 0) {
+    for (int i0 = 0; i0 < a.recent; i0 += kThreads) {
+      const int i = i0 + tid;
+      float v = recent0;
+      if (i < a.recent) {
+        if (i0 > 0) v = w[hi + i];
+        origin[last + i] = hi + i;
+      }
+      __syncthreads();
+      if (i < a.recent) to[last + i] = v;
     }
     __syncthreads();
-    if (i < a.recent) to[last + i] = v;
+    for (int i = a.budget + tid; i < cap; i += kThreads) to[i] = 0.f;
   }
-  __syncthreads();
-  for (int i = a.budget + tid; i < cap; i += kThreads) to[i] = 0.f;
+  if constexpr (kMove) {
+    __syncthreads();                       // the lists, of which this block has written all
+    move_rows<kThreads>(a, lb, moves, via, piece, pieces);
+  }
 }
-
-constexpr int kMoveThreads = 256, kMoveWarps = kMoveThreads / 32;
-constexpr int kSlots = 9, kColSlots = 5;   // 16-byte pieces in flight per thread: rows, columns
 
 // Block (x: one of `pieces`, y: layer and sequence).
 __global__ void __launch_bounds__(kMoveThreads, 2)
 kda_evict_move_kernel(const CacheEvictArgs a, const int32_t pieces, const int64_t lb0) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t lb = lb0 + blockIdx.y;
-  const int32_t *table = a.block_table + (int64_t)(lb % a.B) * a.max_pages;
   const int32_t *scratch = a.moves + lb * scratch_ints(a.budget);
-  const int32_t *dst = scratch + kHead, *src = dst + list_ints(a.budget), *via = src + list_ints(a.budget);
-  unsigned char *pool = static_cast<unsigned char *>(a.cache) +
-                        lb / a.B * a.n_pages * a.page_size * a.row_bytes;
-  const int vecs = (int)(a.row_bytes / 16);
-  const auto pool_row = [&](int pos) {
-    const int pg = pos / a.page_size;
-    return table[pg] * a.page_size + (pos - pg * a.page_size);
-  };
-  const auto piece_at = [&](int row, int col) {
-    return reinterpret_cast<uint4 *>(pool + row * a.row_bytes + (int64_t)col * 16);
-  };
   latent::pdl_wait();
-  const Moves m = *reinterpret_cast<const Moves *>(scratch);
-  if (m.movers == 0 && m.recent == 0) return;
-  const int hi = m.n - m.recent, last = a.budget - m.recent;
-
-  if (m.n - a.budget >= m.recent) {
-    // ---- whole rows, some at a time for each warp: the places of the last rows, then the
-    // movers from behind these
-    const int wide = min(vecs, 32 * kSlots);             // pieces of a row at a time
-    const int group = min(32, 32 * kSlots / wide);       // rows at a time
-    int place[kSlots];                                   // row of the group, piece
-#pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
-      const int v = lane + 32 * j, r = v / wide;
-      place[j] = r < group ? r << 16 | (v - r * wide) : -1;
-    }
-    // rows s to rows d, each by the lane that has that row of the group; -1: none
-    const auto copy = [&](int s, int d) {
-      for (int c0 = 0; c0 < vecs; c0 += wide) {
-        uint4 x[kSlots];
-#pragma unroll
-        for (int j = 0; j < kSlots; ++j) {
-          const int row = __shfl_sync(0xffffffffu, s, place[j] < 0 ? 0 : place[j] >> 16);
-          const int col = c0 + (place[j] & 0xffff);
-          if (place[j] >= 0 && row >= 0 && col < vecs) x[j] = *piece_at(row, col);
-        }
-#pragma unroll
-        for (int j = 0; j < kSlots; ++j) {
-          const int row = __shfl_sync(0xffffffffu, d, place[j] < 0 ? 0 : place[j] >> 16);
-          const int col = c0 + (place[j] & 0xffff);
-          if (place[j] >= 0 && row >= 0 && col < vecs) *piece_at(row, col) = x[j];
-        }
-      }
-    };
-    const int far = m.movers - m.near, all = m.recent + far;
-    for (int i0 = (blockIdx.x * kMoveWarps + warp) * group; i0 < all; i0 += pieces * kMoveWarps * group) {
-      const int i = i0 + lane;
-      int s = -1, d = -1, out = -1;
-      if (lane < group && i < all) {
-        if (i < m.recent) {
-          s = pool_row(hi + i);
-          d = pool_row(last + i);
-          out = via[i] >= 0 ? pool_row(via[i]) : -1;
-        } else {
-          s = pool_row(src[m.near + i - m.recent]);
-          d = pool_row(dst[m.near + i - m.recent]);
-        }
-      }
-      if (__any_sync(0xffffffffu, out >= 0)) copy(out >= 0 ? d : -1, out);   // the same lanes, in order
-      copy(s, d);
-    }
-    return;
-  }
-
-  // ---- some columns of all rows, chunks in order, a chunk read before it is written
-  const int per = (vecs + pieces - 1) / pieces, c0 = blockIdx.x * per, c1 = min(c0 + per, vecs);
-  for (int cc = c0; cc < c1; cc += kMoveThreads) {
-    const int width = min(c1 - cc, kMoveThreads), lanes = kMoveThreads / width;
-    const int col = cc + tid % width, r = tid / width;
-    for (int kind = 0; kind < 2; ++kind) {               // movers, then the last rows
-      const int rows = kind ? m.recent : m.movers;
-      for (int i0 = 0; i0 < rows; i0 += lanes * kColSlots) {
-        uint4 x[kColSlots];
-#pragma unroll
-        for (int j = 0; j < kColSlots; ++j) {
-          const int i = i0 + j * lanes + r;
-          if (r < lanes && i < rows) x[j] = *piece_at(pool_row(kind ? hi + i : src[i]), col);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kColSlots; ++j) {
-          const int i = i0 + j * lanes + r;
-          if (r < lanes && i < rows) *piece_at(pool_row(kind ? last + i : dst[i]), col) = x[j];
-        }
-      }
-    }
-  }
+  move_rows<kMoveThreads>(a, lb, *reinterpret_cast<const Moves *>(scratch),
+                          scratch + kHead + 2 * list_ints(a.budget), blockIdx.x, pieces);
 }
+
 
 }  // namespace
 
@@ -424,12 +447,22 @@ cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
   const int64_t all = (int64_t)a.L * a.B;
   if (all == 0) return cudaSuccess;
   const int64_t cap = (int64_t)a.max_pages * a.page_size;
-  const int32_t room = (int32_t)(cap < kKeep ? cap : kKeep);
-  if (!latent::kernel_ready<kda_evict_select_kernel>(kKeep * 4, 0)) return cudaErrorNotSupported;
-  kda_evict_select_kernel<<<(unsigned)all, kThreads, (size_t)room * 4, stream>>>(a, room);
-  cudaError_t e = cudaGetLastError();
   const int64_t sms = latent::sm_count() > 0 ? latent::sm_count() : 1;
+  const int32_t room = (int32_t)(cap < kKeep ? cap : kKeep);
   const int64_t want = 2 * sms / all;      // blocks of a (layer, sequence)
+  const int64_t one = sms / all;           // where one of them is on an SM
+  if (cap <= kShort && one >= kLeast && a.weights != a.weights_out) {
+    const int32_t pieces = (int32_t)(one < 32 ? one : 32);
+    const int64_t via = a.recent < cap ? a.recent : cap;
+    if (!latent::kernel_ready<kda_evict_select_kernel<true>>(2 * kShort * 4, 0))
+      return cudaErrorNotSupported;
+    kda_evict_select_kernel<true>
+        <<<(unsigned)(all * pieces), kThreads, (size_t)(room + via) * 4, stream>>>(a, room, pieces);
+    return cudaGetLastError();
+  }
+  if (!latent::kernel_ready<kda_evict_select_kernel<false>>(kKeep * 4, 0)) return cudaErrorNotSupported;
+  kda_evict_select_kernel<false><<<(unsigned)all, kThreads, (size_t)room * 4, stream>>>(a, room, 1);
+  cudaError_t e = cudaGetLastError();
   const int32_t pieces = (int32_t)(want < 8 ? 8 : want > 64 ? 64 : want);
   for (int64_t lb = 0; lb < all && e == cudaSuccess; lb += 65535) {
     cudaLaunchConfig_t cfg = {};

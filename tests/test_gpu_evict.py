@@ -72,7 +72,9 @@ def _check(d, budget, first, recent, in_place=False, layered=True):
     ([0, 1, 17, 16, 15], 16, 16, 0, 0), ([40, 100, 7], 16, 30, 4, 8), ([100, 200, 300], 64, 99, 0, 99),
     ([100, 200, 300], 64, 99, 99, 0), ([100, 200], 64, 60, 30, 30), ([2049, 2048, 2047], 64, 2048, 4, 64),
     ([1000, 5000, 33, 4096], 48, 700, 3, 100), ([1500], 512, 1499, 0, 700), ([777, 1200], 7, 333, 5, 300),
-    ([5, 600], 64, 2000, 1, 1), ([40000], 64, 5000, 10, 1000)])
+    ([5, 600], 64, 2000, 1, 1), ([40000], 64, 5000, 10, 1000), ([4080, 4000], 16, 4050, 1, 4040),
+    ([4080, 4000], 16, 2020, 0, 2020), ([4080], 16, 2000, 5, 1990), ([300] * 40, 16, 100, 4, 30),
+    ([17000, 16385, 100], 64, 16380, 0, 9), ([20000], 16, 3, 1, 1)])
 @pytest.mark.parametrize("in_place", [False, True])
 def test_against_the_plain_form(lens, page, budget, first, recent, in_place):
     _check(_data(lens, page, spare=1), budget, first, recent, in_place, layered=False)
