@@ -465,24 +465,29 @@ __device__ __forceinline__ void grad_finish(const NormArgs &a, const R &x, const
   });
 }
 // A block's sums, its groups' added in their order: rows 2 blockIdx (dw) and 2 blockIdx + 1 (db)
-// of the scratch.  sums: [kGroups][W], where there are several.
-template <int N, int E, int kGroups, class R>
-__device__ __forceinline__ void leave_sums(const NormArgs &a, const float (&v)[E], int which,
-                                           float *sums) {
-  float *to = a.partial + ((int64_t)blockIdx.x * 2 + which) * a.W;
+// of the scratch.  sums: [2][kGroups][W], where there are several; dw[i], db[i]: functions.
+template <int N, int E, int kGroups, class R, class F, class G>
+__device__ __forceinline__ void leave_sums(const NormArgs &a, F dw, G db, float *sums) {
+  float *to = a.partial + (int64_t)blockIdx.x * 2 * a.W;
   float *at = kGroups > 1 ? sums + (int)threadIdx.x / N * a.W : to;
+  const int next = kGroups > 1 ? kGroups * a.W : a.W;    // from dw to db
 #pragma unroll
   for (int i = 0; i < E; ++i)
-    if (R::channel(i) < a.W) at[R::channel(i)] = v[i];
+    if (R::channel(i) < a.W) {
+      at[R::channel(i)] = dw(i);
+      at[next + R::channel(i)] = db(i);
+    }
   if (kGroups == 1) return;
   __syncthreads();
-  for (int c = threadIdx.x; c < a.W; c += blockDim.x) {
-    float all = sums[c];
+  for (int c = threadIdx.x; c < 2 * a.W; c += blockDim.x) {
+    const float *from = sums + (c < a.W ? c : c - a.W + next);
+    float v[kGroups], all = 0.f;
 #pragma unroll
-    for (int p = 1; p < kGroups; ++p) all += sums[p * a.W + c];
+    for (int p = 0; p < kGroups; ++p) v[p] = from[p * a.W];
+#pragma unroll
+    for (int p = 0; p < kGroups; ++p) all += v[p];
     to[c] = all;
   }
-  __syncthreads();
 }
 
 // Rows whose address or distance is no multiple of 16 bytes, one channel at a time.
@@ -492,7 +497,7 @@ __global__ void __launch_bounds__(kSingleThreads, 1) kda_norm_bwd_kernel(const N
   using R = Row<T, N, E, false>;
   constexpr int kGroups = kSingleThreads / N;
   __shared__ float part[kGroups][2][2 * (N / 32)];
-  extern __shared__ float sums[];                        // [kGroups][W], where there are several
+  extern __shared__ float sums[];                        // [2][kGroups][W], where there are several
   latent::pdl_launch_dependents();
   float dw[E], db[E];
 #pragma unroll
@@ -515,8 +520,7 @@ __global__ void __launch_bounds__(kSingleThreads, 1) kda_norm_bwd_kernel(const N
     grad_finish<N, E>(a, x, g, m, r, c1, c2, four, static_cast<T *>(a.d_x) + row * a.dx_rs);
   }
   if (!a.partial) return;
-  leave_sums<N, E, kGroups, R>(a, dw, 0, sums);
-  leave_sums<N, E, kGroups, R>(a, db, 1, sums);
+  leave_sums<N, E, kGroups, R>(a, [&](int i) { return dw[i]; }, [&](int i) { return db[i]; }, sums);
 }
 
 template <typename T, int N, int E>
@@ -624,21 +628,14 @@ __global__ void __launch_bounds__(kBwdThreads, E * N <= kShort ? 2 : 1) kda_norm
   copies_wait<0>();
   __syncthreads();                                       // the ring is free
   if (!a.partial) return;
-  for (int which = 0; which < 2; ++which) {
-    float v[E];
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) {
-      const float2 u = (which ? db[i] : dw[i]).get();
-      v[2 * i] = u.x;
-      v[2 * i + 1] = u.y;
-    }
-    leave_sums<N, E, kGroups, R>(a, v, which, reinterpret_cast<float *>(ring));
-  }
+  const auto one = [](const F2 (&v)[E / 2], int i) { return i % 2 ? v[i / 2].get().y : v[i / 2].get().x; };
+  leave_sums<N, E, kGroups, R>(a, [&](int i) { return one(dw, i); }, [&](int i) { return one(db, i); },
+                               reinterpret_cast<float *>(ring));
 }
 
-// Sums of the blocks' rows, in their order: sixteen stretches of consecutive blocks, a warp each,
+// Sums of the blocks' rows, in their order: 32 stretches of consecutive blocks, a warp each,
 // then the stretches.  Block (x: 32 V channels, y: dw, db).
-constexpr int kJoinWarps = 16;
+constexpr int kJoinWarps = 32;
 template <int V>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 kda_norm_join_kernel(const float *__restrict__ partial, int32_t blocks, int32_t W, float *d_weight,
@@ -654,7 +651,7 @@ kda_norm_join_kernel(const float *__restrict__ partial, int32_t blocks, int32_t 
   float sum[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) sum[k] = 0.f;
-  constexpr int kBatch = 8;                // rows in flight
+  constexpr int kBatch = 5;                // rows in flight
   for (int b = b0; b < b1; b += kBatch) {
     float x[kBatch][V];
 #pragma unroll
@@ -729,7 +726,9 @@ cudaError_t bwd(const NormArgs &a, cudaStream_t stream) {
     kda_norm_bwd_ring_kernel<T, N, E><<<blocks, kBwdThreads, kBytes, stream>>>(a);
   } else {
     blocks = bwd_blocks<kSingleThreads>(a.n, a.W, N);
-    const size_t smem = kSingleThreads / N > 1 ? (size_t)(kSingleThreads / N) * a.W * 4 : 0;
+    const size_t smem = kSingleThreads / N > 1 ? (size_t)(kSingleThreads / N) * a.W * 8 : 0;
+    if (smem > 0 && !latent::kernel_ready<kda_norm_bwd_kernel<T, N, E>>(2 * kSingleThreads * E * 4, 0))
+      return cudaErrorNotSupported;
     kda_norm_bwd_kernel<T, N, E><<<blocks, kSingleThreads, smem, stream>>>(a);
   }
   cudaError_t e = cudaGetLastError();
@@ -772,6 +771,8 @@ cudaError_t pick(const NormArgs &a, cudaStream_t stream) {
   if (a.W <= kShort) return go(warp, least);
   if constexpr (kVector) {
     constexpr integral_constant<int, 64 / sizeof(T)> E{};
+    if constexpr (E > 16)
+      if (a.W <= 32 * 16) return go(warp, integral_constant<int, 16>{});
     if (a.W <= 32 * E) return go(warp, E);
     if (a.W <= 128 * E) return go(four, E);
     if (a.W <= 256 * E) return go(eight, E);
