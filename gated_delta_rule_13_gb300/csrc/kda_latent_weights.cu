@@ -38,7 +38,7 @@ constexpr int kThreads = 384;            // 2 x 4 epilogue warps, two loaders, M
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kLseWarp = 10, kKeepWarp = 11;
 constexpr uint32_t kBlock = 16384;       // 128 rows x 64 channels
 constexpr uint32_t kSmem = 232448;
-constexpr int kMaxBlocks = 9;
+constexpr int kMaxBlocks = 9, kMostTiles = 0x7fff0000;
 
 template <bool kPair>
 constexpr int kKeysLog = kPair ? 8 : 7;  // keys of a tile
@@ -368,9 +368,10 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
       if (w < warp) before += m.warp_sum[w];
       all += m.warp_sum[w];
     }
-    // tiles are counted in 32 bits from here on; a list that is longer is refused
-    const int total = all > 0x7fffffff ? 0 : (int)all;
-    if (all > 0x7fffffff && tid == 0)
+    // tiles are counted in 32 bits from here on, by pairs a little past the last; a list that is
+    // longer is refused
+    const int total = all > kMostTiles ? 0 : (int)all;
+    if (all > kMostTiles && tid == 0)
       record_device_status(&m.error, KDA_ERR_INVALID_ARG, 3, 0, 0);
     const int begin = group_begin(group, p.groups, total);
     if (!kPair && total > 0 && begin >= before && begin < before + mine) {

@@ -288,7 +288,8 @@ int kda_cache_evict(void *cache, const int32_t *block_table, const int32_t *seq_
   const int d = check_evict(L, B, budget);
   if (d != KDA_OK) return d;
   if (n_pages <= 0 || page_size <= 0 || max_pages <= 0 || row_bytes <= 0 || row_bytes % 16 != 0 ||
-      row_bytes > (1 << 30) || (int64_t)max_pages * page_size > (1 << 30) || first < 0 ||
+      row_bytes > (1 << 30) || (int64_t)max_pages * page_size > (1 << 30) ||
+      (int64_t)n_pages * page_size > 0x7fffffffLL || first < 0 ||
       recent < 0 || (int64_t)first + recent > budget)
     return KDA_ERR_INVALID_ARG;
   if (!cache || (B > 0 && (!block_table || !seq_lens || !weights || !weights_out || !new_lens ||

@@ -767,8 +767,8 @@ int kda_cache_copy_pages(void *cache, const int32_t *src, const int32_t *dst, in
  *   k, k_out   [n_tokens, dr] with token strides, or both NULL: the key all heads share,
  *              turned in the same launch
  *   positions  [n_tokens] int32 (any value), DEVICE
- *   inv_freq   [dr / 2] fp64, DEVICE: angle per position; scaling for longer contexts goes
- *              into these and into scale (finite)
+ *   inv_freq   [dr / 2] fp64, finite, DEVICE: angle per position; scaling for longer
+ *              contexts goes into these and into scale (finite)
  * An angle is off by at most 2^-24 of a turn whatever the position.
  * out may be x, k_out may be k (in place).  dr even, at most 512.  Alignment: of an
  * element; rows that start on 16 bytes (address and strides) and whose halves, or pairs,
@@ -882,7 +882,7 @@ int kda_cache_evict_workspace_size(int32_t L, int32_t B, int32_t budget, size_t 
  * call).  No two sequences may share a page of which rows are moved.
  *   workspace  kda_cache_evict_workspace_size() bytes, 16-byte aligned
  * row_bytes is a multiple of 16, cache 16-byte aligned; max_pages * page_size and budget
- * at most 2^30.
+ * at most 2^30, n_pages * page_size at most 2^31 - 1.
  * Errors (before any launch): KDA_ERR_INVALID_ARG, KDA_ERR_WORKSPACE, KDA_ERR_CUDA.
  */
 int kda_cache_evict(void *cache, const int32_t *block_table, const int32_t *seq_lens,

@@ -162,7 +162,7 @@ def _ev(lib, **over):
     (dict(cache=None), 1), (dict(table=None), 1), (dict(lens=None), 1), (dict(w=None), 1),
     (dict(wo=None), 1), (dict(nl=None), 1), (dict(orig=None), 1), (dict(L=0), 1), (dict(B=-1), 1),
     (dict(n_pages=0), 1), (dict(page=0), 1), (dict(rb=8), 1), (dict(rb=0), 1),
-    (dict(max_pages=0), 1), (dict(max_pages=1 << 25), 1), (dict(budget=0), 1),
+    (dict(max_pages=0), 1), (dict(max_pages=1 << 25), 1), (dict(n_pages=1 << 25), 1), (dict(budget=0), 1),
     (dict(budget=(1 << 30) + 1), 1), (dict(first=-1), 1), (dict(recent=-1), 1),
     (dict(first=90, recent=11), 1), (dict(cache=A + 8), 1), (dict(w=4 * A + 2), 1),
     (dict(st=9 * A + 2), 1), (dict(wo=4 * A + 64), 1), (dict(wo=A), 1), (dict(nl=3 * A), 1),
