@@ -11,12 +11,16 @@ What happens to the latent layer:
               (kda_latent_decode)
   acceptance  the accepted rows move together in the cache (kda_cache_write, no rows)
   fork        the last, partly filled page gets a private copy (kda_cache_copy_pages)
-and to the recurrent layer: kda_chunk_fwd over the prompt, kda_decode_replay over the
+  budget      the weight its rows are given is added up (kda_latent_weights), and the
+              rows given least leave (kda_cache_evict)
+Its latents are normalised (kda_norm_fwd) and the rotary channels of queries and rows turned
+by their positions (kda_rope) before anything else.  And to the recurrent layer: kda_chunk_fwd over the prompt, kda_decode_replay over the
 accepted tokens, its state copied for the fork (kda_cache_copy_pages).
 
 Every step's attention output is compared with the expanded form over the tokens the
 step stands for.  A training step of the latent layer (kda_latent_fwd and
-kda_latent_bwd around the projections) closes the example.
+kda_latent_bwd, kda_norm_bwd and kda_rope back, around the projections) closes the
+example.
 """
 from __future__ import annotations
 
@@ -46,25 +50,37 @@ class LatentLayer:
         self.w_kv = randn(g, DC, H * 2 * DH, std=DC ** -0.5)
         up = self.w_kv.view(DC, H, 2 * DH)
         self.w_uk, self.w_uv = up[..., :DH], up[..., DH:]
+        self.gamma = torch.ones(DC, device=DEV)           # of the latents' norm
+        self.freq = kda.kda_rope_inv_freq(DR, device=DEV)
 
-    def queries(self, x):
-        return (x @ self.w_q).view(*x.shape[:-1], H, DH + DR)
+    def project(self, x, pos):
+        """Queries [..., H, 192] and cached rows [..., 576] of tokens at these positions, and
+        for the gradient the latents as they were and their norm's statistics."""
+        q, raw = (x @ self.w_q).view(*x.shape[:-1], H, DH + DR), x @ self.w_c
+        rows = torch.empty_like(raw)
+        _, _, rstd = kda.kda_norm_fwd(raw[..., :DC], self.gamma, center=False, out=rows[..., :DC])
+        kda.kda_rope(q[..., DH:], pos, self.freq, k=raw[..., DC:], out=q[..., DH:],
+                     k_out=rows[..., DC:])
+        return q, rows, raw, rstd
 
-    def rows(self, x):
+    def rows(self, x, pos):
         """The cached row of every token: latent and rotary channels."""
-        return x @ self.w_c
+        return self.project(x, pos)[1]
 
-    def expanded(self, x, cu):
-        rows = self.rows(x)
+    def expanded(self, x, pos, cu):
+        q, rows, _, _ = self.project(x, pos)
         kv = (rows[:, :DC] @ self.w_kv).view(-1, H, 2 * DH)
-        return kda.kda_latent_fwd(self.queries(x), kv[..., :DH], kv[..., DH:],
-                                  rows[:, DC:].contiguous(), cu)
+        return kda.kda_latent_fwd(q, kv[..., :DH], kv[..., DH:], rows[:, DC:].contiguous(), cu)
 
-    def absorbed(self, x, cache, table, lens, tree=None):
-        """x [B, T, D]: attention outputs [B, T, H, 128] of the last T tokens."""
-        q = self.queries(x)
+    def absorbed(self, x, pos, cache, table, lens, tree=None, weights=None):
+        """x [B, T, D]: attention outputs [B, T, H, 128] of the last T tokens, whose weights
+        are added up where asked for."""
+        q = self.project(x, pos)[0]
         q = torch.cat([torch.einsum("bthd,chd->bthc", q[..., :DH], self.w_uk), q[..., DH:]], -1)
-        o = kda.kda_latent_decode(q.contiguous(), cache, table, lens, tree_mask=tree)
+        lse = None if weights is None else torch.empty(q.shape[:3], device=DEV)
+        o = kda.kda_latent_decode(q.contiguous(), cache, table, lens, tree_mask=tree, lse=lse)
+        if weights is not None:
+            kda.kda_latent_weights(q.contiguous(), cache, table, lens, lse, weights)
         return torch.einsum("bthc,chd->bthd", o, self.w_uv)
 
 
@@ -88,9 +104,9 @@ def serve(g):
     table = i32([[3, 0, 7], [1, 9, 4]])
 
     # prompt: both requests packed, expanded form; latent rows into the cache
-    cu = i32([0, n, 2 * n])
-    out, _ = layer.expanded(prompt.view(-1, D_MODEL), cu)
-    kda.kda_cache_write(cache, layer.rows(prompt), table, i32([0, 0]))
+    cu, at = i32([0, n, 2 * n]), i32(range(n)).expand(B, n).contiguous()
+    out, _ = layer.expanded(prompt.view(-1, D_MODEL), at.view(-1), cu)
+    kda.kda_cache_write(cache, layer.rows(prompt, at), table, i32([0, 0]))
 
     # the recurrent layer of the same requests
     k = randn(g, B, n, 3, H, DH)
@@ -111,13 +127,15 @@ def serve(g):
         paths.append((paths[p] if p >= 0 else []) + [i])
     T = len(parent)
     drafts = randn(g, B, T, D_MODEL)
-    kda.kda_cache_write(cache, layer.rows(drafts), table, i32([n, n]))
+    depth = i32([[n + len(p) - 1 for p in paths]] * B)    # a draft's position is its depth
+    kda.kda_cache_write(cache, layer.rows(drafts, depth), table, i32([n, n]))
     tree = torch.tensor([words] * B, device=DEV)
-    got = layer.absorbed(drafts, cache, table, i32([n + T] * B), tree)
+    got = layer.absorbed(drafts, depth, cache, table, i32([n + T] * B), tree)
     for i in (0, 3, 5):
         tokens = torch.cat([prompt, drafts[:, paths[i]]], 1)
         m = tokens.shape[1]
-        want, _ = layer.expanded(tokens.reshape(-1, D_MODEL), i32([0, m, 2 * m]))
+        want, _ = layer.expanded(tokens.reshape(-1, D_MODEL), i32([*range(m)] * B),
+                                 i32([0, m, 2 * m]))
         compare(f"draft {i}, its path of {len(paths[i])}", got[:, i], want.view(B, m, H, DH)[:, -1])
 
     # request 0 accepts 0 - 2 - 4, request 1 accepts 0 - 1
@@ -147,13 +165,35 @@ def serve(g):
     # one more token for each of the three, one step
     step = randn(g, 3, 1, D_MODEL)
     lens = i32(lens + lens[:1])
-    kda.kda_cache_write(cache, layer.rows(step), table, lens)
-    got = layer.absorbed(step, cache, table, lens + 1)
+    kda.kda_cache_write(cache, layer.rows(step, lens[:, None]), table, lens)
+    given = torch.zeros(3, table.shape[1] * PAGE, device=DEV)
+    got = layer.absorbed(step, lens[:, None], cache, table, lens + 1, weights=given)
+    history = []
     for b in range(3):
         r = b % 2 if b < 2 else 0
         tokens = torch.cat([prompt[r], drafts[r, accepted[r]], step[b]])
-        want, _ = layer.expanded(tokens, None)
+        history.append(tokens)
+        want, _ = layer.expanded(tokens, i32(range(len(tokens))), None)
         compare(f"request {b}, the token after acceptance", got[b, 0], want[-1])
+
+    # the fork goes on under a budget: of its 104 rows the 80 stay that its last token gave
+    # most (and its first 4 and last 8); the next token sees these
+    budget, b = 80, 2
+    mine = table[b:b + 1].clone()
+    for i, page in enumerate((8, 10)):                    # its pages are its own first
+        kda.kda_cache_copy_pages(cache.unsqueeze(0), mine[:, i].contiguous(), i32([page]))
+        mine[0, i] = page
+        if i + 1 == last:
+            break
+    left, origin = kda.kda_cache_evict(cache, mine, lens[b:] + 1, given[b:].clone(), budget, first=4,
+                                       recent=8)
+    token, pos = randn(g, 1, 1, D_MODEL), lens[b:, None] + 1
+    kda.kda_cache_write(cache, layer.rows(token, pos), mine, left)
+    got = layer.absorbed(token, pos, cache, mine, left + 1)
+    kept = origin[0].long().sort().values
+    tokens = torch.cat([history[b][kept], token[0]])
+    want, _ = layer.expanded(tokens, torch.cat([kept.to(torch.int32), pos[0]]), None)
+    compare(f"request {b}, {budget} of {len(history[b])} rows kept", got[0, 0], want[-1])
     return out
 
 
@@ -162,32 +202,37 @@ def train(g):
     along them by what they predict."""
     layer = LatentLayer(g)
     lens = [70, 130, 40]
-    cu = i32([0, 70, 200, 240])
+    cu, pos = i32([0, 70, 200, 240]), i32([i for n in lens for i in range(n)])
     x, target = randn(g, sum(lens), D_MODEL), randn(g, sum(lens), H, DH)
 
     def forward():
-        q, rows = layer.queries(x), layer.rows(x)
+        q, rows, raw, rstd = layer.project(x, pos)
         kv = (rows[:, :DC] @ layer.w_kv).view(-1, H, 2 * DH)
         rope = rows[:, DC:].contiguous()
         out, lse = kda.kda_latent_fwd(q, kv[..., :DH], kv[..., DH:], rope, cu)
         diff = out.float() - target.float()
-        return q, rows, kv, rope, out, lse, diff, 0.5 * float((diff * diff).mean())
+        return q, rows, raw, rstd, kv, rope, out, lse, diff, 0.5 * float((diff * diff).mean())
 
-    q, rows, kv, rope, out, lse, diff, before = forward()
+    q, rows, raw, rstd, kv, rope, out, lse, diff, before = forward()
     scale = 1024.0                                       # keeps bf16 gradients in range
     d_out = (diff * (scale / diff.numel())).bfloat16()
     d_kv = torch.empty_like(kv)
     dq, _, _, d_rope = kda.kda_latent_bwd(q, kv[..., :DH], kv[..., DH:], rope, out, lse, d_out, cu,
                                           d_k=d_kv[..., :DH], d_v=d_kv[..., DH:])
     d_kv = d_kv.view(sum(lens), -1)
-    d_rows = torch.cat([d_kv @ layer.w_kv.t(), d_rope], 1)
+    # back through the rotation and the norm
+    d_rows = torch.empty_like(raw)
+    kda.kda_rope(dq[..., DH:], pos, layer.freq, k=d_rope, out=dq[..., DH:], k_out=d_rows[:, DC:],
+                 transpose=True)
+    _, d_gamma, _ = kda.kda_norm_bwd(d_kv @ layer.w_kv.t(), raw[:, :DC], layer.gamma, None, rstd,
+                                     d_x=d_rows[:, :DC])
     grads = [(layer.w_q, x.t() @ dq.view(sum(lens), -1)), (layer.w_c, x.t() @ d_rows),
-             (layer.w_kv, rows[:, :DC].t() @ d_kv)]
+             (layer.w_kv, rows[:, :DC].t() @ d_kv), (layer.gamma, d_gamma)]
     grads = [(w, d.float() / scale) for w, d in grads]
     square = sum(float((d * d).sum()) for _, d in grads)
     step = 0.02 * before / square                        # a first-order drop of 2 %
     for w, d in grads:
-        w.copy_((w.float() - step * d).bfloat16())
+        w.copy_(w.float() - step * d)
     after = forward()[-1]
     print(f"training step: loss {before:.5f} -> {after:.5f}")
     if not 0.005 * before < before - after < 0.04 * before:
