@@ -23,7 +23,7 @@
 namespace kda {
 namespace {
 
-constexpr int kShort = 256;              // channels of a short row
+constexpr int kShort = 256;              // channels of a short row: a warp's or half a warp's
 
 // Two fp32 values at a time: the same roundings in half the instructions.
 struct F2 {
@@ -164,10 +164,12 @@ struct Row {
 // between two places, so that one barrier a call is enough.
 template <int N, int K>
 __device__ __forceinline__ void row_sum(float (&x)[K], float *part) {  // [K][N / 32]
+  constexpr int kLanes = N < 32 ? N : 32;
+  const unsigned mask = N < 32 ? ((1u << kLanes) - 1) << (threadIdx.x & 31 & ~(kLanes - 1)) : ~0u;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+  for (int o = kLanes / 2; o > 0; o >>= 1)
 #pragma unroll
-    for (int k = 0; k < K; ++k) x[k] += __shfl_xor_sync(0xffffffffu, x[k], o);
+    for (int k = 0; k < K; ++k) x[k] += __shfl_xor_sync(mask, x[k], o);
   if constexpr (N > 32) {
     constexpr int kWarps = N / 32;
     const int warp = threadIdx.x % N >> 5, lane = threadIdx.x & 31;
@@ -184,6 +186,8 @@ __device__ __forceinline__ void row_sum(float (&x)[K], float *part) {  // [K][N 
     }
   }
 }
+template <int N>
+constexpr int kPart = N < 32 ? 1 : N / 32;               // floats of `part` for each sum
 
 // Mean and reciprocal deviation of a row held in registers; part: two places of N / 32, `turn`
 // alternates between calls.
@@ -224,7 +228,7 @@ __device__ __forceinline__ void statistics(const NormArgs &a, const R &x, float 
         }
     }
   float v[1] = {(t[0] + t[1]).sum()};
-  row_sum<N, 1>(v, part + (a.center || turn ? N / 32 : 0));
+  row_sum<N, 1>(v, part + (a.center || turn ? kPart<N> : 0));
   r = rsqrtf(fmaf(v[0], inv, a.eps));
 }
 // wb(i, w, b): weight and bias of this thread's pair i of channels.
@@ -251,7 +255,7 @@ template <typename T, int N, int E, bool kVector>
 __global__ void __launch_bounds__(kBlock<N>, kVector ? 1 : 1024 / kBlock<N>) kda_norm_fwd_kernel(const NormArgs a) {
   using R = Row<T, N, E, kVector>;
   constexpr int kRows = kBlock<N> / N;
-  __shared__ float part[kRows][2 * (N / 32)];
+  __shared__ float part[kRows][2 * kPart<N>];
   const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / N;
   if (row >= a.n) return;                                // a whole group
   R x;
@@ -272,14 +276,16 @@ __global__ void __launch_bounds__(kBlock<N>, kVector ? 1 : 1024 / kBlock<N>) kda
 // in shared memory.  Every thread copies the channels it will read itself, some rows ahead,
 // into shared memory (cp.async): no thread waits for another but in the row's sums.
 // The gradient's threads have twice the registers, for the sums of dw and db.
-constexpr int kFwdThreads = 1024, kBwdThreads = 512;
+template <int N, int E>
+constexpr int kFwdThreads = N * E > 8192 ? 512 : 1024;   // (weight and bias of long rows take room)
+constexpr int kBwdThreads = 512;
 constexpr int kRingSpace = 230400;       // shared memory without what is declared
 // Rows ahead, beside `vectors` bytes.
 constexpr int stages(int row_bytes, int vectors) {
   return (kRingSpace - vectors) / row_bytes < 4 ? (kRingSpace - vectors) / row_bytes : 4;
 }
 template <typename T, int N, int E>
-constexpr int kFwdStages = stages(kFwdThreads *E *(int)sizeof(T), 2 * N *E * 4);
+constexpr int kFwdStages = stages(kFwdThreads<N, E> *E *(int)sizeof(T), 2 * N *E * 4);
 template <typename T, int N, int E>
 constexpr int kBwdStages = stages(2 * kBwdThreads * E * (int)sizeof(T), N * E * 4);
 
@@ -336,13 +342,13 @@ __device__ __forceinline__ void copy_row(uint32_t dst, const T *row, int live) {
 }
 
 template <typename T, int N, int E>
-__global__ void __launch_bounds__(kFwdThreads, 1) kda_norm_fwd_ring_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kFwdThreads<N, E>, 1) kda_norm_fwd_ring_kernel(const NormArgs a) {
   using R = Row<T, N, E, true>;
-  constexpr int kGroups = kFwdThreads / N, kD = kFwdStages<T, N, E>;
+  constexpr int kThreads = kFwdThreads<N, E>, kGroups = kThreads / N, kD = kFwdStages<T, N, E>;
   static_assert(kD >= 1, "a row ahead");
-  constexpr uint32_t kStageBytes = kFwdThreads * E * sizeof(T);
+  constexpr uint32_t kStageBytes = kThreads * E * sizeof(T);
   extern __shared__ __align__(128) unsigned char ring[];
-  __shared__ float part[kGroups][2 * (N / 32)];
+  __shared__ float part[kGroups][2 * kPart<N>];
   const int lane = threadIdx.x % N, live = (a.W / R::kV - lane + N - 1) / N;
   const uint32_t mine = sm100::smem_u32(ring) + threadIdx.x * 16;
   const uint32_t sm_w = sm100::smem_u32(ring) + kD * kStageBytes, sm_b = sm_w + N * E * 4;
@@ -353,7 +359,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kda_norm_fwd_ring_kernel(const
 #pragma unroll
   for (int i = 0; i < kD; ++i) {
     if (row + i * step < a.n)
-      copy_row<T, N, E, kFwdThreads>(mine + i * kStageBytes, x_at + i * x_step, live);
+      copy_row<T, N, E, kThreads>(mine + i * kStageBytes, x_at + i * x_step, live);
     sm100::cp_async_commit();
   }
   x_at += kD * x_step;
@@ -371,7 +377,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kda_norm_fwd_ring_kernel(const
 #pragma unroll
     for (int j = 0; j < R::kCount; ++j) {
       uint4 v = make_uint4(0, 0, 0, 0);
-      if (j < live) v = sm100::ld_shared_v4(at + j * kFwdThreads * 16);
+      if (j < live) v = sm100::ld_shared_v4(at + j * kThreads * 16);
       x.raw[4 * j] = v.x;
       x.raw[4 * j + 1] = v.y;
       x.raw[4 * j + 2] = v.z;
@@ -397,7 +403,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kda_norm_fwd_ring_kernel(const
           t[k & 1] = fma2(d, d, t[k & 1]);
         }
     float v[1] = {(t[0] + t[1]).sum()};
-    row_sum<N, 1>(v, part_at + (a.center || turn ? N / 32 : 0));
+    row_sum<N, 1>(v, part_at + (a.center || turn ? kPart<N> : 0));
     const float r = rsqrtf(fmaf(v[0], inv, a.eps));
     if (lane == 0) {
       if (a.mean) a.mean[row] = m;
@@ -419,7 +425,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) kda_norm_fwd_ring_kernel(const
         }
         store16(out + j * N * R::kV, y);
       }
-    if (row + kD * step < a.n) copy_row<T, N, E, kFwdThreads>(at, x_at, live);  // what has been used may go
+    if (row + kD * step < a.n) copy_row<T, N, E, kThreads>(at, x_at, live);  // what has been used may go
     sm100::cp_async_commit();
     x_at += x_step;
     stage = stage + 1 == kD ? 0 : stage + 1;
@@ -481,11 +487,9 @@ __device__ __forceinline__ void leave_sums(const NormArgs &a, F dw, G db, float 
   __syncthreads();
   for (int c = threadIdx.x; c < 2 * a.W; c += blockDim.x) {
     const float *from = sums + (c < a.W ? c : c - a.W + next);
-    float v[kGroups], all = 0.f;
-#pragma unroll
-    for (int p = 0; p < kGroups; ++p) v[p] = from[p * a.W];
-#pragma unroll
-    for (int p = 0; p < kGroups; ++p) all += v[p];
+    float all = 0.f;
+#pragma unroll 16
+    for (int p = 0; p < kGroups; ++p) all += from[p * a.W];
     to[c] = all;
   }
 }
@@ -496,7 +500,7 @@ template <typename T, int N, int E>
 __global__ void __launch_bounds__(kSingleThreads, 1) kda_norm_bwd_kernel(const NormArgs a) {
   using R = Row<T, N, E, false>;
   constexpr int kGroups = kSingleThreads / N;
-  __shared__ float part[kGroups][2][2 * (N / 32)];
+  __shared__ float part[kGroups][2][2 * kPart<N>];
   extern __shared__ float sums[];                        // [2][kGroups][W], where there are several
   latent::pdl_launch_dependents();
   float dw[E], db[E];
@@ -530,7 +534,7 @@ __global__ void __launch_bounds__(kBwdThreads, E * N <= kShort ? 2 : 1) kda_norm
   static_assert(kD >= 1, "a row ahead");
   constexpr uint32_t kRowBytes = kBwdThreads * E * sizeof(T);
   extern __shared__ __align__(128) unsigned char ring[];
-  __shared__ float part[kGroups][2][2 * (N / 32)];
+  __shared__ float part[kGroups][2][2 * kPart<N>];
   latent::pdl_launch_dependents();
   const int lane = threadIdx.x % N, live = (a.W / kV - lane + N - 1) / N;
   const uint32_t mine = sm100::smem_u32(ring) + threadIdx.x * 16;
@@ -700,12 +704,12 @@ template <typename T, int N, int E, bool kVector>
 cudaError_t fwd(const NormArgs &a, cudaStream_t stream) {
   constexpr int kRows = kBlock<N> / N;
   if constexpr (kVector && kFwdStages<T, N, E> >= 1) {
-    constexpr int kGroups = kFwdThreads / N;
-    constexpr int kBytes = kFwdStages<T, N, E> * kFwdThreads * E * (int)sizeof(T) + 2 * N * E * 4;
+    constexpr int kThreads = kFwdThreads<N, E>, kGroups = kThreads / N;
+    constexpr int kBytes = kFwdStages<T, N, E> * kThreads * E * (int)sizeof(T) + 2 * N * E * 4;
     // Rows enough that every group has some to walk over.
     if (a.W % (16 / (int)sizeof(T)) == 0 && a.n >= (int64_t)4 * kGroups * sms() &&
         latent::kernel_ready<kda_norm_fwd_ring_kernel<T, N, E>>(kBytes, 0)) {
-      kda_norm_fwd_ring_kernel<T, N, E><<<sms(), kFwdThreads, kBytes, stream>>>(a);
+      kda_norm_fwd_ring_kernel<T, N, E><<<sms(), kThreads, kBytes, stream>>>(a);
       return cudaGetLastError();
     }
   }
@@ -751,7 +755,7 @@ bool rows_of_16(const void *p, int64_t rs, int esz) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && rs * esz % 16 == 0;
 }
 
-// Threads of a row.  With vectors: a warp for a short one, the fewest that hold it with 64 bytes
+// Threads of a row.  With vectors: half a warp or a warp for a short one, the fewest that hold it with 64 bytes
 // of it each, of the longest fp32 rows 128.  Single channels: eight each, of the longest 16, which
 // leaves registers for 1024 threads an SM.
 template <typename T, bool kVector, bool kForward>
@@ -768,6 +772,7 @@ cudaError_t pick(const NormArgs &a, cudaStream_t stream) {
   constexpr integral_constant<int, 1024> all{};
   constexpr integral_constant<int, 8> least{};
   static_assert(kShort == 32 * 8, "a short row is a warp's with eight channels each");
+  if (a.W <= kShort / 2) return go(integral_constant<int, 16>{}, least);
   if (a.W <= kShort) return go(warp, least);
   if constexpr (kVector) {
     constexpr integral_constant<int, 64 / sizeof(T)> E{};

@@ -134,7 +134,7 @@ def test_not_a_number_stays_in_its_row():
 
 
 @pytest.mark.parametrize("n,W,dtype", [
-    (5000, 512, F32), (3001, 7168, BF), (20001, 40, BF), (20001, 256, F32), (20001, 128, BF),
+    (5000, 512, F32), (3001, 7168, BF), (40001, 40, BF), (40001, 128, BF), (40001, 96, F32), (20001, 256, F32), (20001, 128, BF),
     (20001, 1024, BF), (10001, 500, F32), (5001, 4096, BF), (5001, 2048, F32), (2501, 4096, F32),
     (1301, 16384, BF), (1301, 8192, F32), (1301, 16384, F32), (20001, 25, BF), (5001, 513, BF),
     (3001, 4001, F32), (2001, 7169, BF), (1301, 16383, F32), (1301, 16383, BF)])
