@@ -10,10 +10,10 @@
 //
 // Selection, one block a (layer, sequence): a weight becomes an unsigned number of the same
 // order.  Counts by its upper 11 bits (four bins an octave) tell in which bin the last kept one
-// is; the few in that bin are ranked against each other.  Where they are not few, the bits that
-// are left are fixed some at a time by counts in the same way (a radix selection), and equal
-// weights by their order.  Each warp then walks its own stretch of the candidates in order and,
-// with the counts of the stretches before it, lists holes and movers in the workspace.
+// is; counts by the bits below do so within the bin, 11 and 10 more (a radix selection), until
+// all that share the bits are kept or few do, which are ranked against each other.  Equal weights
+// go by their order.  Each warp then walks its own stretch of the candidates in order and, with
+// the counts of the stretches before it, lists holes and movers in the workspace.
 //
 // Moves, in a second kernel that starts beside the first.  The last rows take places that movers
 // leave, and where n - budget < recent also one another's.  Where they do not, a place and all
@@ -32,8 +32,8 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kKeep = 16384;               // candidates in shared memory
-constexpr int kBins = 2048, kLow = 21;     // of the first count; bits below it
-constexpr int kFew = 1024;                 // ranked directly
+constexpr int kBins = 2048;
+constexpr int kFew = 256;                  // ranked directly
 constexpr int kShort = 4096, kLeast = 4;   // one launch: positions at most, blocks at least
 static_assert(kBins % kThreads == 0 && kBins <= 4 * kThreads, "a thread has four bins at most");
 
@@ -256,25 +256,26 @@ kda_evict_select_kernel(const CacheEvictArgs a, const int32_t room, const int32_
     __syncthreads();
   };
   // Kept: what is above `value`, and of its equals those up to `place`.
-  uint32_t value = ~0u;
-  int place = -1;
-  if (last > lo) {
+  uint32_t value = last > lo ? 0 : ~0u, known = 0;
+  int place = last > lo ? 0x7fffffff : -1, left = last - lo;
+  for (int shift = 21; last > lo && shift >= 0; shift = shift == 21 ? 10 : shift - 10) {
+    const uint32_t mask = shift > 0 ? 2047 : 1023;
     for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
     if (tid == 0) gathered = 0;
     __syncthreads();
     each([&](int i, uint32_t u) {
-      if (i < s1) atomicAdd(&hist[u >> kLow], 1);
+      if (i < s1 && (u & known) == value) atomicAdd(&hist[u >> shift & mask], 1);
     });
     __syncthreads();
-    find(kBins, last - lo);
-    value = (uint32_t)pick[0] << kLow;
-    int left = pick[1];
+    find((int)mask + 1, left);
+    value |= (uint32_t)pick[0] << shift;
+    known |= mask << shift;
+    left = pick[1];
     const int inside = pick[2];
-    place = 0x7fffffff;                    // all of the bin, if they are as many as are left
-    if (left < inside && inside <= kFew) {
+    if (left == inside) break;               // all that share the bits are kept
+    if (inside <= kFew) {
       each([&](int i, uint32_t u) {
-        if (i < s1 && u >> kLow == value >> kLow)
-          few[atomicAdd(&gathered, 1)] = make_uint2(u, (uint32_t)i);
+        if (i < s1 && (u & known) == value) few[atomicAdd(&gathered, 1)] = make_uint2(u, (uint32_t)i);
       });
       __syncthreads();
       for (int k0 = 0; k0 < inside; k0 += kThreads / 4) {   // four threads each
@@ -296,27 +297,9 @@ kda_evict_select_kernel(const CacheEvictArgs a, const int32_t room, const int32_
       __syncthreads();
       value = (uint32_t)pick[0];
       place = pick[1];
-    } else if (left < inside) {
-      uint32_t known = ~0u << kLow;
-      for (int shift = kLow; shift > 0;) {
-        const int bits = min(shift, 8);
-        shift -= bits;
-        for (int i = tid; i < 256; i += kThreads) hist[i] = 0;
-        __syncthreads();
-        each([&](int i, uint32_t u) {      // equal ones are counted by one lane
-          const bool in = i < s1 && (u & known) == value;
-          const int digit = u >> shift & ((1 << bits) - 1);
-          const unsigned peers = __match_any_sync(0xffffffffu, in ? digit : 256);
-          if (in && lane == __ffs(peers) - 1) atomicAdd(&hist[digit], __popc(peers));
-        });
-        __syncthreads();
-        find(1 << bits, left);
-        value |= (uint32_t)pick[0] << shift;
-        known |= ((1u << bits) - 1) << shift;
-        left = pick[1];
-        __syncthreads();
-      }
-      // the place of the left-th of those equal to it
+      break;
+    }
+    if (shift == 0) {                        // more equals: the place of the left-th
       int equal = 0;
       each([&](int i, uint32_t u) { equal += __popc(__ballot_sync(0xffffffffu, i < s1 && u == value)); });
       if (lane == 0) counts[0][warp] = equal;
@@ -362,20 +345,26 @@ kda_evict_select_kernel(const CacheEvictArgs a, const int32_t room, const int32_
     if (m) src[mover + __popc(ms & under)] = i;
     hole += __popc(hs);
     mover += __popc(ms);
-    if (yes && i < last && piece == 0) {
-      origin[i] = i;
-      if (!same) to[i] = w[i];
-    }
   });
-  for (int i = tid; i < lo && piece == 0; i += kThreads) {
-    origin[i] = i;
-    if (!same) to[i] = w[i];
+  constexpr int kBatch = 4;                // in flight per thread
+  for (int i0 = tid; i0 < last && piece == 0; i0 += kBatch * kThreads) {   // what stays in place
+    float v[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) v[k] = w[min(i0 + k * kThreads, last - 1)];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kThreads;
+      const uint32_t u = order_of(v[k]);
+      if (i < last && (i < lo || u > value || (u == value && i <= place))) {
+        origin[i] = i;
+        if (!same) to[i] = v[k];
+      }
+    }
   }
   __syncthreads();                         // the lists; and no weight is looked at again
 
   // ---- weights of movers and of the last rows (chunks in order, read before written)
   int near = 0;
-  constexpr int kBatch = 4;                // moves in flight per thread
   for (int i0 = tid; i0 < total; i0 += kBatch * kThreads) {
     int from[kBatch], at[kBatch];
     float v[kBatch];
