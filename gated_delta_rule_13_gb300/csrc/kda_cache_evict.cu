@@ -20,6 +20,12 @@
 // that goes through it are one warp's: first the mover leaves, then the last row comes.  Where
 // they do (and then there are few movers), a block has some columns of all rows and takes the
 // movers first.  No block waits for another.
+//
+// Measured: prompts of 3000 .. 8192 rows cut to 2048, 8 sequences, 24 layers, 131 us, of which the
+// selection is 19 (latency: a dozen dependent steps) and the moves 110 (638 MB both ways, 5.8
+// TB/s, rows of 1,152 bytes at random places; 95 at a plain copy's rate).  Fewer bytes in flight
+// than 144 a thread, or more threads with less, took 133 to 184 us in all.  One row of each of 16
+// requests of 2049, one launch: 7.5 us (two: 9.3).
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -6,12 +6,19 @@
 //   dx = r (w g - mean(w g) - z mean(w g z))   (without the mean: no second term)
 //   dw = sum over rows of g z,  db = sum over rows of g
 //
-// A row is read once and held in registers, as it was loaded, by a warp or by up to 512
-// threads; the variance is the mean square of what the mean leaves, from the same
-// registers, so that a mean far from zero costs no digits.  Statistics and sums are fp32.
-// The gradient's blocks walk over the rows with the sums of dw and db in registers and
-// leave one pair of rows each in the workspace; a second kernel adds these in the blocks'
-// order, so that results do not vary between calls.
+// Bound by HBM: two passes of bytes forward, three back.  A row is read once: by half a warp or
+// up to 512 threads, into registers (few rows) or, many rows, some rows ahead into shared memory.
+// The variance is the mean square of what the mean leaves, from the row on chip, so that a mean
+// far from zero costs no digits.  Statistics and sums are fp32; values are taken in pairs, which
+// halves the instructions (with one at a time the gradient of 16384 x 7168 was bound by them:
+// 167 us).  The gradient's blocks walk over the rows with the sums of dw and db in registers and
+// leave one pair of rows each in the workspace; a second kernel adds these in the blocks' order,
+// so that results do not vary between calls.
+//
+// Measured (cold): 16384 x 7168 bf16 forward 75 us (6.3 TB/s), gradient 114 us (6.2); gradient of
+// 16384 x 512 fp32 22.8 us (4.4), of which the two sums are 4.5; 64 x 7168 2.9 us; 1 M x 128 bf16
+// 88 us (6.1).  Rows that do not lie on 16 bytes go one channel at a time: 8192 x 7169 bf16 152 and
+// 268 us (1.5 and 1.3 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
