@@ -90,6 +90,32 @@ def test_views(dtype, off, stride):
     assert torch.equal(copy[:, :off], base[:, :off])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,W,stride", [(7, 513, 520), (5000, 513, 520), (900, 7170, 7176), (3, 30, 32),
+                                        (30000, 30, 32)])
+def test_rows_that_end_inside_16_bytes(n, W, stride, dtype):
+    x, g = _in((n, stride), dtype, 1)[:, :W], _in((n, stride), dtype, 2)[:, :W]
+    w = _vec(W, 3, 1.0)
+    to = _in((n, stride), dtype, 5)
+    around = to[:, W:].clone()
+    got = kda.kda_norm_fwd(x, w, w, out=to[:, :W])
+    _check_fwd(got, x, w, w, True, 1e-5)
+    assert torch.equal(to[:, W:], around)
+    _check_bwd(kda.kda_norm_bwd(g, x, w, got[1], got[2], bias=True, d_x=to[:, :W]), g, x, w, *got[1:])
+    assert torch.equal(to[:, W:], around)
+
+
+def test_one_row_and_vectors_anywhere():
+    x, w = _in((300,), BF, 1), _vec(301, 3, 1.0)[1:]          # a weight that starts on 4 bytes
+    got = kda.kda_norm_fwd(x, w)
+    assert got[0].shape == (300,) and got[1].shape == ()
+    _check_fwd(got, x, w, None, True, 1e-5)
+    rows = x.expand(9, 300)                                   # the same row, nine times
+    got = kda.kda_norm_fwd(rows, w)
+    _check_fwd(got, rows, w, None, True, 1e-5)
+    _check_bwd(kda.kda_norm_bwd(rows, rows, w, *got[1:], bias=True), rows, rows, w, *got[1:])
+
+
 def test_a_mean_far_from_zero():
     x = _in((40, 7168), F32, 1, 1.0, 300.0)
     _check_fwd(kda.kda_norm_fwd(x, None, None), x, None, None, True, 1e-5)

@@ -92,6 +92,8 @@ def test_batches_of_tokens_and_no_heads():
     x = one[:, None].expand(7, 3, dr)
     p = _pos((7,), 1000)
     _check(kda.kda_rope(x, p, freq), x, p, freq, True, 1.0, False)
+    here = torch.tensor(77, dtype=torch.int32, device=DEV)   # one token, by itself
+    _check(kda.kda_rope(q[0, 0], here, freq), q[0, 0], here, freq, True, 1.0, False)
     empty = kda.kda_rope(q[:0], pos[:0], freq)
     assert empty.shape == (0, T, H, dr)
 
