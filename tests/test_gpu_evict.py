@@ -131,6 +131,31 @@ def test_bad_lengths_and_pages_are_left_alone():
             assert (origin[:, other] >= 0).all()
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_a_pool_past_two_to_the_32_bytes(in_place):
+    """Two layers of 4.4 GB each, one sequence's pages at their ends."""
+    n_pages, page, W, n, budget, first, recent = 60000, 64, 576, 700, 300, 4, 30
+    cache = torch.empty(2, n_pages, page, W, dtype=torch.bfloat16, device=DEV)
+    ids = torch.tensor([59999, 0, 58000, 30000, 59998, 59001, 58999, 1, 2, 59000, 45000],
+                       dtype=torch.int32, device=DEV)
+    g = torch.Generator().manual_seed(3)
+    rows = torch.randn(2, len(ids), page, W, generator=g).to(torch.bfloat16).to(DEV)
+    cache[:, ids.long()] = rows
+    w = torch.rand(2, 1, len(ids) * page, generator=g).to(DEV)
+    before, out = w.clone(), w if in_place else torch.empty_like(w)
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    new, origin = kda.kda_cache_evict(cache, ids[None], lens, w, budget, first=first, recent=recent,
+                                      weights_out=out)      # in place by name as well
+    assert new.tolist() == [budget]
+    for l in range(2):
+        want = torch.tensor(ru.evict_ref(before[l, 0].tolist(), n, budget, first, recent))
+        assert origin[l, 0].tolist() == want.tolist()
+        got, old = cache[l, ids.long()].view(-1, W), rows[l].view(-1, W)
+        assert torch.equal(got[:budget], old[want.to(DEV)])
+        assert torch.equal(got[n:], old[n:])
+        assert torch.equal(out[l, 0, :budget], before[l, 0, want.to(DEV)])
+
+
 def test_again_on_what_is_left():
     """A budget kept up step by step: rows come and go, the weights follow them."""
     d = _data([64, 64], 16, W=8, spare=2)

@@ -116,6 +116,23 @@ def test_one_row_and_vectors_anywhere():
     _check_bwd(kda.kda_norm_bwd(rows, rows, w, *got[1:], bias=True), rows, rows, w, *got[1:])
 
 
+@pytest.mark.parametrize("n,W,stride", [(3, 512, (1 << 31) + 64), (3, 100, (1 << 31) + 1),
+                                        (4_300_000, 512, 512)])
+def test_rows_past_two_to_the_31_elements(n, W, stride):
+    x = torch.zeros((n - 1) * stride + W, dtype=BF, device=DEV).as_strided((n, W), (stride, 1))
+    few = min(n, 300)
+    x[-few:] = _in((few, W), BF, 1)
+    g, w = x.flip(1) if n == few else x, _vec(W, 3, 1.0)
+    out, mean, rstd = kda.kda_norm_fwd(x, w, w)
+    _check_fwd((out[-few:], mean[-few:], rstd[-few:]), x[-few:], w, w, True, 1e-5)
+    d_x, d_w, d_b = kda.kda_norm_bwd(g, x, w, mean, rstd, bias=True)
+    # the other rows' gradients are zeros: they give the sums nothing
+    _check_bwd((d_x[-few:], d_w, d_b), g[-few:], x[-few:], w, mean[-few:], rstd[-few:])
+    if n == few:
+        kda.kda_norm_fwd(x, w, w, out=x)
+        assert torch.equal(x, out)
+
+
 def test_a_mean_far_from_zero():
     x = _in((40, 7168), F32, 1, 1.0, 300.0)
     _check_fwd(kda.kda_norm_fwd(x, None, None), x, None, None, True, 1e-5)

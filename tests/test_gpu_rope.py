@@ -117,6 +117,19 @@ def test_the_farthest_positions():
     assert ((got.double() - want).abs() <= ru.rope_bound(x, True, 1.0, F32, want)).all()
 
 
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_tokens_past_two_to_the_31_elements(interleaved):
+    far, n, H, dr = (1 << 31) + 64, 3, 5, 64
+    buf = torch.zeros(2 * far + H * dr, dtype=BF, device=DEV)
+    x = buf.as_strided((n, H, dr), (far, dr, 1))
+    x.copy_(_in((n, H, dr), BF, 3))
+    pos, freq = _pos((n,), 1 << 20), _freq(dr)
+    _check(kda.kda_rope(x, pos, freq, interleaved=interleaved), x, pos, freq, interleaved, 1.0, False)
+    want = kda.kda_rope(x, pos, freq, interleaved=interleaved)
+    kda.kda_rope(x, pos, freq, interleaved=interleaved, out=x)
+    assert torch.equal(x, want)
+
+
 def test_turning_back_is_the_gradient():
     """<g, rope(x)> = <rope^T(g), x>, and its difference along any direction."""
     x, g = _in((50, 8, 64), F32), _in((50, 8, 64), F32, 3)

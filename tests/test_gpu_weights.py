@@ -109,6 +109,20 @@ def test_sequences_that_share_pages():
     _check(_run(d, lse), d, lse)
 
 
+@pytest.mark.parametrize("T,H", [(1, 96), (2, 96)])
+def test_a_pool_past_two_to_the_31_elements(T, H):
+    """The same rows and pages' order from a small pool and from a large one's ends."""
+    d = _data([700, 300], T, H, 64, 64, wild=False)
+    lse = _lse(d)
+    want = _run(d, lse)
+    n = d["cache"].shape[0]
+    far = torch.arange(n, device=DEV) * 7 + 60000 - 7 * n
+    pool = torch.empty(60000, 64, 576, dtype=BF, device=DEV)
+    pool[far] = d["cache"]
+    d["cache"], d["table"] = pool, far.to(torch.int32)[d["table"].clamp(0, n - 1).long()].contiguous()
+    assert torch.equal(_run(d, lse), want)
+
+
 @pytest.mark.parametrize("decay", [0.0, 0.5, 1.0, 3.0])
 def test_decay(decay):
     d = _data([100, 300, 0], 2, 16, 64, 64, spare=1)
