@@ -118,3 +118,58 @@ def test_training_around_the_attention():
     for name, x, y in zip(("q", "k_rope", "kv", "gamma"), (dq, d_rope, d_kv, d_gamma), want):
         err = ((x.double() - y).norm() / y.norm()).item()
         assert err < 0.009, f"{name}: {err}"
+
+
+def test_two_streams_at_once():
+    """Every operator on two streams, with workspaces of their own, gives what it gives alone."""
+    g = torch.Generator(device=DEV).manual_seed(11)
+
+    def data(k):
+        B, n_pages = 4 + k, 200
+        lens = torch.randint(500, 1500, (B,), generator=g, device=DEV).to(torch.int32)
+        return dict(q=torch.randn(B, 2, 96, 576, generator=g, device=DEV).to(BF),
+                    cache=torch.randn(n_pages, 64, 576, generator=g, device=DEV).to(BF),
+                    table=torch.randperm(n_pages, generator=g, device=DEV)[:B * 24].to(torch.int32).view(B, 24),
+                    lens=lens, w=torch.rand(B, 24 * 64, generator=g, device=DEV),
+                    x=torch.randn(9000, 512, generator=g, device=DEV).to(BF),
+                    weight=torch.rand(512, generator=g, device=DEV),
+                    pos=torch.arange(9000, dtype=torch.int32, device=DEV),
+                    freq=kda.kda_rope_inv_freq(64, device=DEV))
+
+    def run(d):
+        cache, w = d["cache"].clone(), d["w"].clone()
+        lse = torch.empty(d["q"].shape[:3], device=DEV)
+        out = kda.kda_latent_decode(d["q"], cache, d["table"], d["lens"], lse=lse)
+        kda.kda_latent_weights(d["q"], cache, d["table"], d["lens"], lse, w, decay=0.5)
+        weights = w.clone()
+        evicted = kda.kda_cache_evict(cache, d["table"], d["lens"], w, 400, first=4, recent=64)
+        y, mean, rstd = kda.kda_norm_fwd(d["x"], d["weight"])
+        back = kda.kda_norm_bwd(d["x"], y, d["weight"], mean, rstd, bias=True)
+        turned = kda.kda_rope(d["x"].view(9000, 8, 64), d["pos"], d["freq"])
+        return [out, lse, weights, w, cache, *evicted, y, mean, rstd, *back, turned]
+
+    both = [data(0), data(1)]
+    want = [run(d) for d in both]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [None, None]
+    for _ in range(3):
+        for k in (0, 1):
+            with torch.cuda.stream(streams[k]):
+                got[k] = run(both[k])
+    torch.cuda.synchronize()
+    graphs = []
+    for k in (0, 1):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=streams[k]):
+            captured = run(both[k])
+        graphs.append((graph, captured))
+    for _ in range(3):
+        for k in (0, 1):
+            with torch.cuda.stream(streams[k]):
+                graphs[k][0].replay()
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        for a, b, c in zip(want[k], got[k], graphs[k][1]):
+            a, b, c = (a, b, c) if torch.is_tensor(a) else (a[0], b[0], c[0])
+            assert torch.equal(a, b) and torch.equal(a, c)
