@@ -799,8 +799,8 @@ int kda_norm_fwd(const void *x, int64_t x_row_stride, const float *weight, const
                  int64_t n, int32_t W, int dtype, int center, float eps, void *out,
                  int64_t out_row_stride, float *mean, float *rstd, void *stream);
 
-/* Workspace of kda_norm_bwd: 8 W bytes for each of its blocks (at most two an SM).  A call
- * with neither d_weight nor d_bias needs none. */
+/* Workspace of kda_norm_bwd: 8 bytes a channel (W rounded up to four) for each of its blocks (one
+ * an SM, of short rows four).  A call with neither d_weight nor d_bias needs none. */
 int kda_norm_bwd_workspace_size(int64_t n, int32_t W, int dtype, size_t *bytes);
 
 /*

@@ -105,6 +105,44 @@ def test_rows_that_end_inside_16_bytes(n, W, stride, dtype):
     assert torch.equal(to[:, W:], around)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,W", [(40000, 1), (40000, 25), (20000, 33), (20000, 60), (9000, 100), (5000, 201),
+                                 (5000, 300), (5000, 513), (5000, 999), (1300, 1025), (1300, 2047),
+                                 (1300, 4095), (700, 7169), (700, 8191), (650, 9001), (650, 16383)])
+def test_many_rows_that_start_anywhere(n, W, dtype):
+    """Input, output and gradients each at an address and a distance of their own; between the
+    rows nothing is written."""
+    def view(seed, off, gap):
+        buf = _in((off + n * (W + gap),), dtype, seed)
+        return buf, buf[off:].view(n, W + gap)[:, :W]
+
+    (_, x), (xo, o) = view(1, 1, 1), view(2, 3, 2)
+    (_, g), (xd, d) = view(3, 2, 0), view(4, 0, 5)
+    w, b = _vec(W + 1, 5, 1.0)[1:], _vec(W, 6)
+    x[5, W // 2] = float("nan")                     # stays in its row
+    g[5] = 0.0
+    beside, beside_d = xo.clone(), xd.clone()
+    got = kda.kda_norm_fwd(x, w, b, out=o)
+    keep = torch.arange(n, device=DEV) != 5
+    _check_fwd((o[keep], got[1][keep], got[2][keep]), x[keep], w, b, True, 1e-5)
+    assert o[5].isnan().all()
+    bits = o.clone()
+    o.copy_(beside[3:].view(n, W + 2)[:, :W])
+    assert torch.equal(xo, beside)                  # all but the rows
+    x[5], got[1][5], got[2][5] = 0.0, 0.0, 1.0
+    back = kda.kda_norm_bwd(g, x, w, got[1], got[2], bias=True, d_x=d)
+    _check_bwd(back, g, x, w, got[1], got[2])
+    want = d.clone()
+    again = kda.kda_norm_bwd(g, x, w, got[1], got[2], bias=True)
+    assert all(torch.equal(u, v) for u, v in zip(back, again))
+    d.copy_(beside_d.view(n, W + 5)[:, :W])
+    assert torch.equal(xd, beside_d)
+    kda.kda_norm_bwd(g, x, w, got[1], got[2], bias=True, d_x=g)     # in place
+    assert torch.equal(g, want)
+    kda.kda_norm_fwd(x, w, b, out=x)
+    assert torch.equal(x[keep], bits[keep])
+
+
 def test_one_row_and_vectors_anywhere():
     x, w = _in((300,), BF, 1), _vec(301, 3, 1.0)[1:]          # a weight that starts on 4 bytes
     got = kda.kda_norm_fwd(x, w)
