@@ -18,7 +18,8 @@
 // (cold inputs): 8192 tokens x 96 heads x 64 channels fp32, 403 MB both ways, 60.8 us, 6.6 TB/s;
 // 16384 x 16 bf16 with the shared key, 71 MB, 16.0 us, of which a launch and one block's way are
 // 2.5 (a plain copy of as many bytes: 12.5); 64 x 96 with the key 2.6 us.  Loads and stores
-// past the caches made no difference.
+// past the caches made no difference.  Rows that start on 8, 4 or 2 bytes go in pieces of these,
+// bound by instructions: 16384 x 16 of 74 channels bf16 40 us, of 72 in halves 19.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -29,8 +30,9 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256, kSmThreads = 1024;   // of a block at most, of an SM
-template <bool kInterleaved>
-constexpr int kGroup = kInterleaved ? 6 : 3;   // pieces in flight per thread: 96 bytes
+// Pieces in flight per thread: of 16 bytes 96 bytes of them.
+template <bool kInterleaved, int kB>
+constexpr int kGroup = kInterleaved || kB < 16 ? 6 : 3;
 constexpr int kMaxAngles = 2048;   // of a block
 
 // Turns per position, 2^64 to the turn and modulo a turn, of an angle per position in radians,
@@ -53,41 +55,6 @@ __device__ __forceinline__ uint64_t turns_of(double f) {
   return bits >> 63 ? 0 - t : t;
 }
 
-template <typename T>
-struct Elems;
-template <>
-struct Elems<float> {
-  static constexpr int kVec = 4;
-  static __device__ __forceinline__ void unpack(const uint4 &v, float *x) {
-    x[0] = __uint_as_float(v.x);
-    x[1] = __uint_as_float(v.y);
-    x[2] = __uint_as_float(v.z);
-    x[3] = __uint_as_float(v.w);
-  }
-  static __device__ __forceinline__ uint4 pack(const float *x) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                      __float_as_uint(x[3]));
-  }
-};
-template <>
-struct Elems<__nv_bfloat16> {
-  static constexpr int kVec = 8;
-  static __device__ __forceinline__ void unpack(const uint4 &v, float *x) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = sm100::unpack_bf16x2(w[i]);
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
-  }
-  static __device__ __forceinline__ uint4 pack(const float *x) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = sm100::pack_bf16x2(x[2 * i], x[2 * i + 1]);
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 template <typename T>
@@ -99,77 +66,132 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
-// A piece is what a thread turns at a time: with vectors, 16 bytes (interleaved pairs) or
-// 16 bytes of either half; else one pair.
-template <typename T, bool kInterleaved, bool kVector>
-struct Piece {
-  static constexpr int kE = kVector ? Elems<T>::kVec : 1;
-  static constexpr int kPairs = kInterleaved ? (kVector ? kE / 2 : 1) : kE;
-  static constexpr int kRegs = kVector ? (kInterleaved ? 1 : 2) : 1;   // 16-byte registers
-  uint4 raw[kRegs];
-  __device__ __forceinline__ void load(const T *row, int pair, int half) {
-    if constexpr (kVector) {
-      raw[0] = *reinterpret_cast<const uint4 *>(row + (kInterleaved ? 2 * pair : pair));
-      if constexpr (!kInterleaved) raw[1] = *reinterpret_cast<const uint4 *>(row + half + pair);
+// kB bytes that lie on kB.
+template <typename T, int kB>
+struct Words {
+  static constexpr int kE = kB / (int)sizeof(T);
+  uint32_t w[kB / 4];
+  __device__ __forceinline__ void load(const T *at) {
+    if constexpr (kB == 16) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(at);
+      w[0] = v.x;
+      w[1] = v.y;
+      w[2] = v.z;
+      w[3] = v.w;
+    } else if constexpr (kB == 8) {
+      const uint2 v = *reinterpret_cast<const uint2 *>(at);
+      w[0] = v.x;
+      w[1] = v.y;
     } else {
-      raw[0].x = __float_as_uint(to_float(row[kInterleaved ? 2 * pair : pair]));
-      raw[0].y = __float_as_uint(to_float(row[kInterleaved ? 2 * pair + 1 : half + pair]));
+      w[0] = *reinterpret_cast<const uint32_t *>(at);
     }
   }
+  __device__ __forceinline__ void unpack(float (&x)[kE]) const {
+#pragma unroll
+    for (int i = 0; i < kB / 4; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        x[i] = __uint_as_float(w[i]);
+      } else {
+        const float2 f = sm100::unpack_bf16x2(w[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(T *at, const float (&x)[kE]) {
+    uint32_t w[kB / 4];
+#pragma unroll
+    for (int i = 0; i < kB / 4; ++i) {
+      if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(x[i]);
+      else w[i] = sm100::pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    }
+    if constexpr (kB == 16) *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (kB == 8) *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t *>(at) = w[0];
+  }
+};
+
+// A piece is what a thread turns at a time: kB bytes of pairs (interleaved) or kB bytes of either
+// half; with kB = 0 one pair, channel by channel.
+template <typename T, bool kInterleaved, int kB>
+struct Piece {
+  using V = Words<T, kB>;
+  static constexpr int kE = V::kE, kPairs = kInterleaved ? kE / 2 : kE;
+  static_assert(kPairs >= 1, "a whole pair");
+  V raw[kInterleaved ? 1 : 2];
+  __device__ __forceinline__ void load(const T *row, int pair, int half) {
+    raw[0].load(row + (kInterleaved ? 2 * pair : pair));
+    if constexpr (!kInterleaved) raw[1].load(row + half + pair);
+  }
   __device__ __forceinline__ void turn_store(T *row, int pair, int half, const float2 *cs) const {
-    if constexpr (!kVector) {
-      const float a = __uint_as_float(raw[0].x), b = __uint_as_float(raw[0].y);
-      row[kInterleaved ? 2 * pair : pair] = from_float<T>(a * cs[0].x - b * cs[0].y);
-      row[kInterleaved ? 2 * pair + 1 : half + pair] = from_float<T>(b * cs[0].x + a * cs[0].y);
-    } else if constexpr (kInterleaved) {
-      float x[kE], y[kE];
-      Elems<T>::unpack(raw[0], x);
+    float a[kE];
+    raw[0].unpack(a);
+    if constexpr (kInterleaved) {
+      float y[kE];
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
         const float2 r = cs[i];
-        y[2 * i] = x[2 * i] * r.x - x[2 * i + 1] * r.y;
-        y[2 * i + 1] = x[2 * i + 1] * r.x + x[2 * i] * r.y;
+        y[2 * i] = a[2 * i] * r.x - a[2 * i + 1] * r.y;
+        y[2 * i + 1] = a[2 * i + 1] * r.x + a[2 * i] * r.y;
       }
-      *reinterpret_cast<uint4 *>(row + 2 * pair) = Elems<T>::pack(y);
+      V::store(row + 2 * pair, y);
     } else {
-      float a[kE], b[kE], u[kE], v[kE];
-      Elems<T>::unpack(raw[0], a);
-      Elems<T>::unpack(raw[1], b);
+      float b[kE], u[kE], v[kE];
+      raw[1].unpack(b);
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
         const float2 r = cs[i];
         u[i] = a[i] * r.x - b[i] * r.y;
         v[i] = b[i] * r.x + a[i] * r.y;
       }
-      *reinterpret_cast<uint4 *>(row + pair) = Elems<T>::pack(u);
-      *reinterpret_cast<uint4 *>(row + half + pair) = Elems<T>::pack(v);
+      V::store(row + pair, u);
+      V::store(row + half + pair, v);
     }
+  }
+};
+template <typename T, bool kInterleaved>
+struct Piece<T, kInterleaved, 0> {
+  static constexpr int kPairs = 1;
+  T a, b;
+  __device__ __forceinline__ void load(const T *row, int pair, int half) {
+    a = row[kInterleaved ? 2 * pair : pair];
+    b = row[kInterleaved ? 2 * pair + 1 : half + pair];
+  }
+  __device__ __forceinline__ void turn_store(T *row, int pair, int half, const float2 *cs) const {
+    const float x = to_float(a), y = to_float(b);
+    row[kInterleaved ? 2 * pair : pair] = from_float<T>(x * cs[0].x - y * cs[0].y);
+    row[kInterleaved ? 2 * pair + 1 : half + pair] = from_float<T>(y * cs[0].x + x * cs[0].y);
   }
 };
 
 struct Shape {
-  int unit_bits;    // lanes of a block: pieces of a row, the rest rows
+  int units;        // pieces of a row: as many threads have one row, neighbours the next
   int tokens;       // of a block
   int heads;        // of a block (the key counts as head H)
-  uint32_t magic;   // 2^32 / heads, rounded up
+  int step;         // rows a block takes at a time
+  uint32_t magic, unit_magic;   // 2^32 / heads and / units, rounded up; 0 for one: not used
 };
+// x / by for x by < 2^32
+__device__ __forceinline__ int quotient(int x, int by, uint32_t magic) {
+  return by == 1 ? x : (int)__umulhi((uint32_t)x, magic);
+}
 
 // Block (x: tokens, y: heads); its rows, a token's heads beside one another, go over the lanes in
 // turn.  The cosines and sines of its angles are worked out once, in shared memory, while its
 // first pieces are on their way.
-template <typename T, bool kInterleaved, bool kVector>
+template <typename T, bool kInterleaved, int kB>
 __global__ void __launch_bounds__(kThreads, kSmThreads / kThreads) kda_rope_kernel(const RopeArgs a, const Shape sh) {
-  using P = Piece<T, kInterleaved, kVector>;
+  using P = Piece<T, kInterleaved, kB>;
   extern __shared__ float2 cs[];                         // [tokens][pairs]
   const int half = a.dr / 2, tid = threadIdx.x;
-  const int unit = tid & ((1 << sh.unit_bits) - 1), step = blockDim.x >> sh.unit_bits;
-  const int pair = unit * P::kPairs;
+  const int step = sh.step;
+  int r = quotient(tid, sh.units, sh.unit_magic);
+  const int pair = (tid - r * sh.units) * P::kPairs;
   const int64_t t0 = (int64_t)blockIdx.x * sh.tokens;
   const int nt = (int)min((int64_t)sh.tokens, a.n - t0);
   const int h0 = blockIdx.y * sh.heads, heads = min(sh.heads, a.H + (a.k != nullptr) - h0);
-  const int rows = pair < half ? nt * sh.heads : 0;      // of the last heads some are none
-  int r = tid >> sh.unit_bits;
-  constexpr int G = kGroup<kInterleaved>;
+  const int rows = r < step ? nt * sh.heads : 0;         // of the last heads some are none
+  constexpr int G = kGroup<kInterleaved, kB>;
   P piece[G];
   T *to[G];
   int at[G];                                        // token of the block, -1: none
@@ -177,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, kSmThreads / kThreads) kda_rope_kern
 #pragma unroll
     for (int i = 0; i < G; ++i) {
       at[i] = -1;
-      const int t = sh.heads == 1 ? r : (int)__umulhi((uint32_t)r, sh.magic), h = r - t * sh.heads;
+      const int t = quotient(r, sh.heads, sh.magic), h = r - t * sh.heads;
       if (r < rows && h < heads) {
         const int64_t tok = t0 + t;
         const T *from;
@@ -212,19 +234,17 @@ __global__ void __launch_bounds__(kThreads, kSmThreads / kThreads) kda_rope_kern
   }
 }
 
-template <typename T, bool kInterleaved, bool kVector>
+template <typename T, bool kInterleaved, int kB>
 cudaError_t launch(const RopeArgs &a, cudaStream_t stream) {
-  using P = Piece<T, kInterleaved, kVector>;
+  using P = Piece<T, kInterleaved, kB>;
   const int half = a.dr / 2, units = half / P::kPairs, heads = a.H + (a.k != nullptr);
   const int64_t sms = latent::sm_count() > 0 ? latent::sm_count() : 1;
   Shape sh;
-  sh.unit_bits = 0;
-  while ((1 << sh.unit_bits) < units) ++sh.unit_bits;
+  sh.units = units;
   // Blocks are small, 128 threads, unless a token's heads are more than these have in flight.
-  constexpr int G = kGroup<kInterleaved>;
-  const int threads = (kThreads / 2 >> sh.unit_bits) * G >= heads && units <= kThreads / 2
-                          ? kThreads / 2 : kThreads;
-  const int64_t blocks_sm = kSmThreads / threads, lanes = threads >> sh.unit_bits;  // rows at a time
+  constexpr int G = kGroup<kInterleaved, kB>;
+  const int threads = kThreads / 2 / units * G >= heads ? kThreads / 2 : kThreads;
+  const int64_t blocks_sm = kSmThreads / threads, lanes = threads / units;  // rows at a time
   // A block's rows: what its lanes have in flight, or all heads of a token, whose angles are then
   // worked out once, where tokens are enough to fill the SMs; fewer where SMs would have none.
   int64_t rows = lanes * G;
@@ -238,26 +258,31 @@ cudaError_t launch(const RopeArgs &a, cudaStream_t stream) {
   sh.tokens = (int)(rows / sh.heads);
   if (sh.tokens > kMaxAngles / half) sh.tokens = kMaxAngles / half;
   if (sh.tokens < 1) sh.tokens = 1;
-  sh.magic = (uint32_t)(((1ull << 32) + sh.heads - 1) / sh.heads);   // 0 for one head: not used
+  sh.step = (int)lanes;
+  const auto magic = [](int by) { return (uint32_t)(((1ull << 32) + by - 1) / by); };
+  sh.magic = magic(sh.heads);
+  sh.unit_magic = magic(units);
   const int64_t blocks = (a.n + sh.tokens - 1) / sh.tokens;
   const dim3 grid((unsigned)blocks, (unsigned)((heads + sh.heads - 1) / sh.heads));
-  kda_rope_kernel<T, kInterleaved, kVector>
+  kda_rope_kernel<T, kInterleaved, kB>
       <<<grid, threads, (size_t)sh.tokens * half * sizeof(float2), stream>>>(a, sh);
   return cudaGetLastError();
 }
 
 template <typename T, bool kInterleaved>
 cudaError_t pick(const RopeArgs &a, cudaStream_t stream) {
-  using P = Piece<T, kInterleaved, true>;
-  // 16-byte pieces where every row starts on 16 bytes and has whole ones.
-  constexpr int kV = Elems<T>::kVec;
+  // Pieces of as many bytes as every row starts on and has whole ones of.
+  constexpr int kEsz = sizeof(T);
   uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.out) |
                    reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.k_out);
-  const bool whole = bits % 16 == 0 && (a.dr / 2) % P::kPairs == 0 && a.x_ts % kV == 0 &&
-                     a.x_hs % kV == 0 && a.o_ts % kV == 0 && a.o_hs % kV == 0 &&
-                     a.k_ts % kV == 0 && a.ko_ts % kV == 0;
-  return whole ? launch<T, kInterleaved, true>(a, stream)
-               : launch<T, kInterleaved, false>(a, stream);
+  for (const int64_t v : {a.x_ts, a.x_hs, a.o_ts, a.o_hs, a.k_ts, a.ko_ts,
+                          (int64_t)(kInterleaved ? a.dr : a.dr / 2)})
+    bits |= (uintptr_t)v * kEsz;
+  if (bits % 16 == 0) return launch<T, kInterleaved, 16>(a, stream);
+  if (bits % 8 == 0) return launch<T, kInterleaved, 8>(a, stream);
+  if constexpr (kEsz == 2)
+    if (bits % 4 == 0) return launch<T, kInterleaved, 4>(a, stream);
+  return launch<T, kInterleaved, 0>(a, stream);
 }
 
 }  // namespace

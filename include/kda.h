@@ -772,7 +772,7 @@ int kda_cache_copy_pages(void *cache, const int32_t *src, const int32_t *dst, in
  * An angle is off by at most 2^-24 of a turn whatever the position.
  * out may be x, k_out may be k (in place).  dr even, at most 512.  Alignment: of an
  * element; rows that start on 16 bytes (address and strides) and whose halves, or pairs,
- * fill 16-byte pieces move in these.
+ * fill 16-byte pieces move in these, else in pieces of 8 or 4 bytes or an element's.
  * Errors: KDA_ERR_INVALID_ARG (NULL, sizes, alignment, negative strides, rows of an output
  * that meet, overlap, one of k and k_out), KDA_ERR_UNSUPPORTED (dr above 512, dtype),
  * KDA_ERR_CUDA.

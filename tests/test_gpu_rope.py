@@ -53,6 +53,25 @@ def test_against_64_bits(dtype, interleaved, n, H, dr):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("n,H,dr,off", [(2500, 33, 68, 0), (3000, 40, 20, 0), (700, 16, 126, 0), (40, 3, 510, 2),
+                                        (2000, 96, 72, 4), (1, 200, 12, 0), (900, 17, 64, 2), (20000, 1, 2, 0),
+                                        (5, 7, 200, 1)])
+def test_pieces_of_any_width(dtype, interleaved, n, H, dr, off):
+    """Rows that start on 8, 4 or 2 bytes, and of any number of pieces."""
+    buf, pos, freq = _in((n, H, dr + 2 * off), dtype), _pos((n,), 1 << 20), _freq(dr)
+    before, x = buf.clone(), buf[..., off:off + dr]
+    k = _in((n, dr), dtype, 5)
+    out, k_out = kda.kda_rope(x, pos, freq, k=k, interleaved=interleaved)
+    _check(out, x, pos, freq, interleaved, 1.0, False)
+    _check(k_out, k, pos, freq, interleaved, 1.0, False)
+    kda.kda_rope(x, pos, freq, interleaved=interleaved, out=x)          # in place
+    assert torch.equal(x, out)
+    x.copy_(before[..., off:off + dr])
+    assert torch.equal(buf, before)                                     # nothing around it
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("off", [0, 1, 8])
 def test_views_in_place_and_between_buffers(dtype, off):
     """The rotary channels of wider heads and of cached rows, both parts of one
