@@ -29,13 +29,18 @@ def _code(name, t):
     return code
 
 
-def _like(name, t, x, shape):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not x.dtype:
-        raise TypeError(f"{name} must be a CUDA tensor of {x.dtype}")
-    if t.device != x.device:
-        raise ValueError(f"{name} is on {t.device}, not on {x.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _like(name, t, dtype, device, shape):
+    """A tensor of this dtype and shape on the device, with any strides."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device:
+            return
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype:
+        raise TypeError(f"{name} must be a CUDA tensor of {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _step(name, shape, stride, lead):
@@ -113,7 +118,7 @@ def kda_rope(x, positions, inv_freq, *, k=None, interleaved=True, scale=1.0, tra
     the gradient of the call without it.  ``out`` and ``k_out`` may be views, and x and
     k themselves (in place).  Returns ``out``, with ``k`` ``(out, k_out)``."""
     code = _code("x", x)
-    dev, shape = x.device, x.shape
+    dev, shape, dtype = x.device, x.shape, x.dtype
     raw = _stream(stream, dev)
     _tensor("positions", positions, _I32, None, dev)
     lead, tokens = positions.dim(), positions.shape
@@ -130,9 +135,9 @@ def kda_rope(x, positions, inv_freq, *, k=None, interleaved=True, scale=1.0, tra
     if not math.isfinite(scale):
         raise ValueError(f"scale must be finite, got {scale}")
     if out is None:
-        out = _new(stream, shape, x.dtype, dev)
+        out = _new(stream, shape, dtype, dev)
     else:
-        _like("out", out, x, shape)
+        _like("out", out, dtype, dev, shape)
     x_st, o_st = x.stride(), out.stride()
     x_ts, o_ts = _step("x", shape, x_st, lead), _step("out", shape, o_st, lead)
     x_hs, o_hs = (x_st[-2], o_st[-2]) if heads and H > 1 else (dr, dr)
@@ -140,11 +145,11 @@ def kda_rope(x, positions, inv_freq, *, k=None, interleaved=True, scale=1.0, tra
     k_ts = ko_ts = dr
     if k is not None:
         k_shape = (*tokens, dr)
-        _like("k", k, x, k_shape)
+        _like("k", k, dtype, dev, k_shape)
         if k_out is None:
-            k_out = _new(stream, k_shape, x.dtype, dev)
+            k_out = _new(stream, k_shape, dtype, dev)
         else:
-            _like("k_out", k_out, x, k_shape)
+            _like("k_out", k_out, dtype, dev, k_shape)
             ko_ts = _step("k_out", k_shape, k_out.stride(), lead)
         k_ts = _step("k", k_shape, k.stride(), lead)
         at_k, at_ko = k.data_ptr(), k_out.data_ptr()
@@ -169,7 +174,7 @@ def kda_norm_fwd(x, weight=None, bias=None, *, center=True, eps=1e-5, out=None, 
     Returns ``(out, mean, rstd)``: fp32 ``[*rows]`` for ``kda_norm_bwd``, mean None without
     ``center``, both None without ``stats``."""
     code = _code("x", x)
-    dev, shape = x.device, x.shape
+    dev, shape, dtype = x.device, x.shape, x.dtype
     raw = _stream(stream, dev)
     lead = len(shape) - 1
     if lead < 0:
@@ -185,9 +190,9 @@ def kda_norm_fwd(x, weight=None, bias=None, *, center=True, eps=1e-5, out=None, 
     if not (eps > 0.0 and math.isfinite(eps)):
         raise ValueError(f"eps must be finite and positive, got {eps}")
     if out is None:
-        out, out_rs = _new(stream, shape, x.dtype, dev), W
+        out, out_rs = _new(stream, shape, dtype, dev), W
     else:
-        _like("out", out, x, shape)
+        _like("out", out, dtype, dev, shape)
         out_rs = _step("out", shape, out.stride(), lead)
     mean = _new(stream, rows, _F32, dev) if stats and center else None
     rstd = _new(stream, rows, _F32, dev) if stats else None
@@ -210,7 +215,7 @@ def kda_norm_bwd(d_out, x, weight, mean, rstd, *, bias=False, d_x=None, workspac
     d_bias)``, the sums in fp32, d_weight None without ``weight``, d_bias None without
     ``bias``.  ``d_x`` may be given as a view, and be d_out or x itself."""
     code = _code("x", x)
-    dev, shape = x.device, x.shape
+    dev, shape, dtype = x.device, x.shape, x.dtype
     raw = _stream(stream, dev)
     lead = len(shape) - 1
     if lead < 0:
@@ -218,7 +223,7 @@ def kda_norm_bwd(d_out, x, weight, mean, rstd, *, bias=False, d_x=None, workspac
     W, rows = shape[-1], shape[:-1]
     n = rows[0] if lead == 1 else math.prod(rows)
     x_rs = _step("x", shape, x.stride(), lead)
-    _like("d_out", d_out, x, shape)
+    _like("d_out", d_out, dtype, dev, shape)
     g_rs = _step("d_out", shape, d_out.stride(), lead)
     if weight is not None:
         _tensor("weight", weight, _F32, (W,), dev)
@@ -226,9 +231,9 @@ def kda_norm_bwd(d_out, x, weight, mean, rstd, *, bias=False, d_x=None, workspac
         _tensor("mean", mean, _F32, rows, dev)
     _tensor("rstd", rstd, _F32, rows, dev)
     if d_x is None:
-        d_x, dx_rs = _new(stream, shape, x.dtype, dev), W
+        d_x, dx_rs = _new(stream, shape, dtype, dev), W
     else:
-        _like("d_x", d_x, x, shape)
+        _like("d_x", d_x, dtype, dev, shape)
         dx_rs = _step("d_x", shape, d_x.stride(), lead)
     d_weight = _new(stream, (W,), _F32, dev) if weight is not None else None
     d_bias = _new(stream, (W,), _F32, dev) if bias else None
