@@ -16,13 +16,13 @@
 // so that results do not vary between calls.
 //
 // Rows that start anywhere go through shared memory in 16-byte pieces all the same, put to their
-// places there, and the results back to pieces; their own instructions then bind them (80 % of
-// the issue slots forward).
+// places there, and the results back to pieces; instructions and barriers then bind them (61 and
+// 50 % of the issue slots at 8192 x 7169 bf16).
 //
-// Measured (cold): 16384 x 7168 bf16 forward 75 us (6.3 TB/s), gradient 113 us (6.2); gradient of
+// Measured (cold): 16384 x 7168 bf16 forward 75 us (6.3 TB/s), gradient 110 us (6.4); gradient of
 // 16384 x 512 fp32 22.0 us (4.6), of which the two sums are 4; 64 x 7168 2.9 us; 1 M x 128 bf16
 // 90 us (5.9), 1 M x 64 46 (5.8; with half a warp a row 85).  Anywhere: 8192 x 7169 bf16 65 and
-// 124 us (3.6 and 2.8 TB/s; by single channels 152 and 200), 60000 x 513 45 and 78 (2.7 and 2.4).
+// 121 us (3.6 and 2.9 TB/s; by single channels 192 and 201), 60000 x 513 45 and 78 (2.7 and 2.4).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -300,7 +300,9 @@ constexpr int kSlot = N * E * (int)sizeof(T) + (kAny ? 16 : 0);
 template <typename T, int N, int E, bool kAny>
 constexpr int kFwdStages = stages(kFwdThreads<N, E> / N * kSlot<T, N, E, kAny>, 2 * N *E * 4);
 template <typename T, int N, int E, bool kAny>
-constexpr int kBwdStages = stages(2 * (kBwdThreads / N) * kSlot<T, N, E, kAny>, N *E * 4);
+constexpr int kBwdStages =
+    stages(2 * (kBwdThreads / N) * kSlot<T, N, E, kAny>,
+           kAny && N *E <= kShort ? kRingSpace / 2 + 2048 : N *E * 4);   // (two blocks an SM)
 
 // An fp32 vector [W] into shared memory, laid out as threads read it: [E / 4][N] 16 bytes.
 template <typename T, int N, int E, bool kAny>
@@ -654,19 +656,26 @@ __global__ void __launch_bounds__(kBwdThreads, E * N <= kShort ? 2 : 1) kda_norm
   const T *x_at = static_cast<const T *>(a.x) + row * a.x_rs;
   const T *g_at = static_cast<const T *>(a.d_out) + row * a.do_rs;
   const int64_t x_step = step * a.x_rs, g_step = step * a.do_rs;
+  // The addresses stay at the row itself where they tell how it lies, and where there are few
+  // registers; else they are the next copy's (16384 x 7168 bf16 113.5 -> 110.5 us).
+  constexpr bool kHere = kAny || N * E <= kShort;
   const auto copy = [&](uint32_t to, int ahead) {
     if constexpr (kAny) {
       copy_any<T, N, E>(to, x_at + ahead * x_step, a.W, a.x);
       copy_any<T, N, E>(to + kRowBytes, g_at + ahead * g_step, a.W, a.d_out);
     } else {
-      copy_row<T, N, E>(to, x_at + ahead * x_step, live);
-      copy_row<T, N, E>(to + kRowBytes, g_at + ahead * g_step, live);
+      copy_row<T, N, E>(to, x_at + (kHere ? ahead : 0) * x_step, live);
+      copy_row<T, N, E>(to + kRowBytes, g_at + (kHere ? ahead : 0) * g_step, live);
     }
   };
 #pragma unroll
   for (int i = 0; i < kD; ++i) {
     if (row + i * step < a.n) copy(slot + 2 * i * kRowBytes, i);
     sm100::cp_async_commit();
+    if constexpr (!kHere) {
+      x_at += x_step;
+      g_at += g_step;
+    }
   }
   keep_vector<T, N, E, kAny>(sm100::smem_u32(ring) + kD * 2 * kRowBytes, a.weight, a.W, 1.f);
   __syncthreads();
