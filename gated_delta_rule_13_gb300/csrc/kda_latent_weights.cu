@@ -604,19 +604,19 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
           const int c = 16 * (c0 + 2 * i);
           if (c >= p.cols) continue;
           if (masked) {
-            int tok = (st.rs * kN + c) / p.H, head = st.rs * kN + c - tok * p.H;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              bool see = draft < 0;
-              if (!see && tok < p.T)
-                see = p.mask ? (p.mask[(int64_t)st.b * p.T + tok] >> (draft & 63) & 1) != 0
-                             : draft <= tok;
-              if (!see) x[i][k] = __float_as_uint(-CUDART_INF_F);
-              if (++head == p.H) {
-                head = 0;
-                ++tok;
-              }
+            // a bit a row, a token's rows at a time
+            int tok = (st.rs * kN + c) / p.H, left = (tok + 1) * p.H - (st.rs * kN + c);
+            uint32_t seen = 0;
+#pragma unroll 1
+            for (int k = 0; k < 16 && tok < p.T; k += left, left = p.H, ++tok) {
+              const bool see = draft < 0 || (p.mask ? (p.mask[(int64_t)st.b * p.T + tok] >>
+                                                       (draft & 63) & 1) != 0
+                                                    : draft <= tok);
+              if (see) seen |= (left < 16 ? (1u << left) - 1 : 0xffffu) << k;
             }
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (!(seen >> k & 1)) x[i][k] = __float_as_uint(-CUDART_INF_F);
           }
           const float4 *l4 = reinterpret_cast<const float4 *>(lse + c);
           float part[4] = {0.f, 0.f, 0.f, 0.f};
