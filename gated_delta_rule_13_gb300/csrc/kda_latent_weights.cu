@@ -5,9 +5,11 @@
 //
 // Scores once more, but transposed: S [keys x query rows] = C Q^T, so that a thread of the
 // epilogue has a key, and its sum over the R = T * H query rows is a sum along its own row
-// of the accumulator, in registers, in a fixed order, whatever R is.  No key is touched by
-// two CTAs: nothing is joined and nothing depends on the order of CTAs.  With lse from the
-// decode pass every term is final, and there is no maximum to follow.
+// of the accumulator, in registers, in a fixed order, whatever R is.  With lse from the decode
+// pass every term is final, and there is no maximum to follow.  No key is touched by two CTAs,
+// but where there are few tiles of many query rows: then a tile is cut into ranges of its rows,
+// and who comes last to 32 keys adds the ranges' sums, in their order, so that nothing depends
+// on the order of CTAs.
 //
 // A cached row is 2 W = 1,024 or 1,152 bytes against 2 R W operations: at R = 96 the card's
 // 289 operations a byte leave it bound by HBM, from R = 145 on by the matrix work.  So there
@@ -26,7 +28,9 @@
 // Measured (96 heads): one token of 128 sequences of up to 16384 rows, dr = 64, 1.23 GB, 188 to
 // 200 us cold on several boxes (6.2 to 6.5 TB/s); trees of 16 drafts, 32 sequences, 314 to 338 us
 // (1.6 to 1.7 PFLOP/s, tensor cores 88 % busy, the clock held down by power); one token over
-// 3001 rows, dr = 0, 8.1 us (replayed): start, 230 KB an SM, one tile's way.
+// 3001 rows, dr = 0, 8.1 us (replayed): start, 230 KB an SM, one tile's way.  One tree of 16
+// drafts over 8000 rows 25 us (tiles whole: 35), of 24 over 300 16 us (46), 70 tokens of 128
+// heads over 1000 rows 21 us (131).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -45,6 +49,10 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9, kLseWarp = 10, kKeepWarp = 11;
 constexpr uint32_t kBlock = 16384;       // 128 rows x 64 channels
 constexpr uint32_t kSmem = 232448;
 constexpr int kMaxBlocks = 9, kMostTiles = 0x7fff0000;
+// A pair's tile in several parts, of a range of the query rows each, where there are few tiles.
+constexpr int kMostUnits = 4;            // parts in all, for each pair of the grid
+constexpr int kTileCounts = 8;           // of a tile: parts that have come, for each 32 keys
+constexpr int kUnitKeys = 256;
 
 template <bool kPair>
 constexpr int kKeysLog = kPair ? 8 : 7;  // keys of a tile
@@ -61,8 +69,10 @@ struct Shared {
   uint32_t tmem;
   int abort;
   int seq0, tile0, total;                // the CTA's first sequence and tile; all tiles
+  int parts;                             // of a tile
   DeviceStatus error;
-  // Of a pair: the tiles it takes, one ahead (sequence, -1: no more; tile; length).
+  // Of a pair: the parts of tiles it takes, one ahead (sequence, -1: no more; tile; length; the
+  // part's number among all).
   uint64_t unit_full[2], unit_free[2];
   int4 unit[2];
   uint32_t load_ring, load_kept;         // blocks the loader asked for
@@ -91,7 +101,9 @@ struct Params {
   float lse_hi, lse_lo; // what lse is multiplied by, in two parts
   float *weights;
   DeviceStatus *status;
-  int32_t *taken;       // tiles that pairs have taken beyond their first
+  int32_t *taken;       // parts that pairs have taken beyond their first
+  int32_t *come;        // [tile][kTileCounts]
+  float *part;          // [part][kUnitKeys]
   WaitTest test;
 };
 
@@ -146,8 +158,20 @@ struct OneSteps {
   __device__ bool tile_ends() const { return true; }
   __device__ int number() const { return t - ta; }
 };
+// Into how many parts to cut tiles: in rounds of all pairs, the steps of one and what it takes to
+// start and to end (about two more).  By a warp.
+__device__ __forceinline__ int best_parts(int tiles, int steps, int groups) {
+  const int most = min(steps, kMostUnits * groups / max(tiles, 1));
+  uint32_t least = ~0u;                      // cost, parts
+  for (int s = 1 + (int)(threadIdx.x & 31); s <= most; s += 32) {
+    const int cost = (tiles * s + groups - 1) / groups * ((steps + s - 1) / s + 2);
+    least = min(least, (uint32_t)cost << 12 | (uint32_t)s);
+  }
+  least = __reduce_min_sync(0xffffffffu, least);
+  return most < 2 ? 1 : (int)(least & 4095);
+}
 // The steps of a pair.  Pairs are not equally fast (by 20 % in the same work), so that each takes
-// a tile when it needs one: rank 0 counts them up and tells both CTAs, one ahead.
+// a tile, or a part of one, when it needs it: rank 0 counts them up and tells both CTAs, one ahead.
 struct PairSteps {
   const Params &p;
   Shared<true> &m;
@@ -155,11 +179,12 @@ struct PairSteps {
   const uint32_t rank;
   uint32_t taken = 0;
   int b = 0, n = 0, t = 0, rs = 0;           // current: sequence, its length, tile, row step
+  int r0 = 0, r1 = 0, unit = 0;              // row steps of the part, its number
   __device__ PairSteps(const Params &p_, Shared<true> &m_, const WaitCtx &cx_, uint32_t rank_)
       : p(p_), m(m_), cx(cx_), rank(rank_) {}
   template <bool kLane>                      // by one lane, or by a converged warp
   __device__ bool next() {
-    if (taken > 0 && rs + 1 < p.row_steps) {
+    if (taken > 0 && rs + 1 < r1) {
       ++rs;
       return true;
     }
@@ -175,16 +200,19 @@ struct PairSteps {
       else remote_arrive_relaxed(map_rank(smem_u32(&m.unit_free[s]), 0));
     }
     ++taken;
-    rs = 0;
     b = u.x;
     t = u.y;
     n = u.z;
+    unit = u.w;
+    const int parts = m.parts, part = unit % parts;
+    rs = r0 = part * p.row_steps / parts;
+    r1 = (part + 1) * p.row_steps / parts;
     return more;
   }
-  __device__ bool first() const { return rs == 0; }
-  __device__ bool last() const { return rs + 1 == p.row_steps; }
-  __device__ bool tile_begins() const { return rs == 0; }
-  __device__ bool tile_ends() const { return rs + 1 == p.row_steps; }
+  __device__ bool first() const { return rs == r0; }
+  __device__ bool last() const { return rs + 1 == r1; }
+  __device__ bool tile_begins() const { return first(); }
+  __device__ bool tile_ends() const { return last(); }
   __device__ int number() const { return (int)taken - 1; }
 };
 constexpr int kUnitReaders = 12 + 11;        // loaders, lse, sums of both CTAs, products
@@ -293,13 +321,11 @@ __device__ __forceinline__ void copy_3d(uint32_t dst, const CUtensorMap *map, ui
         : "memory");
 }
 
-// The call's status and the count of tiles are cleared by a kernel of its own, beside which the next one starts.
-__global__ void kda_latent_weights_begin_kernel(DeviceStatus *status, int32_t *taken) {
+// The call's status and counts are cleared by a kernel of its own, beside which the next one starts.
+__global__ void kda_latent_weights_begin_kernel(DeviceStatus *status, int32_t *counts, int32_t n) {
   pdl_launch_dependents();
-  if (threadIdx.x == 0) {
-    set_device_status(status, KDA_OK, 0);
-    *taken = 0;
-  }
+  if (threadIdx.x == 0) set_device_status(status, KDA_OK, 0);
+  for (int i = threadIdx.x; i < n; i += blockDim.x) counts[i] = 0;
 }
 
 template <bool kPair>
@@ -393,7 +419,13 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
         at += k;
       }
     }
-    if (tid == 0) m.total = total;
+    if (warp == 0) {
+      const int parts = kPair ? best_parts(total, p.row_steps, p.groups) : 1;
+      if (lane == 0) {
+        m.total = total;
+        m.parts = parts;
+      }
+    }
   }
   tc_fence_before();
   if constexpr (kPair) cluster_sync_all();  // barriers of both CTAs are ready
@@ -515,11 +547,16 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
           if (lane == 0) x = p.groups + atomicAdd(p.taken, 1);
           x = __shfl_sync(0xffffffffu, x, 0);
         }
-        const int4 u = x < m.total ? finder.find(x) : make_int4(-1, 0, 0, 0);
+        const int parts = m.parts;
+        int4 u = make_int4(-1, 0, 0, 0);
+        if (x / parts < m.total) {
+          u = finder.find(x / parts);
+          u.w = x;
+        }
         if (told > 1) ok = warp_wait<2>(cx, &m.unit_free[s], ((told >> 1) - 1) & 1, 31, (int)told);
         if (ok && lane == 0) {
           st_async_v4(map_rank(smem_u32(&m.unit[s]), 1), (uint32_t)u.x, (uint32_t)u.y, (uint32_t)u.z,
-                      0, map_rank(smem_u32(&m.unit_full[s]), 1));
+                      (uint32_t)u.w, map_rank(smem_u32(&m.unit_full[s]), 1));
           m.unit[s] = u;
           mbar_arrive(&m.unit_full[s]);
         }
@@ -555,6 +592,7 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
     }
   } else if (warp < 8) {
     // ---- sums: thread = key; the warpgroups take 16 of the step's rows in turn
+    if constexpr (kPair) pdl_wait();         // counts have been cleared
     const int wg = warp >> 2, w4 = warp & 3, key = w4 * 32 + lane;
     const uint32_t ts = tm + ((uint32_t)w4 << 21);
     const int chunks = p.cols / 16;
@@ -568,7 +606,7 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
       float *to = p.weights + (int64_t)st.b * p.max_pages * p.page_size + j;
       if (st.tile_begins()) {
         sum = 0.f;
-        if (wg == 0 && p.decay != 0.f && j < st.n) old = *to;
+        if (wg == 0 && p.decay != 0.f && j < st.n && (!kPair || m.parts == 1)) old = *to;
       }
       if (kPair || st.first()) {
         ok = warp_wait<2>(cx, &m.lse_full[item & 1], (item >> 1) & 1, 40, st.t);
@@ -653,9 +691,28 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
       } else {
         ok = warp_wait<2>(cx, &m.part_ready[w4], turn, 43, st.t);
         if (!ok) break;
-        const float all = sum + m.part[key];
+        float all = sum + m.part[key];
         __syncwarp();
         if (lane == 0) mbar_arrive(&m.part_free[w4]);
+        if constexpr (kPair)
+          if (m.parts > 1) {                 // whose part of 32 keys comes last adds all, in order
+            const int parts = m.parts, x = st.unit / parts;
+            float *mine = p.part + (int64_t)x * parts * kUnitKeys + rank * 128 + key;
+            mine[(st.unit - x * parts) * kUnitKeys] = all;
+            __threadfence();
+            __syncwarp();
+            int come = 0;
+            if (lane == 0) come = atomicAdd(&p.come[x * kTileCounts + rank * 4 + w4], 1);
+            come = __shfl_sync(0xffffffffu, come, 0);
+            if (come + 1 < parts) {
+              ++tile;
+              continue;
+            }
+            __threadfence();
+            all = 0.f;
+            for (int k = 0; k < parts; ++k) all += __ldcg(mine + k * kUnitKeys);
+            if (p.decay != 0.f && j < st.n) old = *to;
+          }
         if (j < st.n) *to = p.decay == 0.f ? all : fmaf(old, p.decay, all);
       }
       ++tile;
@@ -733,7 +790,14 @@ int resident_pairs() {
 
 }  // namespace
 
-size_t latent_weights_scratch_bytes(int32_t, int32_t, int32_t, int32_t) { return sizeof(int32_t); }
+// The count of parts taken, and for pairs those of parts that have come, and the parts.
+static int counts_of(bool pair) {
+  return pair ? 4 + kMostUnits / 2 * resident_pairs() * kTileCounts : 1;
+}
+size_t latent_weights_scratch_bytes(int32_t, int32_t T, int32_t H, int32_t) {
+  const bool pair = (int64_t)T * H > 128;
+  return ((size_t)counts_of(pair) + (pair ? kMostUnits * resident_pairs() * kUnitKeys : 0)) * 4;
+}
 
 cudaError_t launch_latent_weights(const LatentWeightsArgs &a, cudaStream_t stream) {
   if (a.B == 0) return cudaMemsetAsync(a.status, 0, sizeof(DeviceStatus), stream);
@@ -768,7 +832,10 @@ cudaError_t launch_latent_weights(const LatentWeightsArgs &a, cudaStream_t strea
   p.lse_hi = (float)lse_by;
   p.lse_lo = (float)(lse_by - p.lse_hi);
   p.decay = a.decay; p.weights = a.weights; p.status = a.status;
+  const int counts = counts_of(pair);
   p.taken = static_cast<int32_t *>(a.scratch);
+  p.come = p.taken + 4;
+  p.part = reinterpret_cast<float *>(p.taken + counts);
   p.test = a.test;
   CUtensorMap mq, mc;
   const cuuint64_t qd[3] = {(cuuint64_t)W, (cuuint64_t)R, (cuuint64_t)a.B};
@@ -780,7 +847,7 @@ cudaError_t launch_latent_weights(const LatentWeightsArgs &a, cudaStream_t strea
   if (!latent::make_bf16_map(&mq, a.q, 3, qd, qs, qb) ||
       !latent::make_bf16_map(&mc, a.cache, 2, cd, cs, cb))
     return cudaErrorInvalidValue;
-  kda_latent_weights_begin_kernel<<<1, 32, 0, stream>>>(a.status, p.taken);
+  kda_latent_weights_begin_kernel<<<1, pair ? 512 : 32, 0, stream>>>(a.status, p.taken, counts);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

@@ -820,8 +820,8 @@ int kda_norm_bwd(const void *d_out, int64_t d_out_row_stride, const void *x, int
                  int dtype, void *d_x, int64_t d_x_row_stride, float *d_weight, float *d_bias,
                  void *workspace, size_t workspace_bytes, void *stream);
 
-/* Workspace of kda_latent_weights: the status word and a counter.  Errors as
- * kda_latent_decode_workspace_size. */
+/* Workspace of kda_latent_weights: the status word and a counter, with T * H above 128 also
+ * counters and sums of parts (about 300 KB).  Errors as kda_latent_decode_workspace_size. */
 int kda_latent_weights_workspace_size(int32_t B, int32_t T, int32_t H, int32_t dc, int32_t dr,
                                       int dtype, size_t *bytes);
 

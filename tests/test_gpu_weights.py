@@ -101,6 +101,23 @@ def test_many_short_sequences(T, H):
     _check(_run(d, lse), d, lse)
 
 
+@pytest.mark.parametrize("decay", [0.0, 0.5])
+@pytest.mark.parametrize("lens,T,H,dr,tree", [
+    ([100], 64, 128, 64, False), ([30, 0, 700], 70, 200, 0, False), ([5000] * 4, 16, 96, 64, True),
+    ([9000, 1, 256], 5, 128, 64, False), ([200] * 50, 3, 100, 0, False), ([64], 64, 5, 64, True)])
+def test_few_tiles_in_parts(lens, T, H, dr, tree, decay):
+    """Keys whose query rows are shared out over pairs, in one round and in several."""
+    d = _data(lens, T, H, dr, 64, tree=tree, spare=1)
+    lse = _lse(d)
+    ws = torch.empty(kda.kda_latent_weights_workspace_size(len(lens), T, H, dr=dr), dtype=torch.uint8,
+                     device=DEV)
+    want = _run(d, lse, decay, workspace=ws)
+    _check(want, d, lse, decay)
+    ws.fill_(255)                             # no call relies on what the last one left
+    for _ in range(3):
+        assert torch.equal(_run(d, lse, decay, workspace=ws), want)
+
+
 def test_sequences_that_share_pages():
     """A prefix held once: the same rows, weights of each sequence's own."""
     d = _data([500, 500, 64], 1, 96, 64, 64)
