@@ -567,8 +567,8 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
       ++told;
     };
     if constexpr (kPair) {
-      pdl_wait();                            // the count has been cleared
       tell();
+      pdl_wait();                            // the count, from the second on, has been cleared
     }
     while (ok && st.template next<false>()) {
       if constexpr (kPair) {
@@ -592,7 +592,6 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
     }
   } else if (warp < 8) {
     // ---- sums: thread = key; the warpgroups take 16 of the step's rows in turn
-    if constexpr (kPair) pdl_wait();         // counts have been cleared
     const int wg = warp >> 2, w4 = warp & 3, key = w4 * 32 + lane;
     const uint32_t ts = tm + ((uint32_t)w4 << 21);
     const int chunks = p.cols / 16;
@@ -700,6 +699,7 @@ __device__ __forceinline__ void weights_body(const CUtensorMap &map_q, const CUt
             float *mine = p.part + (int64_t)x * parts * kUnitKeys + rank * 128 + key;
             mine[(st.unit - x * parts) * kUnitKeys] = all;
             __threadfence();
+            pdl_wait();                      // counts have been cleared
             __syncwarp();
             int come = 0;
             if (lane == 0) come = atomicAdd(&p.come[x * kTileCounts + rank * 4 + w4], 1);
