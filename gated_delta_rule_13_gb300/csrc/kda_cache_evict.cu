@@ -37,7 +37,9 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kKeep = 16384;               // candidates in shared memory
+// Candidates in shared memory: all of a sequence of up to kKeep, of longer ones, whose walks read
+// the weights again, so many that two blocks fit an SM (60000 90 us; one load in flight 163).
+constexpr int kKeep = 49152, kKeepLong = 16384;
 constexpr int kBins = 2048;
 constexpr int kFew = 256;                  // ranked directly
 constexpr int kShort = 4096, kLeast = 4;   // one launch: positions at most, blocks at least
@@ -226,8 +228,17 @@ kda_evict_select_kernel(const CacheEvictArgs a, const int32_t room, const int32_
 #pragma unroll 2
       for (int i0 = s0; i0 < s1; i0 += 32) f(i0 + lane, i0 + lane < s1 ? keys[i0 + lane - lo] : 0);
     } else {
+      constexpr int kAhead = 8;              // in flight
 #pragma unroll 1
-      for (int i0 = s0; i0 < s1; i0 += 32) f(i0 + lane, i0 + lane < s1 ? order_of(w[i0 + lane]) : 0);
+      for (int i0 = s0; i0 < s1; i0 += 32 * kAhead) {
+        float v[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) v[k] = i0 + 32 * k + lane < s1 ? w[i0 + 32 * k + lane] : 0.f;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (i0 + 32 * k < s1)
+            f(i0 + 32 * k + lane, i0 + 32 * k + lane < s1 ? order_of(v[k]) : 0);
+      }
     }
   };
   // Of counts in hist[0 .. bins), the bin of the `left`-th from the top: pick = bin, what is
@@ -443,7 +454,7 @@ cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
   if (all == 0) return cudaSuccess;
   const int64_t cap = (int64_t)a.max_pages * a.page_size;
   const int64_t sms = latent::sm_count() > 0 ? latent::sm_count() : 1;
-  const int32_t room = (int32_t)(cap < kKeep ? cap : kKeep);
+  const int32_t room = (int32_t)(cap <= kKeep ? cap : kKeepLong);
   const int64_t want = 2 * sms / all;      // blocks of a (layer, sequence)
   const int64_t one = sms / all;           // where one of them is on an SM
   if (cap <= kShort && one >= kLeast && a.weights != a.weights_out) {

@@ -104,6 +104,14 @@ def test_one_sequence_shares_its_moves_out():
     _check(_data([3000, 10], 64, W=64), 1100, 0, 1100, layered=False)
 
 
+@pytest.mark.parametrize("lens,budget", [([49000, 30, 20000], 9000), ([60000, 12000], 300), ([49153], 49000)])
+def test_long_sequences(lens, budget):
+    """Candidates that shared memory holds, and more than it does."""
+    d = _data(lens, 64, W=8)
+    _check(d, budget, 3, 100, layered=False)
+    _check(_data(lens, 64, W=8, values=[1.0, 0.5, float("nan")]), budget, 0, 0, True, layered=False)
+
+
 def test_many_sequences():
     _check(_data([20 + i % 50 for i in range(300)], 16, L=2, W=8), 32, 1, 5, in_place=True)
 
