@@ -64,6 +64,7 @@ __device__ __forceinline__ uint32_t order_of(float w) {
 }
 
 constexpr int kMoveThreads = 256;
+constexpr int kLeastPieces = 8;            // blocks of a sequence's moves
 constexpr int kSlots = 9, kColSlots = 5;   // 16-byte pieces in flight per thread: rows, columns
 
 // The moves of a (layer, sequence), shared out over `pieces` blocks of kN threads.
@@ -136,7 +137,11 @@ __device__ __forceinline__ void move_rows(const CacheEvictArgs &a, const int64_t
   }
 
   // ---- some columns of all rows, chunks in order, a chunk read before it is written
-  const int per = (vecs + pieces - 1) / pieces, c0 = piece * per, c1 = min(c0 + per, vecs);
+  // (of few rows of many sequences two pieces, each of half the columns: 384 times 65 rows 33 us,
+  // with eight 44; 1500 rows 338 and 326)
+  const int use = kN == kMoveThreads && pieces == kLeastPieces && m.movers + m.recent < 1024 ? 2 : pieces;
+  if (piece >= use) return;
+  const int per = (vecs + use - 1) / use, c0 = piece * per, c1 = min(c0 + per, vecs);
   for (int cc = c0; cc < c1; cc += kN) {
     const int width = min(c1 - cc, kN), lanes = kN / width;
     const int col = cc + tid % width, r = tid / width;
@@ -163,7 +168,7 @@ __device__ __forceinline__ void move_rows(const CacheEvictArgs &a, const int64_t
 // Where a few sequences are short, one launch: each of `pieces` blocks of a (layer, sequence)
 // selects by itself (they write the same to the lists), and takes its share of the moves.
 template <bool kMove>
-__global__ void __launch_bounds__(kThreads, kMove ? 1 : 2)
+__global__ void __launch_bounds__(kThreads, kMove ? 1 : 3)
 kda_evict_select_kernel(const CacheEvictArgs a, const int32_t room, const int32_t pieces) {
   extern __shared__ uint32_t keys[];       // [room] candidates, as numbers
   __shared__ int hist[kBins], counts[2][kWarps], pick[3], bad, gathered;
@@ -469,7 +474,7 @@ cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
   if (!latent::kernel_ready<kda_evict_select_kernel<false>>(kKeep * 4, 0)) return cudaErrorNotSupported;
   kda_evict_select_kernel<false><<<(unsigned)all, kThreads, (size_t)room * 4, stream>>>(a, room, 1);
   cudaError_t e = cudaGetLastError();
-  const int32_t pieces = (int32_t)(want < 8 ? 8 : want > 64 ? 64 : want);
+  const int32_t pieces = (int32_t)(want < kLeastPieces ? kLeastPieces : want > 64 ? 64 : want);
   for (int64_t lb = 0; lb < all && e == cudaSuccess; lb += 65535) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)pieces, (unsigned)(all - lb < 65535 ? all - lb : 65535));
