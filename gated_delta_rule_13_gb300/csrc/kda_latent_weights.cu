@@ -26,8 +26,8 @@
 // next tile's keys are under way as soon as a block of the last one's is done with.
 //
 // Measured (96 heads): one token of 128 sequences of up to 16384 rows, dr = 64, 1.23 GB, 188 to
-// 200 us cold on several boxes (6.2 to 6.5 TB/s); trees of 16 drafts, 32 sequences, 314 to 338 us
-// (1.6 to 1.7 PFLOP/s, tensor cores 88 % busy, the clock held down by power); one token over
+// 200 us cold on several boxes (6.2 to 6.5 TB/s); trees of 16 drafts, 32 sequences, 310 to 331 us
+// (1.6 to 1.7 PFLOP/s, tensor cores 84 % busy, the clock held down by power); one token over
 // 3001 rows, dr = 0, 8.1 us (replayed): start, 230 KB an SM, one tile's way.  One tree of 16
 // drafts over 8000 rows 25 us (tiles whole: 35), of 24 over 300 16 us (46), 70 tokens of 128
 // heads over 1000 rows 21 us (131).
