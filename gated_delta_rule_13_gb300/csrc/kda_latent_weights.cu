@@ -82,7 +82,7 @@ struct Shared {
     int64_t warp_sum[kThreads / 32];     // at the start
   };
 };
-constexpr uint32_t kSharedBytes = 3072;
+constexpr uint32_t kSharedBytes = 3 * 1024;
 static_assert(sizeof(Shared<false>) <= kSharedBytes, "fits beside the tiles");
 static_assert(sizeof(Shared<true>) <= kSharedBytes, "fits beside the tiles");
 
