@@ -29,10 +29,15 @@ struct View {
   uintptr_t end() const { return begin() + ((n - 1) * ts + (H - 1) * hs + d) * esz; }
 };
 
-// Strides that a row can be found with: no overflow, none negative.
+// What an address reaches, in bytes; larger spans and tensors are refused before 64 bits could
+// not count them.
+constexpr int64_t kReach = (int64_t)1 << 56;
+
+// Strides that a row can be found with: none negative, and all rows of a view within reach.
 bool strides_ok(const View &v) {
-  const int64_t lim = (int64_t)1 << 40;
-  return v.ts >= 0 && v.hs >= 0 && v.ts < lim && v.hs < lim;
+  const int64_t lim = (int64_t)1 << 40, reach = kReach / 16;   // elements; of tokens, of heads
+  return v.ts >= 0 && v.hs >= 0 && v.ts < lim && v.hs < lim && (v.n <= 1 || v.ts <= reach / (v.n - 1)) &&
+         (v.H <= 1 || v.hs <= reach / (v.H - 1));
 }
 // No two rows of a view that is written may meet.
 bool rows_apart(const View &v) {
@@ -267,7 +272,8 @@ int kda_latent_weights(const void *q, const void *cache, const int32_t *block_ta
 }
 
 static int check_evict(int32_t L, int32_t B, int32_t budget) {
-  return L < 1 || B < 0 || budget < 1 || budget > (1 << 30) || (int64_t)L * B > 0x7fffffffLL
+  return L < 1 || B < 0 || budget < 1 || budget > (1 << 30) || (int64_t)L * B > 0x7fffffffLL ||
+                 (int64_t)L * B * budget > kReach / 16      // 12 bytes each in the workspace
              ? KDA_ERR_INVALID_ARG : KDA_OK;
 }
 
@@ -300,8 +306,10 @@ int kda_cache_evict(void *cache, const int32_t *block_table, const int32_t *seq_
       !aligned(origin, 4) || !aligned(status, 4))
     return KDA_ERR_INVALID_ARG;
   const int64_t all = (int64_t)L * B, cap = (int64_t)max_pages * page_size;
+  const int64_t layer = (int64_t)n_pages * page_size * row_bytes;   // at most 2^61
+  if (layer > kReach / L) return KDA_ERR_INVALID_ARG;
   const View vw = flat(weights, all * cap * 4, 1), vwo = flat(weights_out, all * cap * 4, 1);
-  const View outs[] = {flat(cache, (int64_t)L * n_pages * page_size * row_bytes, 1), vwo,
+  const View outs[] = {flat(cache, L * layer, 1), vwo,
                        flat(new_lens, (int64_t)B * 4, 1), flat(origin, all * budget * 4, 1)};
   const View in[] = {flat(block_table, (int64_t)B * max_pages * 4, 1),
                      flat(seq_lens, (int64_t)B * 4, 1), vw};

@@ -172,6 +172,47 @@ def test_evict_refuses(lib, over, code):
     assert _ev(lib, **over) == code
 
 
+FAR = (1 << 31) - 1                          # rows
+
+
+@pytest.mark.parametrize("over", [dict(xts=1 << 39), dict(ots=1 << 39), dict(kts=1 << 39), dict(kots=1 << 39),
+                                  dict(xts=1 << 32), dict(n=2, xts=1 << 62), dict(n=1, H=4, xhs=1 << 61)])
+def test_rope_refuses_views_past_64_bits(lib, over):
+    """Spans of more than 2^63 bytes, which come round to some that meet nothing."""
+    near = dict(n=FAR, xts=192 * 4, ots=64 * 4, kts=64, kots=64)
+    apart = dict(x=1 << 44, out=2 << 44, k=3 << 44, ko=4 << 44, pos=5 << 44, freq=6 << 44)
+    assert _rope(lib, **dict(near, **apart, **over)) == 1
+
+
+@pytest.mark.parametrize("over", [dict(xrs=1 << 39), dict(ors=1 << 39), dict(xrs=1 << 32)])
+def test_norm_refuses_views_past_64_bits(lib, over):
+    apart = dict(n=FAR, x=1 << 44, out=2 << 44, mean=3 << 44, rstd=4 << 44)
+    assert _norm(lib, **dict(apart, **over)) == 1
+
+
+@pytest.mark.parametrize("over", [dict(grs=1 << 39), dict(xrs=1 << 39), dict(dxrs=1 << 39)])
+def test_norm_gradient_refuses_views_past_64_bits(lib, over):
+    apart = dict(n=FAR, g=1 << 44, x=2 << 44, dx=3 << 44, mean=4 << 44, rstd=5 << 44, dw=6 << 44, db=7 << 44)
+    assert _ngrad(lib, **dict(apart, **over)) == 1
+
+
+@pytest.mark.parametrize("over", [
+    dict(L=FAR, B=1, budget=1 << 30, cache=1 << 57, orig=1 << 61),          # the workspace
+    dict(L=1 << 8, n_pages=1 << 20, rb=1 << 30)])                           # the cache
+def test_evict_refuses_tensors_past_64_bits(lib, over):
+    """2^64 bytes are counted as none."""
+    apart = dict(w=1 << 44, wo=2 << 44, wsb=(1 << 64) - 1)
+    assert _ev(lib, **dict(apart, **over)) == 1
+
+
+def test_evict_workspace_past_64_bits(lib):
+    n = ctypes.c_size_t(0)
+    assert lib.kda_cache_evict_workspace_size(24, 16, 2048, ctypes.byref(n)) == 0
+    assert 24 * 16 * 2048 * 12 <= n.value <= 24 * 16 * (2048 * 12 + 64)
+    assert lib.kda_cache_evict_workspace_size(FAR, 1, 1 << 30, ctypes.byref(n)) == 1
+    assert lib.kda_cache_evict_workspace_size(1 << 15, 1 << 15, 1 << 30, ctypes.byref(n)) == 1
+
+
 def test_evict_of_no_sequences_launches_nothing(lib):
     assert _ev(lib, B=0) == 0
 
