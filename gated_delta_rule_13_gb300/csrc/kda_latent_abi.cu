@@ -55,13 +55,15 @@ size_t base_bytes(int32_t n_seqs) { return kStatusBytes + 2 * cu_bytes(n_seqs); 
 // its first to its last element.
 bool strides_ok(int64_t ts, int64_t hs, int32_t H, int64_t n) {
   if (ts % 8 != 0 || hs % 8 != 0 || ts <= 0 || hs <= 0) return false;
+  const int64_t lim = (int64_t)1 << 39;  // tensor-map strides are below 2^40 bytes
+  const int64_t reach = (int64_t)1 << 52;  // elements; of tokens, of heads: 64 bits count no more
+  if (ts >= lim || hs >= lim || (n > 1 && ts > reach / (n - 1)) || (H > 1 && hs > reach / (H - 1)))
+    return false;
   // rows must not overlap one another: heads inside a token or tokens inside a head
   const int64_t d = kda::kLatentD;
   if (H > 1 && hs < d) return false;
   if (n > 1 && ts < d) return false;
-  if (H > 1 && n > 1 && ts < (int64_t)(H - 1) * hs + d && hs < (n - 1) * ts + d) return false;
-  const int64_t lim = (int64_t)1 << 39;  // tensor-map strides are below 2^40 bytes
-  return ts < lim && hs < lim;
+  return !(H > 1 && n > 1 && ts < (int64_t)(H - 1) * hs + d && hs < (n - 1) * ts + d);
 }
 size_t span_bytes(int64_t ts, int64_t hs, int32_t H, int64_t n) {
   return n == 0 ? 0 : (size_t)((n - 1) * ts + (int64_t)(H - 1) * hs + kda::kLatentD) * 2;

@@ -7,7 +7,7 @@ import random
 
 import pytest
 
-from test_latent_host import A, _bwd, lib  # noqa: F401
+from test_latent_host import A, _bwd, _fwd, lib  # noqa: F401
 
 REFUSED, TAKEN = 1, 3
 
@@ -61,3 +61,20 @@ def test_against_every_pair_of_rows(lib):  # noqa: F811
         seen[want] += 1
         assert _views(lib, offset, ts, hs, n, H) == want, (offset, ts, hs, n, H)
     assert min(seen.values()) > 50
+
+
+# Spans of 2^64 bytes and more, which come round to some that meet nothing; ws=None: a call
+# that is not refused for its views is refused for its missing workspace.
+FAR = dict(nk=(1 << 31) - 256, H=1, ws=None, k=1 << 44, v=2 << 44, r=3 << 44, gk=5 << 44, gv=6 << 44,
+           gr=7 << 44)
+
+
+@pytest.mark.parametrize("over", [dict(kts=1 << 38), dict(vts=1 << 38), dict(vts=1 << 33)])
+def test_views_past_64_bits(lib, over):  # noqa: F811
+    assert _fwd(lib, **dict(FAR, **over)) == REFUSED
+    assert _bwd(lib, **dict(FAR, **over)) == REFUSED
+
+
+@pytest.mark.parametrize("over", [dict(gkts=1 << 38), dict(gvts=1 << 38), dict(gkts=1 << 38, gvts=1 << 38)])
+def test_gradient_views_past_64_bits(lib, over):  # noqa: F811
+    assert _bwd(lib, **dict(FAR, **over)) == REFUSED
