@@ -22,6 +22,7 @@
 // bound by instructions: 16384 x 16 of 74 channels bf16 40 us, of 72 in halves 19.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <math_constants.h>
 
 #include "kda_latent_tc.cuh"
 #include "kda_rows.h"
@@ -35,9 +36,14 @@ template <bool kInterleaved, int kB>
 constexpr int kGroup = kInterleaved || kB < 16 ? 6 : 3;
 constexpr int kMaxAngles = 2048;   // of a block
 
-// Turns per position, 2^64 to the turn and modulo a turn, of an angle per position in radians,
-// |f| < 2^118: the significand times 2^130 / (2 pi), shifted by what the exponent leaves.  In
-// integers, because the 64-bit floating-point pipe is narrow here: off by one at most.
+// Whether a frequency has an angle here: a number of magnitude below 2^64, up to which turns_of
+// has all its bits.
+__device__ __forceinline__ bool has_angle(double f) {
+  return ((uint64_t)__double_as_longlong(f) >> 52 & 2047) < 1023 + 64;
+}
+// Turns per position, 2^64 to the turn and modulo a turn, of such an angle per position in radians:
+// the significand times 2^130 / (2 pi), shifted by what the exponent leaves.  In integers, because
+// the 64-bit floating-point pipe is narrow here: off by two at most.
 __device__ __forceinline__ uint64_t turns_of(double f) {
   constexpr uint64_t kHi = 0xa2f9836e4e441529ull, kLo = 0xfc2757d1f534ddc1ull;  // 2^130 / (2 pi)
   const uint64_t bits = (uint64_t)__double_as_longlong(f);
@@ -48,7 +54,7 @@ __device__ __forceinline__ uint64_t turns_of(double f) {
   w1 += mid;
   w2 += w1 < mid;
   const int shift = 1141 - exponent, bit = shift & 63;
-  if (shift < 0 || shift >= 192) return 0;
+  if (shift >= 192) return 0;
   const uint64_t lo = shift < 64 ? w0 : shift < 128 ? w1 : w2;
   const uint64_t hi = shift < 64 ? w1 : shift < 128 ? w2 : 0;
   const uint64_t t = bit ? lo >> bit | hi << (64 - bit) : lo;
@@ -219,9 +225,10 @@ __global__ void __launch_bounds__(kThreads, kSmThreads / kThreads) kda_rope_kern
   load();
   for (int i = tid; i < nt * half; i += blockDim.x) {
     const int tok = i / half, p = i - tok * half;
-    const uint64_t turns = (uint64_t)(int64_t)a.positions[t0 + tok] * turns_of(a.inv_freq[p]);
+    const double freq = a.inv_freq[p];
+    const uint64_t turns = (uint64_t)(int64_t)a.positions[t0 + tok] * turns_of(freq);
     float s, c;
-    sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);
+    sincospif(has_angle(freq) ? (float)(int32_t)(turns >> 32) * 0x1p-31f : CUDART_NAN_F, &s, &c);
     cs[i] = make_float2(c * a.scale, (a.transpose ? -s : s) * a.scale);
   }
   __syncthreads();

@@ -136,6 +136,48 @@ def test_the_farthest_positions():
     assert ((got.double() - want).abs() <= ru.rope_bound(x, True, 1.0, F32, want)).all()
 
 
+def _turned_exactly(x, pos, freq):
+    """x [n, 2 m] of neighbouring pairs, by fractions of a turn of integers."""
+    from fractions import Fraction
+    inv = Fraction(0x28be60db9391054a7f09d5f47d4d377036d8a5664f10e4107f9458eaf7ae, 2 ** 240)    # 1 / (2 pi)
+    turns = torch.tensor([[float(Fraction(f) * inv * p % 1) for f in freq.tolist()] for p in pos.tolist()],
+                         dtype=torch.float64, device=DEV)
+    c, s = torch.cos(2 * torch.pi * turns), torch.sin(2 * torch.pi * turns)
+    a, b = x[..., 0::2].double(), x[..., 1::2].double()
+    return torch.stack([a * c - b * s, b * c + a * s], -1).flatten(-2)
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_frequencies_that_have_no_angle(dtype, interleaved):
+    """No number, infinite or of 2^64 and more: no number in their pairs, others as without."""
+    freq = _freq(64)
+    bad = freq.clone()
+    none = {0: float("nan"), 3: float("inf"), 8: float("-inf"), 13: 2.0 ** 64, 14: -2.0 ** 118, 31: 1.5e308}
+    for i, f in none.items():
+        bad[i] = f
+    x, pos = _in((7, 3, 64), dtype), _pos((7,), 1000)
+    pos[2] = 0
+    want, got = (kda.kda_rope(x, pos, f, interleaved=interleaved) for f in (freq, bad))
+    for i in range(32):
+        for ch in ((2 * i, 2 * i + 1) if interleaved else (i, i + 32)):
+            if i in none:
+                assert got[..., ch].isnan().all(), i
+            else:
+                assert torch.equal(got[..., ch], want[..., ch]), i
+
+
+def test_frequencies_of_any_magnitude():
+    """Up to 2^64 radians a position the angle is right, whatever the position."""
+    freq = torch.tensor([2.0 ** -1070, 1e-300, 3e-20, 2.0 ** -40, 0.7, -0.7, 123.456, 1e6 / 3, 2.0 ** 40 + 0.25,
+                         -1.7e15, 1.9 * 2.0 ** 62, -1.99999 * 2.0 ** 63], dtype=torch.float64, device=DEV)
+    pos = torch.tensor([0, 1, -1, 77, 2 ** 31 - 1, -2 ** 31, 123456789], dtype=torch.int32, device=DEV)
+    x = _in((7, 24), F32)
+    want = _turned_exactly(x, pos, freq)
+    got = kda.kda_rope(x, pos, freq)
+    assert ((got.double() - want).abs() <= ru.rope_bound(x, True, 1.0, F32, want)).all()
+
+
 @pytest.mark.parametrize("interleaved", [True, False])
 def test_tokens_past_two_to_the_31_elements(interleaved):
     far, n, H, dr = (1 << 31) + 64, 3, 5, 64
