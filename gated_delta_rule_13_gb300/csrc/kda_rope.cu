@@ -9,14 +9,16 @@
 // frequency is held as turns per position in 64-bit fixed point, 2^-64 of a turn: the
 // product with an integer position, modulo 2^64, is the fraction of a turn itself, by one
 // integer multiplication and without a reduction.  The frequency's own rounding, 2^-64,
-// grows by the position to at most 2^-33 of a turn.  The upper 32 bits as a signed number
-// give t / pi in [-1, 1).
+// grows by the position to at most 2^-32 of a turn.  The upper 32 bits as a signed number
+// give t / pi in [-1, 1), all of them: 24 go to sine and cosine, the others are added to what
+// these give (rounded to 24 bits an angle near half a turn was off by 9e-8, and a sine of
+// 1e-3 by 1e-4 of itself).
 //
 // Bound by HBM: a rotated channel is read and written once, 3 operations each.  96 bytes in
 // flight a thread and 1024 threads an SM (64 and 128 bytes, 1280 threads: up to 10 % slower),
 // rows of all heads of a token in one block so that its angles are worked out once.  Measured
-// (cold inputs): 8192 tokens x 96 heads x 64 channels fp32, 403 MB both ways, 60.8 us, 6.6 TB/s;
-// 16384 x 16 bf16 with the shared key, 71 MB, 16.0 us, of which a launch and one block's way are
+// (cold inputs): 8192 tokens x 96 heads x 64 channels fp32, 403 MB both ways, 61.7 us, 6.5 TB/s;
+// 16384 x 16 bf16 with the shared key, 71 MB, 16.1 us, of which a launch and one block's way are
 // 2.5 (a plain copy of as many bytes: 12.5); 64 x 96 with the key 2.6 us.  Loads and stores
 // past the caches made no difference.  Rows that start on 8, 4 or 2 bytes go in pieces of these,
 // bound by instructions: 16384 x 16 of 74 channels bf16 40 us, of 72 in halves 19.
@@ -228,8 +230,12 @@ __global__ void __launch_bounds__(kThreads, kSmThreads / kThreads) kda_rope_kern
     const double freq = a.inv_freq[p];
     const uint64_t turns = (uint64_t)(int64_t)a.positions[t0 + tok] * turns_of(freq);
     float s, c;
-    sincospif(has_angle(freq) ? (float)(int32_t)(turns >> 32) * 0x1p-31f : CUDART_NAN_F, &s, &c);
-    cs[i] = make_float2(c * a.scale, (a.transpose ? -s : s) * a.scale);
+    // what fp32 holds of t / pi exactly, 24 bits of 32, and the rest d, below 2^-21: the sine of
+    // the sum is s + c d, its cosine c - s d, but for d^2 / 2
+    const uint32_t top = (uint32_t)(turns >> 32), low = top & 255;
+    sincospif(has_angle(freq) ? (float)(int32_t)(top - low) * 0x1p-31f : CUDART_NAN_F, &s, &c);
+    const float d = (float)low * (CUDART_PI_F * 0x1p-31f), u = fmaf(c, d, s), v = fmaf(-s, d, c);
+    cs[i] = make_float2(v * a.scale, (a.transpose ? -u : u) * a.scale);
   }
   __syncthreads();
   for (;;) {

@@ -770,7 +770,7 @@ int kda_cache_copy_pages(void *cache, const int32_t *src, const int32_t *dst, in
  *   inv_freq   [dr / 2] fp64, DEVICE: angle per position; scaling for longer contexts
  *              goes into these and into scale (finite).  One that is no number, or whose
  *              magnitude is 2^64 or more, makes no number of its pairs and no others.
- * An angle is off by at most 2^-24 of a turn whatever the position.
+ * An angle is off by at most 2^-31 of a turn whatever the position.
  * out may be x, k_out may be k (in place).  dr even, at most 512.  Alignment: of an
  * element; rows that start on 16 bytes (address and strides) and whose halves, or pairs,
  * fill 16-byte pieces move in these, else in pieces of 8 or 4 bytes or an element's.

@@ -251,3 +251,22 @@ def test_refusals():
             kda.kda_rope(wide[..., :64], pos, freq, out=bad)
     with pytest.raises(kda.KDAError):
         kda.kda_rope(x, pos, freq, out=x[:1, :1].expand(8, 4, 64))
+
+
+def test_small_sines_keep_their_digits():
+    """Positions that come to within 2^-10 of half a turn and of whole ones: an angle in fp32
+    would be off by 2^-25 of half a turn there, 9e-8.  Of 32 bits and the ones below it is off
+    by at most 2^-32 of a turn, and the frequency's share; a small sine rounds by little: four
+    times by half a step, and CUDA's own 2 steps, 8 u of itself."""
+    pos = torch.arange(-(1 << 20), 1 << 20, dtype=torch.int32, device=DEV)
+    sine = torch.sin(pos.double())
+    pos = pos[sine.abs() < 2.0 ** -10]
+    assert len(pos) > 1000
+    sine, x = torch.sin(pos.double()), torch.zeros(len(pos), 2, device=DEV)
+    x[:, 0] = 1.0
+    freq = torch.ones(1, dtype=torch.float64, device=DEV)
+    tol = 2 * torch.pi * 2.0 ** -31 + 8 * ru.U * sine.abs()
+    for transpose in (False, True):
+        got = kda.kda_rope(x, pos, freq, transpose=transpose)
+        err = (got[:, 1].double() - (-sine if transpose else sine)).abs()
+        assert (err <= tol).all(), f"worst {(err / tol).max().item():.3g} of the bound"
