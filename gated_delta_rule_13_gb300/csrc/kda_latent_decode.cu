@@ -100,7 +100,8 @@ struct Params {
   int32_t warps;        // 32-row groups in use
   int32_t stages[2];    // of either rank
   int32_t rope_slots;   // of rank 0
-  float scale2;         // scale * log2(e)
+  float scale2;         // scale * log2(e), see launch_latent_decode
+  float ln_hi, ln_lo;   // a logarithm by that scale to the natural one, in two parts
   __nv_bfloat16 *out;
   float *lse;
   DeviceStatus *status;
@@ -110,6 +111,10 @@ struct Params {
   float *part_ml;       // [row tiles][G][2][2][128]
   WaitTest test;
 };
+
+__device__ __forceinline__ float natural(const Params &p, float x) {
+  return fmaf(x, p.ln_hi, x * p.ln_lo);
+}
 
 // Length of sequence b, 0 when it is out of range.
 __device__ __forceinline__ int seq_len(const Params &p, int b) {
@@ -632,7 +637,7 @@ kda_latent_decode_kernel(const __grid_constant__ CUtensorMap map_q,
       if (rank == 0) {
         if (whole) {
           if (p.lse && row < p.R)
-            p.lse[out_row] = l == 0.f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
+            p.lse[out_row] = l == 0.f ? -CUDART_INF_F : natural(p, ref + log2f(l));
         } else {
           p.part_ml[slot * 2 * kRows + r] = ref;
           p.part_ml[slot * 2 * kRows + kRows + r] = l;
@@ -801,7 +806,7 @@ kda_latent_join_kernel(const Params p) {
     to[0] = make_uint4(w[0], w[1], w[2], w[3]);
     to[1] = make_uint4(w[4], w[5], w[6], w[7]);
     if (p.lse && ch == 0)
-      p.lse[out_row] = l == 0.f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
+      p.lse[out_row] = l == 0.f ? -CUDART_INF_F : natural(p, ref + log2f(l));
     return;
   }
   __shared__ float s_o[kJoinWarps][kJoinCh][32], s_ref[kJoinWarps][32], s_l[kJoinWarps][32];
@@ -831,7 +836,7 @@ kda_latent_join_kernel(const Params p) {
   *reinterpret_cast<uint32_t *>(p.out + out_row * kLatentC + ch + 2 * warp) =
       pack_bf16x2(u * inv, v * inv);
   if (p.lse && ch == 0 && warp == 0)
-    p.lse[out_row] = l == 0.f ? -CUDART_INF_F : (ref + log2f(l)) * kLn2;
+    p.lse[out_row] = l == 0.f ? -CUDART_INF_F : natural(p, ref + log2f(l));
 }
 
 // Pairs of CTAs the device runs at once (0 without a device).
@@ -922,7 +927,14 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs &a, cudaStream_t stream)
     if (n > kMaxStages) n = kMaxStages;
   p.rope_slots = a.dr ? (int)((space0 - p.stages[0] * kStage) / kBlock) : 1;
   if (p.rope_slots > kMaxStages) p.rope_slots = kMaxStages;
-  p.scale2 = a.scale * kLog2e;
+  // Scores are made up for what the tensor cores cut off of their two parts: lse was 5e-6 too small
+  // at scores of 24, and the probabilities that kda_latent_weights takes from it, whose scores are
+  // one sum, by as much too large.  The scale's rounding is taken back from lse.
+  const double more = latent::cut_off(W, 2);
+  p.scale2 = (float)(a.scale * 1.4426950408889634 * more);
+  const double ln = p.scale2 > 1e-30f && p.scale2 < 1e30f ? a.scale * more / p.scale2 : 0.6931471805599453;
+  p.ln_hi = (float)ln;
+  p.ln_lo = (float)(ln - p.ln_hi);
   p.out = static_cast<__nv_bfloat16 *>(a.out); p.lse = a.lse; p.status = a.status;
   unsigned char *ws = static_cast<unsigned char *>(a.scratch);
   p.joins = reinterpret_cast<int4 *>(ws);

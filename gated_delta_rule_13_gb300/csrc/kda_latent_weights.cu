@@ -821,12 +821,10 @@ cudaError_t launch_latent_weights(const LatentWeightsArgs &a, cudaStream_t strea
   const int most = pair ? kMaxSlots<true> : kMaxSlots<false>;
   if (p.slots > most) p.slots = most;
   p.groups = pair ? resident_pairs() : sm_count();
-  // The tensor cores cut their sums off: each of W / 16 steps loses half a unit in the last place
-  // on average, of a partial sum that on average is about half the whole.  Scores come out 7 to 10
-  // times 2^-24 of themselves too near to zero (measured, 32 and 36 steps), which the scale makes
-  // up for.  And lse is taken times what the rounded scale stands for, so that the rounding
-  // cancels in the exponent: against 64 bits a short sequence's weights went from 1.5e-6 to 3e-7.
-  const double more = 1.0 + W / 16 * 0x1p-26;
+  // Scores are made up for what is cut off of them, and lse is taken times what the rounded scale
+  // stands for, so that the rounding cancels in the exponent: with an lse of 64 bits a short
+  // sequence's weights went from 1.5e-6 to 3e-7.
+  const double more = latent::cut_off(W, 1);
   p.scale2 = (float)(a.scale * 1.4426950408889634 * more);
   const double lse_by = p.scale2 > 1e-30f && p.scale2 < 1e30f ? p.scale2 / (a.scale * more) : 1.4426950408889634;
   p.lse_hi = (float)lse_by;

@@ -163,6 +163,39 @@ def test_a_row_of_probabilities_sums_to_one(T, H):
     assert ((got.double().sum(1) - rows).abs() <= 2 * REL * rows).all()
 
 
+@pytest.mark.parametrize("H", [96, 200])
+@pytest.mark.parametrize("dr", [0, 64])
+def test_cut_off_sums_are_made_up_for(H, dr):
+    """Scores of deviation 6, against 64 bits, by the mean over heads: a score that comes out
+    too near to zero by a part c of itself takes c times the mean score from lse, and from the
+    weights by an exact lse.  The tensor cores' c is about W / 16 steps x 2^-26, in decode, which
+    adds two halves of the channels, half as much.  A call makes up for it but for a quarter
+    (measured over operands 7 to 10 units of 2^-24 where the steps give 8 and 9).  A head's lse,
+    of about 22, is rounded in steps of 2^-18 (as a logarithm to the base 2) and 2^-19, each
+    off by a third of a step in the mean square, and with its sum's roundings by no more than
+    1.5e-6; the mean of H of them by six times that over sqrt H at most.  A factor left out, or
+    one taken for the other, is off by the whole or the half."""
+    n, W = 3000, 512 + dr
+    d = _data([n], 1, H, dr, 64, seed=11)
+    d["scale"] = 6.0 / W ** 0.5
+    scale = float(torch.tensor(d["scale"], dtype=F32))            # as the call has it
+    s = d["q"][0, 0].double() @ ru.rows_of(d["cache"], d["table"], 0, n).double().T * scale
+    exact = torch.logsumexp(s, -1)
+    cut = W / 16 * 2.0 ** -26 * (torch.exp(s - exact[:, None]) * s).sum(-1).mean().item()
+    rounded = 6 * 1.5e-6 / H ** 0.5
+    assert cut > 6 * rounded
+    lse = torch.empty(1, 1, H, device=DEV)
+    kda.kda_latent_decode(d["q"], d["cache"], d["table"], d["seq_lens"], scale=scale, lse=lse)
+    off = (lse[0, 0].double() - exact).mean().item()
+    assert abs(off) <= cut / 8 + rounded, f"lse {off:.3g} of {cut:.3g}"
+    d["old"].zero_()
+    for lse, more in ((exact.float()[None, None], 0.0), (lse, cut / 8 + rounded)):
+        given = torch.exp(exact - lse[0, 0].double()).sum().item()  # by this lse, rounded as it is
+        total = _run(d, lse, scale=scale)[0, :n].double().sum().item()
+        assert abs(total - given) / H <= cut / 4 + rounded / 3, f"{(total - given) / H:.3g} of {cut:.3g}"
+        assert abs(total / H - 1) <= cut / 4 + more + rounded
+
+
 def test_tokens_left_out():
     """A draft of lse +inf gives nothing, whatever the others do; so does one of -inf."""
     d = _data([400, 90], 6, 16, 64, 64, tree=True)
