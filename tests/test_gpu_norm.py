@@ -235,6 +235,45 @@ def test_many_rows_and_the_same_bits(n, W, dtype):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("W,gap", [(8, 0), (16, 0), (32, 0), (40, 0), (48, 0), (64, 0), (25, 0), (31, 1), (55, 2)])
+def test_short_rows_many_for_each_group(dtype, W, gap):
+    """Four or eight threads a row, every group with more rows than it copies ahead (four): on
+    16 bytes and anywhere."""
+    group = 4 if W <= 32 else 8
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    # of the forward 1024 threads an SM, of the gradient 4 blocks of 512
+    n = 6 * sms * (4 * 512 // group) + 1
+    x, g = _in((n, W + gap), dtype, 1, 1.2, 0.1)[:, :W], _in((n, W + gap), dtype, 2)[:, :W]
+    w, b = _vec(W, 3, 1.0), _vec(W, 4)
+    got = kda.kda_norm_fwd(x, w, b)
+    _check_fwd(got, x, w, b, True, 1e-5)
+    back = kda.kda_norm_bwd(g, x, w, got[1], got[2], bias=True)
+    _check_bwd(back, g, x, w, got[1], got[2])
+    again = kda.kda_norm_bwd(g, x, w, got[1], got[2], bias=True)
+    assert all(torch.equal(u, v) for u, v in zip(back, again))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("center", [False, True])
+@pytest.mark.parametrize("n,W", [(1, 8), (400001, 8), (500003, 32), (500003, 27), (300007, 64), (300007, 61), (160001, 128),
+                                 (160001, 100), (100003, 256), (50001, 512), (40001, 1000), (20001, 1025),
+                                 (9001, 4096), (4001, 7169), (3001, 16384)])
+def test_sums_over_rows_lose_no_row(n, W, center, dtype):
+    """Rows of whole numbers a whole mean apart, of deviation 1: z is -1 or 1 and the gradient
+    a small whole number, so that every partial sum, below 3 n < 2^24, is exact in fp32 and a
+    row left out or taken twice shows."""
+    gen = torch.Generator(device=DEV).manual_seed(7)
+    z = torch.randint(0, 2, (n, W), generator=gen, device=DEV, dtype=torch.int32) * 2 - 1
+    g = torch.randint(-3, 4, (n, W), generator=gen, device=DEV, dtype=torch.int32)
+    m = torch.randint(-9, 10, (n, 1), generator=gen, device=DEV, dtype=torch.int32) if center else 0
+    mean = m[:, 0].to(F32) if center else None
+    one = torch.ones(n, dtype=F32, device=DEV)
+    _, d_w, d_b = kda.kda_norm_bwd(g.to(dtype), (z + m).to(dtype), _vec(W, 3, 1.0), mean, one, bias=True)
+    assert torch.equal(d_w, (g * z).sum(0).to(F32))
+    assert torch.equal(d_b, g.sum(0).to(F32))
+
+
 def test_gradient_against_differences():
     """f = <g, y>: f(x + h v) - f(x - h v) is the gradient along the step, but for the
     bounds of the values, those of the gradient, and what a central difference leaves, which
