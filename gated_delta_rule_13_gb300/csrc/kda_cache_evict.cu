@@ -25,7 +25,11 @@
 // selection is 19 (latency: a dozen dependent steps) and the moves 110 (638 MB both ways, 5.8
 // TB/s, rows of 1,152 bytes at random places; 95 at a plain copy's rate).  Fewer bytes in flight
 // than 144 a thread, or more threads with less, took 133 to 184 us in all.  One row of each of 16
-// requests of 2049, one launch: 7.5 us (two: 9.3).
+// requests of 2049 (a table of 2112 places): 7.8 us in one launch, 7.9 in place, which takes two.
+//
+// A call writes every place of the weights, so that it costs by the table's capacity too, the zeros
+// of a sequence being one block's: the same row with 16 K places 8.9 us in place (10.9 to another
+// buffer), with 128 K 16 (18); of 24 layers of these requests, in place, 28, 32 and 66.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -37,12 +41,14 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-// Candidates in shared memory: all of a sequence of up to kKeep, of longer ones, whose walks read
-// the weights again, so many that two blocks fit an SM (60000 90 us; one load in flight 163).
+// Candidates in shared memory, by the table's capacity, which is what the host knows: of up to
+// kKeep places room for all; of more so many that three blocks fit an SM, and a sequence with more
+// candidates than these reads its weights again in every walk, also where SMs have one block each
+// (60000 rows to 8000 80 to 90 us, one load in flight 163; 20000 rows in place 30).
 constexpr int kKeep = 49152, kKeepLong = 16384;
 constexpr int kBins = 2048;
 constexpr int kFew = 256;                  // ranked directly
-constexpr int kShort = 4096, kLeast = 4;   // one launch: positions at most, blocks at least
+constexpr int kShort = 4096, kLeast = 4;   // one launch: places of the table at most, blocks at least
 static_assert(kBins % kThreads == 0 && kBins <= 4 * kThreads, "a thread has four bins at most");
 
 // Scratch of a (layer, sequence): what to move, then as many numbers as the budget each of
@@ -138,7 +144,7 @@ __device__ __forceinline__ void move_rows(const CacheEvictArgs &a, const int64_t
 
   // ---- some columns of all rows, chunks in order, a chunk read before it is written
   // (of few rows of many sequences two pieces, each of half the columns: 384 times 65 rows 33 us,
-  // with eight 44; 1500 rows 338 and 326)
+  // with eight 44; 1500 rows 338 and 326.  Where between these the two meet has not been measured.)
   const int use = kN == kMoveThreads && pieces == kLeastPieces && m.movers + m.recent < 1024 ? 2 : pieces;
   if (piece >= use) return;
   const int per = (vecs + use - 1) / use, c0 = piece * per, c1 = min(c0 + per, vecs);
@@ -165,8 +171,9 @@ __device__ __forceinline__ void move_rows(const CacheEvictArgs &a, const int64_t
   }
 }
 
-// Where a few sequences are short, one launch: each of `pieces` blocks of a (layer, sequence)
-// selects by itself (they write the same to the lists), and takes its share of the moves.
+// Where sequences are few, their table is short and the weights go to another buffer, one launch:
+// each of `pieces` blocks of a (layer, sequence) selects by itself (they write the same to the
+// lists, and in place would write what the others read), and takes its share of the moves.
 template <bool kMove>
 __global__ void __launch_bounds__(kThreads, kMove ? 1 : 3)
 kda_evict_select_kernel(const CacheEvictArgs a, const int32_t room, const int32_t pieces) {

@@ -9,7 +9,8 @@
 // pass every term is final, and there is no maximum to follow.  No key is touched by two CTAs,
 // but where there are few tiles of many query rows: then a tile is cut into ranges of its rows,
 // and who comes last to 32 keys adds the ranges' sums, in their order, so that nothing depends
-// on the order of CTAs.
+// on the order of CTAs.  Into how many ranges goes by the tiles of the whole call, so that the
+// last bits of a sequence depend on what else the call holds.
 //
 // A cached row is 2 W = 1,024 or 1,152 bytes against 2 R W operations: at R = 96 the card's
 // 289 operations a byte leave it bound by HBM, from R = 145 on by the matrix work.  So there
@@ -26,7 +27,7 @@
 // next tile's keys are under way as soon as a block of the last one's is done with.
 //
 // Measured (96 heads): one token of 128 sequences of up to 16384 rows, dr = 64, 1.23 GB, 188 to
-// 200 us cold on several boxes (6.2 to 6.5 TB/s); trees of 16 drafts, 32 sequences, 310 to 331 us
+// 209 us cold on several boxes (5.9 to 6.5 TB/s); trees of 16 drafts, 32 sequences, 310 to 331 us
 // (1.6 to 1.7 PFLOP/s, tensor cores 84 % busy, the clock held down by power); one token over
 // 3001 rows, dr = 0, 8.1 us (replayed): start, 230 KB an SM, one tile's way.  One tree of 16
 // drafts over 8000 rows 25 us (tiles whole: 35), of 24 over 300 16 us (46), 70 tokens of 128

@@ -9,7 +9,7 @@
 // Bound by HBM: two passes of bytes forward, three back.  A row is read once: by four to 512
 // threads, into registers (few rows) or, many rows, some rows ahead into shared memory.
 // The variance is the mean square of what the mean leaves, from the row on chip, so that a mean
-// far from zero costs no digits.  Statistics and sums are fp32; values are taken in pairs, which
+// far from zero costs no more digits than its own rounding.  Statistics and sums are fp32; values are taken in pairs, which
 // halves the instructions (with one at a time the gradient of 16384 x 7168 was bound by them:
 // 167 us).  The gradient's blocks walk over the rows with the sums of dw and db in registers and
 // leave one pair of rows each in the workspace; a second kernel adds these in the blocks' order,
@@ -19,8 +19,8 @@
 // places there, and the results back to pieces; instructions and barriers then bind them (61 and
 // 50 % of the issue slots at 8192 x 7169 bf16).
 //
-// Measured (cold): 16384 x 7168 bf16 forward 75 us (6.3 TB/s), gradient 110 us (6.4); gradient of
-// 16384 x 512 fp32 22.0 us (4.6), of which the two sums are 4; 64 x 7168 2.9 us; 1 M x 128 bf16
+// Measured (cold): 16384 x 7168 bf16 forward 76 us (6.2 TB/s), gradient 110 us (6.4); gradient of
+// 16384 x 512 fp32 21.6 us (4.6), of which the two sums are 4; 64 x 7168 2.9 us; 1 M x 128 bf16
 // 90 us (5.9), 1 M x 64 46 (5.8; with half a warp a row 85).  Anywhere: 8192 x 7169 bf16 65 and
 // 121 us (3.6 and 2.9 TB/s; by single channels 192 and 201), 60000 x 513 45 and 78 (2.7 and 2.4).
 #include <cuda_bf16.h>

@@ -76,7 +76,11 @@ def kda_rope_inv_freq(dim, base=10000.0, *, scaling=None, factor=1.0, original=N
     ``"ramp"``    pairs that turn more than ``beta_fast`` times over the ``original``
                   context as before, those that turn less than ``beta_slow`` times
                   divided by ``factor``, those between in proportion to their index
-                  (such models multiply by ``0.1 log(factor) + 1``: ``kda_rope``'s scale)."""
+                  (such models multiply by ``0.1 log(factor) + 1``: ``kda_rope``'s scale).
+
+    "ramp" is the method of Peng, Quesnelle, Fan and Shippole, "YaRN: Efficient Context
+    Window Extension of Large Language Models" (2023), with the borders rounded outwards and
+    held to 0 and ``dim - 1``, as models trained with it have them."""
     if dim < 2 or dim % 2:
         raise ValueError(f"dim must be even and positive, got {dim}")
     if not (base > 1.0 and math.isfinite(base)):

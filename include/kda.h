@@ -841,8 +841,9 @@ int kda_latent_weights_workspace_size(int32_t B, int32_t T, int32_t H, int32_t d
  * A sequence whose length is out of range, or with a page id outside [0, n_pages), records
  * KDA_ERR_INVALID_ARG in the status; its weights stay as they are where the length is out
  * of range, and are undefined where a page is.
- * Results do not vary between calls.  Queries must be finite; a cached row that is not
- * makes its own weight so and no other.
+ * Results do not vary between calls with the same arguments; with T * H above 128 the last
+ * bits of a sequence's weights depend on what other sequences the call has.  Queries must be
+ * finite; a cached row that is not makes its own weight so and no other.
  * Workspace: kda_latent_weights_workspace_size() bytes, 16-byte aligned; the status word is
  * set by the call (kda_read_device_status), and kda_latent_test_timeout arms its waits too.
  * Alignment: q, cache 16 bytes; tree_mask 8; the others 4.  Limits and errors as
@@ -872,7 +873,8 @@ int kda_cache_evict_workspace_size(int32_t L, int32_t B, int32_t budget, size_t 
  * as few of them move as can.  Sequences of at most budget rows stay as they are.
  *   weights      [L, B, max_pages * page_size] fp32
  *   weights_out  the same shape, or weights itself: the kept rows' weights at their new
- *                places, and 0 from the new length on
+ *                places, and 0 from the new length on, to the table's end: all of it is
+ *                written, and costs time, in every call
  *   new_lens     [B] int32: min(n, budget)
  *   origin       [L, B, budget] int32: the former position of the row now at each place,
  *                -1 from the new length on
